@@ -6,7 +6,8 @@ tensor's device pointer, and the current HIP stream of torch unless a stream
 is given).  All arithmetic runs in the library's HIP kernels; there is no
 fallback: if the library is missing every call raises.
 
-``Plan`` and ``E3ConvFunction`` are conveniences over the same calls.
+``Plan``, ``E3ConvFunction``, ``AttentionFunction`` and ``GroupNormFunction`` are
+conveniences over the same calls.
 """
 
 import ctypes
@@ -25,6 +26,9 @@ E3CONV_SENDER = 1
 E3CONV_ACCUMULATE_GRAD_X = 1
 E3CONV_ACCUMULATE_GRAD_Y = 2
 E3CONV_ACCUMULATE_GRAD_S = 4
+E3CONV_ACT_NONE, E3CONV_ACT_RELU, E3CONV_ACT_SILU, E3CONV_ACT_GELU = 0, 1, 2, 3
+ACTIVATIONS = {"none": E3CONV_ACT_NONE, "relu": E3CONV_ACT_RELU, "silu": E3CONV_ACT_SILU,
+               "gelu": E3CONV_ACT_GELU}
 
 STATUS_NAMES = {
     0: "E3CONV_OK", 1: "E3CONV_ERR_INVALID_ARGUMENT", 2: "E3CONV_ERR_PARSE",
@@ -45,6 +49,8 @@ EXPORTED = [
     "e3conv_stream_reference", "e3conv_second_derivatives", "e3conv_backward_pairs", "e3conv_pair_layout", "e3conv_forward_linear", "e3conv_forward_pairs",
     "e3conv_plan_set_variant",
     "e3conv_plan_num_variants",
+    "e3conv_attention_workspace_size", "e3conv_attention", "e3conv_attention_backward",
+    "e3conv_group_norm_workspace_size", "e3conv_group_norm", "e3conv_group_norm_backward",
     "e3conv_status_string", "e3conv_last_error_detail",
 ]
 
@@ -61,6 +67,23 @@ _lib = None
 P = ctypes.c_void_p
 I32P = ctypes.POINTER(ctypes.c_int)
 I64 = ctypes.c_int64
+
+
+class AttentionArgs(ctypes.Structure):
+    """e3conv_attention_args."""
+    _fields_ = [("dtype", ctypes.c_int), ("num_graphs", ctypes.c_int32), ("heads_q", ctypes.c_int32),
+                ("heads_kv", ctypes.c_int32), ("dim_qk", ctypes.c_int32), ("dim_v", ctypes.c_int32),
+                ("num_q", I64), ("num_k", I64), ("scale", ctypes.c_float), ("q_ptr", P), ("k_ptr", P),
+                ("q_mask", P), ("k_mask", P), ("q", P), ("k", P), ("v", P), ("q_row", I64),
+                ("q_head", I64), ("k_row", I64), ("k_head", I64), ("v_row", I64), ("v_head", I64)]
+
+
+class GroupNormArgs(ctypes.Structure):
+    """e3conv_group_norm_args."""
+    _fields_ = [("dtype", ctypes.c_int), ("num_graphs", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("activation", ctypes.c_int), ("eps", ctypes.c_float),
+                ("num_rows", I64), ("row_ptr", P), ("row_mask", P), ("x", P), ("x_row", I64),
+                ("weight", P), ("bias", P)]
 
 
 def load_library(path=LIB_PATH):
@@ -121,6 +144,12 @@ def load_library(path=LIB_PATH):
                                        P, P, P, P, P], ctypes.c_int),
         "e3conv_plan_set_variant": ([P, ctypes.c_int, ctypes.c_int], ctypes.c_int),
         "e3conv_plan_num_variants": ([P, ctypes.c_int, I32P, I32P], ctypes.c_int),
+        "e3conv_attention_workspace_size": ([P, ctypes.c_int, P], ctypes.c_int),
+        "e3conv_attention": ([P, P, I64, I64, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "e3conv_attention_backward": ([P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "e3conv_group_norm_workspace_size": ([P, ctypes.c_int, P], ctypes.c_int),
+        "e3conv_group_norm": ([P, P, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "e3conv_group_norm_backward": ([P, P, P, P, I64, P, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "e3conv_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "e3conv_last_error_detail": ([], ctypes.c_char_p),
     }
@@ -548,6 +577,251 @@ def e3conv_last_error_detail():
     return load_library().e3conv_last_error_detail().decode()
 
 
+# --------------------------------------- graph attention, group norm ---
+
+def _rows_of(t, name, dtype, device, shape):
+    """A device operand whose last axis has unit stride; other strides are free."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride along its last axis")
+
+
+def _dense(t, name, dtype, device, n):
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
+
+
+def _node_mask(t, name, device, n):
+    """Address of a node mask (bool or uint8, one byte per node), or None."""
+    if t is None:
+        return None
+    import torch
+    _dense(t, name, torch.bool if t.dtype == torch.bool else torch.uint8, device, n)
+    return t.data_ptr()
+
+
+def _written(t, name):
+    """An output whose elements do not overlap (the kernels write every one of them)."""
+    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} is written and must not repeat elements (zero stride)")
+
+
+def _enter(device, stream):
+    """(stream handle, stream object to record allocations on or None) of a call on `device`."""
+    import torch
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"operands are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    current = torch.cuda.current_stream(device)
+    if stream is None:
+        return current.cuda_stream, None
+    handle = int(getattr(stream, "cuda_stream", stream))
+    if handle == current.cuda_stream:
+        return handle, None
+    return handle, stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=device)
+
+
+def _workspace(given, need, device, other):
+    """(address, bytes, tensor) of the caller's workspace, or of one allocated for the call."""
+    import torch
+    if given is not None:
+        if not given.is_cuda or given.device != device or not given.is_contiguous() or given.data_ptr() % 16:
+            raise ValueError(f"workspace must be a contiguous, 16-byte aligned tensor on {device}")
+        return given.data_ptr(), given.numel() * given.element_size(), given
+    if need == 0:
+        return None, 0, None
+    t = torch.empty(need, dtype=torch.uint8, device=device)
+    if other is not None:
+        t.record_stream(other)
+    return t.data_ptr(), need, t
+
+
+def _allocate(shape, dtype, device, other):
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if other is not None:
+        t.record_stream(other)   # freed memory is not reused before that stream is done with it
+    return t
+
+
+def _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask):
+    import torch
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q (num_q, heads_q, dim_qk), k (num_k, heads_kv, dim_qk), v (num_k, heads_kv, dim_v)")
+    code, dev = _dtype_code(q), q.device
+    nq, hq, d = q.shape
+    nk, hk, _ = k.shape
+    dv = v.shape[2]
+    _rows_of(q, "q", q.dtype, dev, q.shape)
+    _rows_of(k, "k", q.dtype, dev, (nk, hk, d))
+    _rows_of(v, "v", q.dtype, dev, (nk, hk, dv))
+    graphs = q_ptr.numel() - 1
+    if graphs < 0:
+        raise ValueError("q_ptr must hold num_graphs + 1 offsets")
+    _dense(q_ptr, "q_ptr", torch.int32, dev, graphs + 1)
+    _dense(k_ptr, "k_ptr", torch.int32, dev, graphs + 1)
+    scale = d ** -0.5 if scale is None else float(scale)
+    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, scale, q_ptr.data_ptr(), k_ptr.data_ptr(),
+                         _node_mask(q_mask, "q_mask", dev, nq), _node_mask(k_mask, "k_mask", dev, nk),
+                         q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), q.stride(1), k.stride(0),
+                         k.stride(1), v.stride(0), v.stride(1))
+
+
+def e3conv_attention_workspace_size(args, backward=False):
+    """Bytes of workspace for the sizes in an AttentionArgs."""
+    n = ctypes.c_size_t()
+    _check(load_library().e3conv_attention_workspace_size(ctypes.byref(args), int(bool(backward)),
+                                                          ctypes.byref(n)))
+    return n.value
+
+
+def e3conv_attention(q, k, v, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None, out=None, lse=None,
+                     workspace=None, stream=None):
+    """(out, lse): every query of graph g attends to the unmasked keys of graph g.
+
+    q (num_q, heads_q, dim_qk), k (num_k, heads_kv, dim_qk), v (num_k, heads_kv, dim_v), fp32 or bf16, any
+    strides but unit along the last axis; q_ptr, k_ptr int32 offsets of the graphs; scale defaults to
+    dim_qk ** -0.5; masks are bool or uint8, one value per row, 0 for padding.  lse fp32 (num_q, heads_q).
+    """
+    import torch
+    args = _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask)
+    dev, shape = q.device, (args.num_q, args.heads_q, args.dim_v)
+    handle, other = _enter(dev, stream)
+    if out is None:
+        out = _allocate(shape, q.dtype, dev, other)
+    else:
+        _rows_of(out, "out", q.dtype, dev, shape)
+        _written(out, "out")
+    if lse is None:
+        lse = _allocate(shape[:2], torch.float32, dev, other)
+    else:
+        _dense(lse, "lse", torch.float32, dev, args.num_q * args.heads_q)
+    ws, nbytes, _keep = _workspace(workspace, 0 if workspace is not None else e3conv_attention_workspace_size(args),
+                                   dev, other)
+    _check(load_library().e3conv_attention(ctypes.byref(args), out.data_ptr(), out.stride(0), out.stride(1),
+                                           lse.data_ptr(), ws, nbytes, handle))
+    return out, lse
+
+
+def e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None,
+                              grads=None, workspace=None, stream=None):
+    """(grad_q, grad_k, grad_v) of <grad_out, out>, with out and lse from e3conv_attention.
+
+    grads: three output tensors (strides free but unit along the last axis), or None to allocate them.
+    """
+    import torch
+    args = _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask)
+    dev, shape = q.device, (args.num_q, args.heads_q, args.dim_v)
+    _rows_of(out, "out", q.dtype, dev, shape)
+    _rows_of(grad_out, "grad_out", q.dtype, dev, shape)
+    _dense(lse, "lse", torch.float32, dev, args.num_q * args.heads_q)
+    handle, other = _enter(dev, stream)
+    if grads is None:
+        grads = tuple(_allocate(t.shape, t.dtype, dev, other) for t in (q, k, v))
+    else:
+        for t, ref, name in zip(grads, (q, k, v), ("grad_q", "grad_k", "grad_v")):
+            _rows_of(t, name, q.dtype, dev, ref.shape)
+            _written(t, name)
+    gq, gk, gv = grads
+    ws, nbytes, _keep = _workspace(workspace, 0 if workspace is not None
+                                   else e3conv_attention_workspace_size(args, True), dev, other)
+    strides = (I64 * 10)(*(s for t in (out, grad_out, gq, gk, gv) for s in t.stride()[:2]))
+    _check(load_library().e3conv_attention_backward(
+        ctypes.byref(args), out.data_ptr(), lse.data_ptr(), grad_out.data_ptr(), gq.data_ptr(), gk.data_ptr(),
+        gv.data_ptr(), strides, ws, nbytes, handle))
+    return gq, gk, gv
+
+
+def _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask):
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be (num_rows, channels)")
+    code, dev = _dtype_code(x), x.device
+    n, c = x.shape
+    _rows_of(x, "x", x.dtype, dev, x.shape)
+    graphs = row_ptr.numel() - 1
+    if graphs < 0:
+        raise ValueError("row_ptr must hold num_graphs + 1 offsets")
+    _dense(row_ptr, "row_ptr", torch.int32, dev, graphs + 1)
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _dense(t, name, torch.float32, dev, c)
+    act = ACTIVATIONS.get(activation, activation)
+    if not isinstance(act, int):
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    return GroupNormArgs(code, graphs, c, int(groups), act, float(eps), n, row_ptr.data_ptr(),
+                         _node_mask(row_mask, "row_mask", dev, n), x.data_ptr(), x.stride(0),
+                         None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr())
+
+
+def e3conv_group_norm_workspace_size(args, backward=False):
+    """Bytes of workspace for the sizes in a GroupNormArgs."""
+    n = ctypes.c_size_t()
+    _check(load_library().e3conv_group_norm_workspace_size(ctypes.byref(args), int(bool(backward)),
+                                                           ctypes.byref(n)))
+    return n.value
+
+
+def e3conv_group_norm(x, row_ptr, groups, weight=None, bias=None, eps=1e-5, activation="none", row_mask=None,
+                      out=None, workspace=None, stream=None):
+    """(y, mean, rstd): act(weight * xhat + bias) with statistics per graph and group of channels.
+
+    x (num_rows, channels) fp32 or bf16, unit stride along the channels (x[:, 0, :] of node features is
+    fine); row_ptr int32 offsets of the graphs; weight, bias fp32 or None; activation "none", "relu", "silu"
+    or "gelu"; row_mask bool or uint8, 0 for padding.  mean, rstd fp32 (num_graphs, groups).
+    """
+    import torch
+    args = _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask)
+    dev = x.device
+    handle, other = _enter(dev, stream)
+    if out is None:
+        out = _allocate(x.shape, x.dtype, dev, other)
+    else:
+        _rows_of(out, "out", x.dtype, dev, x.shape)
+        _written(out, "out")
+    mean = _allocate((args.num_graphs, args.groups), torch.float32, dev, other)
+    rstd = _allocate((args.num_graphs, args.groups), torch.float32, dev, other)
+    ws, nbytes, _keep = _workspace(workspace, 0 if workspace is not None else e3conv_group_norm_workspace_size(args),
+                                   dev, other)
+    _check(load_library().e3conv_group_norm(ctypes.byref(args), out.data_ptr(), out.stride(0), mean.data_ptr(),
+                                            rstd.data_ptr(), ws, nbytes, handle))
+    return out, mean, rstd
+
+
+def e3conv_group_norm_backward(x, row_ptr, groups, weight, bias, activation, mean, rstd, grad_y, row_mask=None,
+                               grad_x=None, workspace=None, stream=None):
+    """(grad_x, grad_weight, grad_bias); a gradient is None where its operand is."""
+    import torch
+    # eps is already in rstd
+    args = _group_norm_args(x, row_ptr, groups, weight, bias, 1.0, activation, row_mask)
+    dev = x.device
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _dense(t, name, torch.float32, dev, args.num_graphs * args.groups)
+    _rows_of(grad_y, "grad_y", x.dtype, dev, x.shape)
+    handle, other = _enter(dev, stream)
+    if grad_x is None:
+        grad_x = _allocate(x.shape, x.dtype, dev, other)
+    else:
+        _rows_of(grad_x, "grad_x", x.dtype, dev, x.shape)
+        _written(grad_x, "grad_x")
+    gw, gb = (None if t is None else _allocate(t.shape, torch.float32, dev, other) for t in (weight, bias))
+    ws, nbytes, _keep = _workspace(workspace, 0 if workspace is not None
+                                   else e3conv_group_norm_workspace_size(args, True), dev, other)
+    _check(load_library().e3conv_group_norm_backward(
+        ctypes.byref(args), mean.data_ptr(), rstd.data_ptr(), grad_y.data_ptr(), grad_y.stride(0),
+        grad_x.data_ptr(), grad_x.stride(0), None if gw is None else gw.data_ptr(),
+        None if gb is None else gb.data_ptr(), ws, nbytes, handle))
+    return grad_x, gw, gb
+
+
 # ------------------------------------------------------ convenience ---
 
 class Plan:
@@ -782,7 +1056,68 @@ def _autograd_function():
     return E3ConvFunction
 
 
+def _attention_function():
+    import torch
+
+    class AttentionFunction(torch.autograd.Function):
+        """out of e3conv_attention, differentiable in q, k and v.
+
+        apply(q, k, v, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None).
+        """
+
+        @staticmethod
+        def forward(ctx, q, k, v, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None):
+            out, lse = e3conv_attention(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask)
+            ctx.save_for_backward(q, k, v, out, lse)
+            ctx.graph = (q_ptr, k_ptr, scale, q_mask, k_mask)
+            return out
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_out):
+            if grad_out.stride(-1) != 1:
+                grad_out = grad_out.contiguous()
+            return e3conv_attention_backward(*ctx.saved_tensors, grad_out, *ctx.graph) + (None,) * 5
+
+    return AttentionFunction
+
+
+def _group_norm_function():
+    import torch
+
+    class GroupNormFunction(torch.autograd.Function):
+        """y of e3conv_group_norm, differentiable in x, weight and bias.
+
+        apply(x, row_ptr, groups, weight=None, bias=None, eps=1e-5, activation="none", row_mask=None).
+        """
+
+        @staticmethod
+        def forward(ctx, x, row_ptr, groups, weight=None, bias=None, eps=1e-5, activation="none",
+                    row_mask=None):
+            y, mean, rstd = e3conv_group_norm(x, row_ptr, groups, weight, bias, eps, activation, row_mask)
+            ctx.save_for_backward(x, weight, bias, mean, rstd)
+            ctx.graph = (row_ptr, groups, activation, row_mask)
+            return y
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_y):
+            x, weight, bias, mean, rstd = ctx.saved_tensors
+            row_ptr, groups, activation, row_mask = ctx.graph
+            if grad_y.stride(-1) != 1:
+                grad_y = grad_y.contiguous()
+            gx, gw, gb = e3conv_group_norm_backward(x, row_ptr, groups, weight, bias, activation, mean, rstd,
+                                                    grad_y, row_mask)
+            return gx, None, None, gw, gb, None, None, None
+
+    return GroupNormFunction
+
+
+_FUNCTIONS = {"E3ConvFunction": _autograd_function, "AttentionFunction": _attention_function,
+              "GroupNormFunction": _group_norm_function}
+
+
 def __getattr__(name):
-    if name == "E3ConvFunction":
-        return _autograd_function()
+    if name in _FUNCTIONS:
+        return _FUNCTIONS[name]()
     raise AttributeError(name)

@@ -447,6 +447,140 @@ e3conv_status e3conv_pair_layout(const int32_t* row_ptr, const int32_t* src, int
                                  int64_t num_edges, int cluster, int32_t* stored,
                                  int32_t* pair_of);
 
+/* Attention among the nodes of each graph, beside the local convolution: the
+ * queries of graph g are rows q_ptr[g] .. q_ptr[g+1]-1 of q and see the keys
+ * k_ptr[g] .. k_ptr[g+1]-1 of k and v, and no others.  For query row i and
+ * query head h, with kv head c = h / (heads_q / heads_kv) (consecutive query
+ * heads share a kv head),
+ *     P[i, h, j] = exp(scale <q[i, h], k[j, c]> - lse[i, h]) over the seen keys j,
+ *     out[i, h]  = sum_j P[i, h, j] v[j, c],   lse the log of the sum of exponentials.
+ * Nodes form a set, so there is no order among keys.  Self attention passes the
+ * same offsets twice; pooling by query tokens, or one new node against a grown
+ * structure, passes few queries per graph.
+ * - dtype: storage of q, k, v, out and of all gradients (fp32 or bf16); lse,
+ *   the softmax statistics and every sum are fp32.  With fp32 the products are
+ *   of fp32 accuracy; with bf16 the probabilities (and, in the reverse pass,
+ *   their gradients) are rounded to bf16 before their product.
+ * - q (num_q, heads_q, dim_qk), k (num_k, heads_kv, dim_qk), v (num_k, heads_kv,
+ *   dim_v): unit stride along the last axis, row and head strides in elements
+ *   (*_row, *_head >= 0; a zero stride repeats the operand).  1 <= dim <= 128;
+ *   element alignment is enough (16-byte aligned rows are read faster).
+ * - q_ptr, k_ptr: device int32[num_graphs + 1], non-decreasing from 0 to num_q /
+ *   num_k (anything else gives undefined values, but no access out of range).
+ * - q_mask (num_q), k_mask (num_k): device bytes or NULL (all rows count).  A key
+ *   whose byte is 0 is not seen, whatever its k and v hold (NaN too); a query
+ *   whose byte is 0 sees no key.  Both get zero gradients.
+ * - A query that sees no key has out = 0, lse = -infinity and a zero gradient.
+ * heads_q must be a multiple of heads_kv; num_q * heads_q and num_k * heads_kv < 2^31 - 2^20;
+ * scale finite.  Offsets into the tensors are 64 bits wide. */
+typedef struct {
+  e3conv_dtype dtype;
+  int32_t num_graphs;
+  int32_t heads_q, heads_kv;
+  int32_t dim_qk, dim_v;
+  int64_t num_q, num_k;
+  float scale;
+  const int32_t* q_ptr;
+  const int32_t* k_ptr;
+  const uint8_t* q_mask;
+  const uint8_t* k_mask;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+} e3conv_attention_args;
+
+/* Bytes of device workspace (16-byte aligned) that e3conv_attention (backward
+ * = 0) or e3conv_attention_backward (backward = 1) needs for these sizes; the
+ * pointers of args are not read. */
+e3conv_status e3conv_attention_workspace_size(const e3conv_attention_args* args, int backward,
+                                              size_t* bytes);
+
+/* out (num_q, heads_q, dim_v) with strides out_row, out_head, fully written; lse
+ * float (num_q, heads_q), dense, or NULL.  Asynchronous on hip_stream; the
+ * workspace may be reused once the stream has passed the call. */
+e3conv_status e3conv_attention(const e3conv_attention_args* args, void* out, int64_t out_row,
+                               int64_t out_head, float* lse, void* workspace,
+                               size_t workspace_bytes, void* hip_stream);
+
+/* Reverse pass of L = <grad_out, out>.  The probabilities are formed again
+ * from q, k and the forward's lse; with delta[i, h] = <grad_out[i, h], out[i, h]>,
+ *     dP = <grad_out, v>,   dS = P (dP - delta),
+ *     grad_q = scale sum_j dS k,   grad_k = scale sum dS q,   grad_v = sum P grad_out,
+ * the last two summed over the rows and the query heads that share the kv
+ * head.  All three gradients are fully written, without atomics: the same
+ * inputs give the same bits.  out and grad_out as (num_q, heads_q, dim_v),
+ * gradients shaped as their operands, each with its own row and head strides:
+ * strides holds (row, head) of out, grad_out, grad_q, grad_k, grad_v in turn. */
+e3conv_status e3conv_attention_backward(const e3conv_attention_args* args, const void* out,
+                                        const float* lse, const void* grad_out, void* grad_q,
+                                        void* grad_k, void* grad_v, const int64_t strides[10],
+                                        void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* Activations of e3conv_group_norm: z, max(z, 0), z / (1 + e^-z) and
+ * z (1 + erf(z / sqrt 2)) / 2. */
+typedef enum {
+  E3CONV_ACT_NONE = 0,
+  E3CONV_ACT_RELU = 1,
+  E3CONV_ACT_SILU = 2,
+  E3CONV_ACT_GELU = 3
+} e3conv_activation;
+
+/* Group norm with an activation over the rows of each graph, channels last:
+ * the channels split into `groups` runs of channels / groups, and with mean and
+ * var over the counted rows of graph g and the channels of a group,
+ *     xhat = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),
+ *     y    = act(weight[c] xhat + bias[c]).
+ * It acts on the scalar (l = 0) channels of node features: with x_row =
+ * num_x * C the scalar block is normalised in place in its (N, num_x, C) array.
+ * - x, y (num_rows, channels) in dtype (fp32 or bf16), unit stride along the
+ *   channels, row strides in elements; weight, bias fp32 (channels) or NULL
+ *   (1 and 0); statistics and arithmetic fp32.
+ * - row_ptr: device int32[num_graphs + 1], non-decreasing from 0 to num_rows (as
+ *   q_ptr above); row_mask: device bytes (num_rows) or NULL; a row whose byte
+ *   is 0 is not counted, whatever it holds, and gets y = 0 and a zero gradient.
+ * - mean, rstd: fp32 (num_graphs, groups), dense; a graph without counted rows
+ *   has mean = 0 and rstd = 1 / sqrt(eps).
+ * channels <= 4096, a multiple of groups; eps > 0; num_rows + num_graphs < 2^31 - 2^20. */
+typedef struct {
+  e3conv_dtype dtype;
+  int32_t num_graphs;
+  int32_t channels, groups;
+  e3conv_activation activation;
+  float eps;
+  int64_t num_rows;
+  const int32_t* row_ptr;
+  const uint8_t* row_mask;
+  const void* x;
+  int64_t x_row;
+  const float* weight;
+  const float* bias;
+} e3conv_group_norm_args;
+
+/* Bytes of device workspace (16-byte aligned) of the two calls below. */
+e3conv_status e3conv_group_norm_workspace_size(const e3conv_group_norm_args* args, int backward,
+                                               size_t* bytes);
+
+/* y, mean and rstd are fully written (mean and rstd may be NULL).  y may be x
+ * itself, with the same stride. */
+e3conv_status e3conv_group_norm(const e3conv_group_norm_args* args, void* y, int64_t y_row,
+                                float* mean, float* rstd, void* workspace, size_t workspace_bytes,
+                                void* hip_stream);
+
+/* Reverse pass: with z = weight xhat + bias from x and the forward's mean and
+ * rstd, dz = grad_y act'(z) (act'(0) = 0 for the rectifier) and means over the
+ * counted rows and the group,
+ *     grad_x = rstd (weight dz - mean(weight dz) - xhat mean(weight dz xhat)),
+ *     grad_weight[c] = sum dz xhat,   grad_bias[c] = sum dz   over all counted rows.
+ * grad_x may be grad_y itself, with the same stride.  grad_weight and
+ * grad_bias are fp32 (channels) or NULL (not computed); all outputs are fully
+ * written, without atomics: the same inputs give the same bits. */
+e3conv_status e3conv_group_norm_backward(const e3conv_group_norm_args* args, const float* mean,
+                                         const float* rstd, const void* grad_y, int64_t grad_y_row,
+                                         void* grad_x, int64_t grad_x_row, float* grad_weight,
+                                         float* grad_bias, void* workspace, size_t workspace_bytes,
+                                         void* hip_stream);
+
 /* Check a graph (the e3j Convolution page, __call__: indices lie in
  * [0, num_nodes); the fused kernels need edges sorted by receiver): row_ptr[0]
  * = 0, row_ptr non-decreasing and within [0, num_edges], row_ptr[num_nodes] =

@@ -29,9 +29,11 @@ variants -- SENDER graph ordering, pair storage (one row of y and s per
 linear  -- the output linear (channel mixing per irrep block) and its gradients.
 radial  -- edge scalars from edge lengths (radial basis, cutoff, two-layer
            network) and the convolution they feed.
+attention -- attention among the nodes of each graph and its gradients.
+norm    -- group norm with an activation per graph and its gradients.
 
 Pins (what ties this oracle to something other than itself) live in
 ``tests/test_oracle_*.py``; every function here is pinned there.
 """
 
-from . import irreps, so3, conv, variants, linear, radial  # noqa: F401
+from . import irreps, so3, conv, variants, linear, radial, attention, norm  # noqa: F401

@@ -1,0 +1,240 @@
+"""Group norm with an activation per graph and its reverse pass against oracle.norm.
+
+Tolerances are the elementwise bounds oracle.norm.group_norm derives from fp32
+roundings of u = 2^-24 and, for bf16 storage, one rounding of 2^-8 (eight significant bits) of y and dx.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import norm
+from equivariant_gnn_message_amd import e3conv as E
+
+from ._gpu import say
+from .test_gpu_attention import U, dev, dtype_of, host, ptr
+
+pytestmark = pytest.mark.gpu
+
+
+def check(dtype, lens, channels, groups, act="silu", affine=True, mask=None, shift=0.5, spread=1.5, eps=1e-5,
+          poison=False, seed=0):
+    import torch
+    gen = torch.Generator().manual_seed(seed + channels)
+    n = int(sum(lens))
+    x = (spread * torch.randn((n, channels), generator=gen) + shift).to(dtype_of(dtype)).cuda()
+    g = torch.randn((n, channels), generator=gen).to(dtype_of(dtype)).cuda()
+    w = (1 + 0.3 * torch.randn(channels, generator=gen)).cuda() if affine else None
+    b = (0.3 * torch.randn(channels, generator=gen)).cuda() if affine else None
+    if act == "relu" and n:      # keep z away from the corner: its derivative is a step there
+        z = norm.group_norm(host(x), ptr(lens), groups, None if w is None else host(w),
+                            None if b is None else host(b), eps, "none", mask)[0]["y"]
+        g[dev(np.abs(z) < 1e-3)] = 0
+    if poison:
+        x[dev(mask == 0)] = float("nan")
+        g[dev(mask == 0)] = float("inf")
+    m = None if mask is None else dev(mask)
+    p = dev(ptr(lens))
+    say(f"[group norm] {dtype} rows {n} in {len(lens)} graphs, {channels} channels, {groups} groups, {act}")
+    y, mean, rstd = E.e3conv_group_norm(x, p, groups, w, b, eps, act, m)
+    gx, gw, gb = E.e3conv_group_norm_backward(x, p, groups, w, b, act, mean, rstd, g, m)
+    torch.cuda.synchronize()
+    u, r = U[dtype]
+    clean = lambda t: host(t) if mask is None else np.where(np.asarray(mask, bool)[:, None], host(t), 0.0)
+    val, tol = norm.group_norm(clean(x), ptr(lens), groups, None if w is None else host(w),
+                               None if b is None else host(b), float(np.float32(eps)), act, mask, clean(g), u, r)
+    got = {"y": y, "mean": mean, "rstd": rstd, "dx": gx}
+    if affine:
+        got.update(dw=gw, dc=gb)
+    else:
+        assert gw is None and gb is None
+    for name, t in got.items():
+        off = np.abs(host(t) - val[name])
+        worst = float(np.max(off - tol[name], initial=-1.0))
+        say(f"  {name}: max err {float(np.max(off, initial=0.0)):.3e}, over its bound by {worst:.3e}")
+        finite = bool(np.all(np.isfinite(off)))
+        assert finite and worst <= 1e-30, (name, worst)
+    return {k: host(t) for k, t in got.items()}
+
+
+LENS = [0, 1, 2, 63, 64, 65, 300]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("channels,groups", [(1, 1), (6, 3), (8, 1), (32, 8), (33, 11), (64, 64), (72, 4), (128, 32),
+                                             (160, 1), (256, 2), (1000, 5)])
+def test_shapes(dtype, channels, groups):
+    check(dtype, LENS, channels, groups)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+@pytest.mark.parametrize("affine", [True, False])
+def test_activations(dtype, act, affine):
+    check(dtype, [40, 0, 129], 32, 4, act, affine)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[20011], [7, 9001, 0, 4000], [30] * 300, [1] * 50, [0, 0, 5, 0]],
+                         ids=["one", "unlike", "many", "single-rows", "mostly-empty"])
+def test_lengths(dtype, lens):
+    check(dtype, lens, 64, 8)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_mean_far_from_zero(dtype):
+    """Mean 300 times the spread: the variance is taken about the mean, not from squares."""
+    check(dtype, [5000, 70], 32, 4, "none", shift=300.0, spread=1.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_constant_rows(dtype):
+    check(dtype, [64, 3], 16, 2, "none", spread=0.0, eps=1e-3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("channels,groups", [(32, 4), (33, 3), (64, 64)])
+def test_masked_rows_hold_anything(dtype, channels, groups):
+    lens = [40, 6, 200, 0, 3000]
+    mask = (np.random.default_rng(1).random(sum(lens)) < 0.6).astype(np.uint8)
+    mask[40:46] = 0
+    got = check(dtype, lens, channels, groups, mask=mask, poison=True)
+    assert np.all(got["y"][mask == 0] == 0) and np.all(got["dx"][mask == 0] == 0)
+    assert np.all(got["mean"][1] == 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_strides(dtype):
+    """The scalar block of (N, num_x, C) features, unaligned rows, outputs in place and in strided storage."""
+    import torch
+    lens = [100, 0, 2500]
+    n, p = sum(lens), dev(ptr(lens))
+    gen = torch.Generator().manual_seed(4)
+    x = torch.randn((n, 64), generator=gen).to(dtype_of(dtype)).cuda()
+    g = torch.randn((n, 64), generator=gen).to(dtype_of(dtype)).cuda()
+    w, b = torch.rand(64, generator=gen).cuda(), torch.rand(64, generator=gen).cuda()
+    ref = E.e3conv_group_norm(x, p, 8, w, b, 1e-5, "silu")
+    back = E.e3conv_group_norm_backward(x, p, 8, w, b, "silu", ref[1], ref[2], g)
+    torch.cuda.synchronize()
+    feats = torch.full((n, 4, 64), 9.0, dtype=x.dtype, device="cuda")
+    feats[:, 0] = x
+    wide = torch.full((n, 67), 9.0, dtype=x.dtype, device="cuda")
+    wide[:, 1:65] = x
+    gwide = torch.full((n, 65), 9.0, dtype=x.dtype, device="cuda")
+    gwide[:, 1:] = g
+    for xs, gs in ((feats[:, 0], g), (wide[:, 1:65], gwide[:, 1:]), (x, gwide[:, 1:])):
+        got = E.e3conv_group_norm(xs, p, 8, w, b, 1e-5, "silu")
+        grads = E.e3conv_group_norm_backward(xs, p, 8, w, b, "silu", got[1], got[2], gs)
+        torch.cuda.synchronize()
+        for a, c in zip(got + grads, ref + back):
+            torch.testing.assert_close(a, c, rtol=2e-2 if dtype == "bf16" else 1e-5, atol=1e-4)
+    gin = g.clone()
+    grads = E.e3conv_group_norm_backward(x, p, 8, w, b, "silu", ref[1], ref[2], gin, grad_x=gin)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(grads, back))
+    y = feats[:, 0]
+    E.e3conv_group_norm(y, p, 8, w, b, 1e-5, "silu", out=y)          # in place in its array
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref[0]) and bool((feats[:, 1:] == 9).all())
+
+
+@pytest.mark.parametrize("lens", [[50, 0, 31], [40000, 3]])
+def test_same_bits_streams_and_graph_replays(lens):
+    import torch
+    n, p = sum(lens), dev(ptr(lens))
+    gen = torch.Generator().manual_seed(5)
+    x, g = (torch.randn((n, 64), generator=gen).cuda() for _ in range(2))
+    w, b = torch.rand(64, generator=gen).cuda(), torch.rand(64, generator=gen).cuda()
+
+    def step(stream=None):
+        y, mean, rstd = E.e3conv_group_norm(x, p, 4, w, b, 1e-5, "gelu", stream=stream)
+        return (y, mean, rstd) + E.e3conv_group_norm_backward(x, p, 4, w, b, "gelu", mean, rstd, g, stream=stream)
+
+    ref = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        got = step(stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(got, ref))
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(4):
+        for t in got:
+            t.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(got, ref))
+
+
+def test_offsets_past_32_bits():
+    import torch
+    n, step = 1100, 1 << 21
+    store = torch.empty(n * step, dtype=torch.bfloat16, device="cuda").view(n, step)
+    gen = torch.Generator().manual_seed(6)
+    x, g = (torch.randn((n, 16), generator=gen).bfloat16().cuda() for _ in range(2))
+    fx, fg = store[:, :16], store[:, 16:32]
+    fx.copy_(x)
+    fg.copy_(g)
+    p = dev(ptr([n]))
+    ref = E.e3conv_group_norm(x, p, 2, activation="silu")
+    back = E.e3conv_group_norm_backward(x, p, 2, None, None, "silu", ref[1], ref[2], g)
+    got = E.e3conv_group_norm(fx, p, 2, activation="silu", out=store[:, 32:48])
+    grads = E.e3conv_group_norm_backward(fx, p, 2, None, None, "silu", got[1], got[2], fg, grad_x=store[:, 48:64])
+    torch.cuda.synchronize()
+    for a, c in zip(got, ref):
+        assert torch.equal(a, c)
+    assert torch.equal(grads[0], back[0])
+
+
+def test_autograd():
+    """GroupNormFunction against a directional difference in fp32: the five-point rule at h = 1/32 has a
+    truncation of h^4/30 of an O(100) fifth derivative, rounding u sqrt(n) / h; both below 1e-2 of the scale."""
+    import torch
+    p = dev(ptr([30, 0, 21]))
+    gen = torch.Generator().manual_seed(7)
+    x, g = (torch.randn((51, 24), generator=gen).cuda() for _ in range(2))
+    w, b = torch.rand(24, generator=gen).cuda() + 0.5, torch.rand(24, generator=gen).cuda()
+    leaves = [t.clone().requires_grad_() for t in (x, w, b)]
+    F = lambda x, w, b: E.GroupNormFunction.apply(x, p, 4, w, b, 1e-5, "silu")
+    (F(*leaves) * g).sum().backward()
+    way = [torch.randn(t.shape, generator=gen).cuda() for t in (x, w, b)]
+    at = lambda h: float((F(*(t + h * d for t, d in zip((x, w, b), way))).double() * g.double()).sum())
+    slope = sum(float((t.grad.double() * d.double()).sum()) for t, d in zip(leaves, way))
+    h = 1 / 32
+    diff = (8 * (at(h) - at(-h)) - (at(2 * h) - at(-2 * h))) / (12 * h)
+    scale = sum(float(t.grad.double().norm()) for t in leaves)
+    assert abs(diff - slope) <= 1e-2 * scale
+
+
+def test_empty_calls_and_refusals():
+    import torch
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = torch.empty((0, 8), device="cuda")
+    y, mean, rstd = E.e3conv_group_norm(x, z, 2)
+    assert y.shape == (0, 8) and mean.shape == (0, 2)
+    w = torch.ones(8, device="cuda")
+    two = dev(ptr([0, 0]))
+    y, mean, rstd = E.e3conv_group_norm(x, two, 2, w, w, eps=0.25)
+    gx, gw, gb = E.e3conv_group_norm_backward(x, two, 2, w, w, "none", mean, rstd, x)
+    torch.cuda.synchronize()
+    assert not mean.any() and bool((rstd == 2).all()) and not gw.any() and not gb.any()
+    x, p = torch.ones((4, 8), device="cuda"), dev(ptr([4]))
+    for err, call in (
+            (E.E3ConvError, lambda: E.e3conv_group_norm(x, p, 3)),
+            (E.E3ConvError, lambda: E.e3conv_group_norm(x, p, 0)),
+            (E.E3ConvError, lambda: E.e3conv_group_norm(x, p, 2, eps=0.0)),
+            (E.E3ConvError, lambda: E.e3conv_group_norm(x, p, 2, activation=9)),
+            (ValueError, lambda: E.e3conv_group_norm(x, p, 2, activation="swish2")),
+            (ValueError, lambda: E.e3conv_group_norm(x.t(), p, 2)),
+            (ValueError, lambda: E.e3conv_group_norm(x, p, 2, w[:4])),
+            (TypeError, lambda: E.e3conv_group_norm(x, p, 2, w.bfloat16())),
+            (TypeError, lambda: E.e3conv_group_norm(x.double(), p, 2)),
+            (ValueError, lambda: E.e3conv_group_norm(x, p, 2, out=x[:1].expand(4, 8))),
+            (ValueError, lambda: E.e3conv_group_norm(x, p, 2, row_mask=torch.ones(3, dtype=torch.bool, device="cuda")))):
+        with pytest.raises(err):
+            call()
