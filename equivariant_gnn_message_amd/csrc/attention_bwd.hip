@@ -1,0 +1,442 @@
+// Reverse pass of attention on the matrix cores (contract in e3conv.h, tiles in
+// attention_tile.h).  Two kernels, each forming P = exp(S - lse) again, none with atomics:
+//
+// attn_bwd_q   a wave owns 32 rows and walks over the keys.  Rows along the columns:
+//                S^T = K Q^T,  dP^T = V G^T,  dS^T = P^T (dP^T - delta),  dQ^T += K^T dS^T;
+//              it also forms delta = <grad_out, out> of its rows and leaves it for
+// attn_bwd_kv  a wave owns 32 keys and walks over the rows of all query heads that
+//              share its kv head.  Keys along the columns:
+//                S = Q K^T,  dP = G V^T,  dV^T += G^T P,  dK^T += Q^T dS.
+// Seven products instead of the five of a single kernel that adds dQ by atomics: the
+// result is the same bits every time, and nothing but delta passes through memory.
+#include "attention_tile.h"
+#include "kernels.h"
+
+namespace e3c {
+namespace attn {
+namespace {
+
+template <class T, int D, int RW, int TK>
+__global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
+  constexpr int P = planes<T>(), U = D / 8, KS = D / 16, NT = 64 * RW, E = TK * U / NT;
+  static_assert(TK * U % NT == 0, "");
+  __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kt, vt;
+  const e3conv_attention_args& a = p.a;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
+
+  const int split = blockIdx.x % p.splits, slot = blockIdx.x / p.splits % p.slots;
+  const int c = blockIdx.x / p.splits / p.slots;
+  constexpr int BM = 32 * RW;
+  const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
+  const int q0 = offset(a.q_ptr, g, a.num_q);
+  const int nrows = (offset(a.q_ptr, g + 1, a.num_q) - q0) * p.group;
+  const int r0 = (slot - first_slot(a.q_ptr, g, a.num_q, p.group, BM)) * BM;
+  if (r0 >= nrows) return;
+
+  const int r = r0 + 32 * w + n;
+  const bool row = r < nrows;
+  const int qi = q0 + (row ? r / p.group : 0), head = c * p.group + (row ? r % p.group : 0);
+  const long at = (long)qi * a.heads_q + head;
+  float lse = p.lse[at];
+  const bool live = row && (!a.q_mask || a.q_mask[qi]) && lse != -INFINITY;
+  lse = live ? lse * kLog2e : 0.0f;
+
+  const int kb = offset(a.k_ptr, g, a.num_k), ke = offset(a.k_ptr, g + 1, a.num_k);
+  const int tiles = ke > kb ? (ke - kb + TK - 1) / TK : 0, per = (tiles + p.splits - 1) / p.splits;
+  int k0 = kb + min(split * per, tiles) * TK;
+  const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
+
+  const T* kbase = (const T*)a.k + c * a.k_head;
+  const T* vbase = (const T*)a.v + c * a.v_head;
+  Raw<T> kr[E], vr[E];
+  bool keep[E], key = false;
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int t = threadIdx.x + e * NT, j = k0 + t / U, d = t % U * 8;
+      const bool in = j < k1;
+      kr[e] = fetch8(kbase + j * a.k_row + d, in ? a.dim_qk - d : 0, p.vec);
+      vr[e] = fetch8(vbase + j * a.v_row + d, in ? a.dim_v - d : 0, p.vec);
+      keep[e] = in && (!a.k_mask || a.k_mask[j]);
+    }
+    const int j = k0 + lane;
+    key = lane < TK && j < k1 && (!a.k_mask || a.k_mask[j]);
+  };
+  if (k0 < k1) load(k0);
+
+  Frag<P> q[KS], go[KS];
+  const T* qp = (const T*)a.q + qi * a.q_row + head * a.q_head;
+  const T* gp = (const T*)p.go + qi * p.go_row + head * p.go_head;
+  const T* op = (const T*)p.out + qi * p.out_row + head * p.out_head;
+  float delta = 0.0f;
+#pragma unroll
+  for (int t = 0; t < KS; ++t) {
+    const int d = 16 * t + 8 * h;
+    q[t] = frag_of(fetch8(qp + d, live ? a.dim_qk - d : 0, p.vec), live);
+    if (p.negate) flip_sign(q[t]);
+    const Raw<T> gr = fetch8(gp + d, live ? a.dim_v - d : 0, p.vec);
+    const Raw<T> orow = fetch8(op + d, live ? a.dim_v - d : 0, p.vec);
+    go[t] = frag_of(gr, live);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) delta = fmaf(gr.at(i), orow.at(i), delta);
+  }
+  delta = live ? delta + other_half(delta) : 0.0f;
+  if (row && h == 0 && split == 0) p.delta[at] = delta;
+
+  f32x16 dq[D / 32];
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt) dq[dt] = f32x16{};
+
+  for (; k0 < k1; k0 += TK) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int t = threadIdx.x + e * NT;
+      kt.store(t / U, t % U, frag_of(kr[e], keep[e]));
+      vt.store(t / U, t % U, frag_of(vr[e], keep[e]));
+    }
+    const unsigned long seen = __ballot(key);
+    __syncthreads();
+    if (k0 + TK < k1) load(k0 + TK);
+    const bool whole = seen == (TK == 64 ? ~0ul : (1ul << (TK & 63)) - 1);
+    const unsigned long bits = seen >> (4 * h);
+
+#pragma unroll
+    for (int b = 0; b < TK / 32; ++b) {
+      f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+      for (int t = 0; t < KS; ++t) {
+        s = mma(kt.rows(32 * b, t, lane), q[t], s);
+        dp = mma(vt.rows(32 * b, t, lane), go[t], dp);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], p.c, -lse));
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!(bits >> (32 * b + 8 * (i / 4) + i % 4) & 1)) s[i] = 0.0f;
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = s[8 * t + i] * (dp[8 * t + i] - delta);
+        Frag<P> f;   // bf16: dS rounded for its product
+        to_frag(e, f);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) dq[dt] = mma(kt.columns(32 * b + 16 * t, dt, lane), f, dq[dt]);
+      }
+    }
+  }
+
+  if (!row) return;
+  if (p.splits > 1) {
+    float* to = p.part + (split * (a.num_q * a.heads_q) + at) * a.dim_qk;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float v[4] = {dq[dt][4 * b], dq[dt][4 * b + 1], dq[dt][4 * b + 2], dq[dt][4 * b + 3]};
+        store4(to, 32 * dt + 8 * b + 4 * h, a.dim_qk, v, a.dim_qk % 4 == 0);
+      }
+    return;
+  }
+  T* to = (T*)p.gq + qi * p.gq_row + head * p.gq_head;
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = live ? dq[dt][4 * b + i] * a.scale : 0.0f;
+      store4(to, 32 * dt + 8 * b + 4 * h, a.dim_qk, v, p.vec_st);
+    }
+}
+
+template <class T, int D, int RW, int TQ>
+__global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
+  constexpr int P = planes<T>(), U = D / 8, KS = D / 16, NT = 64 * RW, E = TQ * U / NT;
+  static_assert(TQ * U % NT == 0 && TQ <= NT, "");
+  __shared__ __attribute__((aligned(16))) Tile<P, TQ, D> qt, gt;
+  __shared__ __attribute__((aligned(16))) float lse_s[TQ], delta_s[TQ];
+  const e3conv_attention_args& a = p.a;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
+
+  const int split = blockIdx.x % p.splits, slot = blockIdx.x / p.splits % p.slots;
+  const int c = blockIdx.x / p.splits / p.slots;
+  constexpr int BN = 32 * RW;
+  const int g = graph_of_slot(a.k_ptr, a.num_graphs, a.num_k, 1, BN, slot);
+  const int kb = offset(a.k_ptr, g, a.num_k), ke = offset(a.k_ptr, g + 1, a.num_k);
+  const int j0 = kb + (slot - first_slot(a.k_ptr, g, a.num_k, 1, BN)) * BN;
+  if (j0 >= ke) return;
+
+  const int j = j0 + 32 * w + n;
+  const bool key = j < ke;
+  const bool live = key && (!a.k_mask || a.k_mask[j]);
+
+  // this split's rows: whole tiles of the graph's
+  const int q0 = offset(a.q_ptr, g, a.num_q);
+  const int nrows = (offset(a.q_ptr, g + 1, a.num_q) - q0) * p.group;
+  const int tiles = nrows > 0 ? (nrows + TQ - 1) / TQ : 0, per = (tiles + p.splits - 1) / p.splits;
+  int r0 = min(split * per, tiles) * TQ;
+  const int r1 = min(nrows, min((split + 1) * per, tiles) * TQ);
+
+  const T* qbase = (const T*)a.q + q0 * a.q_row + c * p.group * a.q_head;
+  const T* gbase = (const T*)p.go + q0 * p.go_row + c * p.group * p.go_head;
+  const long at0 = (long)q0 * a.heads_q + c * p.group;
+  Raw<T> qr[E], gr[E];
+  bool keep[E];
+  float lse = INFINITY, delta = 0.0f;
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int t = threadIdx.x + e * NT, r = r0 + t / U, d = t % U * 8;
+      const bool in = r < r1;
+      const int i = in ? r / p.group : 0, x = in ? r % p.group : 0;
+      qr[e] = fetch8(qbase + i * a.q_row + x * a.q_head + d, in ? a.dim_qk - d : 0, p.vec);
+      gr[e] = fetch8(gbase + i * p.go_row + x * p.go_head + d, in ? a.dim_v - d : 0, p.vec);
+      keep[e] = in && (!a.q_mask || a.q_mask[q0 + i]) && p.lse[at0 + (long)i * a.heads_q + x] != -INFINITY;
+    }
+    // a row that sees no key: lse = +infinity makes its P zero
+    lse = INFINITY;
+    delta = 0.0f;
+    const int r = r0 + (int)threadIdx.x;
+    if (threadIdx.x < TQ && r < r1) {
+      const long at = at0 + (long)(r / p.group) * a.heads_q + r % p.group;
+      const float v = p.lse[at];
+      if (v != -INFINITY && (!a.q_mask || a.q_mask[q0 + r / p.group])) {
+        lse = v * kLog2e;
+        delta = p.delta[at];
+      }
+    }
+  };
+  if (r0 < r1) load(r0);
+
+  Frag<P> k[KS], v[KS];
+  const T* kp = (const T*)a.k + j * a.k_row + c * a.k_head;
+  const T* vp = (const T*)a.v + j * a.v_row + c * a.v_head;
+#pragma unroll
+  for (int t = 0; t < KS; ++t) {
+    const int d = 16 * t + 8 * h;
+    k[t] = frag_of(fetch8(kp + d, live ? a.dim_qk - d : 0, p.vec), live);
+    v[t] = frag_of(fetch8(vp + d, live ? a.dim_v - d : 0, p.vec), live);
+    if (p.negate) flip_sign(k[t]);
+  }
+
+  f32x16 dk[D / 32], dv[D / 32];
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt) dk[dt] = dv[dt] = f32x16{};
+
+  for (; r0 < r1; r0 += TQ) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int t = threadIdx.x + e * NT;
+      qt.store(t / U, t % U, frag_of(qr[e], keep[e]));
+      gt.store(t / U, t % U, frag_of(gr[e], keep[e]));
+    }
+    if (threadIdx.x < TQ) {
+      lse_s[threadIdx.x] = lse;
+      delta_s[threadIdx.x] = delta;
+    }
+    __syncthreads();
+    if (r0 + TQ < r1) load(r0 + TQ);
+
+#pragma unroll
+    for (int b = 0; b < TQ / 32; ++b) {
+      f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+      for (int t = 0; t < KS; ++t) {
+        s = mma(qt.rows(32 * b, t, lane), k[t], s);
+        dp = mma(gt.rows(32 * b, t, lane), v[t], dp);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(&lse_s[32 * b + 8 * x + 4 * h]);
+        const f32x4 de = *reinterpret_cast<const f32x4*>(&delta_s[32 * b + 8 * x + 4 * h]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(s[4 * x + i], p.c, -ls[i]));
+          s[4 * x + i] = e;
+          dp[4 * x + i] = e * (dp[4 * x + i] - de[i]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float e[8];
+        Frag<P> f;   // bf16: P and dS rounded for their products
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = s[8 * t + i];
+        to_frag(e, f);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) dv[dt] = mma(gt.columns(32 * b + 16 * t, dt, lane), f, dv[dt]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = dp[8 * t + i];
+        to_frag(e, f);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) dk[dt] = mma(qt.columns(32 * b + 16 * t, dt, lane), f, dk[dt]);
+      }
+    }
+  }
+
+  if (!key) return;
+  if (p.splits > 1) {
+    const int width = a.dim_qk + a.dim_v;
+    float* to = p.part + (split * (a.num_k * a.heads_kv) + (long)j * a.heads_kv + c) * width;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = live ? dk[dt][4 * b + i] : 0.0f;
+          y[i] = live ? dv[dt][4 * b + i] : 0.0f;
+        }
+        const bool vec = a.dim_qk % 4 == 0 && a.dim_v % 4 == 0;
+        store4(to, 32 * dt + 8 * b + 4 * h, a.dim_qk, x, vec);
+        store4(to + a.dim_qk, 32 * dt + 8 * b + 4 * h, a.dim_v, y, vec);
+      }
+    return;
+  }
+  T* tk = (T*)p.gk + j * p.gk_row + c * p.gk_head;
+  T* tv = (T*)p.gv + j * p.gv_row + c * p.gv_head;
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      float x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = live ? dk[dt][4 * b + i] * a.scale : 0.0f;
+        y[i] = live ? dv[dt][4 * b + i] : 0.0f;
+      }
+      store4(tk, 32 * dt + 8 * b + 4 * h, a.dim_qk, x, p.vec_st);
+      store4(tv, 32 * dt + 8 * b + 4 * h, a.dim_v, y, p.vec_st);
+    }
+}
+
+// Sums the splits: element d < dim of row (i, head) of `width` floats, times factor.
+template <class T>
+__global__ void __launch_bounds__(256) attn_sum(const float* part, long rows, int width, int from, int dim, int heads,
+                                                int splits, float factor, T* out, long out_row, long out_head) {
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * dim) return;
+  const long at = i / dim;
+  const int d = (int)(i % dim);
+  float v = 0.0f;
+  for (int s = 0; s < splits; ++s) v += part[(s * rows + at) * width + from + d];
+  out[at / heads * out_row + at % heads * out_head + d] = (T)(v * factor);
+}
+
+template <class T>
+hipError_t sum(const Params& p, long rows, int width, int from, int dim, int heads, float factor, void* out, long row,
+               long head, hipStream_t s) {
+  const long blocks = (rows * dim + 255) / 256;
+  if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+  if (blocks > 0)
+    hipLaunchKernelGGL(attn_sum<T>, dim3((unsigned)blocks), dim3(256), 0, s, p.part, rows, width, from, dim, heads,
+                       p.splits, factor, (T*)out, row, head);
+  return hipGetLastError();
+}
+
+struct Shape {
+  int rw, slots, splits;
+};
+
+// As the forward's: four waves share a tile of the other axis where that fills the chip, and
+// the other axis is split while there are fewer than four waves per compute unit.
+Shape shape_of(long rows, long others, long graphs, int heads, int tables) {
+  graphs = graphs > 0 ? graphs : 1;
+  const long avg = (rows + graphs - 1) / graphs, avg_o = (others + graphs - 1) / graphs;
+  const auto tiles = [&](int rw) { return graphs * ((avg + 32 * rw - 1) / (32 * rw)) * heads; };
+  Shape s;
+  s.rw = tiles(4) >= 256 ? 4 : 1;
+  s.slots = (int)(rows / (32 * s.rw) + tables);
+  const long waves = tiles(s.rw) * s.rw, most = (avg_o + 127) / 128, want = waves > 0 ? 1024 / waves : 1;
+  s.splits = (int)(want < most ? want : most);
+  if (s.splits > 256) s.splits = 256;
+  if (s.splits < 1) s.splits = 1;
+  return s;
+}
+Shape shape_q(const e3conv_attention_args& a) {
+  return shape_of(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv, a.num_graphs);
+}
+Shape shape_kv(const e3conv_attention_args& a) {
+  return shape_of(a.num_k, a.num_q * (a.heads_q / a.heads_kv), a.num_graphs, a.heads_kv, a.num_graphs);
+}
+
+size_t delta_bytes(const e3conv_attention_args& a) {
+  return ((size_t)a.num_q * a.heads_q * sizeof(float) + 15) / 16 * 16;
+}
+
+template <class T, int D>
+void launch_q(const Params& p, int rw, unsigned grid, hipStream_t s) {
+  constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_q<T, D, 4, TK4>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_q<T, D, 1, 32>), dim3(grid), dim3(64), 0, s, p);
+}
+template <class T, int D>
+void launch_kv(const Params& p, int rw, unsigned grid, hipStream_t s) {
+  constexpr int TQ4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_kv<T, D, 4, TQ4>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_kv<T, D, 1, 32>), dim3(grid), dim3(64), 0, s, p);
+}
+
+template <class T>
+hipError_t backward(Params p, hipStream_t s) {
+  const e3conv_attention_args& a = p.a;
+  const int dim = a.dim_qk > a.dim_v ? a.dim_qk : a.dim_v;
+  if (a.num_q > 0) {
+    const Shape sh = shape_q(a);
+    const long grid = (long)sh.slots * sh.splits * a.heads_kv;
+    if (grid > 0x7fffffffL) return hipErrorInvalidValue;
+    p.slots = sh.slots;
+    p.splits = sh.splits;
+    if (dim <= 32) launch_q<T, 32>(p, sh.rw, (unsigned)grid, s);
+    else if (dim <= 64) launch_q<T, 64>(p, sh.rw, (unsigned)grid, s);
+    else launch_q<T, 128>(p, sh.rw, (unsigned)grid, s);
+    hipError_t err = hipGetLastError();
+    if (err == hipSuccess && sh.splits > 1)
+      err = sum<T>(p, a.num_q * a.heads_q, a.dim_qk, 0, a.dim_qk, a.heads_q, a.scale, p.gq, p.gq_row, p.gq_head, s);
+    if (err != hipSuccess) return err;
+  }
+  if (a.num_k > 0) {
+    const Shape sh = shape_kv(a);
+    const long grid = (long)sh.slots * sh.splits * a.heads_kv;
+    if (grid > 0x7fffffffL) return hipErrorInvalidValue;
+    p.slots = sh.slots;
+    p.splits = sh.splits;
+    if (dim <= 32) launch_kv<T, 32>(p, sh.rw, (unsigned)grid, s);
+    else if (dim <= 64) launch_kv<T, 64>(p, sh.rw, (unsigned)grid, s);
+    else launch_kv<T, 128>(p, sh.rw, (unsigned)grid, s);
+    hipError_t err = hipGetLastError();
+    const int width = a.dim_qk + a.dim_v;
+    const long rows = a.num_k * a.heads_kv;
+    if (err == hipSuccess && sh.splits > 1)
+      err = sum<T>(p, rows, width, 0, a.dim_qk, a.heads_kv, a.scale, p.gk, p.gk_row, p.gk_head, s);
+    if (err == hipSuccess && sh.splits > 1)
+      err = sum<T>(p, rows, width, a.dim_qk, a.dim_v, a.heads_kv, 1.0f, p.gv, p.gv_row, p.gv_head, s);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+// delta, then one region for the partial results of either kernel in turn.
+size_t backward_workspace(const e3conv_attention_args& a) {
+  const Shape sq = shape_q(a), sk = shape_kv(a);
+  const size_t q = sq.splits > 1 ? (size_t)sq.splits * a.num_q * a.heads_q * a.dim_qk : 0;
+  const size_t k = sk.splits > 1 ? (size_t)sk.splits * a.num_k * a.heads_kv * (a.dim_qk + a.dim_v) : 0;
+  return delta_bytes(a) + (q > k ? q : k) * sizeof(float);
+}
+
+hipError_t launch_backward(const Params& given, hipStream_t s) {
+  Params p = given;
+  p.part = p.delta + delta_bytes(p.a) / sizeof(float);
+  return p.a.dtype == E3CONV_F32 ? backward<float>(p, s) : backward<__bf16>(p, s);
+}
+
+}  // namespace attn
+}  // namespace e3c

@@ -1,0 +1,284 @@
+// Attention forward on the matrix cores (contract in e3conv.h, tiles in attention_tile.h).
+//
+// A wave owns 32 rows (a row is one query of one of the query heads that share a
+// kv head) and walks over the graph's keys in tiles that its work-group holds in
+// LDS.  With the rows along the columns of both products,
+//     S^T (keys x rows) = K Q^T,     out^T (dim x rows) += V^T P^T,
+// a lane keeps one row: maximum and sum of its softmax are sums within the lane
+// and one exchange with the other half of the wave, and P^T is the second
+// product's operand where the first one left it.  The next tile is loaded into
+// registers while the current one is used.
+#include "attention_tile.h"
+#include "kernels.h"
+
+namespace e3c {
+namespace attn {
+namespace {
+
+template <class T, int D, int RW, int TK>
+__global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
+  constexpr int P = planes<T>(), U = D / 8, KS = D / 16, NT = 64 * RW, E = TK * U / NT;
+  static_assert(TK * U % NT == 0, "");
+  __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kt, vt;
+  const e3conv_attention_args& a = p.a;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
+
+  // block -> (split, slot, kv head): the row tiles of a head are neighbours
+  const int split = blockIdx.x % p.splits, slot = blockIdx.x / p.splits % p.slots;
+  const int c = blockIdx.x / p.splits / p.slots;
+  constexpr int BM = 32 * RW;
+  const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
+  const int q0 = offset(a.q_ptr, g, a.num_q);
+  const int nrows = (offset(a.q_ptr, g + 1, a.num_q) - q0) * p.group;
+  const int r0 = (slot - first_slot(a.q_ptr, g, a.num_q, p.group, BM)) * BM;
+  if (r0 >= nrows) return;
+
+  const int r = r0 + 32 * w + n;
+  const bool row = r < nrows;
+  const int qi = q0 + (row ? r / p.group : 0), head = c * p.group + (row ? r % p.group : 0);
+  const bool live = row && (!a.q_mask || a.q_mask[qi]);
+
+  // this split's keys: whole tiles of the graph's
+  const int kb = offset(a.k_ptr, g, a.num_k), ke = offset(a.k_ptr, g + 1, a.num_k);
+  const int tiles = ke > kb ? (ke - kb + TK - 1) / TK : 0, per = (tiles + p.splits - 1) / p.splits;
+  int k0 = kb + min(split * per, tiles) * TK;
+  const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
+
+  const T* kbase = (const T*)a.k + c * a.k_head;
+  const T* vbase = (const T*)a.v + c * a.v_head;
+  Raw<T> kr[E], vr[E];
+  bool keep[E], key = false;
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int t = threadIdx.x + e * NT, j = k0 + t / U, d = t % U * 8;
+      const bool in = j < k1;
+      kr[e] = fetch8(kbase + j * a.k_row + d, in ? a.dim_qk - d : 0, p.vec);
+      vr[e] = fetch8(vbase + j * a.v_row + d, in ? a.dim_v - d : 0, p.vec);
+      keep[e] = in && (!a.k_mask || a.k_mask[j]);
+    }
+    const int j = k0 + lane;
+    key = lane < TK && j < k1 && (!a.k_mask || a.k_mask[j]);
+  };
+  if (k0 < k1) load(k0);
+
+  Frag<P> q[KS];
+  const T* qp = (const T*)a.q + qi * a.q_row + head * a.q_head;
+#pragma unroll
+  for (int t = 0; t < KS; ++t) {
+    const int d = 16 * t + 8 * h;
+    q[t] = frag_of(fetch8(qp + d, live ? a.dim_qk - d : 0, p.vec), live);
+    if (p.negate) flip_sign(q[t]);
+  }
+
+  f32x16 o[D / 32];
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt) o[dt] = f32x16{};
+  float m = -INFINITY, l = 0.0f;   // of the logits in units of log 2; l: this half's keys
+
+  for (; k0 < k1; k0 += TK) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int t = threadIdx.x + e * NT;
+      kt.store(t / U, t % U, frag_of(kr[e], keep[e]));
+      vt.store(t / U, t % U, frag_of(vr[e], keep[e]));
+    }
+    const unsigned long seen = __ballot(key);
+    __syncthreads();
+    if (k0 + TK < k1) load(k0 + TK);
+
+    f32x16 s[TK / 32];
+#pragma unroll
+    for (int b = 0; b < TK / 32; ++b) {
+      s[b] = f32x16{};
+#pragma unroll
+      for (int t = 0; t < KS; ++t) s[b] = mma(kt.rows(32 * b, t, lane), q[t], s[b]);
+    }
+    if (seen != (TK == 64 ? ~0ul : (1ul << (TK & 63)) - 1)) {
+      const unsigned long bits = seen >> (4 * h);
+#pragma unroll
+      for (int b = 0; b < TK / 32; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!(bits >> (32 * b + 8 * (i / 4) + i % 4) & 1)) s[b][i] = -INFINITY;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < TK / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+    top = fmaxf(top, other_half(top)) * p.c;
+    if (__ballot(top > m)) {
+      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
+      const float f = __builtin_amdgcn_exp2f(m - base);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int b = 0; b < TK / 32; ++b)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[i] = __builtin_amdgcn_exp2f(fmaf(s[b][8 * t + i], p.c, -base));
+          l += e[i];
+        }
+        // bf16: P rounded for its product, the sum l from the unrounded values
+        Frag<P> f;
+        to_frag(e, f);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) o[dt] = mma(vt.columns(32 * b + 16 * t, dt, lane), f, o[dt]);
+      }
+  }
+
+  l += other_half(l);
+  if (!row) return;
+  const long at = (long)qi * a.heads_q + head;
+  if (!live) {
+    m = -INFINITY;
+    l = 0.0f;
+  }
+  if (p.splits > 1) {
+    const long rows = a.num_q * a.heads_q, i = split * rows + at;
+    float* to = p.part + i * a.dim_v;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float v[4] = {o[dt][4 * b], o[dt][4 * b + 1], o[dt][4 * b + 2], o[dt][4 * b + 3]};
+        store4(to, 32 * dt + 8 * b + 4 * h, a.dim_v, v, a.dim_v % 4 == 0);
+      }
+    if (h == 0) {
+      p.part_ml[2 * i] = m;
+      p.part_ml[2 * i + 1] = l;
+    }
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  T* to = (T*)p.out + qi * p.out_row + head * p.out_head;
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = live ? o[dt][4 * b + i] * inv : 0.0f;
+      store4(to, 32 * dt + 8 * b + 4 * h, a.dim_v, v, p.vec_st);
+    }
+  if (h == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// Joins the splits of one row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
+constexpr int kMaxSplits = 256;
+template <class T>
+__global__ void __launch_bounds__(256) attn_join(Params p) {
+  const e3conv_attention_args& a = p.a;
+  __shared__ float weight[kMaxSplits], sum[4][kMaxDim], red[8];
+  const long rows = a.num_q * a.heads_q, at = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  float m = -INFINITY, l = 0.0f;
+  if (tid < p.splits) {
+    m = p.part_ml[2 * (tid * rows + at)];
+    l = p.part_ml[2 * (tid * rows + at) + 1];
+  }
+  float top = m;
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if (lane == 0) red[w] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float base = top == -INFINITY ? 0.0f : top, f = __builtin_amdgcn_exp2f(m - base);
+  weight[tid] = f;
+  l *= f;
+  for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
+  if (lane == 0) red[4 + w] = l;
+  __syncthreads();
+  l = (red[4] + red[5]) + (red[6] + red[7]);
+  const float* part = p.part + at * a.dim_v;
+  float v0 = 0.0f, v1 = 0.0f;
+  for (int s = w; s < p.splits; s += 4) {
+    const float* o = part + s * rows * a.dim_v;
+    if (lane < a.dim_v) v0 = fmaf(weight[s], o[lane], v0);
+    if (lane + 64 < a.dim_v) v1 = fmaf(weight[s], o[lane + 64], v1);
+  }
+  sum[w][lane] = v0;
+  sum[w][lane + 64] = v1;
+  __syncthreads();
+  const int head = (int)(at % a.heads_q);
+  const long qi = at / a.heads_q;
+  if (tid < a.dim_v) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float v = (sum[0][tid] + sum[1][tid]) + (sum[2][tid] + sum[3][tid]);
+    ((T*)p.out)[qi * p.out_row + head * p.out_head + tid] = (T)(l == 0.0f ? 0.0f : v * inv);
+  }
+  if (tid == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+struct Shape {
+  int rw, slots, splits;
+};
+
+// Waves per work-group and splits of the keys.  Four waves share each tile of keys
+// where that fills the chip, else one wave per work-group; and the keys are
+// split while there are fewer than four waves per compute unit and a split keeps two
+// tiles.  Graph lengths are on the device: their average stands for them.
+Shape shape_of(const e3conv_attention_args& a) {
+  const long rows = a.num_q * (a.heads_q / a.heads_kv), graphs = a.num_graphs > 0 ? a.num_graphs : 1;
+  const long avg_r = (rows + graphs - 1) / graphs, avg_k = (a.num_k + graphs - 1) / graphs;
+  const auto tiles = [&](int rw) { return graphs * ((avg_r + 32 * rw - 1) / (32 * rw)) * a.heads_kv; };
+  Shape s;
+  s.rw = tiles(4) >= 256 ? 4 : 1;
+  s.slots = (int)(rows / (32 * s.rw) + a.num_graphs);
+  const long waves = tiles(s.rw) * s.rw, most = (avg_k + 127) / 128, want = waves > 0 ? 1024 / waves : 1;
+  s.splits = (int)(want < most ? want : most);
+  if (s.splits > kMaxSplits) s.splits = kMaxSplits;
+  if (s.splits < 1) s.splits = 1;
+  return s;
+}
+
+template <class T, int D>
+void launch(const Params& p, int rw, unsigned grid, hipStream_t s) {
+  constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
+  if (rw == 4) hipLaunchKernelGGL((attn_fwd<T, D, 4, TK4>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_fwd<T, D, 1, 32>), dim3(grid), dim3(64), 0, s, p);
+}
+
+template <class T>
+hipError_t forward(const Params& p, int rw, unsigned grid, hipStream_t s) {
+  const int dim = p.a.dim_qk > p.a.dim_v ? p.a.dim_qk : p.a.dim_v;
+  if (dim <= 32) launch<T, 32>(p, rw, grid, s);
+  else if (dim <= 64) launch<T, 64>(p, rw, grid, s);
+  else launch<T, 128>(p, rw, grid, s);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || p.splits == 1) return err;
+  hipLaunchKernelGGL(attn_join<T>, dim3((unsigned)(p.a.num_q * p.a.heads_q)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t forward_workspace(const e3conv_attention_args& a) {
+  const Shape sh = shape_of(a);
+  return sh.splits > 1 ? (size_t)sh.splits * a.num_q * a.heads_q * (a.dim_v + 2) * sizeof(float) : 0;
+}
+
+hipError_t launch_forward(const Params& given, hipStream_t s) {
+  Params p = given;
+  const Shape sh = shape_of(p.a);
+  p.slots = sh.slots;
+  p.splits = sh.splits;
+  p.part_ml = p.part + (size_t)sh.splits * p.a.num_q * p.a.heads_q * p.a.dim_v;
+  const long grid = (long)sh.slots * sh.splits * p.a.heads_kv;
+  if (grid > 0x7fffffffL) return hipErrorInvalidValue;
+  return p.a.dtype == E3CONV_F32 ? forward<float>(p, sh.rw, (unsigned)grid, s)
+                                 : forward<__bf16>(p, sh.rw, (unsigned)grid, s);
+}
+
+}  // namespace attn
+}  // namespace e3c

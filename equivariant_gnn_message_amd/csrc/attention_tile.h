@@ -1,0 +1,267 @@
+// Tiles of the attention kernels: rows of q, k, v and grad_out in LDS, operands of
+// v_mfma_f32_32x32x16_bf16, and the map from work-groups to graphs.
+//
+// The instruction computes C (32 x 32) += A (32 x 16) B (16 x 32).  Lane l = 32 h + n
+// holds A[n][8 h + j], B[8 h + j][n] (j = 0..7) and, in accumulator register i,
+// C[8 (i / 4) + 4 h + i % 4][n].  The contraction may run through its 16 slots
+// in any order, so registers 8 t .. 8 t + 7 of an accumulator are, as they lie, the
+// B operand of a product over the accumulator's rows: slot (h, j) is row
+// 16 t + 8 (j / 4) + 4 h + j % 4.  Probabilities go from the product that forms
+// their logits to the product that uses them without leaving their lane.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "e3conv.h"
+
+namespace e3c {
+namespace attn {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMaxDim = 128;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+struct Params {
+  e3conv_attention_args a;
+  int group;                       // query heads per kv head
+  float c;                         // |scale| log2(e), at least the smallest normal number
+  int negate;                      // scale < 0: q enters with its sign changed
+  int vec;                         // 16-byte loads of q, k, v, grad_out (and out) rows
+  int vec_st;                      // 4-element stores of the outputs
+  int slots;                       // work-group slots of the row (or key) tiles
+  int splits;                      // ranges of the other axis, joined by a second kernel
+  void* out;
+  long out_row, out_head;
+  float* lse;
+  const void* go;
+  long go_row, go_head;
+  void *gq, *gk, *gv;
+  long gq_row, gq_head, gk_row, gk_head, gv_row, gv_head;
+  float* delta;                    // (num_q, heads_q), reverse pass
+  float* part;                     // partial results of the splits
+  float* part_ml;                  // and their softmax maximum and sum
+};
+
+// An fp32 operand is the sum of three bf16 parts (24 significant bits), a bf16
+// operand is one.  P planes of eight elements.
+template <int P>
+struct Frag {
+  bf16x8 p[P];
+};
+
+template <class T>
+constexpr int planes() {
+  return sizeof(T) == 4 ? 3 : 1;
+}
+
+// Products of order up to 2^-16 of the leading one; those left out are below 2^-24.
+__device__ __forceinline__ f32x16 mma(const Frag<1>& a, const Frag<1>& b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(const Frag<3>& a, const Frag<3>& b, f32x16 c) {
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[2], b.p[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[1], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[2], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[1], c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
+}
+
+// Eight fp32 values as an operand: rounded to bf16 (one plane), or split in three parts.
+__device__ __forceinline__ void to_frag(const float (&v)[8], Frag<1>& f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f.p[0][i] = (__bf16)v[i];
+}
+__device__ __forceinline__ void to_frag(const float (&v)[8], Frag<3>& f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    f.p[0][i] = (__bf16)v[i];
+    const float r = v[i] - (float)f.p[0][i];
+    f.p[1][i] = (__bf16)r;
+    f.p[2][i] = (__bf16)(r - (float)f.p[1][i]);
+  }
+}
+
+// Eight consecutive elements of a row as they lie in memory.
+template <class T>
+struct Raw;
+template <>
+struct Raw<__bf16> {
+  bf16x8 v;
+  __device__ __forceinline__ float at(int i) const { return (float)v[i]; }
+};
+template <>
+struct Raw<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ float at(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
+};
+
+// Elements p[0 .. n-1], the others 0; n <= 0 reads nothing.  vec: p is 16-byte aligned
+// and n is 8 or at most 0.
+__device__ __forceinline__ Raw<__bf16> fetch8(const __bf16* p, int n, bool vec) {
+  Raw<__bf16> r;
+  if (vec) {
+    if (n > 0) r.v = *reinterpret_cast<const bf16x8*>(p);
+    else r.v = bf16x8{};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[i] = i < n ? p[i] : (__bf16)0.0f;
+  }
+  return r;
+}
+__device__ __forceinline__ Raw<float> fetch8(const float* p, int n, bool vec) {
+  Raw<float> r;
+  if (vec) {
+    r.a = r.b = f32x4{};
+    if (n > 0) {
+      r.a = *reinterpret_cast<const f32x4*>(p);
+      r.b = *reinterpret_cast<const f32x4*>(p + 4);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.a[i] = i < n ? p[i] : 0.0f;
+      r.b[i] = i + 4 < n ? p[i + 4] : 0.0f;
+    }
+  }
+  return r;
+}
+
+// keep = false: zeros, whatever r holds (NaN too).
+__device__ __forceinline__ Frag<1> frag_of(const Raw<__bf16>& r, bool keep) {
+  Frag<1> f;
+  f.p[0] = keep ? r.v : bf16x8{};
+  return f;
+}
+__device__ __forceinline__ Frag<3> frag_of(const Raw<float>& r, bool keep) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = keep ? r.at(i) : 0.0f;
+  Frag<3> f;
+  to_frag(v, f);
+  return f;
+}
+template <int P>
+__device__ __forceinline__ void flip_sign(Frag<P>& f) {
+#pragma unroll
+  for (int k = 0; k < P; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.p[k][i] = -f.p[k][i];
+}
+
+// ROWS x D elements in LDS, units of eight elements (16 bytes).  Units of a row are
+// permuted by its number so that the two ways of reading meet no bank twice: 16
+// consecutive rows at one unit (row operand), and four consecutive rows (from a
+// multiple of 4) at four consecutive units (column operand).
+template <int P, int ROWS, int D>
+struct Tile {
+  static constexpr int U = D / 8;
+  bf16x8 u[P][ROWS * U];
+
+  static __device__ __forceinline__ int swizzle(int row) {
+    if (D == 32) return (row >> 2) & 3;
+    if (D == 64) return ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
+    return (row & 3) << 2 | ((row >> 2) & 3);
+  }
+  static __device__ __forceinline__ int at(int row, int unit) { return row * U + (unit ^ swizzle(row)); }
+
+  __device__ __forceinline__ void store(int row, int unit, const Frag<P>& f) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) u[k][at(row, unit)] = f.p[k];
+  }
+  // A operand: rows row0 + n, elements 16 step + 8 h + j.
+  __device__ __forceinline__ Frag<P> rows(int row0, int step, int lane) const {
+    Frag<P> f;
+    const int i = at(row0 + (lane & 31), 2 * step + (lane >> 5));
+#pragma unroll
+    for (int k = 0; k < P; ++k) f.p[k] = u[k][i];
+    return f;
+  }
+  // A operand of the transposed tile: element column 32 dt + n, and along the slots the
+  // rows row0 + 8 (j / 4) + 4 h + j % 4 (row0 a multiple of 16).  ds_read_b64_tr_b16:
+  // of 16 lanes, lane i gives the address of columns 4 (i % 4) .. + 3 of row i / 4 and
+  // receives the four rows of column i.
+  __device__ __forceinline__ Frag<P> columns(int row0, int dt, int lane) const {
+    const int i = lane & 15, block = lane >> 4;
+    const int unit = 4 * dt + 2 * (block & 1) + ((i >> 1) & 1);
+    const int row = row0 + 4 * (block >> 1) + (i >> 2);
+    Frag<P> f;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const s16x4 lo = tr(&u[k][at(row, unit)], i & 1), hi = tr(&u[k][at(row + 8, unit)], i & 1);
+      union {
+        s16x4 s[2];
+        bf16x8 b;
+      } both = {{lo, hi}};
+      f.p[k] = both.b;
+    }
+    return f;
+  }
+  static __device__ __forceinline__ s16x4 tr(const bf16x8* p, int half) {
+    typedef __attribute__((address_space(3))) s16x4* lds;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(reinterpret_cast<const s16x4*>(p) + half));
+  }
+};
+
+// Value of the lane with the other h.
+__device__ __forceinline__ float other_half(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// Offset i of a segment table, kept inside [0, n] whatever the table holds.
+__device__ __forceinline__ int offset(const int* ptr, int i, long n) {
+  const int v = ptr[i];
+  return v < 0 ? 0 : (v > n ? (int)n : v);
+}
+
+// Row tiles of graph g (rows first(g) .. first(g + 1)) take the slots first(g) / tile + g
+// and on: enough for ceil(rows / tile) tiles, without a host-side list of lengths.
+// Returns the graph of a slot: the last g whose first slot is not beyond it.  64
+// offsets are tried at a time.
+__device__ __forceinline__ int graph_of_slot(const int* ptr, int graphs, long n, int mult, int tile, int slot) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, count = graphs;
+  while (count > 1) {
+    const int step = (count + 63) >> 6, i = lane * step;
+    bool before = false;
+    if (i < count) before = offset(ptr, lo + i, n) * mult / tile + lo + i <= slot;
+    const int hits = max(__popcll(__ballot(before)), 1);
+    lo += (hits - 1) * step;
+    count = min(step, count - (hits - 1) * step);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+__device__ __forceinline__ int first_slot(const int* ptr, int g, long n, int mult, int tile) {
+  return offset(ptr, g, n) * mult / tile + g;
+}
+
+// Four consecutive elements d .. d + 3 of a row with dim elements.
+template <class T>
+__device__ __forceinline__ void store4(T* p, int d, int dim, const float (&v)[4], bool vec) {
+  if (vec && d + 4 <= dim) {
+    typedef T V __attribute__((ext_vector_type(4)));
+    V o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (T)v[i];
+    *reinterpret_cast<V*>(p + d) = o;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (d + i < dim) p[d + i] = (T)v[i];
+  }
+}
+
+// Launchers.  tile sizes and splits are in the parameters.
+hipError_t launch_forward(const Params& p, hipStream_t s);
+hipError_t launch_backward(const Params& p, hipStream_t s);
+size_t forward_workspace(const e3conv_attention_args& a);
+size_t backward_workspace(const e3conv_attention_args& a);
+
+}  // namespace attn
+}  // namespace e3c

@@ -113,3 +113,18 @@ def test_host_tensors_are_refused():
         E.e3conv_attention(t, t, t, p, p)
     with pytest.raises(ValueError):
         E.e3conv_group_norm(t[:, 0], p, 2)
+
+
+@pytest.mark.parametrize("num_q,num_k,graphs", [(0, 0, 0), (0, 0, 3), (0, 70000, 3), (70000, 0, 1), (1, 100000, 1),
+                                                (100000, 1, 1), (5, 5, 1 << 19)])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_attention_workspace_of_any_sizes(num_q, num_k, graphs, dtype):
+    a = attention_args(dtype=dtype, num_q=num_q, num_k=num_k, num_graphs=graphs)
+    assert E.e3conv_attention_workspace_size(a) >= 0
+    assert E.e3conv_attention_workspace_size(a, True) >= 4 * num_q * 4
+
+
+@pytest.mark.parametrize("rows,graphs", [(0, 0), (0, 5), (1, 1), (1 << 24, 1), (100, 1 << 19)])
+def test_group_norm_workspace_of_any_sizes(rows, graphs):
+    a = norm_args(num_rows=rows, num_graphs=graphs)
+    assert E.e3conv_group_norm_workspace_size(a) >= 0 and E.e3conv_group_norm_workspace_size(a, True) >= 0
