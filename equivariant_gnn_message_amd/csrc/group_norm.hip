@@ -1,9 +1,20 @@
 // Group norm with an activation over the rows of each graph, channels last, and its
 // reverse pass (contract in e3conv.h).
 //
-// One work-group per (graph, group): mean, then the variance about it, then
-// the rows.  The reverse pass takes the two means of a group the same way; the
-// weight and bias gradients are sums over all rows, one work-group per channel.
+// The rows of a graph are cut into chunks of p.chunk rows, one work-group each; a thread
+// keeps one run of V channels (16 bytes) and strides over the rows, so loads are whole
+// lines and per-channel values stay in registers.  A graph of one chunk is finished by the
+// work-group that read it, its rows still in cache; graphs of more chunks take three
+// launches:
+//   sums    per chunk and channel: mean and squared deviations (forward), or
+//           sum dz and sum dz xhat (reverse), to the workspace;
+//   finish  per graph and group: mean and rstd, or the two means of the reverse pass,
+//           from its chunks in chunk order; and the weight and bias gradients;
+//   apply   per chunk: the rows.
+// Sums are taken about the channel's first counted value of the chunk, and chunks are
+// joined about the common mean, so a mean far from zero costs no digits of the variance.
+// Memory bound: the rows are read twice and written once where a graph has more than one
+// chunk (the second time from cache where the tensor fits it), else once and once.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -16,10 +27,14 @@ namespace e3c {
 namespace {
 
 constexpr int kMaxChannels = 4096;
+constexpr int NT = 256;            // threads of a work-group
 
 struct NormParams {
   e3conv_group_norm_args a;
   int gc;                          // channels of a group
+  int units;                       // runs of V channels in a row
+  int chunk;                       // rows of a work-group
+  int slots;                       // chunk slots: rows / chunk + graphs
   void* y;
   long y_row;
   float *mean, *rstd;
@@ -28,29 +43,327 @@ struct NormParams {
   void* gx;
   long gx_row;
   float *gw, *gb;
+  float2* sums;                    // (slots, channels) of the chunks
+  float* counts;                   // (slots) counted rows
+  float2* stats;                   // (graphs, groups): mean and rstd, or the reverse pass's means
 };
 
-__device__ __forceinline__ float load(const float* p) { return *p; }
-__device__ __forceinline__ float load(const __bf16* p) { return (float)*p; }
+// ------------------------------------------------------------------ graphs ---
 
-__device__ __forceinline__ int offset(const int* ptr, int i, int n) {
+__device__ __forceinline__ int offset(const int* ptr, int i, long n) {
   const int v = ptr[i];
-  return v < 0 ? 0 : (v > n ? n : v);
+  return v < 0 ? 0 : (v > n ? (int)n : v);
 }
 
-__device__ __forceinline__ int graph_of(const int* ptr, int graphs, int i) {
-  int lo = 0, hi = graphs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (ptr[mid] <= i) lo = mid;
-    else hi = mid - 1;
+// Chunks of graph g take the slots first / chunk + g and on, first being its first row:
+// enough for ceil(rows / chunk) of them, and one at least.  The graph of a slot is the last
+// whose first slot is not beyond it; 64 are tried at a time.
+__device__ __forceinline__ int first_slot(const NormParams& p, int g) {
+  return offset(p.a.row_ptr, g, p.a.num_rows) / p.chunk + g;
+}
+__device__ __forceinline__ int graph_of_slot(const NormParams& p, int slot) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, count = p.a.num_graphs;
+  while (count > 1) {
+    const int step = (count + 63) >> 6, i = lane * step;
+    bool before = false;
+    if (i < count) before = first_slot(p, lo + i) <= slot;
+    const int hits = max(__popcll(__ballot(before)), 1);
+    lo += (hits - 1) * step;
+    count = min(step, count - (hits - 1) * step);
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// Sum over the 256 threads of a work-group, in every thread.
+// The chunk of a slot: rows [begin, end) of graph g.
+struct Chunk {
+  int g, begin, end;
+  bool first;      // the graph's first chunk
+  bool only;       // and its only one
+  bool none;       // a slot without a chunk
+};
+__device__ __forceinline__ Chunk chunk_of(const NormParams& p, int slot) {
+  Chunk c;
+  c.g = graph_of_slot(p, slot);
+  const int r0 = offset(p.a.row_ptr, c.g, p.a.num_rows);
+  const int r1 = max(r0, offset(p.a.row_ptr, c.g + 1, p.a.num_rows));
+  const int k = slot - first_slot(p, c.g);
+  c.first = k == 0;
+  c.only = c.first && r1 - r0 <= p.chunk && p.units <= NT;
+  c.none = k < 0 || (k > 0 && (long)k * p.chunk >= r1 - r0);
+  c.begin = c.none ? r0 : r0 + k * p.chunk;
+  c.end = min(r1, c.begin + p.chunk);
+  return c;
+}
+
+// --------------------------------------------------------------- elements ---
+
+template <class T, int V>
+struct Run {
+  typedef T type __attribute__((ext_vector_type(V)));
+};
+template <class T>
+struct Run<T, 1> {
+  typedef T type;
+};
+template <class T, int V>
+__device__ __forceinline__ void load(const T* p, float (&v)[V]) {
+  const typename Run<T, V>::type r = *reinterpret_cast<const typename Run<T, V>::type*>(p);
+  if constexpr (V == 1) {
+    v[0] = (float)r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = (float)r[i];
+  }
+}
+template <class T, int V>
+__device__ __forceinline__ void store(T* p, const float (&v)[V]) {
+  typename Run<T, V>::type r;
+  if constexpr (V == 1) {
+    r = (T)v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[i] = (T)v[i];
+  }
+  *reinterpret_cast<typename Run<T, V>::type*>(p) = r;
+}
+
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
+}
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if (ACT == E3CONV_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+  if (ACT == E3CONV_ACT_SILU) return z * sigmoid(z);
+  if (ACT == E3CONV_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  return z;
+}
+template <int ACT>
+__device__ __forceinline__ float activate_grad(float z) {
+  if (ACT == E3CONV_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  if (ACT == E3CONV_ACT_SILU) {
+    const float e = sigmoid(z);
+    return e * fmaf(z, 1.0f - e, 1.0f);
+  }
+  if (ACT == E3CONV_ACT_GELU)
+    return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
+           z * 0.39894228040143268f * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170368f);
+  return 1.0f;
+}
+
+// ---------------------------------------------------------------- threads ---
+
+// Thread -> run of channels and row of each pass.  units > NT: blockIdx.y picks NT of them.
+struct Place {
+  int unit, row, step;     // step: rows of a pass
+  int width;               // units of this work-group
+  bool on;
+};
+__device__ __forceinline__ Place place(const NormParams& p) {
+  Place q;
+  const int from = blockIdx.y * NT;
+  q.width = min(p.units - from, NT);
+  q.step = NT / q.width;
+  q.row = threadIdx.x / q.width;
+  q.unit = from + threadIdx.x % q.width;
+  q.on = q.row < q.step;
+  return q;
+}
+
+// Adds s1 and s2 over the threads of one unit; the result is in those of row 0.
+template <int V>
+__device__ void add_rows(const Place& q, float (&s1)[V], float (&s2)[V]) {
+  __shared__ float2 red[NT * V];
+  int rows = q.step, row = q.row;
+  bool on = q.on;
+  if (64 % q.width == 0) {     // within a wave first
+    for (int o = 32; o >= q.width; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s1[i] += __shfl_xor(s1[i], o);
+        s2[i] += __shfl_xor(s2[i], o);
+      }
+    rows = NT / 64;
+    row = threadIdx.x >> 6;
+    on = (threadIdx.x & 63) < q.width;
+  }
+  int half = 1;
+  while (half < rows) half <<= 1;
+  const int unit = threadIdx.x % q.width;
+  for (half >>= 1; half > 0; half >>= 1) {
+    if (on && row >= half && row < rows)
+#pragma unroll
+      for (int i = 0; i < V; ++i) red[((row - half) * V + i) * q.width + unit] = make_float2(s1[i], s2[i]);
+    __syncthreads();
+    if (on && row < half && row + half < rows)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 r = red[(row * V + i) * q.width + unit];
+        s1[i] += r.x;
+        s2[i] += r.y;
+      }
+    __syncthreads();
+    rows = min(rows, half);
+  }
+}
+
+// Counted rows of a chunk (in every thread), and the first of them (end if none).
+__device__ int count_rows(const NormParams& p, const Chunk& c, int* first) {
+  *first = c.begin;
+  if (!p.a.row_mask) return c.end - c.begin;
+  __shared__ int part[NT / 64], low[NT / 64];
+  int n = 0, f = c.end;
+  for (int r = c.begin + (int)threadIdx.x; r < c.end; r += NT)
+    if (p.a.row_mask[r]) {
+      ++n;
+      f = min(f, r);
+    }
+  for (int o = 32; o > 0; o >>= 1) {
+    n += __shfl_xor(n, o);
+    f = min(f, __shfl_xor(f, o));
+  }
+  if ((threadIdx.x & 63) == 0) {
+    part[threadIdx.x >> 6] = n;
+    low[threadIdx.x >> 6] = f;
+  }
+  __syncthreads();
+  *first = min(min(low[0], low[1]), min(low[2], low[3]));
+  return part[0] + part[1] + part[2] + part[3];
+}
+
+// Calls use(row) for this thread's counted rows of the chunk.
+template <class F>
+__device__ __forceinline__ void each_row(const NormParams& p, const Chunk& c, const Place& q, F use) {
+  if (!q.on) return;
+  if (p.a.row_mask) {
+#pragma unroll 4
+    for (int r = c.begin + q.row; r < c.end; r += q.step) use((long)r, p.a.row_mask[r] != 0);
+  } else {
+#pragma unroll 4
+    for (int r = c.begin + q.row; r < c.end; r += q.step) use((long)r, true);
+  }
+}
+
+// Per-channel constants of a thread's run.
+template <int V>
+struct Channels {
+  float w[V], b[V], mean[V], rstd[V];
+  __device__ __forceinline__ void affine(const NormParams& p, int c0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[i] = p.a.weight ? p.a.weight[c0 + i] : 1.0f;
+      b[i] = p.a.bias ? p.a.bias[c0 + i] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ void moments(const NormParams& p, int g, int c0, const float* mean_of,
+                                          const float* rstd_of) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      mean[i] = mean_of[g * p.a.groups + (c0 + i) / p.gc];
+      rstd[i] = rstd_of[g * p.a.groups + (c0 + i) / p.gc];
+    }
+  }
+};
+
+// ---------------------------------------------------------------- forward ---
+
+template <class T, int V, int ACT>
+__device__ __forceinline__ void write_rows(const NormParams& p, const Chunk& c, const Place& q,
+                                           const Channels<V>& k) {
+  const T* x = (const T*)p.a.x + q.unit * V;
+  T* y = (T*)p.y + q.unit * V;
+  each_row(p, c, q, [&](long r, bool counts) {
+    float v[V];
+    load<T, V>(x + r * p.a.x_row, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      v[i] = counts ? activate<ACT>(fmaf((v[i] - k.mean[i]) * k.rstd[i], k.w[i], k.b[i])) : 0.0f;
+    store<T, V>(y + r * p.y_row, v);
+  });
+}
+
+template <class T, int V, int ACT>
+__global__ void __launch_bounds__(NT) norm_sums(NormParams p) {
+  const Chunk c = chunk_of(p, blockIdx.x);
+  if (c.none) return;
+  const Place q = place(p);
+  const T* x = (const T*)p.a.x + q.unit * V;
+  int first;
+  const int n = count_rows(p, c, &first);
+  float at[V], s1[V], s2[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) at[i] = s1[i] = s2[i] = 0.0f;
+  if (q.on && n > 0) load<T, V>(x + first * p.a.x_row, at);
+  each_row(p, c, q, [&](long r, bool counts) {
+    float v[V];
+    load<T, V>(x + r * p.a.x_row, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float d = counts ? v[i] - at[i] : 0.0f;
+      s1[i] += d;
+      s2[i] = fmaf(d, d, s2[i]);
+    }
+  });
+  add_rows<V>(q, s1, s2);
+  // of the chunk, per channel: mean, and squared deviations from it
+  const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    s1[i] *= inv;
+    s2[i] = fmaxf(s2[i] - (float)n * s1[i] * s1[i], 0.0f);
+    s1[i] += at[i];
+  }
+  const int c0 = q.unit * V;
+  if (!c.only) {
+    if (threadIdx.x < q.width)
+#pragma unroll
+      for (int i = 0; i < V; ++i) p.sums[(long)blockIdx.x * p.a.channels + c0 + i] = make_float2(s1[i], s2[i]);
+    if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = (float)n;
+    return;
+  }
+  // the graph's only chunk: its groups here
+  __shared__ float mean[NT * V], dev[NT * V];
+  if (threadIdx.x < q.width)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      mean[c0 + i] = s1[i];
+      dev[c0 + i] = s2[i];
+    }
+  __syncthreads();
+  Channels<V> k;
+  k.affine(p, c0);
+  // a group's mean and variance by each thread that has one of its channels, in channel order
+  int have = -1;
+  float m = 0.0f, rs = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int g = (c0 + i) / p.gc;
+    if (g != have) {
+      have = g;
+      m = 0.0f;
+      for (int j = g * p.gc; j < (g + 1) * p.gc; ++j) m += mean[j] - mean[g * p.gc];
+      m = mean[g * p.gc] + m / (float)p.gc;
+      float v = 0.0f;
+      for (int j = g * p.gc; j < (g + 1) * p.gc; ++j) {
+        const float d = mean[j] - m;
+        v += fmaf((float)n * d, d, dev[j]);
+      }
+      rs = 1.0f / sqrtf(v * (inv / (float)p.gc) + p.a.eps);
+      if (n == 0) m = 0.0f;
+    }
+    k.mean[i] = m;
+    k.rstd[i] = rs;
+    if (threadIdx.x < q.width && (c0 + i) % p.gc == 0) {
+      if (p.mean) p.mean[c.g * p.a.groups + g] = m;
+      if (p.rstd) p.rstd[c.g * p.a.groups + g] = rs;
+    }
+  }
+  write_rows<T, V, ACT>(p, c, q, k);
+}
+
+// Sum over the threads of a work-group, in every thread.
 __device__ float block_sum(float v) {
-  __shared__ float part[4];
+  __shared__ float part[NT / 64];
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
@@ -58,131 +371,288 @@ __device__ float block_sum(float v) {
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case E3CONV_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case E3CONV_ACT_SILU: return z / (1.0f + expf(-z));
-    case E3CONV_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    default: return z;
+// One work-group per (graph, group): joins the chunks about the common mean.
+__global__ void __launch_bounds__(NT) norm_finish(NormParams p) {
+  const int g = blockIdx.x / p.a.groups, grp = blockIdx.x % p.a.groups;
+  const int s0 = first_slot(p, g);
+  const int rows = offset(p.a.row_ptr, g + 1, p.a.num_rows) - offset(p.a.row_ptr, g, p.a.num_rows);
+  if (rows <= p.chunk && p.units <= NT) return;
+  const int chunks = max((rows + p.chunk - 1) / p.chunk, 1), total = chunks * p.gc;
+  const float2* sums = p.sums + (long)s0 * p.a.channels + grp * p.gc;
+  const float base = sums[0].x;
+  float n = 0.0f, m = 0.0f, v = 0.0f;
+  for (int t = threadIdx.x; t < total; t += NT) {
+    const float k = p.counts[s0 + t / p.gc];
+    n += k;
+    m = fmaf(k, sums[(long)(t / p.gc) * p.a.channels + t % p.gc].x - base, m);
   }
-}
-
-__device__ __forceinline__ float activate_grad(float z, int act) {
-  switch (act) {
-    case E3CONV_ACT_RELU: return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-    case E3CONV_ACT_SILU: {
-      const float e = 1.0f / (1.0f + expf(-z));
-      return e * (1.0f + z * (1.0f - e));
-    }
-    case E3CONV_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
-    default: return 1.0f;
-  }
-}
-
-template <class T>
-__global__ void __launch_bounds__(256) norm_fwd(NormParams p) {
-  const e3conv_group_norm_args& a = p.a;
-  const int b = blockIdx.x / a.groups, grp = blockIdx.x % a.groups, gc = p.gc, c0 = grp * gc;
-  const int r0 = offset(a.row_ptr, b, (int)a.num_rows), r1 = offset(a.row_ptr, b + 1, (int)a.num_rows);
-  const T* x = (const T*)a.x + c0;
-  const long n = (long)(r1 > r0 ? r1 - r0 : 0) * gc;
-  float s = 0.0f, cnt = 0.0f;
-  for (long t = threadIdx.x; t < n; t += 256) {
-    const long r = r0 + t / gc;
-    if (a.row_mask && !a.row_mask[r]) continue;
-    s += load(x + r * a.x_row + t % gc);
-    cnt += 1.0f;
-  }
-  cnt = block_sum(cnt);
-  const float mean = cnt > 0.0f ? block_sum(s) / cnt : (block_sum(s), 0.0f);
-  float v = 0.0f;
-  for (long t = threadIdx.x; t < n; t += 256) {
-    const long r = r0 + t / gc;
-    if (a.row_mask && !a.row_mask[r]) continue;
-    const float d = load(x + r * a.x_row + t % gc) - mean;
-    v = fmaf(d, d, v);
+  n = block_sum(n);
+  m = block_sum(m);
+  m = n > 0.0f ? base + m / n : 0.0f;
+  for (int t = threadIdx.x; t < total; t += NT) {
+    const float2 s = sums[(long)(t / p.gc) * p.a.channels + t % p.gc];
+    const float d = s.x - m;
+    v += fmaf(p.counts[s0 + t / p.gc] * d, d, s.y);
   }
   v = block_sum(v);
-  const float rstd = 1.0f / sqrtf((cnt > 0.0f ? v / cnt : 0.0f) + a.eps);
+  const float rs = 1.0f / sqrtf((n > 0.0f ? v / n : 0.0f) + p.a.eps);
   if (threadIdx.x == 0) {
-    if (p.mean) p.mean[b * a.groups + grp] = mean;
-    if (p.rstd) p.rstd[b * a.groups + grp] = rstd;
+    p.stats[blockIdx.x] = make_float2(m, rs);
+    if (p.mean) p.mean[blockIdx.x] = m;
+    if (p.rstd) p.rstd[blockIdx.x] = rs;
   }
-  for (long t = threadIdx.x; t < n; t += 256) {
-    const long r = r0 + t / gc;
-    const int c = (int)(t % gc);
-    float y = 0.0f;
-    if (!a.row_mask || a.row_mask[r]) {
-      const float xh = (load(x + r * a.x_row + c) - mean) * rstd;
-      y = activate(fmaf(xh, a.weight ? a.weight[c0 + c] : 1.0f, a.bias ? a.bias[c0 + c] : 0.0f), a.activation);
+}
+
+template <class T, int V, int ACT>
+__global__ void __launch_bounds__(NT) norm_apply(NormParams p) {
+  const Chunk c = chunk_of(p, blockIdx.x);
+  if (c.none || c.only) return;
+  const Place q = place(p);
+  const int c0 = q.unit * V;
+  Channels<V> k;
+  k.affine(p, c0);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float2 s = p.stats[c.g * p.a.groups + (c0 + i) / p.gc];
+    k.mean[i] = s.x;
+    k.rstd[i] = s.y;
+  }
+  write_rows<T, V, ACT>(p, c, q, k);
+}
+
+// ---------------------------------------------------------------- reverse ---
+
+// dz and xhat of one row.
+template <class T, int V, int ACT>
+__device__ __forceinline__ void row_grad(const NormParams& p, const Channels<V>& k, long r, int c0, bool counts,
+                                         float (&dz)[V], float (&xh)[V]) {
+  load<T, V>((const T*)p.a.x + r * p.a.x_row + c0, xh);
+  load<T, V>((const T*)p.gy + r * p.gy_row + c0, dz);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    xh[i] = counts ? (xh[i] - k.mean[i]) * k.rstd[i] : 0.0f;
+    dz[i] = counts ? dz[i] * activate_grad<ACT>(fmaf(xh[i], k.w[i], k.b[i])) : 0.0f;
+  }
+}
+
+template <class T, int V, int ACT>
+__device__ __forceinline__ void write_grads(const NormParams& p, const Chunk& c, const Place& q,
+                                            const Channels<V>& k, const float (&m1)[V], const float (&m2)[V]) {
+  T* gx = (T*)p.gx + q.unit * V;
+  each_row(p, c, q, [&](long r, bool counts) {
+    float dz[V], xh[V];
+    row_grad<T, V, ACT>(p, k, r, q.unit * V, counts, dz, xh);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      dz[i] = counts ? k.rstd[i] * (fmaf(dz[i], k.w[i], -m1[i]) - xh[i] * m2[i]) : 0.0f;
+    store<T, V>(gx + r * p.gx_row, dz);
+  });
+}
+
+template <class T, int V, int ACT>
+__global__ void __launch_bounds__(NT) norm_grad_sums(NormParams p) {
+  const Chunk c = chunk_of(p, blockIdx.x);
+  const Place q = place(p);
+  const int c0 = q.unit * V;
+  float s1[V], s2[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
+  if (c.none) {     // the weight gradient sums over all slots
+    if (threadIdx.x < q.width)
+#pragma unroll
+      for (int i = 0; i < V; ++i) p.sums[(long)blockIdx.x * p.a.channels + c0 + i] = make_float2(0.0f, 0.0f);
+    return;
+  }
+  Channels<V> k;
+  k.affine(p, c0);
+  k.moments(p, c.g, c0, p.mean, p.rstd);
+  int first;
+  const int n = count_rows(p, c, &first);
+  each_row(p, c, q, [&](long r, bool counts) {
+    float dz[V], xh[V];
+    row_grad<T, V, ACT>(p, k, r, c0, counts, dz, xh);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s1[i] += dz[i];
+      s2[i] = fmaf(dz[i], xh[i], s2[i]);
     }
-    ((T*)p.y)[r * p.y_row + c0 + c] = (T)y;
+  });
+  add_rows<V>(q, s1, s2);
+  if (threadIdx.x < q.width)
+#pragma unroll
+    for (int i = 0; i < V; ++i) p.sums[(long)blockIdx.x * p.a.channels + c0 + i] = make_float2(s1[i], s2[i]);
+  if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = (float)n;
+  if (!c.only) return;
+  __shared__ float a1[NT * V], a2[NT * V];
+  if (threadIdx.x < q.width)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      a1[c0 + i] = s1[i] * k.w[i];
+      a2[c0 + i] = s2[i] * k.w[i];
+    }
+  __syncthreads();
+  const float inv = n > 0 ? 1.0f / ((float)n * (float)p.gc) : 0.0f;
+  int have = -1;
+  float m1 = 0.0f, m2 = 0.0f, m1s[V], m2s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int g = (c0 + i) / p.gc;
+    if (g != have) {
+      have = g;
+      m1 = m2 = 0.0f;
+      for (int j = g * p.gc; j < (g + 1) * p.gc; ++j) {
+        m1 += a1[j];
+        m2 += a2[j];
+      }
+    }
+    m1s[i] = m1 * inv;
+    m2s[i] = m2 * inv;
   }
+  write_grads<T, V, ACT>(p, c, q, k, m1s, m2s);
 }
 
-// dz of row r, channel c and its xhat.
-template <class T>
-__device__ __forceinline__ float dz_of(const NormParams& p, long r, int c, float mean, float rstd, float& xh) {
-  const e3conv_group_norm_args& a = p.a;
-  xh = (load((const T*)a.x + r * a.x_row + c) - mean) * rstd;
-  const float z = fmaf(xh, a.weight ? a.weight[c] : 1.0f, a.bias ? a.bias[c] : 0.0f);
-  return load((const T*)p.gy + r * p.gy_row + c) * activate_grad(z, a.activation);
+// Work-groups 0 .. graphs x groups - 1: the means of one graph and group.
+__global__ void __launch_bounds__(NT) norm_grad_finish(NormParams p) {
+  const int g = blockIdx.x / p.a.groups, grp = blockIdx.x % p.a.groups;
+  const int s0 = first_slot(p, g);
+  const int rows = offset(p.a.row_ptr, g + 1, p.a.num_rows) - offset(p.a.row_ptr, g, p.a.num_rows);
+  if (rows <= p.chunk && p.units <= NT) return;
+  const int chunks = max((rows + p.chunk - 1) / p.chunk, 1), total = chunks * p.gc;
+  float n = 0.0f, m1 = 0.0f, m2 = 0.0f;
+  for (int t = threadIdx.x; t < total; t += NT) {
+    const int ch = grp * p.gc + t % p.gc;
+    const float2 s = p.sums[(long)(s0 + t / p.gc) * p.a.channels + ch];
+    const float w = p.a.weight ? p.a.weight[ch] : 1.0f;
+    n += p.counts[s0 + t / p.gc];
+    m1 = fmaf(w, s.x, m1);
+    m2 = fmaf(w, s.y, m2);
+  }
+  n = fmaxf(block_sum(n), 1.0f);
+  m1 = block_sum(m1) / n;
+  m2 = block_sum(m2) / n;
+  if (threadIdx.x == 0) p.stats[blockIdx.x] = make_float2(m1, m2);
 }
 
-// Before norm_bwd_x, which may write grad_x over grad_y.
-template <class T>
-__global__ void __launch_bounds__(256) norm_bwd_w(NormParams p) {
-  const e3conv_group_norm_args& a = p.a;
-  const int c = blockIdx.x, grp = c / p.gc;
+// Weight and bias gradients of four channels: 64 threads each over the slots.
+__global__ void __launch_bounds__(NT) norm_grad_affine(NormParams p) {
+  __shared__ float2 red[NT];
+  const int c = blockIdx.x * 4 + (threadIdx.x & 3);
   float w = 0.0f, b = 0.0f;
-  for (long r = threadIdx.x; r < a.num_rows; r += 256) {
-    if (a.row_mask && !a.row_mask[r]) continue;
-    const int g = graph_of(a.row_ptr, a.num_graphs, (int)r) * a.groups + grp;
-    float xh;
-    const float dz = dz_of<T>(p, r, c, p.mean[g], p.rstd[g], xh);
-    w = fmaf(dz, xh, w);
-    b += dz;
+  if (c < p.a.channels)
+    for (int s = threadIdx.x >> 2; s < p.slots; s += NT / 4) {
+      const float2 v = p.sums[(long)s * p.a.channels + c];
+      b += v.x;
+      w += v.y;
+    }
+  red[threadIdx.x] = make_float2(b, w);
+  __syncthreads();
+  for (int o = NT / 2; o >= 4; o >>= 1) {
+    if ((int)threadIdx.x < o) {
+      red[threadIdx.x].x += red[threadIdx.x + o].x;
+      red[threadIdx.x].y += red[threadIdx.x + o].y;
+    }
+    __syncthreads();
   }
-  w = block_sum(w);
-  b = block_sum(b);
-  if (threadIdx.x == 0) {
-    if (p.gw) p.gw[c] = w;
-    if (p.gb) p.gb[c] = b;
+  if (threadIdx.x < 4 && c < p.a.channels) {
+    if (p.gb) p.gb[c] = red[threadIdx.x].x;
+    if (p.gw) p.gw[c] = red[threadIdx.x].y;
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(256) norm_bwd_x(NormParams p) {
-  const e3conv_group_norm_args& a = p.a;
-  const int b = blockIdx.x / a.groups, grp = blockIdx.x % a.groups, gc = p.gc, c0 = grp * gc;
-  const int r0 = offset(a.row_ptr, b, (int)a.num_rows), r1 = offset(a.row_ptr, b + 1, (int)a.num_rows);
-  const long n = (long)(r1 > r0 ? r1 - r0 : 0) * gc;
-  const float mean = p.mean[b * a.groups + grp], rstd = p.rstd[b * a.groups + grp];
-  float s1 = 0.0f, s2 = 0.0f, cnt = 0.0f;
-  for (long t = threadIdx.x; t < n; t += 256) {
-    const long r = r0 + t / gc;
-    if (a.row_mask && !a.row_mask[r]) continue;
-    const int c = c0 + (int)(t % gc);
-    float xh;
-    const float dn = dz_of<T>(p, r, c, mean, rstd, xh) * (a.weight ? a.weight[c] : 1.0f);
-    s1 += dn;
-    s2 = fmaf(dn, xh, s2);
-    cnt += 1.0f;
+template <class T, int V, int ACT>
+__global__ void __launch_bounds__(NT) norm_grad_apply(NormParams p) {
+  const Chunk c = chunk_of(p, blockIdx.x);
+  if (c.none || c.only) return;
+  const Place q = place(p);
+  const int c0 = q.unit * V;
+  Channels<V> k;
+  k.affine(p, c0);
+  k.moments(p, c.g, c0, p.mean, p.rstd);
+  float m1[V], m2[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float2 s = p.stats[c.g * p.a.groups + (c0 + i) / p.gc];
+    m1[i] = s.x;
+    m2[i] = s.y;
   }
-  cnt = fmaxf(block_sum(cnt), 1.0f);
-  const float m1 = block_sum(s1) / cnt, m2 = block_sum(s2) / cnt;
-  for (long t = threadIdx.x; t < n; t += 256) {
-    const long r = r0 + t / gc;
-    const int c = c0 + (int)(t % gc);
-    float dx = 0.0f;
-    if (!a.row_mask || a.row_mask[r]) {
-      float xh;
-      const float dn = dz_of<T>(p, r, c, mean, rstd, xh) * (a.weight ? a.weight[c] : 1.0f);
-      dx = rstd * (dn - m1 - xh * m2);
-    }
-    ((T*)p.gx)[r * p.gx_row + c] = (T)dx;
+  write_grads<T, V, ACT>(p, c, q, k, m1, m2);
+}
+
+// --------------------------------------------------------------- launches ---
+
+template <class T, int V, int ACT>
+hipError_t forward(const NormParams& p, bool one, hipStream_t s) {
+  const dim3 grid((unsigned)p.slots, (unsigned)((p.units + NT - 1) / NT));
+  hipLaunchKernelGGL((norm_sums<T, V, ACT>), grid, dim3(NT), 0, s, p);
+  if (!one) {
+    hipLaunchKernelGGL(norm_finish, dim3((unsigned)(p.a.num_graphs * p.a.groups)), dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((norm_apply<T, V, ACT>), grid, dim3(NT), 0, s, p);
   }
+  return hipGetLastError();
+}
+
+template <class T, int V, int ACT>
+hipError_t backward(const NormParams& p, bool one, hipStream_t s) {
+  const dim3 grid((unsigned)p.slots, (unsigned)((p.units + NT - 1) / NT));
+  hipLaunchKernelGGL((norm_grad_sums<T, V, ACT>), grid, dim3(NT), 0, s, p);
+  if (p.gw || p.gb)
+    hipLaunchKernelGGL(norm_grad_affine, dim3((unsigned)((p.a.channels + 3) / 4)), dim3(NT), 0, s, p);
+  if (!one) {
+    hipLaunchKernelGGL(norm_grad_finish, dim3((unsigned)(p.a.num_graphs * p.a.groups)), dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((norm_grad_apply<T, V, ACT>), grid, dim3(NT), 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+template <class T, int V>
+hipError_t by_activation(const NormParams& p, bool back, bool one, hipStream_t s) {
+  switch (p.a.activation) {
+    case E3CONV_ACT_RELU:
+      return back ? backward<T, V, E3CONV_ACT_RELU>(p, one, s) : forward<T, V, E3CONV_ACT_RELU>(p, one, s);
+    case E3CONV_ACT_SILU:
+      return back ? backward<T, V, E3CONV_ACT_SILU>(p, one, s) : forward<T, V, E3CONV_ACT_SILU>(p, one, s);
+    case E3CONV_ACT_GELU:
+      return back ? backward<T, V, E3CONV_ACT_GELU>(p, one, s) : forward<T, V, E3CONV_ACT_GELU>(p, one, s);
+    default:
+      return back ? backward<T, V, E3CONV_ACT_NONE>(p, one, s) : forward<T, V, E3CONV_ACT_NONE>(p, one, s);
+  }
+}
+
+// Rows of a chunk: all of them where the whole call is small (then every graph is one chunk and
+// one launch does it), else about 2048 work-groups of 8 KiB at least.
+int chunk_rows(const e3conv_group_norm_args& a) {
+  const int64_t n = a.num_rows > 0 ? a.num_rows : 1;
+  if (n * a.channels <= 1 << 18) return (int)n;
+  const int64_t row = (int64_t)a.channels * (a.dtype == E3CONV_F32 ? 4 : 2);
+  const int64_t want = (n + 2047) / 2048, least = (8192 + row - 1) / row;
+  return (int)(want > least ? want : least);
+}
+int chunk_slots(const e3conv_group_norm_args& a) { return (int)(a.num_rows / chunk_rows(a) + a.num_graphs); }
+
+// sums (slots, channels), stats (graphs, groups), counts (slots).
+size_t workspace_bytes(const e3conv_group_norm_args& a) {
+  const size_t slots = (size_t)chunk_slots(a);
+  return (slots * a.channels + (size_t)a.num_graphs * a.groups) * sizeof(float2) + (slots * sizeof(float) + 15) / 16 * 16;
+}
+
+// Whether 16-byte runs of channels are aligned in a tensor.
+bool aligned(const void* p, int64_t row, int v) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row % v == 0; }
+
+hipError_t launch(NormParams p, bool back, bool vec, void* workspace, hipStream_t s) {
+  const bool f32 = p.a.dtype == E3CONV_F32;
+  const int v = f32 ? 4 : 8;
+  if (p.a.channels % v != 0) vec = false;
+  p.gc = p.a.channels / p.a.groups;
+  p.units = vec ? p.a.channels / v : p.a.channels;
+  p.chunk = chunk_rows(p.a);
+  p.slots = chunk_slots(p.a);
+  p.sums = static_cast<float2*>(workspace);
+  p.stats = p.sums + (size_t)p.slots * p.a.channels;
+  p.counts = reinterpret_cast<float*>(p.stats + (size_t)p.a.num_graphs * p.a.groups);
+  const bool one = p.a.num_rows <= p.chunk && p.units <= NT;
+  if ((int64_t)p.a.num_graphs * p.a.groups > 0x7fffffff) return hipErrorInvalidValue;
+  if (f32) return vec ? by_activation<float, 4>(p, back, one, s) : by_activation<float, 1>(p, back, one, s);
+  return vec ? by_activation<__bf16, 8>(p, back, one, s) : by_activation<__bf16, 1>(p, back, one, s);
 }
 
 e3conv_status bad(const char* what) { return api_fail(E3CONV_ERR_INVALID_ARGUMENT, what); }
@@ -219,7 +689,7 @@ e3conv_status e3conv_group_norm_workspace_size(const e3conv_group_norm_args* a, 
   const e3conv_status st = e3c::check_sizes(a);
   if (st != E3CONV_OK) return st;
   if (!bytes) return e3c::bad("bytes is NULL");
-  *bytes = 0;
+  *bytes = e3c::workspace_bytes(*a);
   return e3c::api_ok();
 }
 
@@ -230,18 +700,19 @@ e3conv_status e3conv_group_norm(const e3conv_group_norm_args* a, void* y, int64_
   if (y_row < 0) return e3c::bad("negative stride");
   if (a->num_graphs == 0) return e3c::api_ok();
   if (a->num_rows > 0 && !y) return e3c::bad("NULL device pointer");
+  const size_t need = e3c::workspace_bytes(*a);
+  if (bytes < need || !workspace)
+    return e3c::api_fail(E3CONV_ERR_WORKSPACE, "group norm needs " + std::to_string(need) + " bytes");
   e3c::NormParams p{};
   p.a = *a;
-  p.gc = a->channels / a->groups;
   p.y = y;
   p.y_row = y_row;
   p.mean = mean;
   p.rstd = rstd;
-  const dim3 grid((unsigned)((long)a->num_graphs * a->groups));
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (a->dtype == E3CONV_F32) hipLaunchKernelGGL(e3c::norm_fwd<float>, grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL(e3c::norm_fwd<__bf16>, grid, dim3(256), 0, s, p);
-  const hipError_t err = hipGetLastError();
+  const int v = a->dtype == E3CONV_F32 ? 4 : 8;
+  const hipError_t err =
+      e3c::launch(p, false, e3c::aligned(a->x, a->x_row, v) && e3c::aligned(y, y_row, v), workspace,
+                  static_cast<hipStream_t>(stream));
   if (err != hipSuccess) return e3c::api_hip_fail(err, "group norm launch");
   return e3c::api_ok();
 }
@@ -255,9 +726,18 @@ e3conv_status e3conv_group_norm_backward(const e3conv_group_norm_args* a, const 
   if (grad_y_row < 0 || grad_x_row < 0) return e3c::bad("negative stride");
   if (a->num_graphs > 0 && (!mean || !rstd)) return e3c::bad("NULL device pointer");
   if (a->num_rows > 0 && (!grad_y || !grad_x)) return e3c::bad("NULL device pointer");
+  if (a->num_graphs == 0) {
+    hipError_t e = hipSuccess;
+    for (float* g : {grad_weight, grad_bias})
+      if (g && e == hipSuccess) e = e3c::launch_fill_zero(g, (size_t)a->channels, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return e3c::api_hip_fail(e, "fill launch");
+    return e3c::api_ok();
+  }
+  const size_t need = e3c::workspace_bytes(*a);
+  if (bytes < need || !workspace)
+    return e3c::api_fail(E3CONV_ERR_WORKSPACE, "group norm backward needs " + std::to_string(need) + " bytes");
   e3c::NormParams p{};
   p.a = *a;
-  p.gc = a->channels / a->groups;
   p.mean = const_cast<float*>(mean);
   p.rstd = const_cast<float*>(rstd);
   p.gy = grad_y;
@@ -266,18 +746,10 @@ e3conv_status e3conv_group_norm_backward(const e3conv_group_norm_args* a, const 
   p.gx_row = grad_x_row;
   p.gw = grad_weight;
   p.gb = grad_bias;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (grad_weight || grad_bias) {
-    const dim3 grid((unsigned)a->channels);
-    if (a->dtype == E3CONV_F32) hipLaunchKernelGGL(e3c::norm_bwd_w<float>, grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL(e3c::norm_bwd_w<__bf16>, grid, dim3(256), 0, s, p);
-  }
-  if (a->num_rows > 0) {
-    const dim3 grid((unsigned)((long)a->num_graphs * a->groups));
-    if (a->dtype == E3CONV_F32) hipLaunchKernelGGL(e3c::norm_bwd_x<float>, grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL(e3c::norm_bwd_x<__bf16>, grid, dim3(256), 0, s, p);
-  }
-  const hipError_t err = hipGetLastError();
+  const int v = a->dtype == E3CONV_F32 ? 4 : 8;
+  const bool vec = e3c::aligned(a->x, a->x_row, v) && e3c::aligned(grad_y, grad_y_row, v) &&
+                   e3c::aligned(grad_x, grad_x_row, v);
+  const hipError_t err = e3c::launch(p, true, vec, workspace, static_cast<hipStream_t>(stream));
   if (err != hipSuccess) return e3c::api_hip_fail(err, "group norm backward launch");
   return e3c::api_ok();
 }
