@@ -28,6 +28,10 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
 # object; fp32 atomics map to the hardware instruction.
 DEVICE = ["--offload-arch=gfx950", "-munsafe-fp-atomics",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+# Matrix instructions with their accumulators in the general registers: the vector ALU works on
+# every accumulator between two products, and the copies to and from the accumulator registers
+# were a third of the instructions.
+FILE_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for f in ("attention_fwd.hip", "attention_bwd.hip")}
 
 
 def hipcc():
@@ -41,7 +45,7 @@ def _compile(src, verbose):
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     cmd = [hipcc(), "-c", os.path.join(CSRC, src), "-o", obj] + COMMON
     if src.endswith(".hip"):
-        cmd += DEVICE
+        cmd += DEVICE + FILE_FLAGS.get(src, [])
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)

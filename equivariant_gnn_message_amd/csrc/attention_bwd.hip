@@ -16,11 +16,10 @@ namespace e3c {
 namespace attn {
 namespace {
 
-template <class T, int D, int RW, int TK>
+template <class T, int D, int RW, int TK, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
-  constexpr int P = planes<T>(), U = D / 8, KS = D / 16, NT = 64 * RW, E = TK * U / NT;
-  static_assert(TK * U % NT == 0, "");
-  __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kt, vt;
+  constexpr int P = planes<T>(), KS = D / 16;
+  __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kts[BUF], vts[BUF];
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -35,7 +34,7 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
 
   const int r = r0 + 32 * w + n;
   const bool row = r < nrows;
-  const int qi = q0 + (row ? r / p.group : 0), head = c * p.group + (row ? r % p.group : 0);
+  const int qi = q0 + (row ? query_of(p, r) : 0), head = c * p.group + (row ? r - (qi - q0) * p.group : 0);
   const long at = (long)qi * a.heads_q + head;
   float lse = p.lse[at];
   const bool live = row && (!a.q_mask || a.q_mask[qi]) && lse != -INFINITY;
@@ -48,37 +47,22 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
 
   const T* kbase = (const T*)a.k + c * a.k_head;
   const T* vbase = (const T*)a.v + c * a.v_head;
-  Raw<T> kr[E], vr[E];
-  bool keep[E], key = false;
-  auto load = [&](int k0) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int t = threadIdx.x + e * NT, j = k0 + t / U, d = t % U * 8;
-      const bool in = j < k1;
-      kr[e] = fetch8(kbase + j * a.k_row + d, in ? a.dim_qk - d : 0, p.vec);
-      vr[e] = fetch8(vbase + j * a.v_row + d, in ? a.dim_v - d : 0, p.vec);
-      keep[e] = in && (!a.k_mask || a.k_mask[j]);
-    }
-    const int j = k0 + lane;
-    key = lane < TK && j < k1 && (!a.k_mask || a.k_mask[j]);
-  };
-  if (k0 < k1) load(k0);
+  Keys<T, D, TK, 64 * RW, VEC> keys;
+  if (k0 < k1) keys.load(p, kbase, vbase, k0, k1);
 
   Frag<P> q[KS], go[KS];
-  const T* qp = (const T*)a.q + qi * a.q_row + head * a.q_head;
   const T* gp = (const T*)p.go + qi * p.go_row + head * p.go_head;
   const T* op = (const T*)p.out + qi * p.out_row + head * p.out_head;
+  row_operand<T, D, VEC>((const T*)a.q + qi * a.q_row + head * a.q_head, a.dim_qk, live, q);
+  row_operand<T, D, VEC>(gp, a.dim_v, live, go);
   float delta = 0.0f;
 #pragma unroll
   for (int t = 0; t < KS; ++t) {
     const int d = 16 * t + 8 * h;
-    q[t] = frag_of(fetch8(qp + d, live ? a.dim_qk - d : 0, p.vec), live);
+    const Raw<T> gr = fetch8<VEC>(gp, d, a.dim_v), orow = fetch8<VEC>(op, d, a.dim_v);
     if (p.negate) flip_sign(q[t]);
-    const Raw<T> gr = fetch8(gp + d, live ? a.dim_v - d : 0, p.vec);
-    const Raw<T> orow = fetch8(op + d, live ? a.dim_v - d : 0, p.vec);
-    go[t] = frag_of(gr, live);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) delta = fmaf(gr.at(i), orow.at(i), delta);
+    for (int i = 0; i < 8; ++i) delta = d < a.dim_v ? fmaf(gr.at(i), orow.at(i), delta) : delta;
   }
   delta = live ? delta + other_half(delta) : 0.0f;
   if (row && h == 0 && split == 0) p.delta[at] = delta;
@@ -87,18 +71,14 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) dq[dt] = f32x16{};
 
-  for (; k0 < k1; k0 += TK) {
+  for (int buf = 0; k0 < k1; k0 += TK, buf ^= BUF - 1) {
+    Tile<P, TK, D>&kt = kts[buf], &vt = vts[buf];
+    const unsigned long seen = keys.seen(k0, k1);
+    const bool whole = keys.whole(seen);
+    if (BUF == 1) __syncthreads();
+    keys.store(p, k0, k1, whole, kt, vt);
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int t = threadIdx.x + e * NT;
-      kt.store(t / U, t % U, frag_of(kr[e], keep[e]));
-      vt.store(t / U, t % U, frag_of(vr[e], keep[e]));
-    }
-    const unsigned long seen = __ballot(key);
-    __syncthreads();
-    if (k0 + TK < k1) load(k0 + TK);
-    const bool whole = seen == (TK == 64 ? ~0ul : (1ul << (TK & 63)) - 1);
+    if (k0 + TK < k1) keys.load(p, kbase, vbase, k0 + TK, k1);
     const unsigned long bits = seen >> (4 * h);
 
 #pragma unroll
@@ -153,12 +133,12 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
     }
 }
 
-template <class T, int D, int RW, int TQ>
+template <class T, int D, int RW, int TQ, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
-  constexpr int P = planes<T>(), U = D / 8, KS = D / 16, NT = 64 * RW, E = TQ * U / NT;
+  constexpr int P = planes<T>(), U = D / 8, KS = D / 16, NT = 64 * RW, E = TQ * U / NT, STEP = NT / U;
   static_assert(TQ * U % NT == 0 && TQ <= NT, "");
-  __shared__ __attribute__((aligned(16))) Tile<P, TQ, D> qt, gt;
-  __shared__ __attribute__((aligned(16))) float lse_s[TQ], delta_s[TQ];
+  __shared__ __attribute__((aligned(16))) Tile<P, TQ, D> qts[BUF], gts[BUF];
+  __shared__ __attribute__((aligned(16))) float lse_b[BUF][TQ], delta_b[BUF][TQ];
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -184,60 +164,55 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
   const T* qbase = (const T*)a.q + q0 * a.q_row + c * p.group * a.q_head;
   const T* gbase = (const T*)p.go + q0 * p.go_row + c * p.group * p.go_head;
   const long at0 = (long)q0 * a.heads_q + c * p.group;
+  const int unit = threadIdx.x % U, line = threadIdx.x / U;
   Raw<T> qr[E], gr[E];
-  bool keep[E];
-  float lse = INFINITY, delta = 0.0f;
+  unsigned char qm[E], lm;
+  float ql[E], lse, delta;
+  // issues the loads of the tile from row r0 on; rows beyond the last read the last one
   auto load = [&](int r0) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int t = threadIdx.x + e * NT, r = r0 + t / U, d = t % U * 8;
-      const bool in = r < r1;
-      const int i = in ? r / p.group : 0, x = in ? r % p.group : 0;
-      qr[e] = fetch8(qbase + i * a.q_row + x * a.q_head + d, in ? a.dim_qk - d : 0, p.vec);
-      gr[e] = fetch8(gbase + i * p.go_row + x * p.go_head + d, in ? a.dim_v - d : 0, p.vec);
-      keep[e] = in && (!a.q_mask || a.q_mask[q0 + i]) && p.lse[at0 + (long)i * a.heads_q + x] != -INFINITY;
+      const int r = min(r0 + line + e * STEP, r1 - 1), i = query_of(p, r), x = r - i * p.group;
+      qr[e] = fetch8<VEC>(qbase + i * a.q_row + x * a.q_head, unit * 8, a.dim_qk);
+      gr[e] = fetch8<VEC>(gbase + i * p.go_row + x * p.go_head, unit * 8, a.dim_v);
+      qm[e] = a.q_mask ? a.q_mask[q0 + i] : 1;
+      ql[e] = p.lse[at0 + (long)i * a.heads_q + x];
     }
-    // a row that sees no key: lse = +infinity makes its P zero
-    lse = INFINITY;
-    delta = 0.0f;
-    const int r = r0 + (int)threadIdx.x;
-    if (threadIdx.x < TQ && r < r1) {
-      const long at = at0 + (long)(r / p.group) * a.heads_q + r % p.group;
-      const float v = p.lse[at];
-      if (v != -INFINITY && (!a.q_mask || a.q_mask[q0 + r / p.group])) {
-        lse = v * kLog2e;
-        delta = p.delta[at];
-      }
-    }
+    const int r = min(r0 + (int)(threadIdx.x % TQ), r1 - 1), i = query_of(p, r);
+    const long at = at0 + (long)i * a.heads_q + r - i * p.group;
+    lse = p.lse[at];
+    delta = p.delta[at];
+    lm = a.q_mask ? a.q_mask[q0 + i] : 1;
   };
   if (r0 < r1) load(r0);
 
   Frag<P> k[KS], v[KS];
-  const T* kp = (const T*)a.k + j * a.k_row + c * a.k_head;
-  const T* vp = (const T*)a.v + j * a.v_row + c * a.v_head;
+  const int jr = key ? j : j0;
+  row_operand<T, D, VEC>((const T*)a.k + jr * a.k_row + c * a.k_head, a.dim_qk, live, k);
+  row_operand<T, D, VEC>((const T*)a.v + jr * a.v_row + c * a.v_head, a.dim_v, live, v);
+  if (p.negate)
 #pragma unroll
-  for (int t = 0; t < KS; ++t) {
-    const int d = 16 * t + 8 * h;
-    k[t] = frag_of(fetch8(kp + d, live ? a.dim_qk - d : 0, p.vec), live);
-    v[t] = frag_of(fetch8(vp + d, live ? a.dim_v - d : 0, p.vec), live);
-    if (p.negate) flip_sign(k[t]);
-  }
+    for (int t = 0; t < KS; ++t) flip_sign(k[t]);
 
   f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) dk[dt] = dv[dt] = f32x16{};
 
-  for (; r0 < r1; r0 += TQ) {
-    __syncthreads();
+  for (int buf = 0; r0 < r1; r0 += TQ, buf ^= BUF - 1) {
+    Tile<P, TQ, D>&qt = qts[buf], &gt = gts[buf];
+    float *lse_s = lse_b[buf], *delta_s = delta_b[buf];
+    if (BUF == 1) __syncthreads();
+    // a row that sees no key, or that lies beyond the end: zeros, and lse = +infinity makes its P zero
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int t = threadIdx.x + e * NT;
-      qt.store(t / U, t % U, frag_of(qr[e], keep[e]));
-      gt.store(t / U, t % U, frag_of(gr[e], keep[e]));
+      const bool keep = r0 + line + e * STEP < r1 && qm[e] && ql[e] != -INFINITY;
+      qt.store(line + e * STEP, unit, frag_of(qr[e], keep && unit * 8 < a.dim_qk));
+      gt.store(line + e * STEP, unit, frag_of(gr[e], keep && unit * 8 < a.dim_v));
     }
     if (threadIdx.x < TQ) {
-      lse_s[threadIdx.x] = lse;
-      delta_s[threadIdx.x] = delta;
+      const bool sees = r0 + (int)threadIdx.x < r1 && lm && lse != -INFINITY;
+      lse_s[threadIdx.x] = sees ? lse * kLog2e : INFINITY;
+      delta_s[threadIdx.x] = sees ? delta : 0.0f;
     }
     __syncthreads();
     if (r0 + TQ < r1) load(r0 + TQ);
@@ -370,17 +345,29 @@ size_t delta_bytes(const e3conv_attention_args& a) {
   return ((size_t)a.num_q * a.heads_q * sizeof(float) + 15) / 16 * 16;
 }
 
-template <class T, int D>
+template <class T, int D, bool VEC>
 void launch_q(const Params& p, int rw, unsigned grid, hipStream_t s) {
   constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_q<T, D, 4, TK4>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_q<T, D, 1, 32>), dim3(grid), dim3(64), 0, s, p);
+  constexpr int BUF4 = planes<T>() * TK4 * D * 2 * 2 * 2 <= 65536 ? 2 : 1;
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_q<T, D, 4, TK4, BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_q<T, D, 1, 32, 1, VEC>), dim3(grid), dim3(64), 0, s, p);
+}
+template <class T, int D, bool VEC>
+void launch_kv(const Params& p, int rw, unsigned grid, hipStream_t s) {
+  constexpr int TQ4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
+  constexpr int BUF4 = planes<T>() * TQ4 * D * 2 * 2 * 2 < 65536 ? 2 : 1;
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_kv<T, D, 4, TQ4, BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_kv<T, D, 1, 32, 1, VEC>), dim3(grid), dim3(64), 0, s, p);
+}
+template <class T, int D>
+void launch_q(const Params& p, int rw, unsigned grid, hipStream_t s) {
+  if (p.vec) launch_q<T, D, true>(p, rw, grid, s);
+  else launch_q<T, D, false>(p, rw, grid, s);
 }
 template <class T, int D>
 void launch_kv(const Params& p, int rw, unsigned grid, hipStream_t s) {
-  constexpr int TQ4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_kv<T, D, 4, TQ4>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_kv<T, D, 1, 32>), dim3(grid), dim3(64), 0, s, p);
+  if (p.vec) launch_kv<T, D, true>(p, rw, grid, s);
+  else launch_kv<T, D, false>(p, rw, grid, s);
 }
 
 template <class T>

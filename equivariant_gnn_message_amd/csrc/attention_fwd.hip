@@ -15,11 +15,10 @@ namespace e3c {
 namespace attn {
 namespace {
 
-template <class T, int D, int RW, int TK>
+template <class T, int D, int RW, int TK, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
-  constexpr int P = planes<T>(), U = D / 8, KS = D / 16, NT = 64 * RW, E = TK * U / NT;
-  static_assert(TK * U % NT == 0, "");
-  __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kt, vt;
+  constexpr int P = planes<T>(), KS = D / 16;
+  __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kts[BUF], vts[BUF];
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -35,7 +34,7 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
 
   const int r = r0 + 32 * w + n;
   const bool row = r < nrows;
-  const int qi = q0 + (row ? r / p.group : 0), head = c * p.group + (row ? r % p.group : 0);
+  const int qi = q0 + (row ? query_of(p, r) : 0), head = c * p.group + (row ? r - (qi - q0) * p.group : 0);
   const bool live = row && (!a.q_mask || a.q_mask[qi]);
 
   // this split's keys: whole tiles of the graph's
@@ -46,47 +45,28 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
 
   const T* kbase = (const T*)a.k + c * a.k_head;
   const T* vbase = (const T*)a.v + c * a.v_head;
-  Raw<T> kr[E], vr[E];
-  bool keep[E], key = false;
-  auto load = [&](int k0) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int t = threadIdx.x + e * NT, j = k0 + t / U, d = t % U * 8;
-      const bool in = j < k1;
-      kr[e] = fetch8(kbase + j * a.k_row + d, in ? a.dim_qk - d : 0, p.vec);
-      vr[e] = fetch8(vbase + j * a.v_row + d, in ? a.dim_v - d : 0, p.vec);
-      keep[e] = in && (!a.k_mask || a.k_mask[j]);
-    }
-    const int j = k0 + lane;
-    key = lane < TK && j < k1 && (!a.k_mask || a.k_mask[j]);
-  };
-  if (k0 < k1) load(k0);
+  Keys<T, D, TK, 64 * RW, VEC> keys;
+  if (k0 < k1) keys.load(p, kbase, vbase, k0, k1);
 
   Frag<P> q[KS];
-  const T* qp = (const T*)a.q + qi * a.q_row + head * a.q_head;
+  row_operand<T, D, VEC>((const T*)a.q + qi * a.q_row + head * a.q_head, a.dim_qk, live, q);
+  if (p.negate)
 #pragma unroll
-  for (int t = 0; t < KS; ++t) {
-    const int d = 16 * t + 8 * h;
-    q[t] = frag_of(fetch8(qp + d, live ? a.dim_qk - d : 0, p.vec), live);
-    if (p.negate) flip_sign(q[t]);
-  }
+    for (int t = 0; t < KS; ++t) flip_sign(q[t]);
 
   f32x16 o[D / 32];
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) o[dt] = f32x16{};
   float m = -INFINITY, l = 0.0f;   // of the logits in units of log 2; l: this half's keys
 
-  for (; k0 < k1; k0 += TK) {
+  // two buffers: one barrier a tile, the store of a tile behind the products of the one before
+  for (int buf = 0; k0 < k1; k0 += TK, buf ^= BUF - 1) {
+    Tile<P, TK, D>&kt = kts[buf], &vt = vts[buf];
+    const unsigned long seen = keys.seen(k0, k1);
+    if (BUF == 1) __syncthreads();
+    keys.store(p, k0, k1, keys.whole(seen), kt, vt);
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int t = threadIdx.x + e * NT;
-      kt.store(t / U, t % U, frag_of(kr[e], keep[e]));
-      vt.store(t / U, t % U, frag_of(vr[e], keep[e]));
-    }
-    const unsigned long seen = __ballot(key);
-    __syncthreads();
-    if (k0 + TK < k1) load(k0 + TK);
+    if (k0 + TK < k1) keys.load(p, kbase, vbase, k0 + TK, k1);
 
     f32x16 s[TK / 32];
 #pragma unroll
@@ -95,7 +75,7 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
 #pragma unroll
       for (int t = 0; t < KS; ++t) s[b] = mma(kt.rows(32 * b, t, lane), q[t], s[b]);
     }
-    if (seen != (TK == 64 ? ~0ul : (1ul << (TK & 63)) - 1)) {
+    if (!keys.whole(seen)) {
       const unsigned long bits = seen >> (4 * h);
 #pragma unroll
       for (int b = 0; b < TK / 32; ++b)
@@ -242,11 +222,18 @@ Shape shape_of(const e3conv_attention_args& a) {
   return s;
 }
 
-template <class T, int D>
+// LDS: the tiles of both buffers, at most 64 KiB (two work-groups of a compute unit).
+template <class T, int D, bool VEC>
 void launch(const Params& p, int rw, unsigned grid, hipStream_t s) {
   constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
-  if (rw == 4) hipLaunchKernelGGL((attn_fwd<T, D, 4, TK4>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_fwd<T, D, 1, 32>), dim3(grid), dim3(64), 0, s, p);
+  constexpr int BUF4 = planes<T>() * TK4 * D * 2 * 2 * 2 <= 65536 ? 2 : 1;
+  if (rw == 4) hipLaunchKernelGGL((attn_fwd<T, D, 4, TK4, BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_fwd<T, D, 1, 32, 1, VEC>), dim3(grid), dim3(64), 0, s, p);
+}
+template <class T, int D>
+void launch(const Params& p, int rw, unsigned grid, hipStream_t s) {
+  if (p.vec) launch<T, D, true>(p, rw, grid, s);
+  else launch<T, D, false>(p, rw, grid, s);
 }
 
 template <class T>

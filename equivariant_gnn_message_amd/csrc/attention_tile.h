@@ -29,6 +29,8 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 struct Params {
   e3conv_attention_args a;
   int group;                       // query heads per kv head
+  unsigned magic;                  // r / group = (r magic) >> 32 >> shift for 0 <= r < 2^31, group > 1
+  int shift;
   float c;                         // |scale| log2(e), at least the smallest normal number
   int negate;                      // scale < 0: q enters with its sign changed
   int vec;                         // 16-byte loads of q, k, v, grad_out (and out) rows
@@ -101,32 +103,32 @@ struct Raw<float> {
   __device__ __forceinline__ float at(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
 };
 
-// Elements p[0 .. n-1], the others 0; n <= 0 reads nothing.  vec: p is 16-byte aligned
-// and n is 8 or at most 0.
-__device__ __forceinline__ Raw<__bf16> fetch8(const __bf16* p, int n, bool vec) {
+// Eight elements of a row from element d on, of dim.  VEC: rows are 16-byte aligned and
+// dim is a multiple of 8; a unit beyond dim reads the row's first one (the caller drops
+// it).  Else element by element, zeros beyond dim.
+template <bool VEC>
+__device__ __forceinline__ Raw<__bf16> fetch8(const __bf16* row, int d, int dim) {
   Raw<__bf16> r;
-  if (vec) {
-    if (n > 0) r.v = *reinterpret_cast<const bf16x8*>(p);
-    else r.v = bf16x8{};
+  if (VEC) {
+    r.v = *reinterpret_cast<const bf16x8*>(row + (d < dim ? d : 0));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = i < n ? p[i] : (__bf16)0.0f;
+    for (int i = 0; i < 8; ++i) r.v[i] = d + i < dim ? row[d + i] : (__bf16)0.0f;
   }
   return r;
 }
-__device__ __forceinline__ Raw<float> fetch8(const float* p, int n, bool vec) {
+template <bool VEC>
+__device__ __forceinline__ Raw<float> fetch8(const float* row, int d, int dim) {
   Raw<float> r;
-  if (vec) {
-    r.a = r.b = f32x4{};
-    if (n > 0) {
-      r.a = *reinterpret_cast<const f32x4*>(p);
-      r.b = *reinterpret_cast<const f32x4*>(p + 4);
-    }
+  if (VEC) {
+    const float* p = row + (d < dim ? d : 0);
+    r.a = *reinterpret_cast<const f32x4*>(p);
+    r.b = *reinterpret_cast<const f32x4*>(p + 4);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      r.a[i] = i < n ? p[i] : 0.0f;
-      r.b[i] = i + 4 < n ? p[i + 4] : 0.0f;
+      r.a[i] = d + i < dim ? row[d + i] : 0.0f;
+      r.b[i] = d + i + 4 < dim ? row[d + i + 4] : 0.0f;
     }
   }
   return r;
@@ -239,6 +241,73 @@ __device__ __forceinline__ int graph_of_slot(const int* ptr, int graphs, long n,
 }
 __device__ __forceinline__ int first_slot(const int* ptr, int g, long n, int mult, int tile) {
   return offset(ptr, g, n) * mult / tile + g;
+}
+
+// Row r of a graph's rows is head r % group of query r / group.
+__device__ __forceinline__ int query_of(const Params& p, int r) {
+  return p.group == 1 ? r : (int)(__umulhi((unsigned)r, p.magic) >> p.shift);
+}
+
+// The tiles of the keys of one kv head, ROWS at a time, from memory through registers to
+// LDS.  load() only issues the loads of the tile from key k0 on (rows beyond the last key
+// read the last one); store() writes them with zeros in place of masked keys, of those
+// beyond the end and of dimensions beyond dim, whatever memory holds there.
+template <class T, int D, int ROWS, int NT, bool VEC>
+struct Keys {
+  static constexpr int P = planes<T>(), U = D / 8, E = ROWS * U / NT, STEP = NT / U;
+  static_assert(ROWS * U % NT == 0, "");
+  Raw<T> k[E], v[E];
+  unsigned char m[E], ml;
+
+  __device__ __forceinline__ void load(const Params& p, const T* kb, const T* vb, int k0, int k1) {
+    const e3conv_attention_args& a = p.a;
+    const int unit = threadIdx.x % U, row = threadIdx.x / U;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int j = min(k0 + row + e * STEP, k1 - 1);
+      k[e] = fetch8<VEC>(kb + j * a.k_row, unit * 8, a.dim_qk);
+      v[e] = fetch8<VEC>(vb + j * a.v_row, unit * 8, a.dim_v);
+      m[e] = a.k_mask ? a.k_mask[j] : 1;
+    }
+    ml = a.k_mask ? a.k_mask[min(k0 + (int)(threadIdx.x & 63), k1 - 1)] : 1;
+  }
+  // The keys of the tile that are seen, a bit each.
+  __device__ __forceinline__ unsigned long seen(int k0, int k1) const {
+    const int lane = threadIdx.x & 63;
+    return __ballot(lane < ROWS && k0 + lane < k1 && ml);
+  }
+  static __device__ __forceinline__ bool whole(unsigned long seen) {
+    return seen == (ROWS == 64 ? ~0ul : (1ul << (ROWS & 63)) - 1);
+  }
+  __device__ __forceinline__ void store(const Params& p, int k0, int k1, bool whole, Tile<P, ROWS, D>& kt,
+                                        Tile<P, ROWS, D>& vt) const {
+    const int unit = threadIdx.x % U, row = threadIdx.x / U;
+    if (whole && (!VEC || (p.a.dim_qk == D && p.a.dim_v == D))) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        kt.store(row + e * STEP, unit, frag_of(k[e], true));
+        vt.store(row + e * STEP, unit, frag_of(v[e], true));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const bool keep = k0 + row + e * STEP < k1 && m[e];
+        kt.store(row + e * STEP, unit, frag_of(k[e], keep && unit * 8 < p.a.dim_qk));
+        vt.store(row + e * STEP, unit, frag_of(v[e], keep && unit * 8 < p.a.dim_v));
+      }
+    }
+  }
+};
+
+// The B operands of one row (lane n's, k = 16 t + 8 h + j) from memory; zeros unless live.
+template <class T, int D, bool VEC>
+__device__ __forceinline__ void row_operand(const T* row, int dim, bool live, Frag<planes<T>()> (&f)[D / 16]) {
+  const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int t = 0; t < D / 16; ++t) {
+    const int d = 16 * t + 8 * h;
+    f[t] = frag_of(fetch8<VEC>(row, d, dim), live && d < dim);
+  }
 }
 
 // Four consecutive elements d .. d + 3 of a row with dim elements.
