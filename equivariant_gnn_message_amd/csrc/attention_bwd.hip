@@ -20,6 +20,7 @@ template <class T, int D, int RW, int TK, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
   constexpr int P = planes<T>(), KS = D / 16;
   __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kts[BUF], vts[BUF];
+  __shared__ __attribute__((aligned(16))) float bias[BUF][TK];
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -45,10 +46,9 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
   int k0 = kb + min(split * per, tiles) * TK;
   const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
 
-  const T* kbase = (const T*)a.k + c * a.k_head;
-  const T* vbase = (const T*)a.v + c * a.v_head;
   Keys<T, D, TK, 64 * RW, VEC> keys;
-  if (k0 < k1) keys.load(p, kbase, vbase, k0, k1);
+  keys.begin(p, c, k0, k1);
+  if (k0 < k1) keys.load(p);
 
   Frag<P> q[KS], go[KS];
   const T* gp = (const T*)p.go + qi * p.go_row + head * p.go_head;
@@ -73,17 +73,14 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
 
   for (int buf = 0; k0 < k1; k0 += TK, buf ^= BUF - 1) {
     Tile<P, TK, D>&kt = kts[buf], &vt = vts[buf];
-    const unsigned long seen = keys.seen(k0, k1);
-    const bool whole = keys.whole(seen);
     if (BUF == 1) __syncthreads();
-    keys.store(p, k0, k1, whole, kt, vt);
+    keys.store(p, k0, kt, vt, bias[buf]);
     __syncthreads();
-    if (k0 + TK < k1) keys.load(p, kbase, vbase, k0 + TK, k1);
-    const unsigned long bits = seen >> (4 * h);
+    if (k0 + TK < k1) keys.load(p);
 
 #pragma unroll
     for (int b = 0; b < TK / 32; ++b) {
-      f32x16 s = f32x16{}, dp = f32x16{};
+      f32x16 s = by_row(&bias[buf][32 * b], lane), dp = f32x16{};
 #pragma unroll
       for (int t = 0; t < KS; ++t) {
         s = mma(kt.rows(32 * b, t, lane), q[t], s);
@@ -91,11 +88,6 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], p.c, -lse));
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!(bits >> (32 * b + 8 * (i / 4) + i % 4) & 1)) s[i] = 0.0f;
-      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float e[8];
@@ -225,16 +217,11 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
         s = mma(qt.rows(32 * b, t, lane), k[t], s);
         dp = mma(gt.rows(32 * b, t, lane), v[t], dp);
       }
+      const f32x16 ls = by_row(lse_s + 32 * b, lane), de = by_row(delta_s + 32 * b, lane);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const f32x4 ls = *reinterpret_cast<const f32x4*>(&lse_s[32 * b + 8 * x + 4 * h]);
-        const f32x4 de = *reinterpret_cast<const f32x4*>(&delta_s[32 * b + 8 * x + 4 * h]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(s[4 * x + i], p.c, -ls[i]));
-          s[4 * x + i] = e;
-          dp[4 * x + i] = e * (dp[4 * x + i] - de[i]);
-        }
+      for (int i = 0; i < 16; ++i) {
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], p.c, -ls[i]));
+        dp[i] = s[i] * (dp[i] - de[i]);
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {

@@ -19,6 +19,7 @@ template <class T, int D, int RW, int TK, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
   constexpr int P = planes<T>(), KS = D / 16;
   __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kts[BUF], vts[BUF];
+  __shared__ __attribute__((aligned(16))) float bias[BUF][TK];
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -43,10 +44,9 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
   int k0 = kb + min(split * per, tiles) * TK;
   const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
 
-  const T* kbase = (const T*)a.k + c * a.k_head;
-  const T* vbase = (const T*)a.v + c * a.v_head;
   Keys<T, D, TK, 64 * RW, VEC> keys;
-  if (k0 < k1) keys.load(p, kbase, vbase, k0, k1);
+  keys.begin(p, c, k0, k1);
+  if (k0 < k1) keys.load(p);
 
   Frag<P> q[KS];
   row_operand<T, D, VEC>((const T*)a.q + qi * a.q_row + head * a.q_head, a.dim_qk, live, q);
@@ -62,26 +62,17 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
   // two buffers: one barrier a tile, the store of a tile behind the products of the one before
   for (int buf = 0; k0 < k1; k0 += TK, buf ^= BUF - 1) {
     Tile<P, TK, D>&kt = kts[buf], &vt = vts[buf];
-    const unsigned long seen = keys.seen(k0, k1);
     if (BUF == 1) __syncthreads();
-    keys.store(p, k0, k1, keys.whole(seen), kt, vt);
+    keys.store(p, k0, kt, vt, bias[buf]);
     __syncthreads();
-    if (k0 + TK < k1) keys.load(p, kbase, vbase, k0 + TK, k1);
+    if (k0 + TK < k1) keys.load(p);
 
     f32x16 s[TK / 32];
 #pragma unroll
     for (int b = 0; b < TK / 32; ++b) {
-      s[b] = f32x16{};
+      s[b] = by_row(&bias[buf][32 * b], lane);
 #pragma unroll
       for (int t = 0; t < KS; ++t) s[b] = mma(kt.rows(32 * b, t, lane), q[t], s[b]);
-    }
-    if (!keys.whole(seen)) {
-      const unsigned long bits = seen >> (4 * h);
-#pragma unroll
-      for (int b = 0; b < TK / 32; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!(bits >> (32 * b + 8 * (i / 4) + i % 4) & 1)) s[b][i] = -INFINITY;
     }
     float top = s[0][0];
 #pragma unroll

@@ -249,40 +249,57 @@ __device__ __forceinline__ int query_of(const Params& p, int r) {
 }
 
 // The tiles of the keys of one kv head, ROWS at a time, from memory through registers to
-// LDS.  load() only issues the loads of the tile from key k0 on (rows beyond the last key
-// read the last one); store() writes them with zeros in place of masked keys, of those
-// beyond the end and of dimensions beyond dim, whatever memory holds there.
+// LDS.  load() only issues the loads of the next tile (rows beyond the last key read
+// the last one); store() writes them with zeros in place of masked keys, of those beyond
+// the end and of dimensions beyond dim, whatever memory holds there, and the
+// starting value of each key's logits: 0, or -infinity for a key that is not seen.
 template <class T, int D, int ROWS, int NT, bool VEC>
 struct Keys {
   static constexpr int P = planes<T>(), U = D / 8, E = ROWS * U / NT, STEP = NT / U;
-  static_assert(ROWS * U % NT == 0, "");
+  static_assert(ROWS * U % NT == 0 && ROWS <= 64, "");
   Raw<T> k[E], v[E];
-  unsigned char m[E], ml;
+  unsigned char m;
+  const T *kp, *vp;      // this thread's first row of the next tile
+  int next, end;         // keys of this work-group not yet loaded
 
-  __device__ __forceinline__ void load(const Params& p, const T* kb, const T* vb, int k0, int k1) {
+  __device__ __forceinline__ void begin(const Params& p, int c, int k0, int k1) {
     const e3conv_attention_args& a = p.a;
-    const int unit = threadIdx.x % U, row = threadIdx.x / U;
+    const long j = k0 + (int)threadIdx.x / U;
+    kp = (const T*)a.k + c * a.k_head + j * a.k_row;
+    vp = (const T*)a.v + c * a.v_head + j * a.v_row;
+    next = k0;
+    end = k1;
+  }
+  __device__ __forceinline__ void load(const Params& p) {
+    const e3conv_attention_args& a = p.a;
+    const int d = threadIdx.x % U * 8;
+    if (next + ROWS <= end) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int j = min(k0 + row + e * STEP, k1 - 1);
-      k[e] = fetch8<VEC>(kb + j * a.k_row, unit * 8, a.dim_qk);
-      v[e] = fetch8<VEC>(vb + j * a.v_row, unit * 8, a.dim_v);
-      m[e] = a.k_mask ? a.k_mask[j] : 1;
+      for (int e = 0; e < E; ++e) {
+        k[e] = fetch8<VEC>(kp + e * STEP * a.k_row, d, a.dim_qk);
+        v[e] = fetch8<VEC>(vp + e * STEP * a.v_row, d, a.dim_v);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int back = min(end - 1 - (next + (int)threadIdx.x / U), e * STEP);
+        k[e] = fetch8<VEC>(kp + back * a.k_row, d, a.dim_qk);
+        v[e] = fetch8<VEC>(vp + back * a.v_row, d, a.dim_v);
+      }
     }
-    ml = a.k_mask ? a.k_mask[min(k0 + (int)(threadIdx.x & 63), k1 - 1)] : 1;
+    if (a.k_mask) m = a.k_mask[min(next + (int)(threadIdx.x & 63), end - 1)];
+    kp += ROWS * a.k_row;
+    vp += ROWS * a.v_row;
+    next += ROWS;
   }
-  // The keys of the tile that are seen, a bit each.
-  __device__ __forceinline__ unsigned long seen(int k0, int k1) const {
-    const int lane = threadIdx.x & 63;
-    return __ballot(lane < ROWS && k0 + lane < k1 && ml);
-  }
-  static __device__ __forceinline__ bool whole(unsigned long seen) {
-    return seen == (ROWS == 64 ? ~0ul : (1ul << (ROWS & 63)) - 1);
-  }
-  __device__ __forceinline__ void store(const Params& p, int k0, int k1, bool whole, Tile<P, ROWS, D>& kt,
-                                        Tile<P, ROWS, D>& vt) const {
-    const int unit = threadIdx.x % U, row = threadIdx.x / U;
-    if (whole && (!VEC || (p.a.dim_qk == D && p.a.dim_v == D))) {
+  // k0: the first key of the loaded tile.
+  __device__ __forceinline__ void store(const Params& p, int k0, Tile<P, ROWS, D>& kt, Tile<P, ROWS, D>& vt,
+                                        float* bias) const {
+    const int unit = threadIdx.x % U, row = threadIdx.x / U, lane = threadIdx.x & 63;
+    const bool sees = lane < ROWS && k0 + lane < end && (!p.a.k_mask || m);
+    const unsigned long seen = __ballot(sees);
+    if (threadIdx.x < ROWS) bias[lane] = sees ? 0.0f : -INFINITY;
+    if (seen == (ROWS == 64 ? ~0ul : (1ul << (ROWS & 63)) - 1) && (!VEC || (p.a.dim_qk == D && p.a.dim_v == D))) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         kt.store(row + e * STEP, unit, frag_of(k[e], true));
@@ -291,13 +308,26 @@ struct Keys {
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const bool keep = k0 + row + e * STEP < k1 && m[e];
+        const bool keep = seen >> (row + e * STEP) & 1;
         kt.store(row + e * STEP, unit, frag_of(k[e], keep && unit * 8 < p.a.dim_qk));
         vt.store(row + e * STEP, unit, frag_of(v[e], keep && unit * 8 < p.a.dim_v));
       }
     }
   }
 };
+
+// Values of 32 rows from LDS where an accumulator has them: register i is row 8 (i / 4) +
+// 4 h + i % 4.
+__device__ __forceinline__ f32x16 by_row(const float* rows, int lane) {
+  f32x16 r;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(rows + 8 * x + 4 * (lane >> 5));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[4 * x + i] = v[i];
+  }
+  return r;
+}
 
 // The B operands of one row (lane n's, k = 16 t + 8 h + j) from memory; zeros unless live.
 template <class T, int D, bool VEC>
