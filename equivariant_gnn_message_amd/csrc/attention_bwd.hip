@@ -278,23 +278,41 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
     }
 }
 
-// Sums the splits: element d < dim of row (i, head) of `width` floats, times factor.
+// Sums the splits: element d < dim of row (i, head) of `width` floats, times factor.  Four
+// waves of a work-group take 64 elements, each a quarter of the splits, eight at a time.
 template <class T>
 __global__ void __launch_bounds__(256) attn_sum(const float* part, long rows, int width, int from, int dim, int heads,
                                                 int splits, float factor, T* out, long out_row, long out_head) {
-  const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * dim) return;
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const long i = (long)blockIdx.x * 64 + lane;
   const long at = i / dim;
-  const int d = (int)(i % dim);
+  const int d = (int)(i - at * dim);
+  const float* q = part + at * width + from + d;
   float v = 0.0f;
-  for (int s = 0; s < splits; ++s) v += part[(s * rows + at) * width + from + d];
-  out[at / heads * out_row + at % heads * out_head + d] = (T)(v * factor);
+  if (at < rows) {
+    int s = w;
+    for (; s + 28 < splits; s += 32) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = q[(s + 4 * k) * rows * width];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += x[k];
+    }
+    for (; s < splits; s += 4) v += q[s * rows * width];
+  }
+  red[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && at < rows) {
+    v = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    out[at / heads * out_row + at % heads * out_head + d] = (T)(v * factor);
+  }
 }
 
 template <class T>
 hipError_t sum(const Params& p, long rows, int width, int from, int dim, int heads, float factor, void* out, long row,
                long head, hipStream_t s) {
-  const long blocks = (rows * dim + 255) / 256;
+  const long blocks = (rows * dim + 63) / 64;
   if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
   if (blocks > 0)
     hipLaunchKernelGGL(attn_sum<T>, dim3((unsigned)blocks), dim3(256), 0, s, p.part, rows, width, from, dim, heads,

@@ -126,10 +126,7 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
         const float v[4] = {o[dt][4 * b], o[dt][4 * b + 1], o[dt][4 * b + 2], o[dt][4 * b + 3]};
         store4(to, 32 * dt + 8 * b + 4 * h, a.dim_v, v, a.dim_v % 4 == 0);
       }
-    if (h == 0) {
-      p.part_ml[2 * i] = m;
-      p.part_ml[2 * i + 1] = l;
-    }
+    if (h == 0) reinterpret_cast<float2*>(p.part_ml)[i] = make_float2(m, l);
     return;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -146,47 +143,65 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
   if (h == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// Joins the splits of one row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
-constexpr int kMaxSplits = 256;
+// Joins the splits of one row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  Sixteen
+// waves take the splits in turn, so that their rows are all in flight at once: the time is
+// that of a few dependent reads (the loop of one wave over 64 splits took 20 us).
+constexpr int kMaxSplits = 512, kJoinWaves = 16;
 template <class T>
-__global__ void __launch_bounds__(256) attn_join(Params p) {
+__global__ void __launch_bounds__(64 * kJoinWaves) attn_join(Params p) {
   const e3conv_attention_args& a = p.a;
-  __shared__ float weight[kMaxSplits], sum[4][kMaxDim], red[8];
+  __shared__ float weight[kMaxSplits], sum[kJoinWaves][kMaxDim], red[2][kJoinWaves];
   const long rows = a.num_q * a.heads_q, at = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   float m = -INFINITY, l = 0.0f;
   if (tid < p.splits) {
-    m = p.part_ml[2 * (tid * rows + at)];
-    l = p.part_ml[2 * (tid * rows + at) + 1];
+    const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[tid * rows + at];
+    m = ml.x;
+    l = ml.y;
+  }
+  const float* part = p.part + at * a.dim_v;
+  constexpr int N = kMaxSplits / kJoinWaves;
+  float v0[N], v1[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int s = w + i * kJoinWaves;
+    const float* o = part + s * rows * a.dim_v;
+    v0[i] = s < p.splits && lane < a.dim_v ? o[lane] : 0.0f;
+    v1[i] = s < p.splits && lane + 64 < a.dim_v ? o[lane + 64] : 0.0f;
   }
   float top = m;
   for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  if (lane == 0) red[w] = top;
+  if (lane == 0) red[0][w] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  top = red[0][0];
+#pragma unroll
+  for (int i = 1; i < kJoinWaves; ++i) top = fmaxf(top, red[0][i]);
   const float base = top == -INFINITY ? 0.0f : top, f = __builtin_amdgcn_exp2f(m - base);
-  weight[tid] = f;
+  if (tid < kMaxSplits) weight[tid] = f;
   l *= f;
   for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
-  if (lane == 0) red[4 + w] = l;
+  if (lane == 0) red[1][w] = l;
   __syncthreads();
-  l = (red[4] + red[5]) + (red[6] + red[7]);
-  const float* part = p.part + at * a.dim_v;
-  float v0 = 0.0f, v1 = 0.0f;
-  for (int s = w; s < p.splits; s += 4) {
-    const float* o = part + s * rows * a.dim_v;
-    if (lane < a.dim_v) v0 = fmaf(weight[s], o[lane], v0);
-    if (lane + 64 < a.dim_v) v1 = fmaf(weight[s], o[lane + 64], v1);
+  l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kJoinWaves; ++i) l += red[1][i];
+  float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float f = weight[w + i * kJoinWaves];
+    a0 = fmaf(f, v0[i], a0);
+    a1 = fmaf(f, v1[i], a1);
   }
-  sum[w][lane] = v0;
-  sum[w][lane + 64] = v1;
+  sum[w][lane] = a0;
+  sum[w][lane + 64] = a1;
   __syncthreads();
   const int head = (int)(at % a.heads_q);
   const long qi = at / a.heads_q;
   if (tid < a.dim_v) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const float v = (sum[0][tid] + sum[1][tid]) + (sum[2][tid] + sum[3][tid]);
-    ((T*)p.out)[qi * p.out_row + head * p.out_head + tid] = (T)(l == 0.0f ? 0.0f : v * inv);
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kJoinWaves; ++i) v += sum[i][tid];
+    ((T*)p.out)[qi * p.out_row + head * p.out_head + tid] = (T)(l == 0.0f ? 0.0f : v / l);
   }
   if (tid == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
 }
@@ -235,15 +250,19 @@ hipError_t forward(const Params& p, int rw, unsigned grid, hipStream_t s) {
   else launch<T, 128>(p, rw, grid, s);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.splits == 1) return err;
-  hipLaunchKernelGGL(attn_join<T>, dim3((unsigned)(p.a.num_q * p.a.heads_q)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(attn_join<T>, dim3((unsigned)(p.a.num_q * p.a.heads_q)), dim3(64 * kJoinWaves), 0, s, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Maximum and sum of n partial rows, then (16-byte aligned) the rows.
+static size_t ml_floats(size_t n) { return (2 * n + 3) / 4 * 4; }
+
 size_t forward_workspace(const e3conv_attention_args& a) {
   const Shape sh = shape_of(a);
-  return sh.splits > 1 ? (size_t)sh.splits * a.num_q * a.heads_q * (a.dim_v + 2) * sizeof(float) : 0;
+  const size_t n = (size_t)sh.splits * a.num_q * a.heads_q;
+  return sh.splits > 1 ? (ml_floats(n) + n * a.dim_v) * sizeof(float) : 0;
 }
 
 hipError_t launch_forward(const Params& given, hipStream_t s) {
@@ -251,7 +270,8 @@ hipError_t launch_forward(const Params& given, hipStream_t s) {
   const Shape sh = shape_of(p.a);
   p.slots = sh.slots;
   p.splits = sh.splits;
-  p.part_ml = p.part + (size_t)sh.splits * p.a.num_q * p.a.heads_q * p.a.dim_v;
+  p.part_ml = p.part;
+  p.part += ml_floats((size_t)sh.splits * p.a.num_q * p.a.heads_q);
   const long grid = (long)sh.slots * sh.splits * p.a.heads_kv;
   if (grid > 0x7fffffffL) return hipErrorInvalidValue;
   return p.a.dtype == E3CONV_F32 ? forward<float>(p, sh.rw, (unsigned)grid, s)

@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(NT) norm_finish(NormParams p) {
   const float2* sums = p.sums + (long)s0 * p.a.channels + grp * p.gc;
   const float base = sums[0].x;
   float n = 0.0f, m = 0.0f, v = 0.0f;
+#pragma unroll 4
   for (int t = threadIdx.x; t < total; t += NT) {
     const float k = p.counts[s0 + t / p.gc];
     n += k;
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(NT) norm_finish(NormParams p) {
   n = block_sum(n);
   m = block_sum(m);
   m = n > 0.0f ? base + m / n : 0.0f;
+#pragma unroll 4
   for (int t = threadIdx.x; t < total; t += NT) {
     const float2 s = sums[(long)(t / p.gc) * p.a.channels + t % p.gc];
     const float d = s.x - m;
@@ -519,6 +521,7 @@ __global__ void __launch_bounds__(NT) norm_grad_finish(NormParams p) {
   if (rows <= p.chunk && p.units <= NT) return;
   const int chunks = max((rows + p.chunk - 1) / p.chunk, 1), total = chunks * p.gc;
   float n = 0.0f, m1 = 0.0f, m2 = 0.0f;
+#pragma unroll 4
   for (int t = threadIdx.x; t < total; t += NT) {
     const int ch = grp * p.gc + t % p.gc;
     const float2 s = p.sums[(long)(s0 + t / p.gc) * p.a.channels + ch];
@@ -539,6 +542,7 @@ __global__ void __launch_bounds__(NT) norm_grad_affine(NormParams p) {
   const int c = blockIdx.x * 4 + (threadIdx.x & 3);
   float w = 0.0f, b = 0.0f;
   if (c < p.a.channels)
+#pragma unroll 8
     for (int s = threadIdx.x >> 2; s < p.slots; s += NT / 4) {
       const float2 v = p.sums[(long)s * p.a.channels + c];
       b += v.x;

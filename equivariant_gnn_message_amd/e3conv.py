@@ -579,34 +579,40 @@ def e3conv_last_error_detail():
 
 # --------------------------------------- graph attention, group norm ---
 
-def _rows_of(t, name, dtype, device, shape):
-    """A device operand whose last axis has unit stride; other strides are free."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype:
+# These calls are short on the GPU, so the checks on the way are kept cheap: each property of a
+# tensor is asked once, and devices are compared as indices (-1 on the host).
+
+def _rows_of(t, name, dtype, index, shape):
+    """Strides of a device operand whose last axis has unit stride; the others are free."""
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a tensor on cuda:{max(index, 0)}, got {t.device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride along its last axis")
+    return strides
 
 
-def _dense(t, name, dtype, device, n):
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype:
+def _dense(t, name, dtype, index, n):
+    """Address of a contiguous device tensor of n elements."""
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a tensor on cuda:{max(index, 0)}, got {t.device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _node_mask(t, name, device, n):
+def _node_mask(t, name, index, n):
     """Address of a node mask (bool or uint8, one byte per node), or None."""
     if t is None:
         return None
     import torch
-    _dense(t, name, torch.bool if t.dtype == torch.bool else torch.uint8, device, n)
-    return t.data_ptr()
+    return _dense(t, name, torch.bool if t.dtype is torch.bool else torch.uint8, index, n)
 
 
 def _written(t, name):
@@ -615,38 +621,38 @@ def _written(t, name):
         raise ValueError(f"{name} is written and must not repeat elements (zero stride)")
 
 
-def _enter(device, stream):
-    """(stream handle, stream object to record allocations on or None) of a call on `device`."""
+def _enter(index, stream):
+    """(stream handle, stream object to record allocations on or None) of a call on a device."""
     import torch
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"operands are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    current = torch.cuda.current_stream(device)
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"operands are on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+    current = torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
-        return current.cuda_stream, None
+        return current, None
     handle = int(getattr(stream, "cuda_stream", stream))
-    if handle == current.cuda_stream:
+    if handle == current:
         return handle, None
-    return handle, stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=device)
+    return handle, stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=index)
 
 
-def _workspace(given, need, device, other):
+def _workspace(given, size_of, args, like, other, backward=0):
     """(address, bytes, tensor) of the caller's workspace, or of one allocated for the call."""
     import torch
     if given is not None:
-        if not given.is_cuda or given.device != device or not given.is_contiguous() or given.data_ptr() % 16:
-            raise ValueError(f"workspace must be a contiguous, 16-byte aligned tensor on {device}")
+        if given.get_device() != like.get_device() or not given.is_contiguous() or given.data_ptr() % 16:
+            raise ValueError(f"workspace must be a contiguous, 16-byte aligned tensor on {like.device}")
         return given.data_ptr(), given.numel() * given.element_size(), given
-    if need == 0:
+    n = ctypes.c_size_t()
+    _check(size_of(args, backward, ctypes.byref(n)))
+    if n.value == 0:
         return None, 0, None
-    t = torch.empty(need, dtype=torch.uint8, device=device)
-    if other is not None:
-        t.record_stream(other)
-    return t.data_ptr(), need, t
+    t = _allocate((n.value,), torch.uint8, like, other)
+    return t.data_ptr(), n.value, t
 
 
-def _allocate(shape, dtype, device, other):
+def _allocate(shape, dtype, like, other):
     import torch
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=like.device)
     if other is not None:
         t.record_stream(other)   # freed memory is not reused before that stream is done with it
     return t
@@ -656,23 +662,21 @@ def _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask):
     import torch
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q (num_q, heads_q, dim_qk), k (num_k, heads_kv, dim_qk), v (num_k, heads_kv, dim_v)")
-    code, dev = _dtype_code(q), q.device
-    nq, hq, d = q.shape
-    nk, hk, _ = k.shape
-    dv = v.shape[2]
-    _rows_of(q, "q", q.dtype, dev, q.shape)
-    _rows_of(k, "k", q.dtype, dev, (nk, hk, d))
-    _rows_of(v, "v", q.dtype, dev, (nk, hk, dv))
+    code, dt, index = _dtype_code(q), q.dtype, q.get_device()
+    qs = q.shape
+    nq, hq, d = qs
+    nk, hk, dv = v.shape
+    q_row, q_head, _ = _rows_of(q, "q", dt, index, qs)
+    k_row, k_head, _ = _rows_of(k, "k", dt, index, (nk, hk, d))
+    v_row, v_head, _ = _rows_of(v, "v", dt, index, (nk, hk, dv))
     graphs = q_ptr.numel() - 1
     if graphs < 0:
         raise ValueError("q_ptr must hold num_graphs + 1 offsets")
-    _dense(q_ptr, "q_ptr", torch.int32, dev, graphs + 1)
-    _dense(k_ptr, "k_ptr", torch.int32, dev, graphs + 1)
-    scale = d ** -0.5 if scale is None else float(scale)
-    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, scale, q_ptr.data_ptr(), k_ptr.data_ptr(),
-                         _node_mask(q_mask, "q_mask", dev, nq), _node_mask(k_mask, "k_mask", dev, nk),
-                         q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), q.stride(1), k.stride(0),
-                         k.stride(1), v.stride(0), v.stride(1))
+    qp = _dense(q_ptr, "q_ptr", torch.int32, index, graphs + 1)
+    kp = qp if k_ptr is q_ptr else _dense(k_ptr, "k_ptr", torch.int32, index, graphs + 1)
+    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, d ** -0.5 if scale is None else scale, qp, kp,
+                         _node_mask(q_mask, "q_mask", index, nq), _node_mask(k_mask, "k_mask", index, nk),
+                         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, q_head, k_row, k_head, v_row, v_head)
 
 
 def e3conv_attention_workspace_size(args, backward=False):
@@ -693,21 +697,21 @@ def e3conv_attention(q, k, v, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None
     """
     import torch
     args = _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask)
-    dev, shape = q.device, (args.num_q, args.heads_q, args.dim_v)
-    handle, other = _enter(dev, stream)
+    index, shape = q.get_device(), (args.num_q, args.heads_q, args.dim_v)
+    handle, other = _enter(index, stream)
     if out is None:
-        out = _allocate(shape, q.dtype, dev, other)
+        out = _allocate(shape, q.dtype, q, other)
+        row, head = shape[1] * shape[2], shape[2]
     else:
-        _rows_of(out, "out", q.dtype, dev, shape)
+        row, head, _ = _rows_of(out, "out", q.dtype, index, shape)
         _written(out, "out")
     if lse is None:
-        lse = _allocate(shape[:2], torch.float32, dev, other)
+        lse = _allocate(shape[:2], torch.float32, q, other)
     else:
-        _dense(lse, "lse", torch.float32, dev, args.num_q * args.heads_q)
-    ws, nbytes, _keep = _workspace(workspace, 0 if workspace is not None else e3conv_attention_workspace_size(args),
-                                   dev, other)
-    _check(load_library().e3conv_attention(ctypes.byref(args), out.data_ptr(), out.stride(0), out.stride(1),
-                                           lse.data_ptr(), ws, nbytes, handle))
+        _dense(lse, "lse", torch.float32, index, shape[0] * shape[1])
+    lib, ref = load_library(), ctypes.byref(args)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q, other)
+    _check(lib.e3conv_attention(ref, out.data_ptr(), row, head, lse.data_ptr(), ws, nbytes, handle))
     return out, lse
 
 
@@ -719,24 +723,24 @@ def e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale=N
     """
     import torch
     args = _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask)
-    dev, shape = q.device, (args.num_q, args.heads_q, args.dim_v)
-    _rows_of(out, "out", q.dtype, dev, shape)
-    _rows_of(grad_out, "grad_out", q.dtype, dev, shape)
-    _dense(lse, "lse", torch.float32, dev, args.num_q * args.heads_q)
-    handle, other = _enter(dev, stream)
+    index, dt, shape = q.get_device(), q.dtype, (args.num_q, args.heads_q, args.dim_v)
+    strides = _rows_of(out, "out", dt, index, shape)[:2] + _rows_of(grad_out, "grad_out", dt, index, shape)[:2]
+    lse_at = _dense(lse, "lse", torch.float32, index, shape[0] * shape[1])
+    handle, other = _enter(index, stream)
     if grads is None:
-        grads = tuple(_allocate(t.shape, t.dtype, dev, other) for t in (q, k, v))
+        grads = [_allocate(t.shape, dt, q, other) for t in (q, k, v)]
+        for t in grads:
+            strides += t.stride()[:2]
     else:
         for t, ref, name in zip(grads, (q, k, v), ("grad_q", "grad_k", "grad_v")):
-            _rows_of(t, name, q.dtype, dev, ref.shape)
+            strides += _rows_of(t, name, dt, index, ref.shape)[:2]
             _written(t, name)
     gq, gk, gv = grads
-    ws, nbytes, _keep = _workspace(workspace, 0 if workspace is not None
-                                   else e3conv_attention_workspace_size(args, True), dev, other)
-    strides = (I64 * 10)(*(s for t in (out, grad_out, gq, gk, gv) for s in t.stride()[:2]))
-    _check(load_library().e3conv_attention_backward(
-        ctypes.byref(args), out.data_ptr(), lse.data_ptr(), grad_out.data_ptr(), gq.data_ptr(), gk.data_ptr(),
-        gv.data_ptr(), strides, ws, nbytes, handle))
+    lib, ref = load_library(), ctypes.byref(args)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q, other, 1)
+    _check(lib.e3conv_attention_backward(
+        ref, out.data_ptr(), lse_at, grad_out.data_ptr(), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
+        (I64 * 10)(*strides), ws, nbytes, handle))
     return gq, gk, gv
 
 
@@ -744,22 +748,19 @@ def _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask
     import torch
     if x.dim() != 2:
         raise ValueError("x must be (num_rows, channels)")
-    code, dev = _dtype_code(x), x.device
+    code, index = _dtype_code(x), x.get_device()
     n, c = x.shape
-    _rows_of(x, "x", x.dtype, dev, x.shape)
+    row, _ = _rows_of(x, "x", x.dtype, index, x.shape)
     graphs = row_ptr.numel() - 1
     if graphs < 0:
         raise ValueError("row_ptr must hold num_graphs + 1 offsets")
-    _dense(row_ptr, "row_ptr", torch.int32, dev, graphs + 1)
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _dense(t, name, torch.float32, dev, c)
     act = ACTIVATIONS.get(activation, activation)
     if not isinstance(act, int):
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    return GroupNormArgs(code, graphs, c, int(groups), act, float(eps), n, row_ptr.data_ptr(),
-                         _node_mask(row_mask, "row_mask", dev, n), x.data_ptr(), x.stride(0),
-                         None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr())
+    return GroupNormArgs(code, graphs, c, groups, act, eps, n, _dense(row_ptr, "row_ptr", torch.int32, index, graphs + 1),
+                         _node_mask(row_mask, "row_mask", index, n), x.data_ptr(), row,
+                         None if weight is None else _dense(weight, "weight", torch.float32, index, c),
+                         None if bias is None else _dense(bias, "bias", torch.float32, index, c))
 
 
 def e3conv_group_norm_workspace_size(args, backward=False):
@@ -780,19 +781,17 @@ def e3conv_group_norm(x, row_ptr, groups, weight=None, bias=None, eps=1e-5, acti
     """
     import torch
     args = _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask)
-    dev = x.device
-    handle, other = _enter(dev, stream)
+    index, shape = x.get_device(), (args.num_graphs, args.groups)
+    handle, other = _enter(index, stream)
     if out is None:
-        out = _allocate(x.shape, x.dtype, dev, other)
+        out, row = _allocate(x.shape, x.dtype, x, other), args.channels
     else:
-        _rows_of(out, "out", x.dtype, dev, x.shape)
+        row, _ = _rows_of(out, "out", x.dtype, index, x.shape)
         _written(out, "out")
-    mean = _allocate((args.num_graphs, args.groups), torch.float32, dev, other)
-    rstd = _allocate((args.num_graphs, args.groups), torch.float32, dev, other)
-    ws, nbytes, _keep = _workspace(workspace, 0 if workspace is not None else e3conv_group_norm_workspace_size(args),
-                                   dev, other)
-    _check(load_library().e3conv_group_norm(ctypes.byref(args), out.data_ptr(), out.stride(0), mean.data_ptr(),
-                                            rstd.data_ptr(), ws, nbytes, handle))
+    mean, rstd = _allocate(shape, torch.float32, x, other), _allocate(shape, torch.float32, x, other)
+    lib, ref = load_library(), ctypes.byref(args)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x, other)
+    _check(lib.e3conv_group_norm(ref, out.data_ptr(), row, mean.data_ptr(), rstd.data_ptr(), ws, nbytes, handle))
     return out, mean, rstd
 
 
@@ -802,23 +801,22 @@ def e3conv_group_norm_backward(x, row_ptr, groups, weight, bias, activation, mea
     import torch
     # eps is already in rstd
     args = _group_norm_args(x, row_ptr, groups, weight, bias, 1.0, activation, row_mask)
-    dev = x.device
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _dense(t, name, torch.float32, dev, args.num_graphs * args.groups)
-    _rows_of(grad_y, "grad_y", x.dtype, dev, x.shape)
-    handle, other = _enter(dev, stream)
+    index, size = x.get_device(), args.num_graphs * args.groups
+    mean_at = _dense(mean, "mean", torch.float32, index, size)
+    rstd_at = _dense(rstd, "rstd", torch.float32, index, size)
+    gy_row, _ = _rows_of(grad_y, "grad_y", x.dtype, index, x.shape)
+    handle, other = _enter(index, stream)
     if grad_x is None:
-        grad_x = _allocate(x.shape, x.dtype, dev, other)
+        grad_x, row = _allocate(x.shape, x.dtype, x, other), args.channels
     else:
-        _rows_of(grad_x, "grad_x", x.dtype, dev, x.shape)
+        row, _ = _rows_of(grad_x, "grad_x", x.dtype, index, x.shape)
         _written(grad_x, "grad_x")
-    gw, gb = (None if t is None else _allocate(t.shape, torch.float32, dev, other) for t in (weight, bias))
-    ws, nbytes, _keep = _workspace(workspace, 0 if workspace is not None
-                                   else e3conv_group_norm_workspace_size(args, True), dev, other)
-    _check(load_library().e3conv_group_norm_backward(
-        ctypes.byref(args), mean.data_ptr(), rstd.data_ptr(), grad_y.data_ptr(), grad_y.stride(0),
-        grad_x.data_ptr(), grad_x.stride(0), None if gw is None else gw.data_ptr(),
-        None if gb is None else gb.data_ptr(), ws, nbytes, handle))
+    gw, gb = (None if t is None else _allocate(t.shape, torch.float32, x, other) for t in (weight, bias))
+    lib, ref = load_library(), ctypes.byref(args)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x, other, 1)
+    _check(lib.e3conv_group_norm_backward(
+        ref, mean_at, rstd_at, grad_y.data_ptr(), gy_row, grad_x.data_ptr(), row,
+        None if gw is None else gw.data_ptr(), None if gb is None else gb.data_ptr(), ws, nbytes, handle))
     return grad_x, gw, gb
 
 
