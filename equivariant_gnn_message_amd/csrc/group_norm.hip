@@ -4,13 +4,14 @@
 // The rows of a graph are cut into chunks of p.chunk rows, one work-group each; a thread
 // keeps one run of V channels (16 bytes) and strides over the rows, so loads are whole
 // lines and per-channel values stay in registers.  A graph of one chunk is finished by the
-// work-group that read it, its rows still in cache; graphs of more chunks take three
+// work-group that read it, its rows still in cache; graphs of more chunks take further
 // launches:
 //   sums    per chunk and channel: mean and squared deviations (forward), or
 //           sum dz and sum dz xhat (reverse), to the workspace;
 //   finish  per graph and group: mean and rstd, or the two means of the reverse pass,
-//           from its chunks in chunk order; and the weight and bias gradients;
-//   apply   per chunk: the rows.
+//           from its chunks in chunk order (where graphs have few chunks, every
+//           work-group of the next launch does this for its graph instead);
+//   apply   per chunk: the rows; and in the reverse pass the weight and bias gradients.
 // Sums are taken about the channel's first counted value of the chunk, and chunks are
 // joined about the common mean, so a mean far from zero costs no digits of the variance.
 // Memory bound: the rows are read twice and written once where a graph has more than one
@@ -35,6 +36,7 @@ struct NormParams {
   int units;                       // runs of V channels in a row
   int chunk;                       // rows of a work-group
   int slots;                       // chunk slots: rows / chunk + graphs
+  int inline_finish;               // 1: finish within apply
   void* y;
   long y_row;
   float *mean, *rstd;
@@ -172,8 +174,7 @@ __device__ __forceinline__ Place place(const NormParams& p) {
 
 // Adds s1 and s2 over the threads of one unit; the result is in those of row 0.
 template <int V>
-__device__ void add_rows(const Place& q, float (&s1)[V], float (&s2)[V]) {
-  __shared__ float2 red[NT * V];
+__device__ void add_rows(const Place& q, float2* red, float (&s1)[V], float (&s2)[V]) {
   int rows = q.step, row = q.row;
   bool on = q.on;
   if (64 % q.width == 0) {     // within a wave first
@@ -231,16 +232,31 @@ __device__ int count_rows(const NormParams& p, const Chunk& c, int* first) {
   return part[0] + part[1] + part[2] + part[3];
 }
 
-// Calls use(row) for this thread's counted rows of the chunk.
-template <class F>
+// Calls use(row, whether it counts) for this thread's rows of the chunk, N rows' loads at a time.
+template <int N, class F>
 __device__ __forceinline__ void each_row(const NormParams& p, const Chunk& c, const Place& q, F use) {
   if (!q.on) return;
   if (p.a.row_mask) {
-#pragma unroll 4
+#pragma unroll N
     for (int r = c.begin + q.row; r < c.end; r += q.step) use((long)r, p.a.row_mask[r] != 0);
   } else {
-#pragma unroll 4
+#pragma unroll N
     for (int r = c.begin + q.row; r < c.end; r += q.step) use((long)r, true);
+  }
+}
+
+// Calls use(i, group) for the V channels from c0 on.
+template <int V, class F>
+__device__ __forceinline__ void each_group(int c0, int gc, F use) {
+  int g = c0 / gc, left = (g + 1) * gc - c0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (left == 0) {
+      ++g;
+      left = gc;
+    }
+    --left;
+    use(i, g);
   }
 }
 
@@ -255,15 +271,32 @@ struct Channels {
       b[i] = p.a.bias ? p.a.bias[c0 + i] : 0.0f;
     }
   }
-  __device__ __forceinline__ void moments(const NormParams& p, int g, int c0, const float* mean_of,
-                                          const float* rstd_of) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      mean[i] = mean_of[g * p.a.groups + (c0 + i) / p.gc];
-      rstd[i] = rstd_of[g * p.a.groups + (c0 + i) / p.gc];
-    }
+  __device__ __forceinline__ void moments(const NormParams& p, int g, int c0) {
+    each_group<V>(c0, p.gc, [&](int i, int grp) {
+      mean[i] = p.mean[g * p.a.groups + grp];
+      rstd[i] = p.rstd[g * p.a.groups + grp];
+    });
   }
 };
+
+// Sum over the threads of a work-group, in every thread.
+__device__ float block_sum(float v) {
+  __shared__ float part[NT / 64];
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// The slots of a graph's chunks.
+struct Slots {
+  int first, count;
+};
+__device__ __forceinline__ Slots slots_of(const NormParams& p, int g) {
+  const int rows = offset(p.a.row_ptr, g + 1, p.a.num_rows) - offset(p.a.row_ptr, g, p.a.num_rows);
+  return {first_slot(p, g), max((int)(((long)rows + p.chunk - 1) / p.chunk), 1)};
+}
 
 // ---------------------------------------------------------------- forward ---
 
@@ -272,7 +305,7 @@ __device__ __forceinline__ void write_rows(const NormParams& p, const Chunk& c, 
                                            const Channels<V>& k) {
   const T* x = (const T*)p.a.x + q.unit * V;
   T* y = (T*)p.y + q.unit * V;
-  each_row(p, c, q, [&](long r, bool counts) {
+  each_row<4>(p, c, q, [&](long r, bool counts) {
     float v[V];
     load<T, V>(x + r * p.a.x_row, v);
 #pragma unroll
@@ -294,7 +327,7 @@ __global__ void __launch_bounds__(NT) norm_sums(NormParams p) {
 #pragma unroll
   for (int i = 0; i < V; ++i) at[i] = s1[i] = s2[i] = 0.0f;
   if (q.on && n > 0) load<T, V>(x + first * p.a.x_row, at);
-  each_row(p, c, q, [&](long r, bool counts) {
+  each_row<4>(p, c, q, [&](long r, bool counts) {
     float v[V];
     load<T, V>(x + r * p.a.x_row, v);
 #pragma unroll
@@ -304,7 +337,8 @@ __global__ void __launch_bounds__(NT) norm_sums(NormParams p) {
       s2[i] = fmaf(d, d, s2[i]);
     }
   });
-  add_rows<V>(q, s1, s2);
+  __shared__ float2 red[NT * V];
+  add_rows<V>(q, red, s1, s2);
   // of the chunk, per channel: mean, and squared deviations from it
   const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
 #pragma unroll
@@ -321,69 +355,52 @@ __global__ void __launch_bounds__(NT) norm_sums(NormParams p) {
     if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = (float)n;
     return;
   }
-  // the graph's only chunk: its groups here
-  __shared__ float mean[NT * V], dev[NT * V];
+  // the graph's only chunk: its groups here, each by every thread that has one of its channels,
+  // in channel order
   if (threadIdx.x < q.width)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      mean[c0 + i] = s1[i];
-      dev[c0 + i] = s2[i];
-    }
+    for (int i = 0; i < V; ++i) red[c0 + i] = make_float2(s1[i], s2[i]);
   __syncthreads();
   Channels<V> k;
   k.affine(p, c0);
-  // a group's mean and variance by each thread that has one of its channels, in channel order
   int have = -1;
   float m = 0.0f, rs = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int g = (c0 + i) / p.gc;
+  each_group<V>(c0, p.gc, [&](int i, int g) {
     if (g != have) {
       have = g;
+      const float2* of = red + g * p.gc;
       m = 0.0f;
-      for (int j = g * p.gc; j < (g + 1) * p.gc; ++j) m += mean[j] - mean[g * p.gc];
-      m = mean[g * p.gc] + m / (float)p.gc;
+      for (int j = 0; j < p.gc; ++j) m += of[j].x - of[0].x;
+      m = n > 0 ? of[0].x + m / (float)p.gc : 0.0f;
       float v = 0.0f;
-      for (int j = g * p.gc; j < (g + 1) * p.gc; ++j) {
-        const float d = mean[j] - m;
-        v += fmaf((float)n * d, d, dev[j]);
+      for (int j = 0; j < p.gc; ++j) {
+        const float d = of[j].x - m;
+        v += fmaf((float)n * d, d, of[j].y);
       }
       rs = 1.0f / sqrtf(v * (inv / (float)p.gc) + p.a.eps);
-      if (n == 0) m = 0.0f;
     }
     k.mean[i] = m;
     k.rstd[i] = rs;
-    if (threadIdx.x < q.width && (c0 + i) % p.gc == 0) {
+    if (threadIdx.x < q.width && (c0 + i) == g * p.gc) {
       if (p.mean) p.mean[c.g * p.a.groups + g] = m;
       if (p.rstd) p.rstd[c.g * p.a.groups + g] = rs;
     }
-  }
+  });
   write_rows<T, V, ACT>(p, c, q, k);
-}
-
-// Sum over the threads of a work-group, in every thread.
-__device__ float block_sum(float v) {
-  __shared__ float part[NT / 64];
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
 // One work-group per (graph, group): joins the chunks about the common mean.
 __global__ void __launch_bounds__(NT) norm_finish(NormParams p) {
   const int g = blockIdx.x / p.a.groups, grp = blockIdx.x % p.a.groups;
-  const int s0 = first_slot(p, g);
-  const int rows = offset(p.a.row_ptr, g + 1, p.a.num_rows) - offset(p.a.row_ptr, g, p.a.num_rows);
-  if (rows <= p.chunk && p.units <= NT) return;
-  const int chunks = max((rows + p.chunk - 1) / p.chunk, 1), total = chunks * p.gc;
-  const float2* sums = p.sums + (long)s0 * p.a.channels + grp * p.gc;
+  const Slots s = slots_of(p, g);
+  if (s.count == 1 && p.units <= NT) return;
+  const int total = s.count * p.gc;
+  const float2* sums = p.sums + (long)s.first * p.a.channels + grp * p.gc;
   const float base = sums[0].x;
   float n = 0.0f, m = 0.0f, v = 0.0f;
 #pragma unroll 4
   for (int t = threadIdx.x; t < total; t += NT) {
-    const float k = p.counts[s0 + t / p.gc];
+    const float k = p.counts[s.first + t / p.gc];
     n += k;
     m = fmaf(k, sums[(long)(t / p.gc) * p.a.channels + t % p.gc].x - base, m);
   }
@@ -392,9 +409,9 @@ __global__ void __launch_bounds__(NT) norm_finish(NormParams p) {
   m = n > 0.0f ? base + m / n : 0.0f;
 #pragma unroll 4
   for (int t = threadIdx.x; t < total; t += NT) {
-    const float2 s = sums[(long)(t / p.gc) * p.a.channels + t % p.gc];
-    const float d = s.x - m;
-    v += fmaf(p.counts[s0 + t / p.gc] * d, d, s.y);
+    const float2 x = sums[(long)(t / p.gc) * p.a.channels + t % p.gc];
+    const float d = x.x - m;
+    v += fmaf(p.counts[s.first + t / p.gc] * d, d, x.y);
   }
   v = block_sum(v);
   const float rs = 1.0f / sqrtf((n > 0.0f ? v / n : 0.0f) + p.a.eps);
@@ -405,7 +422,71 @@ __global__ void __launch_bounds__(NT) norm_finish(NormParams p) {
   }
 }
 
-template <class T, int V, int ACT>
+// The same for all groups of a graph by one work-group (units <= NT): each thread joins its
+// channels over its share of the chunks, then the shares and the channels of a group are
+// joined.  In chunk order, so every work-group of the graph gets the same bits.
+template <int V>
+__device__ void finish_here(const NormParams& p, const Chunk& c, const Place& q, float2* red, Channels<V>& k) {
+  const Slots s = slots_of(p, c.g);
+  const int c0 = q.unit * V;
+  const float2* sums = p.sums + (long)s.first * p.a.channels + c0;
+  int some = 0;      // the first chunk with a counted row gives the value to sum about
+  while (some + 1 < s.count && p.counts[s.first + some] == 0.0f) ++some;
+  float n = 0.0f, base[V], s1[V], s2[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    base[i] = sums[(long)some * p.a.channels + i].x;
+    s1[i] = s2[i] = 0.0f;
+  }
+  if (q.on)
+#pragma unroll 2
+    for (int j = q.row; j < s.count; j += q.step) {
+      const float w = p.counts[s.first + j];
+      n += w;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 x = sums[(long)j * p.a.channels + i];
+        const float d = x.x - base[i];
+        s1[i] = fmaf(w, d, s1[i]);
+        s2[i] += fmaf(w * d, d, x.y);
+      }
+    }
+  add_rows<V>(q, red, s1, s2);
+  n = block_sum(q.on && threadIdx.x % q.width == 0 ? n : 0.0f);
+  const float inv = n > 0.0f ? 1.0f / n : 0.0f;
+  if (threadIdx.x < q.width)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float m = s1[i] * inv;
+      red[c0 + i] = make_float2(base[i] + m, fmaxf(s2[i] - n * m * m, 0.0f));
+    }
+  __syncthreads();
+  int have = -1;
+  float m = 0.0f, rs = 0.0f;
+  each_group<V>(c0, p.gc, [&](int i, int g) {
+    if (g != have) {
+      have = g;
+      const float2* of = red + g * p.gc;
+      m = 0.0f;
+      for (int j = 0; j < p.gc; ++j) m += of[j].x - of[0].x;
+      m = n > 0.0f ? of[0].x + m / (float)p.gc : 0.0f;
+      float v = 0.0f;
+      for (int j = 0; j < p.gc; ++j) {
+        const float d = of[j].x - m;
+        v += fmaf(n * d, d, of[j].y);
+      }
+      rs = 1.0f / sqrtf(v * (inv / (float)p.gc) + p.a.eps);
+    }
+    k.mean[i] = m;
+    k.rstd[i] = rs;
+    if (c.first && threadIdx.x < q.width && c0 + i == g * p.gc) {
+      if (p.mean) p.mean[c.g * p.a.groups + g] = m;
+      if (p.rstd) p.rstd[c.g * p.a.groups + g] = rs;
+    }
+  });
+}
+
+template <class T, int V, int ACT, bool HERE>
 __global__ void __launch_bounds__(NT) norm_apply(NormParams p) {
   const Chunk c = chunk_of(p, blockIdx.x);
   if (c.none || c.only) return;
@@ -413,11 +494,15 @@ __global__ void __launch_bounds__(NT) norm_apply(NormParams p) {
   const int c0 = q.unit * V;
   Channels<V> k;
   k.affine(p, c0);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float2 s = p.stats[c.g * p.a.groups + (c0 + i) / p.gc];
-    k.mean[i] = s.x;
-    k.rstd[i] = s.y;
+  if (HERE) {
+    __shared__ float2 red[NT * V];
+    finish_here<V>(p, c, q, red, k);
+  } else {
+    each_group<V>(c0, p.gc, [&](int i, int g) {
+      const float2 s = p.stats[c.g * p.a.groups + g];
+      k.mean[i] = s.x;
+      k.rstd[i] = s.y;
+    });
   }
   write_rows<T, V, ACT>(p, c, q, k);
 }
@@ -441,13 +526,39 @@ template <class T, int V, int ACT>
 __device__ __forceinline__ void write_grads(const NormParams& p, const Chunk& c, const Place& q,
                                             const Channels<V>& k, const float (&m1)[V], const float (&m2)[V]) {
   T* gx = (T*)p.gx + q.unit * V;
-  each_row(p, c, q, [&](long r, bool counts) {
+  each_row<2>(p, c, q, [&](long r, bool counts) {
     float dz[V], xh[V];
     row_grad<T, V, ACT>(p, k, r, q.unit * V, counts, dz, xh);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       dz[i] = counts ? k.rstd[i] * (fmaf(dz[i], k.w[i], -m1[i]) - xh[i] * m2[i]) : 0.0f;
     store<T, V>(gx + r * p.gx_row, dz);
+  });
+}
+
+// Means of w dz and w dz xhat of the groups of a thread's channels, from their sums over n rows.
+template <int V>
+__device__ void group_means(const NormParams& p, const Place& q, const Channels<V>& k, float n, float2* red,
+                            const float (&s1)[V], const float (&s2)[V], float (&m1)[V], float (&m2)[V]) {
+  const int c0 = q.unit * V;
+  if (threadIdx.x < q.width)
+#pragma unroll
+    for (int i = 0; i < V; ++i) red[c0 + i] = make_float2(s1[i] * k.w[i], s2[i] * k.w[i]);
+  __syncthreads();
+  const float inv = n > 0.0f ? 1.0f / (n * (float)p.gc) : 0.0f;
+  int have = -1;
+  float a = 0.0f, b = 0.0f;
+  each_group<V>(c0, p.gc, [&](int i, int g) {
+    if (g != have) {
+      have = g;
+      a = b = 0.0f;
+      for (int j = 0; j < p.gc; ++j) {
+        a += red[g * p.gc + j].x;
+        b += red[g * p.gc + j].y;
+      }
+    }
+    m1[i] = a * inv;
+    m2[i] = b * inv;
   });
 }
 
@@ -467,68 +578,46 @@ __global__ void __launch_bounds__(NT) norm_grad_sums(NormParams p) {
   }
   Channels<V> k;
   k.affine(p, c0);
-  k.moments(p, c.g, c0, p.mean, p.rstd);
-  int first;
-  const int n = count_rows(p, c, &first);
-  each_row(p, c, q, [&](long r, bool counts) {
+  k.moments(p, c.g, c0);
+  float n = 0.0f;
+  each_row<2>(p, c, q, [&](long r, bool counts) {
     float dz[V], xh[V];
     row_grad<T, V, ACT>(p, k, r, c0, counts, dz, xh);
+    n += counts ? 1.0f : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       s1[i] += dz[i];
       s2[i] = fmaf(dz[i], xh[i], s2[i]);
     }
   });
-  add_rows<V>(q, s1, s2);
+  __shared__ float2 red[NT * V];
+  add_rows<V>(q, red, s1, s2);
+  n = block_sum(q.on && threadIdx.x % q.width == 0 ? n : 0.0f);
   if (threadIdx.x < q.width)
 #pragma unroll
     for (int i = 0; i < V; ++i) p.sums[(long)blockIdx.x * p.a.channels + c0 + i] = make_float2(s1[i], s2[i]);
-  if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = (float)n;
+  if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = n;
   if (!c.only) return;
-  __shared__ float a1[NT * V], a2[NT * V];
-  if (threadIdx.x < q.width)
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      a1[c0 + i] = s1[i] * k.w[i];
-      a2[c0 + i] = s2[i] * k.w[i];
-    }
-  __syncthreads();
-  const float inv = n > 0 ? 1.0f / ((float)n * (float)p.gc) : 0.0f;
-  int have = -1;
-  float m1 = 0.0f, m2 = 0.0f, m1s[V], m2s[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int g = (c0 + i) / p.gc;
-    if (g != have) {
-      have = g;
-      m1 = m2 = 0.0f;
-      for (int j = g * p.gc; j < (g + 1) * p.gc; ++j) {
-        m1 += a1[j];
-        m2 += a2[j];
-      }
-    }
-    m1s[i] = m1 * inv;
-    m2s[i] = m2 * inv;
-  }
-  write_grads<T, V, ACT>(p, c, q, k, m1s, m2s);
+  float m1[V], m2[V];
+  group_means<V>(p, q, k, n, red, s1, s2, m1, m2);
+  write_grads<T, V, ACT>(p, c, q, k, m1, m2);
 }
 
-// Work-groups 0 .. graphs x groups - 1: the means of one graph and group.
+// One work-group per (graph, group).
 __global__ void __launch_bounds__(NT) norm_grad_finish(NormParams p) {
   const int g = blockIdx.x / p.a.groups, grp = blockIdx.x % p.a.groups;
-  const int s0 = first_slot(p, g);
-  const int rows = offset(p.a.row_ptr, g + 1, p.a.num_rows) - offset(p.a.row_ptr, g, p.a.num_rows);
-  if (rows <= p.chunk && p.units <= NT) return;
-  const int chunks = max((rows + p.chunk - 1) / p.chunk, 1), total = chunks * p.gc;
+  const Slots s = slots_of(p, g);
+  if (s.count == 1 && p.units <= NT) return;
+  const int total = s.count * p.gc;
   float n = 0.0f, m1 = 0.0f, m2 = 0.0f;
 #pragma unroll 4
   for (int t = threadIdx.x; t < total; t += NT) {
     const int ch = grp * p.gc + t % p.gc;
-    const float2 s = p.sums[(long)(s0 + t / p.gc) * p.a.channels + ch];
+    const float2 x = p.sums[(long)(s.first + t / p.gc) * p.a.channels + ch];
     const float w = p.a.weight ? p.a.weight[ch] : 1.0f;
-    n += p.counts[s0 + t / p.gc];
-    m1 = fmaf(w, s.x, m1);
-    m2 = fmaf(w, s.y, m2);
+    n += p.counts[s.first + t / p.gc];
+    m1 = fmaf(w, x.x, m1);
+    m2 = fmaf(w, x.y, m2);
   }
   n = fmaxf(block_sum(n), 1.0f);
   m1 = block_sum(m1) / n;
@@ -537,9 +626,8 @@ __global__ void __launch_bounds__(NT) norm_grad_finish(NormParams p) {
 }
 
 // Weight and bias gradients of four channels: 64 threads each over the slots.
-__global__ void __launch_bounds__(NT) norm_grad_affine(NormParams p) {
-  __shared__ float2 red[NT];
-  const int c = blockIdx.x * 4 + (threadIdx.x & 3);
+__device__ void affine_grads(const NormParams& p, int c0, float2* red) {
+  const int c = c0 + (threadIdx.x & 3);
   float w = 0.0f, b = 0.0f;
   if (c < p.a.channels)
 #pragma unroll 8
@@ -563,21 +651,48 @@ __global__ void __launch_bounds__(NT) norm_grad_affine(NormParams p) {
   }
 }
 
-template <class T, int V, int ACT>
+// Work-groups from p.slots on take the weight and bias gradients.
+template <class T, int V, int ACT, bool HERE>
 __global__ void __launch_bounds__(NT) norm_grad_apply(NormParams p) {
+  __shared__ float2 red[NT * V];
+  if ((int)blockIdx.x >= p.slots) {
+    if (blockIdx.y == 0) affine_grads(p, ((int)blockIdx.x - p.slots) * 4, red);
+    return;
+  }
   const Chunk c = chunk_of(p, blockIdx.x);
   if (c.none || c.only) return;
   const Place q = place(p);
   const int c0 = q.unit * V;
   Channels<V> k;
   k.affine(p, c0);
-  k.moments(p, c.g, c0, p.mean, p.rstd);
+  k.moments(p, c.g, c0);
   float m1[V], m2[V];
+  if (HERE) {
+    const Slots s = slots_of(p, c.g);
+    const float2* sums = p.sums + (long)s.first * p.a.channels + c0;
+    float n = 0.0f, s1[V], s2[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float2 s = p.stats[c.g * p.a.groups + (c0 + i) / p.gc];
-    m1[i] = s.x;
-    m2[i] = s.y;
+    for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
+    if (q.on)
+#pragma unroll 2
+      for (int j = q.row; j < s.count; j += q.step) {
+        n += p.counts[s.first + j];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float2 x = sums[(long)j * p.a.channels + i];
+          s1[i] += x.x;
+          s2[i] += x.y;
+        }
+      }
+    add_rows<V>(q, red, s1, s2);
+    n = block_sum(q.on && threadIdx.x % q.width == 0 ? n : 0.0f);
+    group_means<V>(p, q, k, n, red, s1, s2, m1, m2);
+  } else {
+    each_group<V>(c0, p.gc, [&](int i, int g) {
+      const float2 s = p.stats[c.g * p.a.groups + g];
+      m1[i] = s.x;
+      m2[i] = s.y;
+    });
   }
   write_grads<T, V, ACT>(p, c, q, k, m1, m2);
 }
@@ -588,22 +703,28 @@ template <class T, int V, int ACT>
 hipError_t forward(const NormParams& p, bool one, hipStream_t s) {
   const dim3 grid((unsigned)p.slots, (unsigned)((p.units + NT - 1) / NT));
   hipLaunchKernelGGL((norm_sums<T, V, ACT>), grid, dim3(NT), 0, s, p);
-  if (!one) {
+  if (one) return hipGetLastError();
+  if (p.inline_finish) {
+    hipLaunchKernelGGL((norm_apply<T, V, ACT, true>), grid, dim3(NT), 0, s, p);
+  } else {
     hipLaunchKernelGGL(norm_finish, dim3((unsigned)(p.a.num_graphs * p.a.groups)), dim3(NT), 0, s, p);
-    hipLaunchKernelGGL((norm_apply<T, V, ACT>), grid, dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((norm_apply<T, V, ACT, false>), grid, dim3(NT), 0, s, p);
   }
   return hipGetLastError();
 }
 
 template <class T, int V, int ACT>
 hipError_t backward(const NormParams& p, bool one, hipStream_t s) {
-  const dim3 grid((unsigned)p.slots, (unsigned)((p.units + NT - 1) / NT));
-  hipLaunchKernelGGL((norm_grad_sums<T, V, ACT>), grid, dim3(NT), 0, s, p);
-  if (p.gw || p.gb)
-    hipLaunchKernelGGL(norm_grad_affine, dim3((unsigned)((p.a.channels + 3) / 4)), dim3(NT), 0, s, p);
-  if (!one) {
+  const unsigned columns = (unsigned)((p.units + NT - 1) / NT);
+  const unsigned affine = p.gw || p.gb ? (unsigned)((p.a.channels + 3) / 4) : 0;
+  hipLaunchKernelGGL((norm_grad_sums<T, V, ACT>), dim3((unsigned)p.slots, columns), dim3(NT), 0, s, p);
+  if (one && affine == 0) return hipGetLastError();
+  const dim3 grid((unsigned)p.slots + affine, columns);
+  if (p.inline_finish || one) {
+    hipLaunchKernelGGL((norm_grad_apply<T, V, ACT, true>), grid, dim3(NT), 0, s, p);
+  } else {
     hipLaunchKernelGGL(norm_grad_finish, dim3((unsigned)(p.a.num_graphs * p.a.groups)), dim3(NT), 0, s, p);
-    hipLaunchKernelGGL((norm_grad_apply<T, V, ACT>), grid, dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((norm_grad_apply<T, V, ACT, false>), grid, dim3(NT), 0, s, p);
   }
   return hipGetLastError();
 }
@@ -623,12 +744,12 @@ hipError_t by_activation(const NormParams& p, bool back, bool one, hipStream_t s
 }
 
 // Rows of a chunk: all of them where the whole call is small (then every graph is one chunk and
-// one launch does it), else about 2048 work-groups of 8 KiB at least.
+// one launch does it), else about four work-groups per compute unit, 16 KiB each at least.
 int chunk_rows(const e3conv_group_norm_args& a) {
   const int64_t n = a.num_rows > 0 ? a.num_rows : 1;
   if (n * a.channels <= 1 << 18) return (int)n;
   const int64_t row = (int64_t)a.channels * (a.dtype == E3CONV_F32 ? 4 : 2);
-  const int64_t want = (n + 2047) / 2048, least = (8192 + row - 1) / row;
+  const int64_t want = (n + 1023) / 1024, least = (16384 + row - 1) / row;
   return (int)(want > least ? want : least);
 }
 int chunk_slots(const e3conv_group_norm_args& a) { return (int)(a.num_rows / chunk_rows(a) + a.num_graphs); }
@@ -654,6 +775,8 @@ hipError_t launch(NormParams p, bool back, bool vec, void* workspace, hipStream_
   p.stats = p.sums + (size_t)p.slots * p.a.channels;
   p.counts = reinterpret_cast<float*>(p.stats + (size_t)p.a.num_graphs * p.a.groups);
   const bool one = p.a.num_rows <= p.chunk && p.units <= NT;
+  // with few chunks a graph, joining them in every work-group of the graph costs less than a launch
+  p.inline_finish = p.units <= NT && p.a.num_rows / p.chunk <= (int64_t)16 * p.a.num_graphs;
   if ((int64_t)p.a.num_graphs * p.a.groups > 0x7fffffff) return hipErrorInvalidValue;
   if (f32) return vec ? by_activation<float, 4>(p, back, one, s) : by_activation<float, 1>(p, back, one, s);
   return vec ? by_activation<__bf16, 8>(p, back, one, s) : by_activation<__bf16, 1>(p, back, one, s);

@@ -87,6 +87,14 @@ def test_mean_far_from_zero(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[30000], [9000] * 4])
+def test_mean_far_from_zero_after_masked_rows(dtype, lens):
+    """The first third of each graph is padding, whole chunks of it: the sums still start at the data."""
+    mask = np.concatenate([(np.arange(n) >= n // 3).astype(np.uint8) for n in lens])
+    check(dtype, lens, 32, 4, "none", mask=mask, shift=300.0, spread=1.0, poison=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_constant_rows(dtype):
     check(dtype, [64, 3], 16, 2, "none", spread=0.0, eps=1e-3)
 
