@@ -30,11 +30,26 @@ namespace {
 constexpr int kMaxChannels = 4096;
 constexpr int NT = 256;            // threads of a work-group
 
+// n / d for 0 <= n < 2^31 by a product: ceil(2^(31 + l) / d) with 2^l >= d.  The runtime divisions
+// of a work-group's start cost as much as its loads where a chunk is a few rows a thread.
+struct Div {
+  int d;
+  unsigned magic;
+  int shift;
+  __device__ __forceinline__ int of(int n) const { return d == 1 ? n : (int)(__umulhi((unsigned)n, magic) >> shift); }
+};
+Div div_by(int d) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  return {d, l > 0 ? (unsigned)((((uint64_t)1 << (31 + l)) + d - 1) / d) : 0, l > 0 ? l - 1 : 0};
+}
+
 struct NormParams {
   e3conv_group_norm_args a;
   int gc;                          // channels of a group
   int units;                       // runs of V channels in a row
-  int chunk;                       // rows of a work-group
+  Div by_gc, by_width;             // by gc, and by min(units, NT)
+  int chunk_log2, chunk;           // rows of a work-group, a power of two
   int slots;                       // chunk slots: rows / chunk + graphs
   int inline_finish;               // 1: finish within apply
   void* y;
@@ -52,30 +67,14 @@ struct NormParams {
 
 // ------------------------------------------------------------------ graphs ---
 
-__device__ __forceinline__ int offset(const int* ptr, int i, long n) {
-  const int v = ptr[i];
-  return v < 0 ? 0 : (v > n ? (int)n : v);
+__device__ __forceinline__ int clamp_row(int v, long n) { return v < 0 ? 0 : (v > n ? (int)n : v); }
+__device__ __forceinline__ int offset(const NormParams& p, int g) {
+  return clamp_row(p.a.row_ptr[g], p.a.num_rows);
 }
 
 // Chunks of graph g take the slots first / chunk + g and on, first being its first row:
-// enough for ceil(rows / chunk) of them, and one at least.  The graph of a slot is the last
-// whose first slot is not beyond it; 64 are tried at a time.
-__device__ __forceinline__ int first_slot(const NormParams& p, int g) {
-  return offset(p.a.row_ptr, g, p.a.num_rows) / p.chunk + g;
-}
-__device__ __forceinline__ int graph_of_slot(const NormParams& p, int slot) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, count = p.a.num_graphs;
-  while (count > 1) {
-    const int step = (count + 63) >> 6, i = lane * step;
-    bool before = false;
-    if (i < count) before = first_slot(p, lo + i) <= slot;
-    const int hits = max(__popcll(__ballot(before)), 1);
-    lo += (hits - 1) * step;
-    count = min(step, count - (hits - 1) * step);
-  }
-  return __builtin_amdgcn_readfirstlane(lo);
-}
+// enough for ceil(rows / chunk) of them, and one at least.
+__device__ __forceinline__ int first_slot(const NormParams& p, int g) { return (offset(p, g) >> p.chunk_log2) + g; }
 
 // The chunk of a slot: rows [begin, end) of graph g.
 struct Chunk {
@@ -84,17 +83,33 @@ struct Chunk {
   bool only;       // and its only one
   bool none;       // a slot without a chunk
 };
+// The graph of a slot is the last whose first slot is not beyond it; 256 offsets are tried at a time.
 __device__ __forceinline__ Chunk chunk_of(const NormParams& p, int slot) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, count = p.a.num_graphs;
+  while (count > 1) {
+    const int step = (count + 255) >> 8;
+    int at[4], hits = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) at[k] = p.a.row_ptr[lo + min((4 * lane + k) * step, count - 1)];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = (4 * lane + k) * step;
+      hits += __popcll(__ballot(i < count && (clamp_row(at[k], p.a.num_rows) >> p.chunk_log2) + lo + i <= slot));
+    }
+    hits = max(hits, 1);
+    lo += (hits - 1) * step;
+    count = min(step, count - (hits - 1) * step);
+  }
   Chunk c;
-  c.g = graph_of_slot(p, slot);
-  const int r0 = offset(p.a.row_ptr, c.g, p.a.num_rows);
-  const int r1 = max(r0, offset(p.a.row_ptr, c.g + 1, p.a.num_rows));
-  const int k = slot - first_slot(p, c.g);
+  c.g = __builtin_amdgcn_readfirstlane(lo);
+  const int r0 = offset(p, c.g), r1 = max(r0, offset(p, c.g + 1));
+  const int k = slot - ((r0 >> p.chunk_log2) + c.g);
   c.first = k == 0;
   c.only = c.first && r1 - r0 <= p.chunk && p.units <= NT;
-  c.none = k < 0 || (k > 0 && (long)k * p.chunk >= r1 - r0);
-  c.begin = c.none ? r0 : r0 + k * p.chunk;
-  c.end = min(r1, c.begin + p.chunk);
+  c.none = k < 0 || (k > 0 && ((long)k << p.chunk_log2) >= r1 - r0);
+  c.begin = c.none ? r0 : r0 + (k << p.chunk_log2);
+  c.end = (int)min((long)r1, (long)c.begin + p.chunk);
   return c;
 }
 
@@ -159,15 +174,18 @@ __device__ __forceinline__ float activate_grad(float z) {
 struct Place {
   int unit, row, step;     // step: rows of a pass
   int width;               // units of this work-group
+  int col;                 // unit within them
   bool on;
 };
 __device__ __forceinline__ Place place(const NormParams& p) {
   Place q;
   const int from = blockIdx.y * NT;
   q.width = min(p.units - from, NT);
-  q.step = NT / q.width;
-  q.row = threadIdx.x / q.width;
-  q.unit = from + threadIdx.x % q.width;
+  const bool usual = q.width == p.by_width.d;
+  q.step = usual ? p.by_width.of(NT) : NT / q.width;
+  q.row = usual ? p.by_width.of(threadIdx.x) : (int)threadIdx.x / q.width;
+  q.col = threadIdx.x - q.row * q.width;
+  q.unit = from + q.col;
   q.on = q.row < q.step;
   return q;
 }
@@ -190,7 +208,7 @@ __device__ void add_rows(const Place& q, float2* red, float (&s1)[V], float (&s2
   }
   int half = 1;
   while (half < rows) half <<= 1;
-  const int unit = threadIdx.x % q.width;
+  const int unit = q.col;
   for (half >>= 1; half > 0; half >>= 1) {
     if (on && row >= half && row < rows)
 #pragma unroll
@@ -247,8 +265,9 @@ __device__ __forceinline__ void each_row(const NormParams& p, const Chunk& c, co
 
 // Calls use(i, group) for the V channels from c0 on.
 template <int V, class F>
-__device__ __forceinline__ void each_group(int c0, int gc, F use) {
-  int g = c0 / gc, left = (g + 1) * gc - c0;
+__device__ __forceinline__ void each_group(const NormParams& p, int c0, F use) {
+  const int gc = p.gc;
+  int g = p.by_gc.of(c0), left = (g + 1) * gc - c0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (left == 0) {
@@ -272,7 +291,7 @@ struct Channels {
     }
   }
   __device__ __forceinline__ void moments(const NormParams& p, int g, int c0) {
-    each_group<V>(c0, p.gc, [&](int i, int grp) {
+    each_group<V>(p, c0, [&](int i, int grp) {
       mean[i] = p.mean[g * p.a.groups + grp];
       rstd[i] = p.rstd[g * p.a.groups + grp];
     });
@@ -294,8 +313,8 @@ struct Slots {
   int first, count;
 };
 __device__ __forceinline__ Slots slots_of(const NormParams& p, int g) {
-  const int rows = offset(p.a.row_ptr, g + 1, p.a.num_rows) - offset(p.a.row_ptr, g, p.a.num_rows);
-  return {first_slot(p, g), max((int)(((long)rows + p.chunk - 1) / p.chunk), 1)};
+  const int r0 = offset(p, g), rows = offset(p, g + 1) - r0;
+  return {(r0 >> p.chunk_log2) + g, max((int)(((long)rows + p.chunk - 1) >> p.chunk_log2), 1)};
 }
 
 // ---------------------------------------------------------------- forward ---
@@ -365,7 +384,7 @@ __global__ void __launch_bounds__(NT) norm_sums(NormParams p) {
   k.affine(p, c0);
   int have = -1;
   float m = 0.0f, rs = 0.0f;
-  each_group<V>(c0, p.gc, [&](int i, int g) {
+  each_group<V>(p, c0, [&](int i, int g) {
     if (g != have) {
       have = g;
       const float2* of = red + g * p.gc;
@@ -400,18 +419,18 @@ __global__ void __launch_bounds__(NT) norm_finish(NormParams p) {
   float n = 0.0f, m = 0.0f, v = 0.0f;
 #pragma unroll 4
   for (int t = threadIdx.x; t < total; t += NT) {
-    const float k = p.counts[s.first + t / p.gc];
+    const float k = p.counts[s.first + p.by_gc.of(t)];
     n += k;
-    m = fmaf(k, sums[(long)(t / p.gc) * p.a.channels + t % p.gc].x - base, m);
+    m = fmaf(k, sums[(long)p.by_gc.of(t) * p.a.channels + (t - p.by_gc.of(t) * p.gc)].x - base, m);
   }
   n = block_sum(n);
   m = block_sum(m);
   m = n > 0.0f ? base + m / n : 0.0f;
 #pragma unroll 4
   for (int t = threadIdx.x; t < total; t += NT) {
-    const float2 x = sums[(long)(t / p.gc) * p.a.channels + t % p.gc];
+    const float2 x = sums[(long)p.by_gc.of(t) * p.a.channels + (t - p.by_gc.of(t) * p.gc)];
     const float d = x.x - m;
-    v += fmaf(p.counts[s.first + t / p.gc] * d, d, x.y);
+    v += fmaf(p.counts[s.first + p.by_gc.of(t)] * d, d, x.y);
   }
   v = block_sum(v);
   const float rs = 1.0f / sqrtf((n > 0.0f ? v / n : 0.0f) + p.a.eps);
@@ -452,7 +471,7 @@ __device__ void finish_here(const NormParams& p, const Chunk& c, const Place& q,
       }
     }
   add_rows<V>(q, red, s1, s2);
-  n = block_sum(q.on && threadIdx.x % q.width == 0 ? n : 0.0f);
+  n = block_sum(q.on && q.col == 0 ? n : 0.0f);
   const float inv = n > 0.0f ? 1.0f / n : 0.0f;
   if (threadIdx.x < q.width)
 #pragma unroll
@@ -463,7 +482,7 @@ __device__ void finish_here(const NormParams& p, const Chunk& c, const Place& q,
   __syncthreads();
   int have = -1;
   float m = 0.0f, rs = 0.0f;
-  each_group<V>(c0, p.gc, [&](int i, int g) {
+  each_group<V>(p, c0, [&](int i, int g) {
     if (g != have) {
       have = g;
       const float2* of = red + g * p.gc;
@@ -498,7 +517,7 @@ __global__ void __launch_bounds__(NT) norm_apply(NormParams p) {
     __shared__ float2 red[NT * V];
     finish_here<V>(p, c, q, red, k);
   } else {
-    each_group<V>(c0, p.gc, [&](int i, int g) {
+    each_group<V>(p, c0, [&](int i, int g) {
       const float2 s = p.stats[c.g * p.a.groups + g];
       k.mean[i] = s.x;
       k.rstd[i] = s.y;
@@ -548,7 +567,7 @@ __device__ void group_means(const NormParams& p, const Place& q, const Channels<
   const float inv = n > 0.0f ? 1.0f / (n * (float)p.gc) : 0.0f;
   int have = -1;
   float a = 0.0f, b = 0.0f;
-  each_group<V>(c0, p.gc, [&](int i, int g) {
+  each_group<V>(p, c0, [&](int i, int g) {
     if (g != have) {
       have = g;
       a = b = 0.0f;
@@ -592,7 +611,7 @@ __global__ void __launch_bounds__(NT) norm_grad_sums(NormParams p) {
   });
   __shared__ float2 red[NT * V];
   add_rows<V>(q, red, s1, s2);
-  n = block_sum(q.on && threadIdx.x % q.width == 0 ? n : 0.0f);
+  n = block_sum(q.on && q.col == 0 ? n : 0.0f);
   if (threadIdx.x < q.width)
 #pragma unroll
     for (int i = 0; i < V; ++i) p.sums[(long)blockIdx.x * p.a.channels + c0 + i] = make_float2(s1[i], s2[i]);
@@ -612,10 +631,10 @@ __global__ void __launch_bounds__(NT) norm_grad_finish(NormParams p) {
   float n = 0.0f, m1 = 0.0f, m2 = 0.0f;
 #pragma unroll 4
   for (int t = threadIdx.x; t < total; t += NT) {
-    const int ch = grp * p.gc + t % p.gc;
-    const float2 x = p.sums[(long)(s.first + t / p.gc) * p.a.channels + ch];
+    const int ch = grp * p.gc + t - p.by_gc.of(t) * p.gc;
+    const float2 x = p.sums[(long)(s.first + p.by_gc.of(t)) * p.a.channels + ch];
     const float w = p.a.weight ? p.a.weight[ch] : 1.0f;
-    n += p.counts[s.first + t / p.gc];
+    n += p.counts[s.first + p.by_gc.of(t)];
     m1 = fmaf(w, x.x, m1);
     m2 = fmaf(w, x.y, m2);
   }
@@ -685,10 +704,10 @@ __global__ void __launch_bounds__(NT) norm_grad_apply(NormParams p) {
         }
       }
     add_rows<V>(q, red, s1, s2);
-    n = block_sum(q.on && threadIdx.x % q.width == 0 ? n : 0.0f);
+    n = block_sum(q.on && q.col == 0 ? n : 0.0f);
     group_means<V>(p, q, k, n, red, s1, s2, m1, m2);
   } else {
-    each_group<V>(c0, p.gc, [&](int i, int g) {
+    each_group<V>(p, c0, [&](int i, int g) {
       const float2 s = p.stats[c.g * p.a.groups + g];
       m1[i] = s.x;
       m2[i] = s.y;
@@ -743,16 +762,19 @@ hipError_t by_activation(const NormParams& p, bool back, bool one, hipStream_t s
   }
 }
 
-// Rows of a chunk: all of them where the whole call is small (then every graph is one chunk and
-// one launch does it), else about four work-groups per compute unit, 16 KiB each at least.
-int chunk_rows(const e3conv_group_norm_args& a) {
-  const int64_t n = a.num_rows > 0 ? a.num_rows : 1;
-  if (n * a.channels <= 1 << 18) return (int)n;
+// Rows of a chunk, as a power of two: all of them where the whole call is small (then every graph
+// is one chunk and one launch does it), else about four work-groups per compute unit, 16 KiB
+// each at least.
+int chunk_rows_log2(const e3conv_group_norm_args& a) {
   const int64_t row = (int64_t)a.channels * (a.dtype == E3CONV_F32 ? 4 : 2);
-  const int64_t want = (n + 1023) / 1024, least = (16384 + row - 1) / row;
-  return (int)(want > least ? want : least);
+  int64_t rows = (a.num_rows + 1023) / 1024;
+  if (rows * row < 16384) rows = (16384 + row - 1) / row;
+  if (a.num_rows * a.channels <= 1 << 18) rows = a.num_rows;
+  int l = 0;
+  while (((int64_t)1 << l) < rows) ++l;
+  return l < 30 ? l : 30;
 }
-int chunk_slots(const e3conv_group_norm_args& a) { return (int)(a.num_rows / chunk_rows(a) + a.num_graphs); }
+int chunk_slots(const e3conv_group_norm_args& a) { return (int)((a.num_rows >> chunk_rows_log2(a)) + a.num_graphs); }
 
 // sums (slots, channels), stats (graphs, groups), counts (slots).
 size_t workspace_bytes(const e3conv_group_norm_args& a) {
@@ -769,7 +791,10 @@ hipError_t launch(NormParams p, bool back, bool vec, void* workspace, hipStream_
   if (p.a.channels % v != 0) vec = false;
   p.gc = p.a.channels / p.a.groups;
   p.units = vec ? p.a.channels / v : p.a.channels;
-  p.chunk = chunk_rows(p.a);
+  p.by_gc = div_by(p.gc);
+  p.by_width = div_by(p.units < NT ? p.units : NT);
+  p.chunk_log2 = chunk_rows_log2(p.a);
+  p.chunk = 1 << p.chunk_log2;
   p.slots = chunk_slots(p.a);
   p.sums = static_cast<float2*>(workspace);
   p.stats = p.sums + (size_t)p.slots * p.a.channels;
