@@ -64,6 +64,7 @@ attn::Params params(const e3conv_attention_args& a) {
   while ((1 << l) < p.group) ++l;
   p.magic = (unsigned)((((uint64_t)1 << (31 + l)) + p.group - 1) / p.group);
   p.shift = l - 1;
+  p.group_log2 = 1 << l == p.group ? l : -1;
   p.negate = a.scale < 0.0f;
   // a zero scale: logits far below one unit of the sums' rounding, infinities as they are
   p.c = std::fabs(a.scale) * attn::kLog2e;

@@ -67,6 +67,9 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
   delta = live ? delta + other_half(delta) : 0.0f;
   if (row && h == 0 && split == 0) p.delta[at] = delta;
 
+  f32x16 less_delta;   // dP - delta from the start: -delta is the accumulator's first value
+#pragma unroll
+  for (int i = 0; i < 16; ++i) less_delta[i] = -delta;
   f32x16 dq[D / 32];
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) dq[dt] = f32x16{};
@@ -80,7 +83,7 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
 
 #pragma unroll
     for (int b = 0; b < TK / 32; ++b) {
-      f32x16 s = by_row(&bias[buf][32 * b], lane), dp = f32x16{};
+      f32x16 s = by_row(&bias[buf][32 * b], lane), dp = less_delta;
 #pragma unroll
       for (int t = 0; t < KS; ++t) {
         s = mma(kt.rows(32 * b, t, lane), q[t], s);
@@ -92,7 +95,7 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
       for (int t = 0; t < 2; ++t) {
         float e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = s[8 * t + i] * (dp[8 * t + i] - delta);
+        for (int i = 0; i < 8; ++i) e[i] = s[8 * t + i] * dp[8 * t + i];
         Frag<P> f;   // bf16: dS rounded for its product
         to_frag(e, f);
 #pragma unroll
@@ -127,8 +130,7 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
 
 template <class T, int D, int RW, int TQ, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
-  constexpr int P = planes<T>(), U = D / 8, KS = D / 16, NT = 64 * RW, E = TQ * U / NT, STEP = NT / U;
-  static_assert(TQ * U % NT == 0 && TQ <= NT, "");
+  constexpr int P = planes<T>(), KS = D / 16;
   __shared__ __attribute__((aligned(16))) Tile<P, TQ, D> qts[BUF], gts[BUF];
   __shared__ __attribute__((aligned(16))) float lse_b[BUF][TQ], delta_b[BUF][TQ];
   const e3conv_attention_args& a = p.a;
@@ -153,30 +155,9 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
   int r0 = min(split * per, tiles) * TQ;
   const int r1 = min(nrows, min((split + 1) * per, tiles) * TQ);
 
-  const T* qbase = (const T*)a.q + q0 * a.q_row + c * p.group * a.q_head;
-  const T* gbase = (const T*)p.go + q0 * p.go_row + c * p.group * p.go_head;
-  const long at0 = (long)q0 * a.heads_q + c * p.group;
-  const int unit = threadIdx.x % U, line = threadIdx.x / U;
-  Raw<T> qr[E], gr[E];
-  unsigned char qm[E], lm;
-  float ql[E], lse, delta;
-  // issues the loads of the tile from row r0 on; rows beyond the last read the last one
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int r = min(r0 + line + e * STEP, r1 - 1), i = query_of(p, r), x = r - i * p.group;
-      qr[e] = fetch8<VEC>(qbase + i * a.q_row + x * a.q_head, unit * 8, a.dim_qk);
-      gr[e] = fetch8<VEC>(gbase + i * p.go_row + x * p.go_head, unit * 8, a.dim_v);
-      qm[e] = a.q_mask ? a.q_mask[q0 + i] : 1;
-      ql[e] = p.lse[at0 + (long)i * a.heads_q + x];
-    }
-    const int r = min(r0 + (int)(threadIdx.x % TQ), r1 - 1), i = query_of(p, r);
-    const long at = at0 + (long)i * a.heads_q + r - i * p.group;
-    lse = p.lse[at];
-    delta = p.delta[at];
-    lm = a.q_mask ? a.q_mask[q0 + i] : 1;
-  };
-  if (r0 < r1) load(r0);
+  Rows<T, D, TQ, 64 * RW, VEC> rows;
+  rows.begin(p, c, q0, r0, r1);
+  if (r0 < r1) rows.load(p);
 
   Frag<P> k[KS], v[KS];
   const int jr = key ? j : j0;
@@ -192,36 +173,25 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
 
   for (int buf = 0; r0 < r1; r0 += TQ, buf ^= BUF - 1) {
     Tile<P, TQ, D>&qt = qts[buf], &gt = gts[buf];
-    float *lse_s = lse_b[buf], *delta_s = delta_b[buf];
     if (BUF == 1) __syncthreads();
-    // a row that sees no key, or that lies beyond the end: zeros, and lse = +infinity makes its P zero
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const bool keep = r0 + line + e * STEP < r1 && qm[e] && ql[e] != -INFINITY;
-      qt.store(line + e * STEP, unit, frag_of(qr[e], keep && unit * 8 < a.dim_qk));
-      gt.store(line + e * STEP, unit, frag_of(gr[e], keep && unit * 8 < a.dim_v));
-    }
-    if (threadIdx.x < TQ) {
-      const bool sees = r0 + (int)threadIdx.x < r1 && lm && lse != -INFINITY;
-      lse_s[threadIdx.x] = sees ? lse * kLog2e : INFINITY;
-      delta_s[threadIdx.x] = sees ? delta : 0.0f;
-    }
+    rows.store(p, r0, qt, gt, lse_b[buf], delta_b[buf]);
     __syncthreads();
-    if (r0 + TQ < r1) load(r0 + TQ);
+    if (r0 + TQ < r1) rows.load(p);
 
 #pragma unroll
     for (int b = 0; b < TQ / 32; ++b) {
-      f32x16 s = f32x16{}, dp = f32x16{};
+      // dP - delta from the start: the rows' -delta are the accumulator's first values
+      f32x16 s = f32x16{}, dp = by_row(&delta_b[buf][32 * b], lane);
 #pragma unroll
       for (int t = 0; t < KS; ++t) {
         s = mma(qt.rows(32 * b, t, lane), k[t], s);
         dp = mma(gt.rows(32 * b, t, lane), v[t], dp);
       }
-      const f32x16 ls = by_row(lse_s + 32 * b, lane), de = by_row(delta_s + 32 * b, lane);
+      const f32x16 ls = by_row(&lse_b[buf][32 * b], lane);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], p.c, -ls[i]));
-        dp[i] = s[i] * (dp[i] - de[i]);
+        dp[i] *= s[i];
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {

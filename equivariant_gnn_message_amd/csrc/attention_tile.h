@@ -19,7 +19,7 @@ namespace attn {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -31,6 +31,7 @@ struct Params {
   int group;                       // query heads per kv head
   unsigned magic;                  // r / group = (r magic) >> 32 >> shift for 0 <= r < 2^31, group > 1
   int shift;
+  int group_log2;                  // of a power of two, else -1
   float c;                         // |scale| log2(e), at least the smallest normal number
   int negate;                      // scale < 0: q enters with its sign changed
   int vec;                         // 16-byte loads of q, k, v, grad_out (and out) rows
@@ -74,19 +75,46 @@ __device__ __forceinline__ f32x16 mma(const Frag<3>& a, const Frag<3>& b, f32x16
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
 }
 
-// Eight fp32 values as an operand: rounded to bf16 (one plane), or split in three parts.
+// Eight fp32 values as an operand: rounded to bf16 (one plane), or split in three parts
+// v0 = bf16(v), v1 = bf16(v - v0), v2 = bf16(v - v0 - v1).  The differences are exact, so the
+// two-term dot product with (-1, 0) or (0, -1) gives them without unpacking v0: seven
+// instructions a pair instead of eleven.
+__device__ __forceinline__ bf16x2 round2(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_convertvector((f32x2{a, b}), bf16x2);
+}
 __device__ __forceinline__ void to_frag(const float (&v)[8], Frag<1>& f) {
+  union {
+    bf16x2 two[4];
+    bf16x8 all;
+  } r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f.p[0][i] = (__bf16)v[i];
+  for (int i = 0; i < 4; ++i) r.two[i] = round2(v[2 * i], v[2 * i + 1]);
+  f.p[0] = r.all;
 }
 __device__ __forceinline__ void to_frag(const float (&v)[8], Frag<3>& f) {
+  // in registers: as an immediate operand the pair would be read as one 32-bit float
+  unsigned first = 0x0000bf80u, second = 0xbf800000u;
+  asm("" : "+s"(first));
+  asm("" : "+s"(second));
+  const bf16x2 lo = __builtin_bit_cast(bf16x2, first), hi = __builtin_bit_cast(bf16x2, second);
+  union {
+    bf16x2 two[4];
+    bf16x8 all;
+  } r[3];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f.p[0][i] = (__bf16)v[i];
-    const float r = v[i] - (float)f.p[0][i];
-    f.p[1][i] = (__bf16)r;
-    f.p[2][i] = (__bf16)(r - (float)f.p[1][i]);
+  for (int i = 0; i < 4; ++i) {
+    float a = v[2 * i], b = v[2 * i + 1];
+    r[0].two[i] = round2(a, b);
+    a = __builtin_amdgcn_fdot2_f32_bf16(r[0].two[i], lo, a, false);
+    b = __builtin_amdgcn_fdot2_f32_bf16(r[0].two[i], hi, b, false);
+    r[1].two[i] = round2(a, b);
+    a = __builtin_amdgcn_fdot2_f32_bf16(r[1].two[i], lo, a, false);
+    b = __builtin_amdgcn_fdot2_f32_bf16(r[1].two[i], hi, b, false);
+    r[2].two[i] = round2(a, b);
   }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) f.p[k] = r[k].all;
 }
 
 // Eight consecutive elements of a row as they lie in memory.
@@ -311,6 +339,89 @@ struct Keys {
         const bool keep = seen >> (row + e * STEP) & 1;
         kt.store(row + e * STEP, unit, frag_of(k[e], keep && unit * 8 < p.a.dim_qk));
         vt.store(row + e * STEP, unit, frag_of(v[e], keep && unit * 8 < p.a.dim_v));
+      }
+    }
+  }
+};
+
+// The tiles of the rows (queries and their heads of one kv head) that a work-group of the
+// reverse pass walks over: q and grad_out as Keys does k and v, and each row's lse
+// (base 2) and -delta.  A row that sees no key or lies beyond the end is stored as zeros
+// with lse = +infinity, which makes its P zero.
+template <class T, int D, int ROWS, int NT, bool VEC>
+struct Rows {
+  static constexpr int P = planes<T>(), U = D / 8, E = ROWS * U / NT, STEP = NT / U;
+  static_assert(ROWS * U % NT == 0 && ROWS <= 64, "");
+  Raw<T> q[E], g[E];
+  float lse, delta;
+  unsigned char m;
+  const T *qb, *gb;      // the kv head's first row of the graph
+  const T *qp, *gp;      // this thread's first row of the next tile
+  long at0;              // of lse and delta
+  int q0, next, end;
+
+  __device__ __forceinline__ void begin(const Params& p, int c, int first_query, int r0, int r1) {
+    const e3conv_attention_args& a = p.a;
+    q0 = first_query;
+    qb = (const T*)a.q + q0 * a.q_row + c * p.group * a.q_head;
+    gb = (const T*)p.go + q0 * p.go_row + c * p.group * p.go_head;
+    at0 = (long)q0 * a.heads_q + c * p.group;
+    next = r0;
+    end = r1;
+    const int r = r0 + (int)threadIdx.x / U, i = query_of(p, r), x = r - i * p.group;
+    qp = qb + i * a.q_row + x * a.q_head;
+    gp = gb + i * p.go_row + x * p.go_head;
+  }
+  __device__ __forceinline__ void load(const Params& p) {
+    const e3conv_attention_args& a = p.a;
+    const int d = threadIdx.x % U * 8;
+    // STEP rows on lie STEP / group queries on where the heads of a group divide STEP
+    const int by = STEP >> p.group_log2;
+    if (next + ROWS <= end && p.group_log2 >= 0 && by << p.group_log2 == STEP) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        q[e] = fetch8<VEC>(qp + e * by * a.q_row, d, a.dim_qk);
+        g[e] = fetch8<VEC>(gp + e * by * p.go_row, d, a.dim_v);
+      }
+      qp += E * by * a.q_row;
+      gp += E * by * p.go_row;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int r = min(next + (int)threadIdx.x / U + e * STEP, end - 1), i = query_of(p, r), x = r - i * p.group;
+        q[e] = fetch8<VEC>(qb + i * a.q_row + x * a.q_head, d, a.dim_qk);
+        g[e] = fetch8<VEC>(gb + i * p.go_row + x * p.go_head, d, a.dim_v);
+      }
+    }
+    const int r = min(next + (int)(threadIdx.x & 63), end - 1), i = query_of(p, r);
+    const long at = at0 + (long)i * (a.heads_q - p.group) + r;
+    lse = p.lse[at];
+    delta = p.delta[at];
+    if (a.q_mask) m = a.q_mask[q0 + i];
+    next += ROWS;
+  }
+  // r0: the first row of the loaded tile.
+  __device__ __forceinline__ void store(const Params& p, int r0, Tile<P, ROWS, D>& qt, Tile<P, ROWS, D>& gt,
+                                        float* lse_of, float* delta_of) const {
+    const int unit = threadIdx.x % U, row = threadIdx.x / U, lane = threadIdx.x & 63;
+    const bool sees = lane < ROWS && r0 + lane < end && lse != -INFINITY && (!p.a.q_mask || m);
+    const unsigned long seen = __ballot(sees);
+    if (threadIdx.x < ROWS) {
+      lse_of[lane] = sees ? lse * kLog2e : INFINITY;
+      delta_of[lane] = sees ? -delta : 0.0f;
+    }
+    if (seen == (ROWS == 64 ? ~0ul : (1ul << (ROWS & 63)) - 1) && (!VEC || (p.a.dim_qk == D && p.a.dim_v == D))) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        qt.store(row + e * STEP, unit, frag_of(q[e], true));
+        gt.store(row + e * STEP, unit, frag_of(g[e], true));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const bool keep = seen >> (row + e * STEP) & 1;
+        qt.store(row + e * STEP, unit, frag_of(q[e], keep && unit * 8 < p.a.dim_qk));
+        gt.store(row + e * STEP, unit, frag_of(g[e], keep && unit * 8 < p.a.dim_v));
       }
     }
   }
