@@ -17,10 +17,13 @@ namespace attn {
 namespace {
 
 template <class T, int D, int RW, int TK, int BUF, bool VEC>
-__global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
-  constexpr int P = planes<T>(), KS = D / 16;
-  __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kts[BUF], vts[BUF];
-  __shared__ __attribute__((aligned(16))) float bias[BUF][TK];
+__global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D) : 1) attn_bwd_q(Params p) {
+  constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
+  struct Buffer {
+    Tile<P, TK, D> k, v;
+    float bias[TK];
+  };
+  __shared__ __attribute__((aligned(16))) Buffer first, second;
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -34,7 +37,7 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
   if (r0 >= nrows) return;
 
   const int r = r0 + 32 * w + n;
-  const bool row = r < nrows;
+  const bool row = r < nrows, idle = r0 + 32 * w >= nrows;   // idle: a wave without rows only loads
   const int qi = q0 + (row ? query_of(p, r) : 0), head = c * p.group + (row ? r - (qi - q0) * p.group : 0);
   const long at = (long)qi * a.heads_q + head;
   float lse = p.lse[at];
@@ -43,12 +46,12 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
 
   const int kb = offset(a.k_ptr, g, a.num_k), ke = offset(a.k_ptr, g + 1, a.num_k);
   const int tiles = ke > kb ? (ke - kb + TK - 1) / TK : 0, per = (tiles + p.splits - 1) / p.splits;
-  int k0 = kb + min(split * per, tiles) * TK;
+  const int k0 = kb + min(split * per, tiles) * TK;
   const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
 
   Keys<T, D, TK, 64 * RW, VEC> keys;
   keys.begin(p, c, k0, k1);
-  if (k0 < k1) keys.load(p);
+  if (k0 < k1) keys.issue(p, first.k, first.v);
 
   Frag<P> q[KS], go[KS];
   const T* gp = (const T*)p.go + qi * p.go_row + head * p.go_head;
@@ -67,42 +70,49 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
   delta = live ? delta + other_half(delta) : 0.0f;
   if (row && h == 0 && split == 0) p.delta[at] = delta;
 
-  f32x16 less_delta;   // dP - delta from the start: -delta is the accumulator's first value
+  // dP - delta from the start: -delta is the accumulator's first value (where its 16
+  // registers do not cost a wave)
+  constexpr bool FOLD = D < 128;
+  f32x16 less_delta;
 #pragma unroll
   for (int i = 0; i < 16; ++i) less_delta[i] = -delta;
   f32x16 dq[D / 32];
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) dq[dt] = f32x16{};
 
-  for (int buf = 0; k0 < k1; k0 += TK, buf ^= BUF - 1) {
-    Tile<P, TK, D>&kt = kts[buf], &vt = vts[buf];
+  const auto use = [&](Buffer& now, int from, Buffer& next) {
+    Tile<P, TK, D>&kt = now.k, &vt = now.v;
     if (BUF == 1) __syncthreads();
-    keys.store(p, k0, kt, vt, bias[buf]);
+    keys.finish(p, from, kt, vt, now.bias);
     __syncthreads();
-    if (k0 + TK < k1) keys.load(p);
+    if (from + TK < k1) keys.issue(p, next.k, next.v);
+    if (idle) return;
 
 #pragma unroll
     for (int b = 0; b < TK / 32; ++b) {
-      f32x16 s = by_row(&bias[buf][32 * b], lane), dp = less_delta;
-#pragma unroll
-      for (int t = 0; t < KS; ++t) {
-        s = mma(kt.rows(32 * b, t, lane), q[t], s);
-        dp = mma(vt.rows(32 * b, t, lane), go[t], dp);
-      }
+      f32x16 s = by_row(now.bias + 32 * b, lane), dp = FOLD ? less_delta : f32x16{};
+      ahead<2 * KS, W, Frag<P>>(
+          [&](int i) { return i & 1 ? vt.rows(32 * b, i >> 1, lane) : kt.rows(32 * b, i >> 1, lane); },
+          [&](int i, const Frag<P>& x) {
+            if (i & 1) dp = mma(x, go[i >> 1], dp);
+            else s = mma(x, q[i >> 1], s);
+          });
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], p.c, -lse));
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = s[8 * t + i] * dp[8 * t + i];
+        for (int i = 0; i < 8; ++i) e[i] = s[8 * t + i] * (FOLD ? dp[8 * t + i] : dp[8 * t + i] - delta);
         Frag<P> f;   // bf16: dS rounded for its product
         to_frag(e, f);
-#pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) dq[dt] = mma(kt.columns(32 * b + 16 * t, dt, lane), f, dq[dt]);
+        ahead<D / 32, W, Frag<P>>([&](int dt) { return kt.columns(32 * b + 16 * t, dt, lane); },
+                                  [&](int dt, const Frag<P>& x) { dq[dt] = mma(x, f, dq[dt]); });
       }
     }
-  }
+  };
+  if constexpr (BUF == 2) walk<2, TK>(k0, k1, first, second, use);
+  else walk<1, TK>(k0, k1, first, first, use);
 
   if (!row) return;
   if (p.splits > 1) {
@@ -129,10 +139,13 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_q(Params p) {
 }
 
 template <class T, int D, int RW, int TQ, int BUF, bool VEC>
-__global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
-  constexpr int P = planes<T>(), KS = D / 16;
-  __shared__ __attribute__((aligned(16))) Tile<P, TQ, D> qts[BUF], gts[BUF];
-  __shared__ __attribute__((aligned(16))) float lse_b[BUF][TQ], delta_b[BUF][TQ];
+__global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D) : 1) attn_bwd_kv(Params p) {
+  constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
+  struct Buffer {
+    Tile<P, TQ, D> q, g;
+    float lse[TQ], delta[TQ];
+  };
+  __shared__ __attribute__((aligned(16))) Buffer first, second;
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -145,19 +158,19 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
   if (j0 >= ke) return;
 
   const int j = j0 + 32 * w + n;
-  const bool key = j < ke;
+  const bool key = j < ke, idle = j0 + 32 * w >= ke;   // idle: a wave without keys only loads
   const bool live = key && (!a.k_mask || a.k_mask[j]);
 
   // this split's rows: whole tiles of the graph's
   const int q0 = offset(a.q_ptr, g, a.num_q);
   const int nrows = (offset(a.q_ptr, g + 1, a.num_q) - q0) * p.group;
   const int tiles = nrows > 0 ? (nrows + TQ - 1) / TQ : 0, per = (tiles + p.splits - 1) / p.splits;
-  int r0 = min(split * per, tiles) * TQ;
+  const int r0 = min(split * per, tiles) * TQ;
   const int r1 = min(nrows, min((split + 1) * per, tiles) * TQ);
 
   Rows<T, D, TQ, 64 * RW, VEC> rows;
   rows.begin(p, c, q0, r0, r1);
-  if (r0 < r1) rows.load(p);
+  if (r0 < r1) rows.issue(p, first.q, first.g);
 
   Frag<P> k[KS], v[KS];
   const int jr = key ? j : j0;
@@ -171,23 +184,25 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) dk[dt] = dv[dt] = f32x16{};
 
-  for (int buf = 0; r0 < r1; r0 += TQ, buf ^= BUF - 1) {
-    Tile<P, TQ, D>&qt = qts[buf], &gt = gts[buf];
+  const auto use = [&](Buffer& now, int from, Buffer& next) {
+    Tile<P, TQ, D>&qt = now.q, &gt = now.g;
     if (BUF == 1) __syncthreads();
-    rows.store(p, r0, qt, gt, lse_b[buf], delta_b[buf]);
+    rows.finish(p, from, qt, gt, now.lse, now.delta);
     __syncthreads();
-    if (r0 + TQ < r1) rows.load(p);
+    if (from + TQ < r1) rows.issue(p, next.q, next.g);
+    if (idle) return;
 
 #pragma unroll
     for (int b = 0; b < TQ / 32; ++b) {
       // dP - delta from the start: the rows' -delta are the accumulator's first values
-      f32x16 s = f32x16{}, dp = by_row(&delta_b[buf][32 * b], lane);
-#pragma unroll
-      for (int t = 0; t < KS; ++t) {
-        s = mma(qt.rows(32 * b, t, lane), k[t], s);
-        dp = mma(gt.rows(32 * b, t, lane), v[t], dp);
-      }
-      const f32x16 ls = by_row(&lse_b[buf][32 * b], lane);
+      f32x16 s = f32x16{}, dp = by_row(now.delta + 32 * b, lane);
+      ahead<2 * KS, W, Frag<P>>(
+          [&](int i) { return i & 1 ? gt.rows(32 * b, i >> 1, lane) : qt.rows(32 * b, i >> 1, lane); },
+          [&](int i, const Frag<P>& x) {
+            if (i & 1) dp = mma(x, v[i >> 1], dp);
+            else s = mma(x, k[i >> 1], s);
+          });
+      const f32x16 ls = by_row(now.lse + 32 * b, lane);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], p.c, -ls[i]));
@@ -196,20 +211,26 @@ __global__ void __launch_bounds__(64 * RW) attn_bwd_kv(Params p) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float e[8];
-        Frag<P> f;   // bf16: P and dS rounded for their products
+        Frag<P> f[2];   // bf16: P and dS rounded for their products
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = s[8 * t + i];
-        to_frag(e, f);
-#pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) dv[dt] = mma(gt.columns(32 * b + 16 * t, dt, lane), f, dv[dt]);
+        to_frag(e, f[0]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = dp[8 * t + i];
-        to_frag(e, f);
-#pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) dk[dt] = mma(qt.columns(32 * b + 16 * t, dt, lane), f, dk[dt]);
+        to_frag(e, f[1]);
+        ahead<D / 16, W, Frag<P>>(
+            [&](int i) {
+              return i & 1 ? qt.columns(32 * b + 16 * t, i >> 1, lane) : gt.columns(32 * b + 16 * t, i >> 1, lane);
+            },
+            [&](int i, const Frag<P>& x) {
+              if (i & 1) dk[i >> 1] = mma(x, f[1], dk[i >> 1]);
+              else dv[i >> 1] = mma(x, f[0], dv[i >> 1]);
+            });
       }
     }
-  }
+  };
+  if constexpr (BUF == 2) walk<2, TQ>(r0, r1, first, second, use);
+  else walk<1, TQ>(r0, r1, first, first, use);
 
   if (!key) return;
   if (p.splits > 1) {
@@ -290,49 +311,43 @@ hipError_t sum(const Params& p, long rows, int width, int from, int dim, int hea
   return hipGetLastError();
 }
 
-struct Shape {
-  int rw, slots, splits;
-};
-
-// As the forward's: four waves share a tile of the other axis where that fills the chip, and
-// the other axis is split while there are fewer than four waves per compute unit.
-Shape shape_of(long rows, long others, long graphs, int heads, int tables) {
-  graphs = graphs > 0 ? graphs : 1;
-  const long avg = (rows + graphs - 1) / graphs, avg_o = (others + graphs - 1) / graphs;
-  const auto tiles = [&](int rw) { return graphs * ((avg + 32 * rw - 1) / (32 * rw)) * heads; };
-  Shape s;
-  s.rw = tiles(4) >= 256 ? 4 : 1;
-  s.slots = (int)(rows / (32 * s.rw) + tables);
-  const long waves = tiles(s.rw) * s.rw, most = (avg_o + 127) / 128, want = waves > 0 ? 1024 / waves : 1;
-  s.splits = (int)(want < most ? want : most);
-  if (s.splits > 256) s.splits = 256;
-  if (s.splits < 1) s.splits = 1;
-  return s;
-}
 Shape shape_q(const e3conv_attention_args& a) {
-  return shape_of(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv, a.num_graphs);
+  const bool f32 = a.dtype == E3CONV_F32;
+  const int dim = a.dim_qk > a.dim_v ? a.dim_qk : a.dim_v;
+  return choose(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv,
+                waves_bwd(f32, padded(dim)), unit_us(f32, dim, true), a.dim_qk);
 }
 Shape shape_kv(const e3conv_attention_args& a) {
-  return shape_of(a.num_k, a.num_q * (a.heads_q / a.heads_kv), a.num_graphs, a.heads_kv, a.num_graphs);
+  const bool f32 = a.dtype == E3CONV_F32;
+  const int dim = a.dim_qk > a.dim_v ? a.dim_qk : a.dim_v;
+  return choose(a.num_k, a.num_q * (a.heads_q / a.heads_kv), a.num_graphs, a.heads_kv,
+                waves_kv(f32, padded(dim)), unit_us(f32, dim, true), a.dim_qk + a.dim_v);
 }
 
 size_t delta_bytes(const e3conv_attention_args& a) {
   return ((size_t)a.num_q * a.heads_q * sizeof(float) + 15) / 16 * 16;
 }
 
+// Rows of a tile and buffers: 64 and two where they fit 64 KiB of LDS and the registers of two
+// waves a SIMD.
+template <class T, int D, bool VEC>
+struct Tiling {
+  static constexpr int ROWS = D == 128 ? 32 : 64;
+  static constexpr int BUF4 = 2 * ROWS * planes<T>() * D * 2 * 2 <= 65536 ? 2 : 1;
+  static constexpr int BUF1 = sizeof(T) == 2 && VEC ? 2 : 1;
+};
 template <class T, int D, bool VEC>
 void launch_q(const Params& p, int rw, unsigned grid, hipStream_t s) {
-  constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
-  constexpr int BUF4 = planes<T>() * TK4 * D * 2 * 2 * 2 <= 65536 ? 2 : 1;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_q<T, D, 4, TK4, BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_q<T, D, 1, 32, 1, VEC>), dim3(grid), dim3(64), 0, s, p);
+  typedef Tiling<T, D, VEC> L;
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_q<T, D, 4, L::ROWS, L::BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_q<T, D, 1, 32, L::BUF1, VEC>), dim3(grid), dim3(64), 0, s, p);
 }
 template <class T, int D, bool VEC>
 void launch_kv(const Params& p, int rw, unsigned grid, hipStream_t s) {
-  constexpr int TQ4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
-  constexpr int BUF4 = planes<T>() * TQ4 * D * 2 * 2 * 2 < 65536 ? 2 : 1;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_kv<T, D, 4, TQ4, BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_kv<T, D, 1, 32, 1, VEC>), dim3(grid), dim3(64), 0, s, p);
+  typedef Tiling<T, D, VEC> L;
+  constexpr int ROWS = sizeof(T) == 2 ? 64 : L::ROWS;
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_kv<T, D, 4, ROWS, L::BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_kv<T, D, 1, 32, L::BUF1, VEC>), dim3(grid), dim3(64), 0, s, p);
 }
 template <class T, int D>
 void launch_q(const Params& p, int rw, unsigned grid, hipStream_t s) {

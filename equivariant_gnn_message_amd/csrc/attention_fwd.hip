@@ -16,10 +16,13 @@ namespace attn {
 namespace {
 
 template <class T, int D, int RW, int TK, int BUF, bool VEC>
-__global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
-  constexpr int P = planes<T>(), KS = D / 16;
-  __shared__ __attribute__((aligned(16))) Tile<P, TK, D> kts[BUF], vts[BUF];
-  __shared__ __attribute__((aligned(16))) float bias[BUF][TK];
+__global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D) : 1) attn_fwd(Params p) {
+  constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
+  struct Buffer {
+    Tile<P, TK, D> k, v;
+    float bias[TK];
+  };
+  __shared__ __attribute__((aligned(16))) Buffer first, second;
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -34,19 +37,19 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
   if (r0 >= nrows) return;
 
   const int r = r0 + 32 * w + n;
-  const bool row = r < nrows;
+  const bool row = r < nrows, idle = r0 + 32 * w >= nrows;   // idle: a wave without rows only loads
   const int qi = q0 + (row ? query_of(p, r) : 0), head = c * p.group + (row ? r - (qi - q0) * p.group : 0);
   const bool live = row && (!a.q_mask || a.q_mask[qi]);
 
   // this split's keys: whole tiles of the graph's
   const int kb = offset(a.k_ptr, g, a.num_k), ke = offset(a.k_ptr, g + 1, a.num_k);
   const int tiles = ke > kb ? (ke - kb + TK - 1) / TK : 0, per = (tiles + p.splits - 1) / p.splits;
-  int k0 = kb + min(split * per, tiles) * TK;
+  const int k0 = kb + min(split * per, tiles) * TK;
   const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
 
   Keys<T, D, TK, 64 * RW, VEC> keys;
   keys.begin(p, c, k0, k1);
-  if (k0 < k1) keys.load(p);
+  if (k0 < k1) keys.issue(p, first.k, first.v);
 
   Frag<P> q[KS];
   row_operand<T, D, VEC>((const T*)a.q + qi * a.q_row + head * a.q_head, a.dim_qk, live, q);
@@ -59,21 +62,20 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
   for (int dt = 0; dt < D / 32; ++dt) o[dt] = f32x16{};
   float m = -INFINITY, l = 0.0f;   // of the logits in units of log 2; l: this half's keys
 
-  // two buffers: one barrier a tile, the store of a tile behind the products of the one before
-  for (int buf = 0; k0 < k1; k0 += TK, buf ^= BUF - 1) {
-    Tile<P, TK, D>&kt = kts[buf], &vt = vts[buf];
+  const auto use = [&](Buffer& now, int from, Buffer& next) {
+    Tile<P, TK, D>&kt = now.k, &vt = now.v;
     if (BUF == 1) __syncthreads();
-    keys.store(p, k0, kt, vt, bias[buf]);
+    keys.finish(p, from, kt, vt, now.bias);
     __syncthreads();
-    if (k0 + TK < k1) keys.load(p);
+    if (from + TK < k1) keys.issue(p, next.k, next.v);
+    if (idle) return;
 
     f32x16 s[TK / 32];
+    constexpr int NB = TK / 32;
 #pragma unroll
-    for (int b = 0; b < TK / 32; ++b) {
-      s[b] = by_row(&bias[buf][32 * b], lane);
-#pragma unroll
-      for (int t = 0; t < KS; ++t) s[b] = mma(kt.rows(32 * b, t, lane), q[t], s[b]);
-    }
+    for (int b = 0; b < NB; ++b) s[b] = by_row(now.bias + 32 * b, lane);
+    ahead<NB * KS, W, Frag<P>>([&](int i) { return kt.rows(32 * (i % NB), i / NB, lane); },
+                               [&](int i, const Frag<P>& x) { s[i % NB] = mma(x, q[i / NB], s[i % NB]); });
     float top = s[0][0];
 #pragma unroll
     for (int b = 0; b < TK / 32; ++b)
@@ -104,10 +106,12 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
         // bf16: P rounded for its product, the sum l from the unrounded values
         Frag<P> f;
         to_frag(e, f);
-#pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) o[dt] = mma(vt.columns(32 * b + 16 * t, dt, lane), f, o[dt]);
+        ahead<D / 32, W, Frag<P>>([&](int dt) { return vt.columns(32 * b + 16 * t, dt, lane); },
+                                  [&](int dt, const Frag<P>& x) { o[dt] = mma(x, f, o[dt]); });
       }
-  }
+  };
+  if constexpr (BUF == 2) walk<2, TK>(k0, k1, first, second, use);
+  else walk<1, TK>(k0, k1, first, first, use);
 
   l += other_half(l);
   if (!row) return;
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(64 * RW) attn_fwd(Params p) {
 // Joins the splits of one row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  Sixteen
 // waves take the splits in turn, so that their rows are all in flight at once: the time is
 // that of a few dependent reads (the loop of one wave over 64 splits took 20 us).
-constexpr int kMaxSplits = 512, kJoinWaves = 16;
+constexpr int kJoinWaves = 16;
 template <class T>
 __global__ void __launch_bounds__(64 * kJoinWaves) attn_join(Params p) {
   const e3conv_attention_args& a = p.a;
@@ -206,35 +210,20 @@ __global__ void __launch_bounds__(64 * kJoinWaves) attn_join(Params p) {
   if (tid == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-struct Shape {
-  int rw, slots, splits;
-};
-
-// Waves per work-group and splits of the keys.  Four waves share each tile of keys
-// where that fills the chip, else one wave per work-group; and the keys are
-// split while there are fewer than four waves per compute unit and a split keeps two
-// tiles.  Graph lengths are on the device: their average stands for them.
 Shape shape_of(const e3conv_attention_args& a) {
-  const long rows = a.num_q * (a.heads_q / a.heads_kv), graphs = a.num_graphs > 0 ? a.num_graphs : 1;
-  const long avg_r = (rows + graphs - 1) / graphs, avg_k = (a.num_k + graphs - 1) / graphs;
-  const auto tiles = [&](int rw) { return graphs * ((avg_r + 32 * rw - 1) / (32 * rw)) * a.heads_kv; };
-  Shape s;
-  s.rw = tiles(4) >= 256 ? 4 : 1;
-  s.slots = (int)(rows / (32 * s.rw) + a.num_graphs);
-  const long waves = tiles(s.rw) * s.rw, most = (avg_k + 127) / 128, want = waves > 0 ? 1024 / waves : 1;
-  s.splits = (int)(want < most ? want : most);
-  if (s.splits > kMaxSplits) s.splits = kMaxSplits;
-  if (s.splits < 1) s.splits = 1;
-  return s;
+  const bool f32 = a.dtype == E3CONV_F32;
+  const int dim = a.dim_qk > a.dim_v ? a.dim_qk : a.dim_v;
+  return choose(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv,
+                waves_fwd(f32, padded(dim)), unit_us(f32, dim, false), a.dim_v);
 }
 
 // LDS: the tiles of both buffers, at most 64 KiB (two work-groups of a compute unit).
 template <class T, int D, bool VEC>
 void launch(const Params& p, int rw, unsigned grid, hipStream_t s) {
-  constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64;
-  constexpr int BUF4 = planes<T>() * TK4 * D * 2 * 2 * 2 <= 65536 ? 2 : 1;
+  constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64, TILE = planes<T>() * D * 2 * 2;
+  constexpr int BUF4 = 2 * TK4 * TILE <= 65536 ? 2 : 1, BUF1 = sizeof(T) == 2 && VEC ? 2 : 1;
   if (rw == 4) hipLaunchKernelGGL((attn_fwd<T, D, 4, TK4, BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_fwd<T, D, 1, 32, 1, VEC>), dim3(grid), dim3(64), 0, s, p);
+  else hipLaunchKernelGGL((attn_fwd<T, D, 1, 32, BUF1, VEC>), dim3(grid), dim3(64), 0, s, p);
 }
 template <class T, int D>
 void launch(const Params& p, int rw, unsigned grid, hipStream_t s) {

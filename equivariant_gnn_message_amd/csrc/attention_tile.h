@@ -276,43 +276,103 @@ __device__ __forceinline__ int query_of(const Params& p, int r) {
   return p.group == 1 ? r : (int)(__umulhi((unsigned)r, p.magic) >> p.shift);
 }
 
-// The tiles of the keys of one kv head, ROWS at a time, from memory through registers to
-// LDS.  load() only issues the loads of the next tile (rows beyond the last key read
-// the last one); store() writes them with zeros in place of masked keys, of those beyond
-// the end and of dimensions beyond dim, whatever memory holds there, and the
-// starting value of each key's logits: 0, or -infinity for a key that is not seen.
+// A work-group's loads of a tile of ROWS rows of two operands that share their row order (k and
+// v, or q and grad_out): issue() starts them, finish() leaves the tile in LDS, with zeros
+// in place of the rows that do not count, whatever memory holds there (the caller
+// waits at a barrier after it).  bf16 rows of whole units go from memory to LDS by
+// themselves, the lane's unit chosen so that the tile's permutation comes out; dimensions
+// beyond dim then hold the row's first unit, and meet zeros in the other operand or
+// rows of the result that are not stored.  Others pass through registers: fp32 is split on
+// the way.
+template <class T, int D, int ROWS, int NT, bool VEC>
+struct Pair {
+  static constexpr int P = planes<T>(), U = D / 8, E = ROWS * U / NT, STEP = NT / U;
+  static constexpr bool DMA = sizeof(T) == 2 && VEC;
+  typedef Tile<P, ROWS, D> TileT;
+  static_assert(ROWS * U % NT == 0 && ROWS <= 64, "");
+  Raw<T> x[DMA ? 1 : E], y[DMA ? 1 : E];
+
+  static __device__ __forceinline__ int row(int e) { return (int)threadIdx.x / U + e * STEP; }
+  static __device__ __forceinline__ int unit(int e) {
+    const int slot = threadIdx.x % U;
+    return DMA ? slot ^ TileT::swizzle(row(e)) : slot;
+  }
+  // The rows at xp and yp are row e of this thread's.
+  __device__ __forceinline__ void issue(int e, const T* xp, const T* yp, int dim_x, int dim_y, TileT& xt, TileT& yt) {
+    const int d = unit(e) * 8;
+    if constexpr (DMA) {
+      typedef const __attribute__((address_space(1))) void* from;
+      typedef __attribute__((address_space(3))) void* to;
+      const int at = e * NT + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63);   // the wave's first unit
+      __builtin_amdgcn_global_load_lds((from)(xp + (d < dim_x ? d : 0)), (to)&xt.u[0][at], 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((from)(yp + (d < dim_y ? d : 0)), (to)&yt.u[0][at], 16, 0, 0);
+    } else {
+      x[e] = fetch8<VEC>(xp, d, dim_x);
+      y[e] = fetch8<VEC>(yp, d, dim_y);
+    }
+  }
+  // seen: a bit for each row of the tile that counts.
+  __device__ __forceinline__ void finish(unsigned long seen, int dim_x, int dim_y, TileT& xt, TileT& yt) const {
+    const bool whole = seen == (ROWS == 64 ? ~0ul : (1ul << (ROWS & 63)) - 1);
+    if constexpr (DMA) {
+      arrive();
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (!(seen >> row(e) & 1)) {      // a unit that this thread has loaded itself
+            xt.u[0][e * NT + threadIdx.x] = bf16x8{};
+            yt.u[0][e * NT + threadIdx.x] = bf16x8{};
+          }
+      }
+    } else if (whole && (!VEC || (dim_x == D && dim_y == D))) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        xt.store(row(e), unit(e), frag_of(x[e], true));
+        yt.store(row(e), unit(e), frag_of(y[e], true));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const bool keep = seen >> row(e) & 1;
+        xt.store(row(e), unit(e), frag_of(x[e], keep && unit(e) * 8 < dim_x));
+        yt.store(row(e), unit(e), frag_of(y[e], keep && unit(e) * 8 < dim_y));
+      }
+    }
+  }
+  // Waits until all loads that this wave has issued are there.
+  static __device__ __forceinline__ void arrive() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
+};
+
+// The tiles of the keys of one kv head, and the starting value of each key's logits: 0, or
+// -infinity for a key that is not seen.  Rows beyond the last key read the last one.
 template <class T, int D, int ROWS, int NT, bool VEC>
 struct Keys {
-  static constexpr int P = planes<T>(), U = D / 8, E = ROWS * U / NT, STEP = NT / U;
-  static_assert(ROWS * U % NT == 0 && ROWS <= 64, "");
-  Raw<T> k[E], v[E];
+  typedef Pair<T, D, ROWS, NT, VEC> PairT;
+  typedef typename PairT::TileT TileT;
+  PairT pair;
   unsigned char m;
   const T *kp, *vp;      // this thread's first row of the next tile
   int next, end;         // keys of this work-group not yet loaded
 
   __device__ __forceinline__ void begin(const Params& p, int c, int k0, int k1) {
     const e3conv_attention_args& a = p.a;
-    const long j = k0 + (int)threadIdx.x / U;
+    const long j = k0 + PairT::row(0);
     kp = (const T*)a.k + c * a.k_head + j * a.k_row;
     vp = (const T*)a.v + c * a.v_head + j * a.v_row;
     next = k0;
     end = k1;
   }
-  __device__ __forceinline__ void load(const Params& p) {
+  __device__ __forceinline__ void issue(const Params& p, TileT& kt, TileT& vt) {
     const e3conv_attention_args& a = p.a;
-    const int d = threadIdx.x % U * 8;
     if (next + ROWS <= end) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        k[e] = fetch8<VEC>(kp + e * STEP * a.k_row, d, a.dim_qk);
-        v[e] = fetch8<VEC>(vp + e * STEP * a.v_row, d, a.dim_v);
-      }
+      for (int e = 0; e < PairT::E; ++e)
+        pair.issue(e, kp + e * PairT::STEP * a.k_row, vp + e * PairT::STEP * a.v_row, a.dim_qk, a.dim_v, kt, vt);
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int back = min(end - 1 - (next + (int)threadIdx.x / U), e * STEP);
-        k[e] = fetch8<VEC>(kp + back * a.k_row, d, a.dim_qk);
-        v[e] = fetch8<VEC>(vp + back * a.v_row, d, a.dim_v);
+      for (int e = 0; e < PairT::E; ++e) {
+        const int back = min(end - 1 - (next + PairT::row(0)), e * PairT::STEP);
+        pair.issue(e, kp + back * a.k_row, vp + back * a.v_row, a.dim_qk, a.dim_v, kt, vt);
       }
     }
     if (a.k_mask) m = a.k_mask[min(next + (int)(threadIdx.x & 63), end - 1)];
@@ -320,39 +380,23 @@ struct Keys {
     vp += ROWS * a.v_row;
     next += ROWS;
   }
-  // k0: the first key of the loaded tile.
-  __device__ __forceinline__ void store(const Params& p, int k0, Tile<P, ROWS, D>& kt, Tile<P, ROWS, D>& vt,
-                                        float* bias) const {
-    const int unit = threadIdx.x % U, row = threadIdx.x / U, lane = threadIdx.x & 63;
+  // k0: the first key of the issued tile.
+  __device__ __forceinline__ void finish(const Params& p, int k0, TileT& kt, TileT& vt, float* bias) const {
+    const int lane = threadIdx.x & 63;
     const bool sees = lane < ROWS && k0 + lane < end && (!p.a.k_mask || m);
-    const unsigned long seen = __ballot(sees);
     if (threadIdx.x < ROWS) bias[lane] = sees ? 0.0f : -INFINITY;
-    if (seen == (ROWS == 64 ? ~0ul : (1ul << (ROWS & 63)) - 1) && (!VEC || (p.a.dim_qk == D && p.a.dim_v == D))) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        kt.store(row + e * STEP, unit, frag_of(k[e], true));
-        vt.store(row + e * STEP, unit, frag_of(v[e], true));
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const bool keep = seen >> (row + e * STEP) & 1;
-        kt.store(row + e * STEP, unit, frag_of(k[e], keep && unit * 8 < p.a.dim_qk));
-        vt.store(row + e * STEP, unit, frag_of(v[e], keep && unit * 8 < p.a.dim_v));
-      }
-    }
+    pair.finish(__ballot(sees), p.a.dim_qk, p.a.dim_v, kt, vt);
   }
 };
 
 // The tiles of the rows (queries and their heads of one kv head) that a work-group of the
-// reverse pass walks over: q and grad_out as Keys does k and v, and each row's lse
-// (base 2) and -delta.  A row that sees no key or lies beyond the end is stored as zeros
-// with lse = +infinity, which makes its P zero.
+// reverse pass walks over, and each row's lse (base 2) and -delta.  A row that sees no key
+// or lies beyond the end has lse = +infinity, which makes its P zero.
 template <class T, int D, int ROWS, int NT, bool VEC>
 struct Rows {
-  static constexpr int P = planes<T>(), U = D / 8, E = ROWS * U / NT, STEP = NT / U;
-  static_assert(ROWS * U % NT == 0 && ROWS <= 64, "");
-  Raw<T> q[E], g[E];
+  typedef Pair<T, D, ROWS, NT, VEC> PairT;
+  typedef typename PairT::TileT TileT;
+  PairT pair;
   float lse, delta;
   unsigned char m;
   const T *qb, *gb;      // the kv head's first row of the graph
@@ -368,29 +412,25 @@ struct Rows {
     at0 = (long)q0 * a.heads_q + c * p.group;
     next = r0;
     end = r1;
-    const int r = r0 + (int)threadIdx.x / U, i = query_of(p, r), x = r - i * p.group;
+    const int r = r0 + PairT::row(0), i = query_of(p, r), x = r - i * p.group;
     qp = qb + i * a.q_row + x * a.q_head;
     gp = gb + i * p.go_row + x * p.go_head;
   }
-  __device__ __forceinline__ void load(const Params& p) {
+  __device__ __forceinline__ void issue(const Params& p, TileT& qt, TileT& gt) {
     const e3conv_attention_args& a = p.a;
-    const int d = threadIdx.x % U * 8;
     // STEP rows on lie STEP / group queries on where the heads of a group divide STEP
-    const int by = STEP >> p.group_log2;
-    if (next + ROWS <= end && p.group_log2 >= 0 && by << p.group_log2 == STEP) {
+    const int by = PairT::STEP >> p.group_log2;
+    if (next + ROWS <= end && p.group_log2 >= 0 && by << p.group_log2 == PairT::STEP) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        q[e] = fetch8<VEC>(qp + e * by * a.q_row, d, a.dim_qk);
-        g[e] = fetch8<VEC>(gp + e * by * p.go_row, d, a.dim_v);
-      }
-      qp += E * by * a.q_row;
-      gp += E * by * p.go_row;
+      for (int e = 0; e < PairT::E; ++e)
+        pair.issue(e, qp + e * by * a.q_row, gp + e * by * p.go_row, a.dim_qk, a.dim_v, qt, gt);
+      qp += PairT::E * by * a.q_row;
+      gp += PairT::E * by * p.go_row;
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int r = min(next + (int)threadIdx.x / U + e * STEP, end - 1), i = query_of(p, r), x = r - i * p.group;
-        q[e] = fetch8<VEC>(qb + i * a.q_row + x * a.q_head, d, a.dim_qk);
-        g[e] = fetch8<VEC>(gb + i * p.go_row + x * p.go_head, d, a.dim_v);
+      for (int e = 0; e < PairT::E; ++e) {
+        const int r = min(next + PairT::row(e), end - 1), i = query_of(p, r), x = r - i * p.group;
+        pair.issue(e, qb + i * a.q_row + x * a.q_head, gb + i * p.go_row + x * p.go_head, a.dim_qk, a.dim_v, qt, gt);
       }
     }
     const int r = min(next + (int)(threadIdx.x & 63), end - 1), i = query_of(p, r);
@@ -400,32 +440,36 @@ struct Rows {
     if (a.q_mask) m = a.q_mask[q0 + i];
     next += ROWS;
   }
-  // r0: the first row of the loaded tile.
-  __device__ __forceinline__ void store(const Params& p, int r0, Tile<P, ROWS, D>& qt, Tile<P, ROWS, D>& gt,
-                                        float* lse_of, float* delta_of) const {
-    const int unit = threadIdx.x % U, row = threadIdx.x / U, lane = threadIdx.x & 63;
+  // r0: the first row of the issued tile.
+  __device__ __forceinline__ void finish(const Params& p, int r0, TileT& qt, TileT& gt, float* lse_of,
+                                         float* delta_of) const {
+    const int lane = threadIdx.x & 63;
     const bool sees = lane < ROWS && r0 + lane < end && lse != -INFINITY && (!p.a.q_mask || m);
-    const unsigned long seen = __ballot(sees);
     if (threadIdx.x < ROWS) {
       lse_of[lane] = sees ? lse * kLog2e : INFINITY;
       delta_of[lane] = sees ? -delta : 0.0f;
     }
-    if (seen == (ROWS == 64 ? ~0ul : (1ul << (ROWS & 63)) - 1) && (!VEC || (p.a.dim_qk == D && p.a.dim_v == D))) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        qt.store(row + e * STEP, unit, frag_of(q[e], true));
-        gt.store(row + e * STEP, unit, frag_of(g[e], true));
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const bool keep = seen >> (row + e * STEP) & 1;
-        qt.store(row + e * STEP, unit, frag_of(q[e], keep && unit * 8 < p.a.dim_qk));
-        gt.store(row + e * STEP, unit, frag_of(g[e], keep && unit * 8 < p.a.dim_v));
-      }
-    }
+    pair.finish(__ballot(sees), p.a.dim_qk, p.a.dim_v, qt, gt);
   }
 };
+
+// Walks over the tiles of [from, to), STEP rows each: start(buffer) issues a tile's loads,
+// use(buffer, first row, next buffer) has it finished and used; the next tile's loads are
+// issued after the barrier that follows finish.  Two buffers need one barrier a tile; they
+// are separate variables, so that the compiler knows the loads in flight from the
+// reads of the other one.
+template <int BUF, int STEP, class Buffer, class Use>
+__device__ __forceinline__ void walk(int from, int to, Buffer& a, Buffer& b, Use use) {
+  while (from < to) {
+    use(a, from, b);
+    from += STEP;
+    if (BUF == 2) {
+      if (from >= to) break;
+      use(b, from, a);
+      from += STEP;
+    }
+  }
+}
 
 // Values of 32 rows from LDS where an accumulator has them: register i is row 8 (i / 4) +
 // 4 h + i % 4.
@@ -467,7 +511,77 @@ __device__ __forceinline__ void store4(T* p, int d, int dim, const float (&v)[4]
   }
 }
 
-// Launchers.  tile sizes and splits are in the parameters.
+// use(i, load(i)) for i < N, the loads W steps ahead of their use.  The fences keep loads
+// and products in this order (vector instructions may pass): left alone, the compiler
+// puts each LDS read right before its product, and every product waits for its read.
+template <int N, int W, class F, class Load, class Use>
+__device__ __forceinline__ void ahead(Load load, Use use) {
+  F ring[W];
+#pragma unroll
+  for (int i = 0; i < W && i < N; ++i) ring[i] = load(i);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_barrier(0x6);
+    use(i, ring[i % W]);
+    if (i + W < N) ring[i % W] = load(i + W);
+  }
+  __builtin_amdgcn_sched_barrier(0x6);
+}
+
+// ------------------------------------------------------------ launch shapes ---
+
+// Waves of a SIMD that the registers are kept to: with one, nothing covers the latency of LDS
+// and the barriers.  Forward; the reverse kernels hold twice the operands.
+constexpr int waves_fwd(bool f32, int d) { return f32 ? (d == 32 ? 3 : d == 64 ? 2 : 1) : (d == 32 ? 4 : d == 64 ? 3 : 2); }
+constexpr int waves_bwd(bool f32, int d) { return f32 ? (d == 32 ? 2 : 1) : (d == 32 ? 3 : 2); }
+constexpr int waves_kv(bool f32, int d) { return f32 ? (d == 32 ? 2 : 1) : (d == 32 ? 3 : d == 64 ? 2 : 1); }
+
+constexpr int kMaxSplits = 512;
+inline int padded(int dim) { return dim <= 32 ? 32 : dim <= 64 ? 64 : 128; }   // of the tiles
+
+struct Shape {
+  int rw;        // waves of a work-group, 32 rows each
+  int slots;     // its row tiles: rows / (32 rw) + graphs
+  int splits;    // ranges of the other axis
+};
+
+// Work-groups of four waves share each tile of the other axis where a graph has more than 64
+// rows (of a graph of 64 rows two of the four would idle), else of one wave.  The other
+// axis is split where the row tiles leave compute units idle, in the first round of
+// work-groups or the last (628 work-groups on 512 places: 2 rounds; split in four 5 rounds of a
+// quarter each).  The choice minimises the time estimated from `unit`, the us of one
+// work-group for one row of the other axis (measured, below), and the partial results'
+// bytes.  Lengths are on the device: averages stand for them.
+inline Shape choose(long rows, long others, int graphs, int heads, int waves, double unit, int width) {
+  const long g = graphs > 0 ? graphs : 1, avg = (rows + g - 1) / g, avg_o = (others + g - 1) / g;
+  Shape s;
+  s.rw = avg > 64 ? 4 : 1;
+  s.slots = (int)(rows / (32 * s.rw) + graphs);
+  const long n = g * ((avg + 32 * s.rw - 1) / (32 * s.rw)) * heads;
+  const long places = 256 * (s.rw == 4 ? waves : 4);
+  long most = (avg_o + 127) / 128;
+  if (most > kMaxSplits) most = kMaxSplits;
+  double best = 1e30;
+  s.splits = 1;
+  for (long k = 1; k <= most; ++k) {
+    const long rounds = (n * k + places - 1) / places;
+    const double join = k > 1 ? 5.0 + (double)k * rows * heads * width * 8e-6 / 3.0 : 0.0;
+    const double us = rounds * (double)avg_o / k * unit + join;
+    if (us < 0.95 * best) {
+      best = us;
+      s.splits = (int)k;
+    }
+  }
+  return s;
+}
+// us of a work-group for one key (forward) or one row or key (reverse), with its
+// neighbours on the compute unit: bf16, 64 dimensions, 0.04; three products more and fp32's
+// six-fold products in proportion to what was measured.
+inline double unit_us(bool f32, int dim, bool backward) {
+  return 0.04 * (dim <= 32 ? 0.7 : dim <= 64 ? 1.0 : 2.0) * (f32 ? 1.7 : 1.0) * (backward ? 1.5 : 1.0);
+}
+
+// Launchers.
 hipError_t launch_forward(const Params& p, hipStream_t s);
 hipError_t launch_backward(const Params& p, hipStream_t s);
 size_t forward_workspace(const e3conv_attention_args& a);
