@@ -297,18 +297,25 @@ struct Pair {
     const int slot = threadIdx.x % U;
     return DMA ? slot ^ TileT::swizzle(row(e)) : slot;
   }
-  // The rows at xp and yp are row e of this thread's.
-  __device__ __forceinline__ void issue(int e, const T* xp, const T* yp, int dim_x, int dim_y, TileT& xt, TileT& yt) {
+  // First element of this thread's unit of row e, as far as the row has it.
+  static __device__ __forceinline__ int first(int e, int dim) {
     const int d = unit(e) * 8;
+    return DMA && d >= dim ? 0 : d;
+  }
+  // Whether all rows of a thread have the same unit (their numbers differ by multiples of 16).
+  static constexpr bool SAME = !DMA || STEP % 16 == 0;
+  // xp and yp: this thread's unit of its row e.
+  __device__ __forceinline__ void issue(int e, const T* xp, const T* yp, int dim_x, int dim_y, TileT& xt, TileT& yt) {
     if constexpr (DMA) {
       typedef const __attribute__((address_space(1))) void* from;
       typedef __attribute__((address_space(3))) void* to;
       const int at = e * NT + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63);   // the wave's first unit
-      __builtin_amdgcn_global_load_lds((from)(xp + (d < dim_x ? d : 0)), (to)&xt.u[0][at], 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((from)(yp + (d < dim_y ? d : 0)), (to)&yt.u[0][at], 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((from)xp, (to)&xt.u[0][at], 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((from)yp, (to)&yt.u[0][at], 16, 0, 0);
     } else {
-      x[e] = fetch8<VEC>(xp, d, dim_x);
-      y[e] = fetch8<VEC>(yp, d, dim_y);
+      const int d = unit(e) * 8;
+      x[e] = fetch8<VEC>(xp - d, d, dim_x);
+      y[e] = fetch8<VEC>(yp - d, d, dim_y);
     }
   }
   // seen: a bit for each row of the tile that counts.
@@ -351,28 +358,33 @@ struct Keys {
   typedef typename PairT::TileT TileT;
   PairT pair;
   unsigned char m;
-  const T *kp, *vp;      // this thread's first row of the next tile
+  const T *kp, *vp;      // this thread's unit of its first row of the next tile
   int next, end;         // keys of this work-group not yet loaded
 
   __device__ __forceinline__ void begin(const Params& p, int c, int k0, int k1) {
     const e3conv_attention_args& a = p.a;
     const long j = k0 + PairT::row(0);
-    kp = (const T*)a.k + c * a.k_head + j * a.k_row;
-    vp = (const T*)a.v + c * a.v_head + j * a.v_row;
+    kp = (const T*)a.k + c * a.k_head + j * a.k_row + PairT::first(0, a.dim_qk);
+    vp = (const T*)a.v + c * a.v_head + j * a.v_row + PairT::first(0, a.dim_v);
     next = k0;
     end = k1;
+  }
+  static __device__ __forceinline__ int shift(int e, int dim) {
+    return PairT::SAME ? 0 : PairT::first(e, dim) - PairT::first(0, dim);
   }
   __device__ __forceinline__ void issue(const Params& p, TileT& kt, TileT& vt) {
     const e3conv_attention_args& a = p.a;
     if (next + ROWS <= end) {
 #pragma unroll
       for (int e = 0; e < PairT::E; ++e)
-        pair.issue(e, kp + e * PairT::STEP * a.k_row, vp + e * PairT::STEP * a.v_row, a.dim_qk, a.dim_v, kt, vt);
+        pair.issue(e, kp + (e * PairT::STEP * a.k_row + shift(e, a.dim_qk)),
+                   vp + (e * PairT::STEP * a.v_row + shift(e, a.dim_v)), a.dim_qk, a.dim_v, kt, vt);
     } else {
 #pragma unroll
       for (int e = 0; e < PairT::E; ++e) {
         const int back = min(end - 1 - (next + PairT::row(0)), e * PairT::STEP);
-        pair.issue(e, kp + back * a.k_row, vp + back * a.v_row, a.dim_qk, a.dim_v, kt, vt);
+        pair.issue(e, kp + (back * a.k_row + shift(e, a.dim_qk)), vp + (back * a.v_row + shift(e, a.dim_v)), a.dim_qk,
+                   a.dim_v, kt, vt);
       }
     }
     if (a.k_mask) m = a.k_mask[min(next + (int)(threadIdx.x & 63), end - 1)];
@@ -400,7 +412,7 @@ struct Rows {
   float lse, delta;
   unsigned char m;
   const T *qb, *gb;      // the kv head's first row of the graph
-  const T *qp, *gp;      // this thread's first row of the next tile
+  const T *qp, *gp;      // this thread's unit of its first row of the next tile
   long at0;              // of lse and delta
   int q0, next, end;
 
@@ -413,8 +425,11 @@ struct Rows {
     next = r0;
     end = r1;
     const int r = r0 + PairT::row(0), i = query_of(p, r), x = r - i * p.group;
-    qp = qb + i * a.q_row + x * a.q_head;
-    gp = gb + i * p.go_row + x * p.go_head;
+    qp = qb + i * a.q_row + x * a.q_head + PairT::first(0, a.dim_qk);
+    gp = gb + i * p.go_row + x * p.go_head + PairT::first(0, a.dim_v);
+  }
+  static __device__ __forceinline__ int shift(int e, int dim) {
+    return PairT::SAME ? 0 : PairT::first(e, dim) - PairT::first(0, dim);
   }
   __device__ __forceinline__ void issue(const Params& p, TileT& qt, TileT& gt) {
     const e3conv_attention_args& a = p.a;
@@ -423,14 +438,16 @@ struct Rows {
     if (next + ROWS <= end && p.group_log2 >= 0 && by << p.group_log2 == PairT::STEP) {
 #pragma unroll
       for (int e = 0; e < PairT::E; ++e)
-        pair.issue(e, qp + e * by * a.q_row, gp + e * by * p.go_row, a.dim_qk, a.dim_v, qt, gt);
+        pair.issue(e, qp + (e * by * a.q_row + shift(e, a.dim_qk)), gp + (e * by * p.go_row + shift(e, a.dim_v)),
+                   a.dim_qk, a.dim_v, qt, gt);
       qp += PairT::E * by * a.q_row;
       gp += PairT::E * by * p.go_row;
     } else {
 #pragma unroll
       for (int e = 0; e < PairT::E; ++e) {
         const int r = min(next + PairT::row(e), end - 1), i = query_of(p, r), x = r - i * p.group;
-        pair.issue(e, qb + i * a.q_row + x * a.q_head, gb + i * p.go_row + x * p.go_head, a.dim_qk, a.dim_v, qt, gt);
+        pair.issue(e, qb + i * a.q_row + x * a.q_head + PairT::first(e, a.dim_qk),
+                   gb + i * p.go_row + x * p.go_head + PairT::first(e, a.dim_v), a.dim_qk, a.dim_v, qt, gt);
       }
     }
     const int r = min(next + (int)(threadIdx.x & 63), end - 1), i = query_of(p, r);
