@@ -27,8 +27,8 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
-  const int split = blockIdx.x % p.splits, slot = blockIdx.x / p.splits % p.slots;
-  const int c = blockIdx.x / p.splits / p.slots;
+  const Where place = where(p);
+  const int split = place.split, slot = place.slot, c = place.c;
   constexpr int BM = 32 * RW;
   const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
   const int q0 = offset(a.q_ptr, g, a.num_q);
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D
 
 #pragma unroll
     for (int b = 0; b < TK / 32; ++b) {
+      if (b > 0 && from + 32 * b >= k1) break;
       f32x16 s = by_row(now.bias + 32 * b, lane), dp = FOLD ? less_delta : f32x16{};
       ahead<2 * KS, W, Frag<P>>(
           [&](int i) { return i & 1 ? vt.rows(32 * b, i >> 1, lane) : kt.rows(32 * b, i >> 1, lane); },
@@ -149,8 +150,8 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D)
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
-  const int split = blockIdx.x % p.splits, slot = blockIdx.x / p.splits % p.slots;
-  const int c = blockIdx.x / p.splits / p.slots;
+  const Where place = where(p);
+  const int split = place.split, slot = place.slot, c = place.c;
   constexpr int BN = 32 * RW;
   const int g = graph_of_slot(a.k_ptr, a.num_graphs, a.num_k, 1, BN, slot);
   const int kb = offset(a.k_ptr, g, a.num_k), ke = offset(a.k_ptr, g + 1, a.num_k);
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D)
 
 #pragma unroll
     for (int b = 0; b < TQ / 32; ++b) {
+      if (b > 0 && from + 32 * b >= r1) break;
       // dP - delta from the start: the rows' -delta are the accumulator's first values
       f32x16 s = f32x16{}, dp = by_row(now.delta + 32 * b, lane);
       ahead<2 * KS, W, Frag<P>>(

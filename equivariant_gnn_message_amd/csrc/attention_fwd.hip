@@ -26,9 +26,8 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
-  // block -> (split, slot, kv head): the row tiles of a head are neighbours
-  const int split = blockIdx.x % p.splits, slot = blockIdx.x / p.splits % p.slots;
-  const int c = blockIdx.x / p.splits / p.slots;
+  const Where place = where(p);
+  const int split = place.split, slot = place.slot, c = place.c;
   constexpr int BM = 32 * RW;
   const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
   const int q0 = offset(a.q_ptr, g, a.num_q);

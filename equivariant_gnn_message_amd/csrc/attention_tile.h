@@ -238,6 +238,28 @@ struct Tile {
   }
 };
 
+// Work-group -> (split, slot, kv head).  Work-groups go to the eight dies in turn, each with
+// an L2 of its own: runs of 32 consecutive places, which share a graph's keys (or rows),
+// are put on one die.
+struct Where {
+  int split, slot, c;
+};
+__device__ __forceinline__ Where where(const Params& p) {
+  constexpr int DIES = 8, RUN = 32;
+  int b = blockIdx.x;
+  const int whole = (int)gridDim.x / (DIES * RUN) * (DIES * RUN);
+  if (b < whole) {
+    const int r = b % (DIES * RUN);
+    b = b - r + r % DIES * RUN + r / DIES;
+  }
+  Where w;
+  w.slot = b % p.slots;
+  b /= p.slots;
+  w.split = b % p.splits;
+  w.c = b / p.splits;
+  return w;
+}
+
 // Value of the lane with the other h.
 __device__ __forceinline__ float other_half(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
