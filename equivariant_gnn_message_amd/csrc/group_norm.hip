@@ -52,6 +52,7 @@ struct NormParams {
   int chunk_log2, chunk;           // rows of a work-group, a power of two
   int slots;                       // chunk slots: rows / chunk + graphs
   int inline_finish;               // 1: finish within apply
+  int vec_affine;                  // weight and bias are 16-byte aligned
   void* y;
   long y_row;
   float *mean, *rstd;
@@ -283,17 +284,41 @@ __device__ __forceinline__ void each_group(const NormParams& p, int c0, F use) {
 template <int V>
 struct Channels {
   float w[V], b[V], mean[V], rstd[V];
+  // Few and wide loads: one of four bytes for each channel and constant cost a chunk of a few
+  // rows a thread more than its rows.
   __device__ __forceinline__ void affine(const NormParams& p, int c0) {
+    read(p.a.weight, c0, p.vec_affine, 1.0f, w);
+    read(p.a.bias, c0, p.vec_affine, 0.0f, b);
+  }
+  static __device__ __forceinline__ void read(const float* from, int c0, int vec, float none, float (&v)[V]) {
+    if (!from) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[i] = p.a.weight ? p.a.weight[c0 + i] : 1.0f;
-      b[i] = p.a.bias ? p.a.bias[c0 + i] : 0.0f;
+      for (int i = 0; i < V; ++i) v[i] = none;
+    } else if (V % 4 == 0 && vec) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        const float4 x = reinterpret_cast<const float4*>(from + c0)[i];
+        v[4 * i] = x.x;
+        v[4 * i + 1] = x.y;
+        v[4 * i + 2] = x.z;
+        v[4 * i + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = from[c0 + i];
     }
   }
   __device__ __forceinline__ void moments(const NormParams& p, int g, int c0) {
+    int have = -1;
+    float m = 0.0f, r = 0.0f;
     each_group<V>(p, c0, [&](int i, int grp) {
-      mean[i] = p.mean[g * p.a.groups + grp];
-      rstd[i] = p.rstd[g * p.a.groups + grp];
+      if (grp != have) {
+        have = grp;
+        m = p.mean[g * p.a.groups + grp];
+        r = p.rstd[g * p.a.groups + grp];
+      }
+      mean[i] = m;
+      rstd[i] = r;
     });
   }
 };
@@ -306,6 +331,37 @@ __device__ float block_sum(float v) {
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
   return (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// The V sums from c0 on of a slot.
+template <int V>
+__device__ __forceinline__ void read_sums(const NormParams& p, long slot, int c0, float (&s1)[V], float (&s2)[V]) {
+  const float2* at = p.sums + slot * p.a.channels + c0;
+  if constexpr (V == 1) {
+    s1[0] = at[0].x;
+    s2[0] = at[0].y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(at)[i];
+      s1[2 * i] = x.x;
+      s2[2 * i] = x.y;
+      s1[2 * i + 1] = x.z;
+      s2[2 * i + 1] = x.w;
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void write_sums(const NormParams& p, long slot, int c0, const float (&s1)[V],
+                                           const float (&s2)[V]) {
+  float2* at = p.sums + slot * p.a.channels + c0;
+  if constexpr (V == 1) {
+    at[0] = make_float2(s1[0], s2[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+      reinterpret_cast<float4*>(at)[i] = make_float4(s1[2 * i], s2[2 * i], s1[2 * i + 1], s2[2 * i + 1]);
+  }
 }
 
 // The slots of a graph's chunks.
@@ -368,9 +424,7 @@ __global__ void __launch_bounds__(NT) norm_sums(NormParams p) {
   }
   const int c0 = q.unit * V;
   if (!c.only) {
-    if (threadIdx.x < q.width)
-#pragma unroll
-      for (int i = 0; i < V; ++i) p.sums[(long)blockIdx.x * p.a.channels + c0 + i] = make_float2(s1[i], s2[i]);
+    if (threadIdx.x < q.width) write_sums<V>(p, blockIdx.x, c0, s1, s2);
     if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = (float)n;
     return;
   }
@@ -448,26 +502,24 @@ template <int V>
 __device__ void finish_here(const NormParams& p, const Chunk& c, const Place& q, float2* red, Channels<V>& k) {
   const Slots s = slots_of(p, c.g);
   const int c0 = q.unit * V;
-  const float2* sums = p.sums + (long)s.first * p.a.channels + c0;
   int some = 0;      // the first chunk with a counted row gives the value to sum about
   while (some + 1 < s.count && p.counts[s.first + some] == 0.0f) ++some;
   float n = 0.0f, base[V], s1[V], s2[V];
+  read_sums<V>(p, s.first + some, c0, base, s1);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    base[i] = sums[(long)some * p.a.channels + i].x;
-    s1[i] = s2[i] = 0.0f;
-  }
+  for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
   if (q.on)
 #pragma unroll 2
     for (int j = q.row; j < s.count; j += q.step) {
       const float w = p.counts[s.first + j];
       n += w;
+      float m1[V], m2[V];
+      read_sums<V>(p, s.first + j, c0, m1, m2);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float2 x = sums[(long)j * p.a.channels + i];
-        const float d = x.x - base[i];
+        const float d = m1[i] - base[i];
         s1[i] = fmaf(w, d, s1[i]);
-        s2[i] += fmaf(w * d, d, x.y);
+        s2[i] += fmaf(w * d, d, m2[i]);
       }
     }
   add_rows<V>(q, red, s1, s2);
@@ -517,8 +569,13 @@ __global__ void __launch_bounds__(NT) norm_apply(NormParams p) {
     __shared__ float2 red[NT * V];
     finish_here<V>(p, c, q, red, k);
   } else {
+    int have = -1;
+    float2 s = make_float2(0.0f, 0.0f);
     each_group<V>(p, c0, [&](int i, int g) {
-      const float2 s = p.stats[c.g * p.a.groups + g];
+      if (g != have) {
+        have = g;
+        s = p.stats[c.g * p.a.groups + g];
+      }
       k.mean[i] = s.x;
       k.rstd[i] = s.y;
     });
@@ -590,9 +647,7 @@ __global__ void __launch_bounds__(NT) norm_grad_sums(NormParams p) {
 #pragma unroll
   for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
   if (c.none) {     // the weight gradient sums over all slots
-    if (threadIdx.x < q.width)
-#pragma unroll
-      for (int i = 0; i < V; ++i) p.sums[(long)blockIdx.x * p.a.channels + c0 + i] = make_float2(0.0f, 0.0f);
+    if (threadIdx.x < q.width) write_sums<V>(p, blockIdx.x, c0, s1, s2);
     return;
   }
   Channels<V> k;
@@ -612,9 +667,7 @@ __global__ void __launch_bounds__(NT) norm_grad_sums(NormParams p) {
   __shared__ float2 red[NT * V];
   add_rows<V>(q, red, s1, s2);
   n = block_sum(q.on && q.col == 0 ? n : 0.0f);
-  if (threadIdx.x < q.width)
-#pragma unroll
-    for (int i = 0; i < V; ++i) p.sums[(long)blockIdx.x * p.a.channels + c0 + i] = make_float2(s1[i], s2[i]);
+  if (threadIdx.x < q.width) write_sums<V>(p, blockIdx.x, c0, s1, s2);
   if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = n;
   if (!c.only) return;
   float m1[V], m2[V];
@@ -688,7 +741,6 @@ __global__ void __launch_bounds__(NT) norm_grad_apply(NormParams p) {
   float m1[V], m2[V];
   if (HERE) {
     const Slots s = slots_of(p, c.g);
-    const float2* sums = p.sums + (long)s.first * p.a.channels + c0;
     float n = 0.0f, s1[V], s2[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
@@ -696,19 +748,25 @@ __global__ void __launch_bounds__(NT) norm_grad_apply(NormParams p) {
 #pragma unroll 2
       for (int j = q.row; j < s.count; j += q.step) {
         n += p.counts[s.first + j];
+        float a1[V], a2[V];
+        read_sums<V>(p, s.first + j, c0, a1, a2);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float2 x = sums[(long)j * p.a.channels + i];
-          s1[i] += x.x;
-          s2[i] += x.y;
+          s1[i] += a1[i];
+          s2[i] += a2[i];
         }
       }
     add_rows<V>(q, red, s1, s2);
     n = block_sum(q.on && q.col == 0 ? n : 0.0f);
     group_means<V>(p, q, k, n, red, s1, s2, m1, m2);
   } else {
+    int have = -1;
+    float2 s = make_float2(0.0f, 0.0f);
     each_group<V>(p, c0, [&](int i, int g) {
-      const float2 s = p.stats[c.g * p.a.groups + g];
+      if (g != have) {
+        have = g;
+        s = p.stats[c.g * p.a.groups + g];
+      }
       m1[i] = s.x;
       m2[i] = s.y;
     });
@@ -762,14 +820,15 @@ hipError_t by_activation(const NormParams& p, bool back, bool one, hipStream_t s
   }
 }
 
-// Rows of a chunk, as a power of two: all of them where the whole call is small (then every graph
-// is one chunk and one launch does it), else about four work-groups per compute unit, 16 KiB
+// Rows of a chunk, as a power of two: all of them where the call is small and has many graphs (then
+// every graph is one chunk and one launch does it; a graph with all 2^18 elements to itself
+// takes its work-group some 50 us), else about four work-groups per compute unit, 16 KiB
 // each at least.
 int chunk_rows_log2(const e3conv_group_norm_args& a) {
-  const int64_t row = (int64_t)a.channels * (a.dtype == E3CONV_F32 ? 4 : 2);
+  const int64_t row = (int64_t)a.channels * (a.dtype == E3CONV_F32 ? 4 : 2), all = a.num_rows * a.channels;
   int64_t rows = (a.num_rows + 1023) / 1024;
   if (rows * row < 16384) rows = (16384 + row - 1) / row;
-  if (a.num_rows * a.channels <= 1 << 18) rows = a.num_rows;
+  if (all <= 1 << 18 && all <= (int64_t)16384 * a.num_graphs) rows = a.num_rows;
   int l = 0;
   while (((int64_t)1 << l) < rows) ++l;
   return l < 30 ? l : 30;
@@ -795,6 +854,7 @@ hipError_t launch(NormParams p, bool back, bool vec, void* workspace, hipStream_
   p.by_width = div_by(p.units < NT ? p.units : NT);
   p.chunk_log2 = chunk_rows_log2(p.a);
   p.chunk = 1 << p.chunk_log2;
+  p.vec_affine = (reinterpret_cast<uintptr_t>(p.a.weight) | reinterpret_cast<uintptr_t>(p.a.bias)) % 16 == 0;
   p.slots = chunk_slots(p.a);
   p.sums = static_cast<float2*>(workspace);
   p.stats = p.sums + (size_t)p.slots * p.a.channels;
