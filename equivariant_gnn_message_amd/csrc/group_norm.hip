@@ -835,8 +835,9 @@ int chunk_rows_log2(const e3conv_group_norm_args& a) {
 }
 int chunk_slots(const e3conv_group_norm_args& a) { return (int)((a.num_rows >> chunk_rows_log2(a)) + a.num_graphs); }
 
-// sums (slots, channels), stats (graphs, groups), counts (slots).
-size_t workspace_bytes(const e3conv_group_norm_args& a) {
+// sums (slots, channels), stats (graphs, groups), counts (slots); none for a forward of one launch.
+size_t workspace_bytes(const e3conv_group_norm_args& a, bool back) {
+  if (!back && a.channels <= NT && a.num_rows <= (int64_t)1 << chunk_rows_log2(a)) return 0;
   const size_t slots = (size_t)chunk_slots(a);
   return (slots * a.channels + (size_t)a.num_graphs * a.groups) * sizeof(float2) + (slots * sizeof(float) + 15) / 16 * 16;
 }
@@ -901,7 +902,7 @@ e3conv_status e3conv_group_norm_workspace_size(const e3conv_group_norm_args* a, 
   const e3conv_status st = e3c::check_sizes(a);
   if (st != E3CONV_OK) return st;
   if (!bytes) return e3c::bad("bytes is NULL");
-  *bytes = e3c::workspace_bytes(*a);
+  *bytes = e3c::workspace_bytes(*a, backward != 0);
   return e3c::api_ok();
 }
 
@@ -912,8 +913,8 @@ e3conv_status e3conv_group_norm(const e3conv_group_norm_args* a, void* y, int64_
   if (y_row < 0) return e3c::bad("negative stride");
   if (a->num_graphs == 0) return e3c::api_ok();
   if (a->num_rows > 0 && !y) return e3c::bad("NULL device pointer");
-  const size_t need = e3c::workspace_bytes(*a);
-  if (bytes < need || !workspace)
+  const size_t need = e3c::workspace_bytes(*a, false);
+  if (bytes < need || (need > 0 && !workspace))
     return e3c::api_fail(E3CONV_ERR_WORKSPACE, "group norm needs " + std::to_string(need) + " bytes");
   e3c::NormParams p{};
   p.a = *a;
@@ -945,7 +946,7 @@ e3conv_status e3conv_group_norm_backward(const e3conv_group_norm_args* a, const 
     if (e != hipSuccess) return e3c::api_hip_fail(e, "fill launch");
     return e3c::api_ok();
   }
-  const size_t need = e3c::workspace_bytes(*a);
+  const size_t need = e3c::workspace_bytes(*a, true);
   if (bytes < need || !workspace)
     return e3c::api_fail(E3CONV_ERR_WORKSPACE, "group norm backward needs " + std::to_string(need) + " bytes");
   e3c::NormParams p{};

@@ -63,6 +63,7 @@ class E3ConvError(RuntimeError):
 
 
 _lib = None
+_torch = None    # the module, once the library is loaded
 
 P = ctypes.c_void_p
 I32P = ctypes.POINTER(ctypes.c_int)
@@ -88,7 +89,7 @@ class GroupNormArgs(ctypes.Structure):
 
 def load_library(path=LIB_PATH):
     """Load libe3conv.so (once) and declare its signatures; raises if absent."""
-    global _lib
+    global _lib, _torch
     if _lib is not None:
         return _lib
     # torch first: its HIP runtime is then the one the library's dependency
@@ -157,6 +158,7 @@ def load_library(path=LIB_PATH):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res
+    _torch = torch
     _lib = lib
     return lib
 
@@ -181,7 +183,7 @@ def _stream(stream):
 
 
 def _dtype_code(t):
-    import torch
+    torch = _torch or load_library() and _torch
     if t.dtype == torch.float32:
         return E3CONV_F32
     if t.dtype == torch.bfloat16:
@@ -579,8 +581,9 @@ def e3conv_last_error_detail():
 
 # --------------------------------------- graph attention, group norm ---
 
-# These calls are short on the GPU, so the checks on the way are kept cheap: each property of a
-# tensor is asked once, and devices are compared as indices (-1 on the host).
+# These calls are short on the GPU, so the way to them is kept short: each property of a
+# tensor is asked once, devices are compared as indices (-1 on the host), and operands that
+# are as they should be pass one test together.
 
 def _rows_of(t, name, dtype, index, shape):
     """Strides of a device operand whose last axis has unit stride; the others are free."""
@@ -611,8 +614,7 @@ def _node_mask(t, name, index, n):
     """Address of a node mask (bool or uint8, one byte per node), or None."""
     if t is None:
         return None
-    import torch
-    return _dense(t, name, torch.bool if t.dtype is torch.bool else torch.uint8, index, n)
+    return _dense(t, name, _torch.bool if t.dtype is _torch.bool else _torch.uint8, index, n)
 
 
 def _written(t, name):
@@ -623,21 +625,19 @@ def _written(t, name):
 
 def _enter(index, stream):
     """(stream handle, stream object to record allocations on or None) of a call on a device."""
-    import torch
-    if index != torch._C._cuda_getDevice():
-        raise ValueError(f"operands are on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
-    current = torch._C._cuda_getCurrentRawStream(index)
+    if index != _torch._C._cuda_getDevice():
+        raise ValueError(f"operands are on cuda:{index}, the current device is cuda:{_torch.cuda.current_device()}")
+    current = _torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
         return current, None
     handle = int(getattr(stream, "cuda_stream", stream))
     if handle == current:
         return handle, None
-    return handle, stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=index)
+    return handle, stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(handle, device=index)
 
 
 def _workspace(given, size_of, args, like, other, backward=0):
     """(address, bytes, tensor) of the caller's workspace, or of one allocated for the call."""
-    import torch
     if given is not None:
         if given.get_device() != like.get_device() or not given.is_contiguous() or given.data_ptr() % 16:
             raise ValueError(f"workspace must be a contiguous, 16-byte aligned tensor on {like.device}")
@@ -646,36 +646,40 @@ def _workspace(given, size_of, args, like, other, backward=0):
     _check(size_of(args, backward, ctypes.byref(n)))
     if n.value == 0:
         return None, 0, None
-    t = _allocate((n.value,), torch.uint8, like, other)
+    t = _recorded(like.new_empty((n.value,), dtype=_torch.uint8), other)
     return t.data_ptr(), n.value, t
 
 
-def _allocate(shape, dtype, like, other):
-    import torch
-    t = torch.empty(shape, dtype=dtype, device=like.device)
+def _recorded(t, other):
+    """A new tensor; its memory, once freed, is not reused before the other stream is done with it."""
     if other is not None:
-        t.record_stream(other)   # freed memory is not reused before that stream is done with it
+        t.record_stream(other)
     return t
 
 
 def _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask):
-    import torch
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q (num_q, heads_q, dim_qk), k (num_k, heads_kv, dim_qk), v (num_k, heads_kv, dim_v)")
-    code, dt, index = _dtype_code(q), q.dtype, q.get_device()
-    qs = q.shape
-    nq, hq, d = qs
+    dt, index = q.dtype, q.get_device()
+    code, i32 = _dtype_code(q), _torch.int32
+    nq, hq, d = q.shape
     nk, hk, dv = v.shape
-    q_row, q_head, _ = _rows_of(q, "q", dt, index, qs)
-    k_row, k_head, _ = _rows_of(k, "k", dt, index, (nk, hk, d))
-    v_row, v_head, _ = _rows_of(v, "v", dt, index, (nk, hk, dv))
+    q_row, q_head, q_one = q.stride()
+    k_row, k_head, k_one = k.stride()
+    v_row, v_head, v_one = v.stride()
+    if not (index >= 0 and k.dtype is dt and v.dtype is dt and k.get_device() == index and v.get_device() == index
+            and k.shape == (nk, hk, d) and q_one == 1 and k_one == 1 and v_one == 1):
+        _rows_of(q, "q", dt, index, (nq, hq, d))      # says what is wrong, if anything
+        _rows_of(k, "k", dt, index, (nk, hk, d))
+        _rows_of(v, "v", dt, index, (nk, hk, dv))
     graphs = q_ptr.numel() - 1
     if graphs < 0:
         raise ValueError("q_ptr must hold num_graphs + 1 offsets")
-    qp = _dense(q_ptr, "q_ptr", torch.int32, index, graphs + 1)
-    kp = qp if k_ptr is q_ptr else _dense(k_ptr, "k_ptr", torch.int32, index, graphs + 1)
-    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, d ** -0.5 if scale is None else scale, qp, kp,
-                         _node_mask(q_mask, "q_mask", index, nq), _node_mask(k_mask, "k_mask", index, nk),
+    qp = _dense(q_ptr, "q_ptr", i32, index, graphs + 1)
+    kp = qp if k_ptr is q_ptr else _dense(k_ptr, "k_ptr", i32, index, graphs + 1)
+    qm = None if q_mask is None else _node_mask(q_mask, "q_mask", index, nq)
+    km = None if k_mask is None else _node_mask(k_mask, "k_mask", index, nk)
+    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, d ** -0.5 if scale is None else scale, qp, kp, qm, km,
                          q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, q_head, k_row, k_head, v_row, v_head)
 
 
@@ -695,21 +699,21 @@ def e3conv_attention(q, k, v, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None
     strides but unit along the last axis; q_ptr, k_ptr int32 offsets of the graphs; scale defaults to
     dim_qk ** -0.5; masks are bool or uint8, one value per row, 0 for padding.  lse fp32 (num_q, heads_q).
     """
-    import torch
+    lib = _lib or load_library()
     args = _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask)
     index, shape = q.get_device(), (args.num_q, args.heads_q, args.dim_v)
     handle, other = _enter(index, stream)
     if out is None:
-        out = _allocate(shape, q.dtype, q, other)
+        out = _recorded(q.new_empty(shape), other)
         row, head = shape[1] * shape[2], shape[2]
     else:
         row, head, _ = _rows_of(out, "out", q.dtype, index, shape)
         _written(out, "out")
     if lse is None:
-        lse = _allocate(shape[:2], torch.float32, q, other)
+        lse = _recorded(q.new_empty(shape[:2], dtype=_torch.float32), other)
     else:
-        _dense(lse, "lse", torch.float32, index, shape[0] * shape[1])
-    lib, ref = load_library(), ctypes.byref(args)
+        _dense(lse, "lse", _torch.float32, index, shape[0] * shape[1])
+    ref = ctypes.byref(args)
     ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q, other)
     _check(lib.e3conv_attention(ref, out.data_ptr(), row, head, lse.data_ptr(), ws, nbytes, handle))
     return out, lse
@@ -721,14 +725,14 @@ def e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale=N
 
     grads: three output tensors (strides free but unit along the last axis), or None to allocate them.
     """
-    import torch
+    lib = _lib or load_library()
     args = _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask)
     index, dt, shape = q.get_device(), q.dtype, (args.num_q, args.heads_q, args.dim_v)
     strides = _rows_of(out, "out", dt, index, shape)[:2] + _rows_of(grad_out, "grad_out", dt, index, shape)[:2]
-    lse_at = _dense(lse, "lse", torch.float32, index, shape[0] * shape[1])
+    lse_at = _dense(lse, "lse", _torch.float32, index, shape[0] * shape[1])
     handle, other = _enter(index, stream)
     if grads is None:
-        grads = [_allocate(t.shape, dt, q, other) for t in (q, k, v)]
+        grads = [_recorded(_torch.empty_like(t), other) for t in (q, k, v)]
         for t in grads:
             strides += t.stride()[:2]
     else:
@@ -736,7 +740,7 @@ def e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale=N
             strides += _rows_of(t, name, dt, index, ref.shape)[:2]
             _written(t, name)
     gq, gk, gv = grads
-    lib, ref = load_library(), ctypes.byref(args)
+    ref = ctypes.byref(args)
     ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q, other, 1)
     _check(lib.e3conv_attention_backward(
         ref, out.data_ptr(), lse_at, grad_out.data_ptr(), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
@@ -745,7 +749,6 @@ def e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale=N
 
 
 def _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask):
-    import torch
     if x.dim() != 2:
         raise ValueError("x must be (num_rows, channels)")
     code, index = _dtype_code(x), x.get_device()
@@ -757,10 +760,10 @@ def _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask
     act = ACTIVATIONS.get(activation, activation)
     if not isinstance(act, int):
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    return GroupNormArgs(code, graphs, c, groups, act, eps, n, _dense(row_ptr, "row_ptr", torch.int32, index, graphs + 1),
+    return GroupNormArgs(code, graphs, c, groups, act, eps, n, _dense(row_ptr, "row_ptr", _torch.int32, index, graphs + 1),
                          _node_mask(row_mask, "row_mask", index, n), x.data_ptr(), row,
-                         None if weight is None else _dense(weight, "weight", torch.float32, index, c),
-                         None if bias is None else _dense(bias, "bias", torch.float32, index, c))
+                         None if weight is None else _dense(weight, "weight", _torch.float32, index, c),
+                         None if bias is None else _dense(bias, "bias", _torch.float32, index, c))
 
 
 def e3conv_group_norm_workspace_size(args, backward=False):
@@ -779,17 +782,18 @@ def e3conv_group_norm(x, row_ptr, groups, weight=None, bias=None, eps=1e-5, acti
     fine); row_ptr int32 offsets of the graphs; weight, bias fp32 or None; activation "none", "relu", "silu"
     or "gelu"; row_mask bool or uint8, 0 for padding.  mean, rstd fp32 (num_graphs, groups).
     """
-    import torch
+    lib = _lib or load_library()
     args = _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask)
     index, shape = x.get_device(), (args.num_graphs, args.groups)
     handle, other = _enter(index, stream)
     if out is None:
-        out, row = _allocate(x.shape, x.dtype, x, other), args.channels
+        out, row = _recorded(x.new_empty(x.shape), other), args.channels
     else:
         row, _ = _rows_of(out, "out", x.dtype, index, x.shape)
         _written(out, "out")
-    mean, rstd = _allocate(shape, torch.float32, x, other), _allocate(shape, torch.float32, x, other)
-    lib, ref = load_library(), ctypes.byref(args)
+    mean = _recorded(x.new_empty(shape, dtype=_torch.float32), other)
+    rstd = _recorded(_torch.empty_like(mean), other)
+    ref = ctypes.byref(args)
     ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x, other)
     _check(lib.e3conv_group_norm(ref, out.data_ptr(), row, mean.data_ptr(), rstd.data_ptr(), ws, nbytes, handle))
     return out, mean, rstd
@@ -798,21 +802,21 @@ def e3conv_group_norm(x, row_ptr, groups, weight=None, bias=None, eps=1e-5, acti
 def e3conv_group_norm_backward(x, row_ptr, groups, weight, bias, activation, mean, rstd, grad_y, row_mask=None,
                                grad_x=None, workspace=None, stream=None):
     """(grad_x, grad_weight, grad_bias); a gradient is None where its operand is."""
-    import torch
+    lib = _lib or load_library()
     # eps is already in rstd
     args = _group_norm_args(x, row_ptr, groups, weight, bias, 1.0, activation, row_mask)
     index, size = x.get_device(), args.num_graphs * args.groups
-    mean_at = _dense(mean, "mean", torch.float32, index, size)
-    rstd_at = _dense(rstd, "rstd", torch.float32, index, size)
+    mean_at = _dense(mean, "mean", _torch.float32, index, size)
+    rstd_at = _dense(rstd, "rstd", _torch.float32, index, size)
     gy_row, _ = _rows_of(grad_y, "grad_y", x.dtype, index, x.shape)
     handle, other = _enter(index, stream)
     if grad_x is None:
-        grad_x, row = _allocate(x.shape, x.dtype, x, other), args.channels
+        grad_x, row = _recorded(x.new_empty(x.shape), other), args.channels
     else:
         row, _ = _rows_of(grad_x, "grad_x", x.dtype, index, x.shape)
         _written(grad_x, "grad_x")
-    gw, gb = (None if t is None else _allocate(t.shape, torch.float32, x, other) for t in (weight, bias))
-    lib, ref = load_library(), ctypes.byref(args)
+    gw, gb = (None if t is None else _recorded(_torch.empty_like(t), other) for t in (weight, bias))
+    ref = ctypes.byref(args)
     ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x, other, 1)
     _check(lib.e3conv_group_norm_backward(
         ref, mean_at, rstd_at, grad_y.data_ptr(), gy_row, grad_x.data_ptr(), row,

@@ -106,6 +106,15 @@ def test_group_norm_refuses_outputs():
     assert lib.e3conv_group_norm_workspace_size(ref, 0, None) == 1
 
 
+def test_group_norm_refuses_a_small_workspace():
+    lib = E.load_library()
+    a = norm_args(num_rows=1 << 20, x_row=32)
+    ref = ctypes.byref(a)
+    for ws in ((None, 0), (FAKE, 16)):
+        assert lib.e3conv_group_norm(ref, FAKE, 32, None, None, *ws, None) == 6
+        assert lib.e3conv_group_norm_backward(ref, FAKE, FAKE, FAKE, 32, FAKE, 32, None, None, *ws, None) == 6
+
+
 def test_host_tensors_are_refused():
     import torch
     t, p = torch.ones((4, 2, 8)), torch.tensor([0, 4], dtype=torch.int32)
