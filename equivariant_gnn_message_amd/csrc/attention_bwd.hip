@@ -9,6 +9,9 @@
 //                S = Q K^T,  dP = G V^T,  dV^T += G^T P,  dK^T += Q^T dS.
 // Seven products instead of the five of a single kernel that adds dQ by atomics: the
 // result is the same bits every time, and nothing but delta passes through memory.
+// Where graphs have at most 64 rows and keys both run in one launch (attn_bwd_small), the
+// second forming delta itself: there the launches are the time (16 us as two, 12 as one
+// for 64 graphs of 64 nodes).
 #include "attention_tile.h"
 #include "kernels.h"
 
@@ -17,17 +20,17 @@ namespace attn {
 namespace {
 
 template <class T, int D, int RW, int TK, int BUF, bool VEC>
-__global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D) : 1) attn_bwd_q(Params p) {
+__device__ __forceinline__ void bwd_q(const Params& p, const Where& place) {
   constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
   struct Buffer {
     Tile<P, TK, D> k, v;
     float bias[TK];
   };
+  static_assert(BUF == 2 || !(sizeof(T) == 2 && VEC), "loads straight to LDS need the other buffer");
   __shared__ __attribute__((aligned(16))) Buffer first, second;
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
-  const Where place = where(p);
   const int split = place.split, slot = place.slot, c = place.c;
   constexpr int BM = 32 * RW;
   const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
@@ -68,7 +71,7 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D
     for (int i = 0; i < 8; ++i) delta = d < a.dim_v ? fmaf(gr.at(i), orow.at(i), delta) : delta;
   }
   delta = live ? delta + other_half(delta) : 0.0f;
-  if (row && h == 0 && split == 0) p.delta[at] = delta;
+  if (p.delta && row && h == 0 && split == 0) p.delta[at] = delta;
 
   // dP - delta from the start: -delta is the accumulator's first value (where its 16
   // registers do not cost a wave)
@@ -139,18 +142,18 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D
     }
 }
 
-template <class T, int D, int RW, int TQ, int BUF, bool VEC>
-__global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D) : 1) attn_bwd_kv(Params p) {
+template <class T, int D, int RW, int TQ, int BUF, bool VEC, bool OWN>
+__device__ __forceinline__ void bwd_kv(const Params& p, const Where& place) {
   constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
   struct Buffer {
     Tile<P, TQ, D> q, g;
     float lse[TQ], delta[TQ];
   };
+  static_assert(BUF == 2 || !(sizeof(T) == 2 && VEC), "loads straight to LDS need the other buffer");
   __shared__ __attribute__((aligned(16))) Buffer first, second;
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
-  const Where place = where(p);
   const int split = place.split, slot = place.slot, c = place.c;
   constexpr int BN = 32 * RW;
   const int g = graph_of_slot(a.k_ptr, a.num_graphs, a.num_k, 1, BN, slot);
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D)
   const int r0 = min(split * per, tiles) * TQ;
   const int r1 = min(nrows, min((split + 1) * per, tiles) * TQ);
 
-  Rows<T, D, TQ, 64 * RW, VEC> rows;
+  Rows<T, D, TQ, 64 * RW, VEC, OWN> rows;
   rows.begin(p, c, q0, r0, r1);
   if (r0 < r1) rows.issue(p, first.q, first.g);
 
@@ -271,6 +274,22 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D)
     }
 }
 
+template <class T, int D, int RW, int TK, int BUF, bool VEC>
+__global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D) : 1) attn_bwd_q(Params p) {
+  bwd_q<T, D, RW, TK, BUF, VEC>(p, where(blockIdx.x, gridDim.x, p.slots, p.splits));
+}
+template <class T, int D, int RW, int TQ, int BUF, bool VEC>
+__global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D) : 1) attn_bwd_kv(Params p) {
+  bwd_kv<T, D, RW, TQ, BUF, VEC, false>(p, where(blockIdx.x, gridDim.x, p.slots, p.splits));
+}
+template <class T, int D, bool VEC>
+__global__ void __launch_bounds__(64) attn_bwd_small(Params p) {
+  constexpr int BUF = sizeof(T) == 2 && VEC ? 2 : 1;
+  const int b = blockIdx.x, n = p.first_blocks;
+  if (b < n) bwd_q<T, D, 1, 32, BUF, VEC>(p, where(b, n, p.slots, 1));
+  else bwd_kv<T, D, 1, 32, BUF, VEC, true>(p, where(b - n, gridDim.x - n, p.slots_kv, 1));
+}
+
 // Sums the splits: element d < dim of row (i, head) of `width` floats, times factor.  Four
 // waves of a work-group take 64 elements, each a quarter of the splits, eight at a time.
 template <class T>
@@ -362,10 +381,36 @@ void launch_kv(const Params& p, int rw, unsigned grid, hipStream_t s) {
   else launch_kv<T, D, false>(p, rw, grid, s);
 }
 
+template <class T, int D>
+void launch_small(const Params& p, unsigned grid, hipStream_t s) {
+  if (p.vec) hipLaunchKernelGGL((attn_bwd_small<T, D, true>), dim3(grid), dim3(64), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_small<T, D, false>), dim3(grid), dim3(64), 0, s, p);
+}
+
+// Whether both kernels have work-groups of one wave and no splits.
+bool small(const e3conv_attention_args& a) {
+  const Shape q = shape_q(a), kv = shape_kv(a);
+  return q.rw == 1 && kv.rw == 1 && q.splits == 1 && kv.splits == 1 &&
+         ((long)q.slots + kv.slots) * a.heads_kv <= 0x7fffffffL;
+}
+
 template <class T>
 hipError_t backward(Params p, hipStream_t s) {
   const e3conv_attention_args& a = p.a;
   const int dim = a.dim_qk > a.dim_v ? a.dim_qk : a.dim_v;
+  if (small(a)) {
+    const Shape q = shape_q(a), kv = shape_kv(a);
+    p.delta = nullptr;
+    p.splits = 1;
+    p.slots = q.slots;
+    p.slots_kv = kv.slots;
+    p.first_blocks = q.slots * a.heads_kv;
+    const unsigned grid = (unsigned)(p.first_blocks + kv.slots * a.heads_kv);
+    if (dim <= 32) launch_small<T, 32>(p, grid, s);
+    else if (dim <= 64) launch_small<T, 64>(p, grid, s);
+    else launch_small<T, 128>(p, grid, s);
+    return hipGetLastError();
+  }
   if (a.num_q > 0) {
     const Shape sh = shape_q(a);
     const long grid = (long)sh.slots * sh.splits * a.heads_kv;
@@ -405,6 +450,7 @@ hipError_t backward(Params p, hipStream_t s) {
 
 // delta, then one region for the partial results of either kernel in turn.
 size_t backward_workspace(const e3conv_attention_args& a) {
+  if (small(a)) return 0;
   const Shape sq = shape_q(a), sk = shape_kv(a);
   const size_t q = sq.splits > 1 ? (size_t)sq.splits * a.num_q * a.heads_q * a.dim_qk : 0;
   const size_t k = sk.splits > 1 ? (size_t)sk.splits * a.num_k * a.heads_kv * (a.dim_qk + a.dim_v) : 0;

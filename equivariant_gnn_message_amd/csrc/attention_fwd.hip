@@ -22,11 +22,12 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D
     Tile<P, TK, D> k, v;
     float bias[TK];
   };
+  static_assert(BUF == 2 || !(sizeof(T) == 2 && VEC), "loads straight to LDS need the other buffer");
   __shared__ __attribute__((aligned(16))) Buffer first, second;
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
-  const Where place = where(p);
+  const Where place = where(blockIdx.x, gridDim.x, p.slots, p.splits);
   const int split = place.split, slot = place.slot, c = place.c;
   constexpr int BM = 32 * RW;
   const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);

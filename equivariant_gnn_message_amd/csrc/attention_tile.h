@@ -38,6 +38,8 @@ struct Params {
   int vec_st;                      // 4-element stores of the outputs
   int slots;                       // work-group slots of the row (or key) tiles
   int splits;                      // ranges of the other axis, joined by a second kernel
+  int first_blocks;                // reverse pass in one launch: its work-groups for grad_q,
+  int slots_kv;                    // and the slots of the others
   void* out;
   long out_row, out_head;
   float* lse;
@@ -244,19 +246,18 @@ struct Tile {
 struct Where {
   int split, slot, c;
 };
-__device__ __forceinline__ Where where(const Params& p) {
+__device__ __forceinline__ Where where(int b, int blocks, int slots, int splits) {
   constexpr int DIES = 8, RUN = 32;
-  int b = blockIdx.x;
-  const int whole = (int)gridDim.x / (DIES * RUN) * (DIES * RUN);
+  const int whole = blocks / (DIES * RUN) * (DIES * RUN);
   if (b < whole) {
     const int r = b % (DIES * RUN);
     b = b - r + r % DIES * RUN + r / DIES;
   }
   Where w;
-  w.slot = b % p.slots;
-  b /= p.slots;
-  w.split = b % p.splits;
-  w.c = b / p.splits;
+  w.slot = b % slots;
+  b /= slots;
+  w.split = b % splits;
+  w.c = b / splits;
   return w;
 }
 
@@ -425,8 +426,9 @@ struct Keys {
 
 // The tiles of the rows (queries and their heads of one kv head) that a work-group of the
 // reverse pass walks over, and each row's lse (base 2) and -delta.  A row that sees no key
-// or lies beyond the end has lse = +infinity, which makes its P zero.
-template <class T, int D, int ROWS, int NT, bool VEC>
+// or lies beyond the end has lse = +infinity, which makes its P zero.  OWN: delta is formed
+// here, else it was left in memory.
+template <class T, int D, int ROWS, int NT, bool VEC, bool OWN>
 struct Rows {
   typedef Pair<T, D, ROWS, NT, VEC> PairT;
   typedef typename PairT::TileT TileT;
@@ -475,7 +477,19 @@ struct Rows {
     const int r = min(next + (int)(threadIdx.x & 63), end - 1), i = query_of(p, r);
     const long at = at0 + (long)i * (a.heads_q - p.group) + r;
     lse = p.lse[at];
-    delta = p.delta[at];
+    if constexpr (OWN) {
+      const int x = r - i * p.group;
+      const T* g = gb + i * p.go_row + x * p.go_head;
+      const T* o = (const T*)p.out + (q0 + i) * p.out_row + ((at0 - (long)q0 * a.heads_q) + x) * p.out_head;
+      delta = 0.0f;
+      for (int d = 0; d < a.dim_v; d += 8) {
+        const Raw<T> u = fetch8<VEC>(g, d, a.dim_v), v = fetch8<VEC>(o, d, a.dim_v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) delta = fmaf(u.at(j), v.at(j), delta);
+      }
+    } else {
+      delta = p.delta[at];
+    }
     if (a.q_mask) m = a.q_mask[q0 + i];
     next += ROWS;
   }

@@ -299,6 +299,19 @@ def test_autograd_and_shared_heads():
     assert abs(diff - slope) <= 1e-2 * scale, (diff, slope, scale)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,dv", [(16, 16), (33, 20), (64, 64), (100, 128)])
+def test_many_small_graphs(dtype, d, dv):
+    """Graphs of at most 64 rows on average take one launch for the whole reverse pass; one of them is much longer."""
+    lens = [5, 0, 64, 1, 33, 64, 200, 17, 2, 63] * 2
+    rng = np.random.default_rng(8)
+    mask = (rng.random(sum(lens)) < 0.8).astype(np.uint8)
+    check(dtype, *draw(101, dtype, lens, lens, 4, 4, d, dv), lens, lens, q_mask=mask, k_mask=mask)
+    some = [1, 3, 0, 2, 4, 1, 2, 0, 1, 1] * 2
+    check(dtype, *draw(102, dtype, some, lens, 4, 2, d, dv), some, lens, k_mask=mask)
+    check(dtype, *draw(103, dtype, lens, some, 1, 1, d, dv), lens, some)
+
+
 def test_empty_calls():
     import torch
     z = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -322,6 +335,9 @@ def test_refusals_on_device():
     q, k, v, g = draw(91, "f32", lens, lens, 2, 2, 8, 8)
     p = dev(ptr(lens))
     out, lse = E.e3conv_attention(q, k, v, p, p)
+    lq, lk, lv, lg = draw(92, "f32", [300], [300], 2, 2, 8, 8)
+    lp = dev(ptr([300]))
+    lout, llse = E.e3conv_attention(lq, lk, lv, lp, lp)
     for err, call in (
             (TypeError, lambda: E.e3conv_attention(q, k.bfloat16(), v, p, p)),
             (TypeError, lambda: E.e3conv_attention(q.half(), k.half(), v.half(), p, p)),
@@ -335,6 +351,6 @@ def test_refusals_on_device():
             (E.E3ConvError, lambda: E.e3conv_attention(q, k, v, p, p, scale=float("inf"))),
             (E.E3ConvError, lambda: E.e3conv_attention(q.expand(4, 2, 8)[:, :1].repeat(1, 3, 1), k, v, p, p)),
             (E.E3ConvError, lambda: E.e3conv_attention_backward(
-                q, k, v, out, lse, g, p, p, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")))):
+                lq, lk, lv, lout, llse, lg, lp, lp, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")))):
         with pytest.raises(err):
             call()
