@@ -9,9 +9,9 @@
 //                S = Q K^T,  dP = G V^T,  dV^T += G^T P,  dK^T += Q^T dS.
 // Seven products instead of the five of a single kernel that adds dQ by atomics: the
 // result is the same bits every time, and nothing but delta passes through memory.
-// Where graphs have at most 64 rows and keys both run in one launch (attn_bwd_small), the
-// second forming delta itself: there the launches are the time (16 us as two, 12 as one
-// for 64 graphs of 64 nodes).
+// Where the work-groups are few both run in one launch (attn_bwd_both), the second forming
+// delta itself: there the launches are the time (16 us as two, 12 as one for 64 graphs of
+// 64 nodes).
 #include "attention_tile.h"
 #include "kernels.h"
 
@@ -19,15 +19,24 @@ namespace e3c {
 namespace attn {
 namespace {
 
+// A tile of keys, and one of rows, in LDS.
+template <class T, int D, int ROWS>
+struct KeyBuffer {
+  Tile<planes<T>(), ROWS, D> k, v;
+  float bias[ROWS];
+};
+template <class T, int D, int ROWS>
+struct RowBuffer {
+  Tile<planes<T>(), ROWS, D> q, g;
+  float lse[ROWS], delta[ROWS];
+};
+
 template <class T, int D, int RW, int TK, int BUF, bool VEC>
-__device__ __forceinline__ void bwd_q(const Params& p, const Where& place) {
-  constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
-  struct Buffer {
-    Tile<P, TK, D> k, v;
-    float bias[TK];
-  };
+__device__ __forceinline__ void bwd_q(const Params& p, const Where& place, KeyBuffer<T, D, TK>& first,
+                                      KeyBuffer<T, D, TK>& second) {
+  typedef KeyBuffer<T, D, TK> Buffer;
   static_assert(BUF == 2 || !(sizeof(T) == 2 && VEC), "loads straight to LDS need the other buffer");
-  __shared__ __attribute__((aligned(16))) Buffer first, second;
+  constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -143,14 +152,11 @@ __device__ __forceinline__ void bwd_q(const Params& p, const Where& place) {
 }
 
 template <class T, int D, int RW, int TQ, int BUF, bool VEC, bool OWN>
-__device__ __forceinline__ void bwd_kv(const Params& p, const Where& place) {
-  constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
-  struct Buffer {
-    Tile<P, TQ, D> q, g;
-    float lse[TQ], delta[TQ];
-  };
+__device__ __forceinline__ void bwd_kv(const Params& p, const Where& place, RowBuffer<T, D, TQ>& first,
+                                       RowBuffer<T, D, TQ>& second) {
+  typedef RowBuffer<T, D, TQ> Buffer;
   static_assert(BUF == 2 || !(sizeof(T) == 2 && VEC), "loads straight to LDS need the other buffer");
-  __shared__ __attribute__((aligned(16))) Buffer first, second;
+  constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
@@ -168,7 +174,7 @@ __device__ __forceinline__ void bwd_kv(const Params& p, const Where& place) {
   // this split's rows: whole tiles of the graph's
   const int q0 = offset(a.q_ptr, g, a.num_q);
   const int nrows = (offset(a.q_ptr, g + 1, a.num_q) - q0) * p.group;
-  const int tiles = nrows > 0 ? (nrows + TQ - 1) / TQ : 0, per = (tiles + p.splits - 1) / p.splits;
+  const int tiles = nrows > 0 ? (nrows + TQ - 1) / TQ : 0, per = (tiles + p.splits_kv - 1) / p.splits_kv;
   const int r0 = min(split * per, tiles) * TQ;
   const int r1 = min(nrows, min((split + 1) * per, tiles) * TQ);
 
@@ -238,9 +244,9 @@ __device__ __forceinline__ void bwd_kv(const Params& p, const Where& place) {
   else walk<1, TQ>(r0, r1, first, first, use);
 
   if (!key) return;
-  if (p.splits > 1) {
+  if (p.splits_kv > 1) {
     const int width = a.dim_qk + a.dim_v;
-    float* to = p.part + (split * (a.num_k * a.heads_kv) + (long)j * a.heads_kv + c) * width;
+    float* to = p.part_kv + (split * (a.num_k * a.heads_kv) + (long)j * a.heads_kv + c) * width;
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
@@ -276,59 +282,102 @@ __device__ __forceinline__ void bwd_kv(const Params& p, const Where& place) {
 
 template <class T, int D, int RW, int TK, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D) : 1) attn_bwd_q(Params p) {
-  bwd_q<T, D, RW, TK, BUF, VEC>(p, where(blockIdx.x, gridDim.x, p.slots, p.splits));
+  __shared__ __attribute__((aligned(16))) KeyBuffer<T, D, TK> first, second;
+  bwd_q<T, D, RW, TK, BUF, VEC>(p, where(blockIdx.x, gridDim.x, p.slots, p.splits), first, second);
 }
 template <class T, int D, int RW, int TQ, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D) : 1) attn_bwd_kv(Params p) {
-  bwd_kv<T, D, RW, TQ, BUF, VEC, false>(p, where(blockIdx.x, gridDim.x, p.slots, p.splits));
+  __shared__ __attribute__((aligned(16))) RowBuffer<T, D, TQ> first, second;
+  bwd_kv<T, D, RW, TQ, BUF, VEC, false>(p, where(blockIdx.x, gridDim.x, p.slots_kv, p.splits_kv), first, second);
 }
-template <class T, int D, bool VEC>
-__global__ void __launch_bounds__(64) attn_bwd_small(Params p) {
-  constexpr int BUF = sizeof(T) == 2 && VEC ? 2 : 1;
+template <class T, int D, int RW, int ROWS, int BUF, bool VEC>
+__global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D) : 1) attn_bwd_both(Params p) {
+  union Buffer {
+    KeyBuffer<T, D, ROWS> keys;
+    RowBuffer<T, D, ROWS> rows;
+  };
+  __shared__ __attribute__((aligned(16))) Buffer first, second;
   const int b = blockIdx.x, n = p.first_blocks;
-  if (b < n) bwd_q<T, D, 1, 32, BUF, VEC>(p, where(b, n, p.slots, 1));
-  else bwd_kv<T, D, 1, 32, BUF, VEC, true>(p, where(b - n, gridDim.x - n, p.slots_kv, 1));
+  if (b < n)
+    bwd_q<T, D, RW, ROWS, BUF, VEC>(p, where(b, n, p.slots, p.splits), first.keys, second.keys);
+  else
+    bwd_kv<T, D, RW, ROWS, BUF, VEC, true>(p, where(b - n, gridDim.x - n, p.slots_kv, p.splits_kv), first.rows,
+                                           second.rows);
 }
 
-// Sums the splits: element d < dim of row (i, head) of `width` floats, times factor.  Four
-// waves of a work-group take 64 elements, each a quarter of the splits, eight at a time.
+// Sums the splits of all three gradients.  `each` elements to a work-group: 256, a thread each,
+// or 64, and four waves share each one's splits, eight at a time.
+struct Sum {
+  const float* part;
+  long rows;            // (i, head)
+  int width, from, dim; // elements from .. from + dim - 1 of `width`
+  int heads, splits, each;
+  unsigned blocks;
+  float factor;
+  void* out;
+  long out_row, out_head;
+};
+struct Sums {
+  Sum of[3];
+};
 template <class T>
-__global__ void __launch_bounds__(256) attn_sum(const float* part, long rows, int width, int from, int dim, int heads,
-                                                int splits, float factor, T* out, long out_row, long out_head) {
+__global__ void __launch_bounds__(256) attn_sum(Sums all) {
   __shared__ float red[4][64];
+  unsigned b = blockIdx.x;
+  int which = 0;
+  while (which < 2 && b >= all.of[which].blocks) b -= all.of[which++].blocks;
+  const Sum& m = all.of[which];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const long i = (long)blockIdx.x * 64 + lane;
-  const long at = i / dim;
-  const int d = (int)(i - at * dim);
-  const float* q = part + at * width + from + d;
+  const bool wide = m.each == 256;
+  const long i = (long)b * m.each + (wide ? (int)threadIdx.x : lane), at = i / m.dim;
+  const int d = (int)(i - at * m.dim);
+  const float* q = m.part + at * m.width + m.from + d;
+  const long step = m.rows * m.width;
   float v = 0.0f;
-  if (at < rows) {
-    int s = w;
-    for (; s + 28 < splits; s += 32) {
-      float x[8];
+  if (at < m.rows) {
+    if (wide) {
+#pragma unroll 4
+      for (int s = 0; s < m.splits; ++s) v += q[s * step];
+    } else {
+      int s = w;
+      for (; s + 28 < m.splits; s += 32) {
+        float x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = q[(s + 4 * k) * rows * width];
+        for (int k = 0; k < 8; ++k) x[k] = q[(s + 4 * k) * step];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v += x[k];
+        for (int k = 0; k < 8; ++k) v += x[k];
+      }
+      for (; s < m.splits; s += 4) v += q[s * step];
     }
-    for (; s < splits; s += 4) v += q[s * rows * width];
   }
-  red[w][lane] = v;
-  __syncthreads();
-  if (w == 0 && at < rows) {
+  if (!wide) {
+    red[w][lane] = v;
+    __syncthreads();
+    if (w > 0) return;
     v = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
-    out[at / heads * out_row + at % heads * out_head + d] = (T)(v * factor);
   }
+  if (at < m.rows)
+    ((T*)m.out)[at / m.heads * m.out_row + at % m.heads * m.out_head + d] = (T)(v * m.factor);
 }
 
+// The sums that p's splits ask for; none (blocks 0) where there is one split.
+Sum sum_of(const float* part, long rows, int width, int from, int dim, int heads, int splits, float factor, void* out,
+           long row, long head) {
+  Sum m{part, rows, width, from, dim, heads, splits, splits <= 8 ? 256 : 64, 0, factor, out, row, head};
+  if (splits > 1) m.blocks = (unsigned)((rows * dim + m.each - 1) / m.each);
+  return m;
+}
 template <class T>
-hipError_t sum(const Params& p, long rows, int width, int from, int dim, int heads, float factor, void* out, long row,
-               long head, hipStream_t s) {
-  const long blocks = (rows * dim + 63) / 64;
-  if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
-  if (blocks > 0)
-    hipLaunchKernelGGL(attn_sum<T>, dim3((unsigned)blocks), dim3(256), 0, s, p.part, rows, width, from, dim, heads,
-                       p.splits, factor, (T*)out, row, head);
+hipError_t sums(const Params& p, hipStream_t s) {
+  const e3conv_attention_args& a = p.a;
+  const long nq = a.num_q * a.heads_q, nk = a.num_k * a.heads_kv;
+  const int width = a.dim_qk + a.dim_v;
+  const Sums all{{sum_of(p.part, nq, a.dim_qk, 0, a.dim_qk, a.heads_q, p.splits, a.scale, p.gq, p.gq_row, p.gq_head),
+                  sum_of(p.part_kv, nk, width, 0, a.dim_qk, a.heads_kv, p.splits_kv, a.scale, p.gk, p.gk_row, p.gk_head),
+                  sum_of(p.part_kv, nk, width, a.dim_qk, a.dim_v, a.heads_kv, p.splits_kv, 1.0f, p.gv, p.gv_row,
+                         p.gv_head)}};
+  const unsigned blocks = all.of[0].blocks + all.of[1].blocks + all.of[2].blocks;
+  if (blocks > 0) hipLaunchKernelGGL(attn_sum<T>, dim3(blocks), dim3(256), 0, s, all);
   return hipGetLastError();
 }
 
@@ -343,10 +392,6 @@ Shape shape_kv(const e3conv_attention_args& a) {
   const int dim = a.dim_qk > a.dim_v ? a.dim_qk : a.dim_v;
   return choose(a.num_k, a.num_q * (a.heads_q / a.heads_kv), a.num_graphs, a.heads_kv,
                 waves_kv(f32, padded(dim)), unit_us(f32, dim, true), a.dim_qk + a.dim_v);
-}
-
-size_t delta_bytes(const e3conv_attention_args& a) {
-  return ((size_t)a.num_q * a.heads_q * sizeof(float) + 15) / 16 * 16;
 }
 
 // Rows of a tile and buffers: 64 and two where they fit 64 KiB of LDS and the registers of two
@@ -381,86 +426,85 @@ void launch_kv(const Params& p, int rw, unsigned grid, hipStream_t s) {
   else launch_kv<T, D, false>(p, rw, grid, s);
 }
 
+template <class T, int D, bool VEC>
+void launch_both(const Params& p, int rw, unsigned grid, hipStream_t s) {
+  typedef Tiling<T, D, VEC> L;
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_both<T, D, 4, L::ROWS, L::BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_both<T, D, 1, 32, L::BUF1, VEC>), dim3(grid), dim3(64), 0, s, p);
+}
 template <class T, int D>
-void launch_small(const Params& p, unsigned grid, hipStream_t s) {
-  if (p.vec) hipLaunchKernelGGL((attn_bwd_small<T, D, true>), dim3(grid), dim3(64), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_small<T, D, false>), dim3(grid), dim3(64), 0, s, p);
+void launch_both(const Params& p, int rw, unsigned grid, hipStream_t s) {
+  if (p.vec) launch_both<T, D, true>(p, rw, grid, s);
+  else launch_both<T, D, false>(p, rw, grid, s);
 }
 
-// Whether both kernels have work-groups of one wave and no splits.
-bool small(const e3conv_attention_args& a) {
-  const Shape q = shape_q(a), kv = shape_kv(a);
-  return q.rw == 1 && kv.rw == 1 && q.splits == 1 && kv.splits == 1 &&
-         ((long)q.slots + kv.slots) * a.heads_kv <= 0x7fffffffL;
+// Whether both kernels go in one launch: work-groups of one size, and either of one wave without
+// splits (small graphs), or not more of them than places.
+bool together(const e3conv_attention_args& a, const Shape& q, const Shape& kv) {
+  if (q.rw != kv.rw) return false;
+  const long blocks = ((long)q.slots * q.splits + (long)kv.slots * kv.splits) * a.heads_kv;
+  if (q.rw == 1 && q.splits == 1 && kv.splits == 1) return blocks <= 0x7fffffffL;
+  const int dim = a.dim_qk > a.dim_v ? a.dim_qk : a.dim_v;
+  return blocks <= 256 * (q.rw == 1 ? 4 : waves_kv(a.dtype == E3CONV_F32, padded(dim)));
 }
 
 template <class T>
-hipError_t backward(Params p, hipStream_t s) {
+hipError_t backward(Params p, const Shape& q, const Shape& kv, hipStream_t s) {
   const e3conv_attention_args& a = p.a;
   const int dim = a.dim_qk > a.dim_v ? a.dim_qk : a.dim_v;
-  if (small(a)) {
-    const Shape q = shape_q(a), kv = shape_kv(a);
+  p.slots = q.slots;
+  p.splits = q.splits;
+  p.slots_kv = kv.slots;
+  p.splits_kv = kv.splits;
+  const long nq = (long)q.slots * q.splits * a.heads_kv, nk = (long)kv.slots * kv.splits * a.heads_kv;
+  if (nq > 0x7fffffffL || nk > 0x7fffffffL) return hipErrorInvalidValue;
+  if (together(a, q, kv)) {
     p.delta = nullptr;
-    p.splits = 1;
-    p.slots = q.slots;
-    p.slots_kv = kv.slots;
-    p.first_blocks = q.slots * a.heads_kv;
-    const unsigned grid = (unsigned)(p.first_blocks + kv.slots * a.heads_kv);
-    if (dim <= 32) launch_small<T, 32>(p, grid, s);
-    else if (dim <= 64) launch_small<T, 64>(p, grid, s);
-    else launch_small<T, 128>(p, grid, s);
-    return hipGetLastError();
+    p.first_blocks = (int)nq;
+    if (dim <= 32) launch_both<T, 32>(p, q.rw, (unsigned)(nq + nk), s);
+    else if (dim <= 64) launch_both<T, 64>(p, q.rw, (unsigned)(nq + nk), s);
+    else launch_both<T, 128>(p, q.rw, (unsigned)(nq + nk), s);
+  } else {
+    if (a.num_q > 0) {
+      if (dim <= 32) launch_q<T, 32>(p, q.rw, (unsigned)nq, s);
+      else if (dim <= 64) launch_q<T, 64>(p, q.rw, (unsigned)nq, s);
+      else launch_q<T, 128>(p, q.rw, (unsigned)nq, s);
+    }
+    if (a.num_k > 0) {
+      if (dim <= 32) launch_kv<T, 32>(p, kv.rw, (unsigned)nk, s);
+      else if (dim <= 64) launch_kv<T, 64>(p, kv.rw, (unsigned)nk, s);
+      else launch_kv<T, 128>(p, kv.rw, (unsigned)nk, s);
+    }
   }
-  if (a.num_q > 0) {
-    const Shape sh = shape_q(a);
-    const long grid = (long)sh.slots * sh.splits * a.heads_kv;
-    if (grid > 0x7fffffffL) return hipErrorInvalidValue;
-    p.slots = sh.slots;
-    p.splits = sh.splits;
-    if (dim <= 32) launch_q<T, 32>(p, sh.rw, (unsigned)grid, s);
-    else if (dim <= 64) launch_q<T, 64>(p, sh.rw, (unsigned)grid, s);
-    else launch_q<T, 128>(p, sh.rw, (unsigned)grid, s);
-    hipError_t err = hipGetLastError();
-    if (err == hipSuccess && sh.splits > 1)
-      err = sum<T>(p, a.num_q * a.heads_q, a.dim_qk, 0, a.dim_qk, a.heads_q, a.scale, p.gq, p.gq_row, p.gq_head, s);
-    if (err != hipSuccess) return err;
-  }
-  if (a.num_k > 0) {
-    const Shape sh = shape_kv(a);
-    const long grid = (long)sh.slots * sh.splits * a.heads_kv;
-    if (grid > 0x7fffffffL) return hipErrorInvalidValue;
-    p.slots = sh.slots;
-    p.splits = sh.splits;
-    if (dim <= 32) launch_kv<T, 32>(p, sh.rw, (unsigned)grid, s);
-    else if (dim <= 64) launch_kv<T, 64>(p, sh.rw, (unsigned)grid, s);
-    else launch_kv<T, 128>(p, sh.rw, (unsigned)grid, s);
-    hipError_t err = hipGetLastError();
-    const int width = a.dim_qk + a.dim_v;
-    const long rows = a.num_k * a.heads_kv;
-    if (err == hipSuccess && sh.splits > 1)
-      err = sum<T>(p, rows, width, 0, a.dim_qk, a.heads_kv, a.scale, p.gk, p.gk_row, p.gk_head, s);
-    if (err == hipSuccess && sh.splits > 1)
-      err = sum<T>(p, rows, width, a.dim_qk, a.dim_v, a.heads_kv, 1.0f, p.gv, p.gv_row, p.gv_head, s);
-    if (err != hipSuccess) return err;
-  }
-  return hipSuccess;
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess ? err : sums<T>(p, s);
+}
+
+// Floats of the workspace: delta (where the kernels are two), and the partial results.
+struct Space {
+  size_t delta, q, kv;
+};
+Space space(const e3conv_attention_args& a, const Shape& q, const Shape& kv) {
+  const size_t nq = (size_t)a.num_q * a.heads_q, nk = (size_t)a.num_k * a.heads_kv;
+  const auto aligned = [](size_t n) { return (n + 3) / 4 * 4; };
+  return {together(a, q, kv) ? 0 : aligned(nq), q.splits > 1 ? aligned(q.splits * nq * a.dim_qk) : 0,
+          kv.splits > 1 ? aligned(kv.splits * nk * (a.dim_qk + a.dim_v)) : 0};
 }
 
 }  // namespace
 
-// delta, then one region for the partial results of either kernel in turn.
 size_t backward_workspace(const e3conv_attention_args& a) {
-  if (small(a)) return 0;
-  const Shape sq = shape_q(a), sk = shape_kv(a);
-  const size_t q = sq.splits > 1 ? (size_t)sq.splits * a.num_q * a.heads_q * a.dim_qk : 0;
-  const size_t k = sk.splits > 1 ? (size_t)sk.splits * a.num_k * a.heads_kv * (a.dim_qk + a.dim_v) : 0;
-  return delta_bytes(a) + (q > k ? q : k) * sizeof(float);
+  const Space n = space(a, shape_q(a), shape_kv(a));
+  return (n.delta + n.q + n.kv) * sizeof(float);
 }
 
 hipError_t launch_backward(const Params& given, hipStream_t s) {
   Params p = given;
-  p.part = p.delta + delta_bytes(p.a) / sizeof(float);
-  return p.a.dtype == E3CONV_F32 ? backward<float>(p, s) : backward<__bf16>(p, s);
+  const Shape q = shape_q(p.a), kv = shape_kv(p.a);
+  const Space n = space(p.a, q, kv);
+  p.part = p.delta + n.delta;
+  p.part_kv = p.part + n.q;
+  return p.a.dtype == E3CONV_F32 ? backward<float>(p, q, kv, s) : backward<__bf16>(p, q, kv, s);
 }
 
 }  // namespace attn

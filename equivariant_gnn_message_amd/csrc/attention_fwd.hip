@@ -214,6 +214,33 @@ __global__ void __launch_bounds__(64 * kJoinWaves) attn_join(Params p) {
   if (tid == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+// The same for many rows of few splits: a thread for each element, consecutive ones side by side.
+// (By 16 waves a row, 36 000 rows of 3 splits took 0.6 ms.)
+constexpr int kFewSplits = 32;
+template <class T>
+__global__ void __launch_bounds__(256) attn_join_rows(Params p) {
+  const e3conv_attention_args& a = p.a;
+  const long rows = a.num_q * a.heads_q, i = (long)blockIdx.x * 256 + threadIdx.x, at = i / a.dim_v;
+  if (at >= rows) return;
+  const int d = (int)(i - at * a.dim_v);
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + at;
+  const float* part = p.part + at * a.dim_v + d;
+  float top = -INFINITY, l = 0.0f, v = 0.0f;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, ml[s * rows].x);
+  const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 x = ml[s * rows];
+    const float f = __builtin_amdgcn_exp2f(x.x - base);
+    l = fmaf(f, x.y, l);
+    v = fmaf(f, part[s * rows * a.dim_v], v);
+  }
+  const long qi = at / a.heads_q;
+  const int head = (int)(at - qi * a.heads_q);
+  ((T*)p.out)[qi * p.out_row + head * p.out_head + d] = (T)(l == 0.0f ? 0.0f : v / l);
+  if (d == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
 Shape shape_of(const e3conv_attention_args& a) {
   const bool f32 = a.dtype == E3CONV_F32;
   const int dim = a.dim_qk > a.dim_v ? a.dim_qk : a.dim_v;
@@ -243,6 +270,12 @@ hipError_t forward(const Params& p, int rw, unsigned grid, hipStream_t s) {
   else launch<T, 128>(p, rw, grid, s);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.splits == 1) return err;
+  if (p.splits <= kFewSplits) {
+    const long blocks = ((long)p.a.num_q * p.a.heads_q * p.a.dim_v + 255) / 256;
+    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(attn_join_rows<T>, dim3((unsigned)blocks), dim3(256), 0, s, p);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(attn_join<T>, dim3((unsigned)(p.a.num_q * p.a.heads_q)), dim3(64 * kJoinWaves), 0, s, p);
   return hipGetLastError();
 }

@@ -39,7 +39,7 @@ struct Params {
   int slots;                       // work-group slots of the row (or key) tiles
   int splits;                      // ranges of the other axis, joined by a second kernel
   int first_blocks;                // reverse pass in one launch: its work-groups for grad_q,
-  int slots_kv;                    // and the slots of the others
+  int slots_kv, splits_kv;         // and the slots and splits of the others
   void* out;
   long out_row, out_head;
   float* lse;
@@ -49,6 +49,7 @@ struct Params {
   long gq_row, gq_head, gk_row, gk_head, gv_row, gv_head;
   float* delta;                    // (num_q, heads_q), reverse pass
   float* part;                     // partial results of the splits
+  float* part_kv;                  // and those of grad_k and grad_v
   float* part_ml;                  // and their softmax maximum and sum
 };
 

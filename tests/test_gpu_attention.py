@@ -300,6 +300,14 @@ def test_autograd_and_shared_heads():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens_q,lens_k", [([300], [2000]), ([577, 40], [527, 1500]), ([2247], [2247])], ids=str)
+def test_rows_and_keys_split_in_few(dtype, lens_q, lens_k):
+    """Too few row tiles to fill the device, but many rows: a few splits, joined element by element."""
+    mask = (np.random.default_rng(9).random(sum(lens_k)) < 0.9).astype(np.uint8)
+    check(dtype, *draw(111, dtype, lens_q, lens_k, 4, 2, 24, 40), lens_q, lens_k, k_mask=mask)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d,dv", [(16, 16), (33, 20), (64, 64), (100, 128)])
 def test_many_small_graphs(dtype, d, dv):
     """Graphs of at most 64 rows on average take one launch for the whole reverse pass; one of them is much longer."""
@@ -335,8 +343,8 @@ def test_refusals_on_device():
     q, k, v, g = draw(91, "f32", lens, lens, 2, 2, 8, 8)
     p = dev(ptr(lens))
     out, lse = E.e3conv_attention(q, k, v, p, p)
-    lq, lk, lv, lg = draw(92, "f32", [300], [300], 2, 2, 8, 8)
-    lp = dev(ptr([300]))
+    lq, lk, lv, lg = draw(92, "f32", [9000], [9000], 2, 2, 8, 8)
+    lp = dev(ptr([9000]))
     lout, llse = E.e3conv_attention(lq, lk, lv, lp, lp)
     for err, call in (
             (TypeError, lambda: E.e3conv_attention(q, k.bfloat16(), v, p, p)),
