@@ -2,6 +2,7 @@
 // checks, and the parameters of the kernels in attention_fwd.hip and attention_bwd.hip.
 #include <hip/hip_runtime_api.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <string>
@@ -50,9 +51,12 @@ bool vector_rows(const void* p, int64_t row, int64_t head, int dim, int size) {
   const int64_t unit = 16 / size;
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row % unit == 0 && head % unit == 0 && dim % 8 == 0;
 }
-// Whether groups of four elements of the rows are aligned for one store.
-bool vector_stores(const void* p, int64_t row, int64_t head, int size) {
-  return reinterpret_cast<uintptr_t>(p) % (4 * size) == 0 && row % 4 == 0 && head % 4 == 0;
+// Elements of the rows' aligned stores: 8 of bf16, 4, or 0.
+int vector_stores(const void* p, int64_t row, int64_t head, int dim, int size) {
+  const auto aligned = [&](int n) {
+    return reinterpret_cast<uintptr_t>(p) % (n * size) == 0 && row % n == 0 && head % n == 0;
+  };
+  return size == 2 && dim % 8 == 0 && aligned(8) ? 8 : aligned(4) ? 4 : 0;
 }
 
 attn::Params params(const e3conv_attention_args& a) {
@@ -102,7 +106,7 @@ e3conv_status e3conv_attention(const e3conv_attention_args* a, void* out, int64_
   p.out = out;
   p.out_row = out_row;
   p.out_head = out_head;
-  p.vec_st = e3c::vector_stores(out, out_row, out_head, a->dtype == E3CONV_F32 ? 4 : 2);
+  p.vec_st = e3c::vector_stores(out, out_row, out_head, a->dim_v, a->dtype == E3CONV_F32 ? 4 : 2);
   p.lse = lse;
   p.part = static_cast<float*>(workspace);
   const hipError_t err = e3c::attn::launch_forward(p, static_cast<hipStream_t>(stream));
@@ -138,9 +142,9 @@ e3conv_status e3conv_attention_backward(const e3conv_attention_args* a, const vo
   const int size = a->dtype == E3CONV_F32 ? 4 : 2;
   p.vec = p.vec && e3c::vector_rows(out, p.out_row, p.out_head, a->dim_v, size) &&
           e3c::vector_rows(grad_out, p.go_row, p.go_head, a->dim_v, size);
-  p.vec_st = e3c::vector_stores(grad_q, p.gq_row, p.gq_head, size) &&
-             e3c::vector_stores(grad_k, p.gk_row, p.gk_head, size) &&
-             e3c::vector_stores(grad_v, p.gv_row, p.gv_head, size);
+  p.vec_st = std::min({e3c::vector_stores(grad_q, p.gq_row, p.gq_head, a->dim_qk, size),
+                       e3c::vector_stores(grad_k, p.gk_row, p.gk_head, a->dim_qk, size),
+                       e3c::vector_stores(grad_v, p.gv_row, p.gv_head, a->dim_v, size)});
   p.delta = static_cast<float*>(workspace);
   const hipError_t err = e3c::attn::launch_backward(p, static_cast<hipStream_t>(stream));
   if (err != hipSuccess) return e3c::api_hip_fail(err, "attention backward launch");

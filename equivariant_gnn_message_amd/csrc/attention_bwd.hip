@@ -129,26 +129,10 @@ __device__ __forceinline__ void bwd_q(const Params& p, const Where& place, KeyBu
 
   if (!row) return;
   if (p.splits > 1) {
-    float* to = p.part + (split * (a.num_q * a.heads_q) + at) * a.dim_qk;
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float v[4] = {dq[dt][4 * b], dq[dt][4 * b + 1], dq[dt][4 * b + 2], dq[dt][4 * b + 3]};
-        store4(to, 32 * dt + 8 * b + 4 * h, a.dim_qk, v, a.dim_qk % 4 == 0);
-      }
+    store_row(p.part + (split * (a.num_q * a.heads_q) + at) * a.dim_qk, dq, a.dim_qk, 1.0f, true, a.dim_qk % 4 == 0);
     return;
   }
-  T* to = (T*)p.gq + qi * p.gq_row + head * p.gq_head;
-#pragma unroll
-  for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = live ? dq[dt][4 * b + i] * a.scale : 0.0f;
-      store4(to, 32 * dt + 8 * b + 4 * h, a.dim_qk, v, p.vec_st);
-    }
+  store_row((T*)p.gq + qi * p.gq_row + head * p.gq_head, dq, a.dim_qk, a.scale, live, p.vec_st);
 }
 
 template <class T, int D, int RW, int TQ, int BUF, bool VEC, bool OWN>
@@ -247,37 +231,13 @@ __device__ __forceinline__ void bwd_kv(const Params& p, const Where& place, RowB
   if (p.splits_kv > 1) {
     const int width = a.dim_qk + a.dim_v;
     float* to = p.part_kv + (split * (a.num_k * a.heads_kv) + (long)j * a.heads_kv + c) * width;
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        float x[4], y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = live ? dk[dt][4 * b + i] : 0.0f;
-          y[i] = live ? dv[dt][4 * b + i] : 0.0f;
-        }
-        const bool vec = a.dim_qk % 4 == 0 && a.dim_v % 4 == 0;
-        store4(to, 32 * dt + 8 * b + 4 * h, a.dim_qk, x, vec);
-        store4(to + a.dim_qk, 32 * dt + 8 * b + 4 * h, a.dim_v, y, vec);
-      }
+    const bool vec = a.dim_qk % 4 == 0 && a.dim_v % 4 == 0;
+    store_row(to, dk, a.dim_qk, 1.0f, live, vec);
+    store_row(to + a.dim_qk, dv, a.dim_v, 1.0f, live, vec);
     return;
   }
-  T* tk = (T*)p.gk + j * p.gk_row + c * p.gk_head;
-  T* tv = (T*)p.gv + j * p.gv_row + c * p.gv_head;
-#pragma unroll
-  for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      float x[4], y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = live ? dk[dt][4 * b + i] * a.scale : 0.0f;
-        y[i] = live ? dv[dt][4 * b + i] : 0.0f;
-      }
-      store4(tk, 32 * dt + 8 * b + 4 * h, a.dim_qk, x, p.vec_st);
-      store4(tv, 32 * dt + 8 * b + 4 * h, a.dim_v, y, p.vec_st);
-    }
+  store_row((T*)p.gk + j * p.gk_row + c * p.gk_head, dk, a.dim_qk, a.scale, live, p.vec_st);
+  store_row((T*)p.gv + j * p.gv_row + c * p.gv_head, dv, a.dim_v, 1.0f, live, p.vec_st);
 }
 
 template <class T, int D, int RW, int TK, int BUF, bool VEC>

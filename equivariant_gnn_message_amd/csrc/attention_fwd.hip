@@ -127,27 +127,12 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D
   if (p.splits > 1) {
     const long rows = a.num_q * a.heads_q, i = split * rows + at;
     float* to = p.part + i * a.dim_v;
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float v[4] = {o[dt][4 * b], o[dt][4 * b + 1], o[dt][4 * b + 2], o[dt][4 * b + 3]};
-        store4(to, 32 * dt + 8 * b + 4 * h, a.dim_v, v, a.dim_v % 4 == 0);
-      }
+    store_row(to, o, a.dim_v, 1.0f, true, a.dim_v % 4 == 0);
     if (h == 0) reinterpret_cast<float2*>(p.part_ml)[i] = make_float2(m, l);
     return;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  T* to = (T*)p.out + qi * p.out_row + head * p.out_head;
-#pragma unroll
-  for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = live ? o[dt][4 * b + i] * inv : 0.0f;
-      store4(to, 32 * dt + 8 * b + 4 * h, a.dim_v, v, p.vec_st);
-    }
+  store_row((T*)p.out + qi * p.out_row + head * p.out_head, o, a.dim_v, inv, live, p.vec_st);
   if (h == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 

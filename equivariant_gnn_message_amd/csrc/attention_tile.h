@@ -35,7 +35,7 @@ struct Params {
   float c;                         // |scale| log2(e), at least the smallest normal number
   int negate;                      // scale < 0: q enters with its sign changed
   int vec;                         // 16-byte loads of q, k, v, grad_out (and out) rows
-  int vec_st;                      // 4-element stores of the outputs
+  int vec_st;                      // elements of the outputs' aligned stores: 8 (bf16), 4 or 0
   int slots;                       // work-group slots of the row (or key) tiles
   int splits;                      // ranges of the other axis, joined by a second kernel
   int first_blocks;                // reverse pass in one launch: its work-groups for grad_q,
@@ -580,6 +580,36 @@ __device__ __forceinline__ void ahead(Load load, Use use) {
     if (i + W < N) ring[i % W] = load(i + W);
   }
   __builtin_amdgcn_sched_barrier(0x6);
+}
+
+// Stores a wave's transposed result: lane (h, n) has elements 32 dt + 8 b + 4 h + 0 .. 3 of row
+// `to`, in o[dt][4 b ..]; zeros unless live.  bf16 with 16-byte rows: the halves of the wave
+// exchange every other group of four, so that each lane stores eight in a row.
+template <class T, int N>
+__device__ __forceinline__ void store_row(T* to, const f32x16 (&o)[N], int dim, float factor, bool live, int vec) {
+  const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int dt = 0; dt < N; ++dt) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = live ? o[dt][i] * factor : 0.0f;
+    if (sizeof(T) == 2 && vec == 8) {
+#pragma unroll
+      for (int b = 0; b < 4; b += 2) {
+        const auto pair = [&](int i) { return __builtin_bit_cast(unsigned, round2(v[i], v[i + 1])); };
+        const auto r0 = __builtin_amdgcn_permlane32_swap(pair(4 * b), pair(4 * b + 4), false, false);
+        const auto r1 = __builtin_amdgcn_permlane32_swap(pair(4 * b + 2), pair(4 * b + 6), false, false);
+        const int d = 32 * dt + 8 * (b + h);
+        if (d < dim) *reinterpret_cast<uint4*>(to + d) = make_uint4(r0[0], r1[0], r0[1], r1[1]);
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float x[4] = {v[4 * b], v[4 * b + 1], v[4 * b + 2], v[4 * b + 3]};
+        store4(to, 32 * dt + 8 * b + 4 * h, dim, x, vec != 0);
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------ launch shapes ---
