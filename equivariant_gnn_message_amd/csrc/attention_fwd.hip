@@ -6,8 +6,17 @@
 //     S^T (keys x rows) = K Q^T,     out^T (dim x rows) += V^T P^T,
 // a lane keeps one row: maximum and sum of its softmax are sums within the lane
 // and one exchange with the other half of the wave, and P^T is the second
-// product's operand where the first one left it.  The next tile is loaded into
-// registers while the current one is used.
+// product's operand where the first one left it.  One pass over the keys with the running
+// maximum and sum; the next tile is on its way while the current one is used.
+//
+// What bounds it (100 000 nodes in ragged graphs, 8 / 2 heads of 64, bf16: 307 us,
+// 700 TFLOP/s): the vector ALU.  A tile of 64 keys costs a wave 16 products (512
+// cycles) and some 230 vector instructions, 32 of them exponentials at double cost, and the
+// two hardly overlap on a SIMD: multiply-adds of one wave and matrix instructions of another
+// take the sum of their times.  Vector instructions were 74 % of the cycles, products 32 %.
+// LDS conflicts are none (the tiles' permutation); reads are a third of its rate.
+// fp32 has the same form with six products for one; with few rows (one query against 100 000
+// keys, 17.7 us) it is bound by the keys' bytes and the join of the splits.
 #include "attention_tile.h"
 #include "kernels.h"
 

@@ -615,7 +615,9 @@ __device__ __forceinline__ void store_row(T* to, const f32x16 (&o)[N], int dim, 
 // ------------------------------------------------------------ launch shapes ---
 
 // Waves of a SIMD that the registers are kept to: with one, nothing covers the latency of LDS
-// and the barriers.  Forward; the reverse kernels hold twice the operands.
+// and the barriers (grad_q with 128 dimensions, bf16: 322 us with one, 255 with two).
+// Forward, grad_q, and grad_k with grad_v, whose 128-wide bf16 form spills 40 registers when
+// kept to two (628 against 470 us).
 constexpr int waves_fwd(bool f32, int d) { return f32 ? (d == 32 ? 3 : d == 64 ? 2 : 1) : (d == 32 ? 4 : d == 64 ? 3 : 2); }
 constexpr int waves_bwd(bool f32, int d) { return f32 ? (d == 32 ? 2 : 1) : (d == 32 ? 3 : 2); }
 constexpr int waves_kv(bool f32, int d) { return f32 ? (d == 32 ? 2 : 1) : (d == 32 ? 3 : d == 64 ? 2 : 1); }
@@ -631,11 +633,11 @@ struct Shape {
 
 // Work-groups of four waves share each tile of the other axis where a graph has more than 64
 // rows (of a graph of 64 rows two of the four would idle), else of one wave.  The other
-// axis is split where the row tiles leave compute units idle, in the first round of
-// work-groups or the last (628 work-groups on 512 places: 2 rounds; split in four 5 rounds of a
-// quarter each).  The choice minimises the time estimated from `unit`, the us of one
-// work-group for one row of the other axis (measured, below), and the partial results'
-// bytes.  Lengths are on the device: averages stand for them.
+// axis is split where the row tiles leave compute units idle, in the first filling of the
+// chip or the last (628 work-groups on 512 places are 2 fillings; split in four, 5 of a
+// quarter each: 4.3 against 3.7 ms for the reverse pass of 20 000 nodes).  The choice minimises
+// an estimate from `unit`, the us of one work-group for one row of the other axis (below),
+// and the partial results' bytes.  Lengths are on the device: averages stand for them.
 inline Shape choose(long rows, long others, int graphs, int heads, int waves, double unit, int width) {
   const long g = graphs > 0 ? graphs : 1, avg = (rows + g - 1) / g, avg_o = (others + g - 1) / g;
   Shape s;
@@ -647,10 +649,10 @@ inline Shape choose(long rows, long others, int graphs, int heads, int waves, do
   if (most > kMaxSplits) most = kMaxSplits;
   double best = 1e30;
   s.splits = 1;
-  for (long k = 1; k <= most; ++k) {
-    const long rounds = (n * k + places - 1) / places;
+  for (long k = 1; k <= most; k += k < 16 ? 1 : k / 8) {
+    const long fillings = (n * k + places - 1) / places;
     const double join = k > 1 ? 5.0 + (double)k * rows * heads * width * 8e-6 / 3.0 : 0.0;
-    const double us = rounds * (double)avg_o / k * unit + join;
+    const double us = fillings * (double)avg_o / k * unit + join;
     if (us < 0.95 * best) {
       best = us;
       s.splits = (int)k;
@@ -658,9 +660,9 @@ inline Shape choose(long rows, long others, int graphs, int heads, int waves, do
   }
   return s;
 }
-// us of a work-group for one key (forward) or one row or key (reverse), with its
-// neighbours on the compute unit: bf16, 64 dimensions, 0.04; three products more and fp32's
-// six-fold products in proportion to what was measured.
+// us of a work-group of four waves for one key or row, with its neighbours on the compute unit.
+// Measured: forward in bf16 with 64 dimensions, 309 us for 8.2 fillings of the chip over 1000 keys; the
+// others in proportion to their own measurements.  It decides between splits only.
 inline double unit_us(bool f32, int dim, bool backward) {
   return 0.04 * (dim <= 32 ? 0.7 : dim <= 64 ? 1.0 : 2.0) * (f32 ? 1.7 : 1.0) * (backward ? 1.5 : 1.0);
 }
