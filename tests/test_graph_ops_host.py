@@ -137,3 +137,16 @@ def test_attention_workspace_of_any_sizes(num_q, num_k, graphs, dtype):
 def test_group_norm_workspace_of_any_sizes(rows, graphs):
     a = norm_args(num_rows=rows, num_graphs=graphs)
     assert E.e3conv_group_norm_workspace_size(a) >= 0 and E.e3conv_group_norm_workspace_size(a, True) >= 0
+
+
+def test_sources_of_these_operators_leave_the_counter_records_valid(tmp_path, monkeypatch):
+    """The convolution's counter records are keyed by its own sources."""
+    import bench
+    csrc = tmp_path / "equivariant_gnn_message_amd" / "csrc"
+    csrc.mkdir(parents=True)
+    (csrc / "k.hip").write_text("__global__ void k() {}\n")
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    before = bench.kernel_source_hash()
+    (csrc / "attention.hip").write_text("__global__ void a() {}\n")
+    (csrc / "group_norm.hip").write_text("__global__ void g() {}\n")
+    assert bench.kernel_source_hash() == before
