@@ -63,12 +63,10 @@ attn::Params params(const e3conv_attention_args& a) {
   attn::Params p{};
   p.a = a;
   p.group = a.heads_q / a.heads_kv;
-  // ceil(2^(31 + l) / group) with 2^l >= group: exact for every row below 2^31
-  int l = 0;
-  while ((1 << l) < p.group) ++l;
-  p.magic = (unsigned)((((uint64_t)1 << (31 + l)) + p.group - 1) / p.group);
-  p.shift = l - 1;
-  p.group_log2 = 1 << l == p.group ? l : -1;
+  const attn::GroupDiv by = attn::group_div(p.group);
+  p.magic = by.magic;
+  p.shift = by.shift;
+  p.group_log2 = by.log2;
   p.negate = a.scale < 0.0f;
   // a zero scale: logits far below one unit of the sums' rounding, infinities as they are
   p.c = std::fabs(a.scale) * attn::kLog2e;

@@ -52,8 +52,8 @@ __device__ __forceinline__ void bwd_q(const Params& p, const Where& place, KeyBu
   const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
   const int q0 = offset(a.q_ptr, g, a.num_q);
   const int nrows = (offset(a.q_ptr, g + 1, a.num_q) - q0) * p.group;
-  const int r0 = (slot - first_slot(a.q_ptr, g, a.num_q, p.group, BM)) * BM;
-  if (r0 >= nrows) return;
+  const int r0 = tile_start(slot, first_slot(a.q_ptr, g, a.num_q, p.group, BM), BM, nrows);
+  if (r0 < 0) return;
 
   const int r = r0 + 32 * w + n;
   const bool row = r < nrows, idle = r0 + 32 * w >= nrows;   // idle: a wave without rows only loads
@@ -155,8 +155,9 @@ __device__ __forceinline__ void bwd_kv(const Params& p, const Where& place, RowB
   constexpr int BN = 32 * RW;
   const int g = graph_of_slot(a.k_ptr, a.num_graphs, a.num_k, 1, BN, slot);
   const int kb = offset(a.k_ptr, g, a.num_k), ke = offset(a.k_ptr, g + 1, a.num_k);
-  const int j0 = kb + (slot - first_slot(a.k_ptr, g, a.num_k, 1, BN)) * BN;
-  if (j0 >= ke) return;
+  const int first_key = tile_start(slot, first_slot(a.k_ptr, g, a.num_k, 1, BN), BN, ke - kb);
+  if (first_key < 0) return;
+  const int j0 = kb + first_key;
 
   const int j = j0 + 32 * w + n;
   const bool key = j < ke, idle = j0 + 32 * w >= ke;   // idle: a wave without keys only loads

@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D
   const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
   const int q0 = offset(a.q_ptr, g, a.num_q);
   const int nrows = (offset(a.q_ptr, g + 1, a.num_q) - q0) * p.group;
-  const int r0 = (slot - first_slot(a.q_ptr, g, a.num_q, p.group, BM)) * BM;
-  if (r0 >= nrows) return;
+  const int r0 = tile_start(slot, first_slot(a.q_ptr, g, a.num_q, p.group, BM), BM, nrows);
+  if (r0 < 0) return;
 
   const int r = r0 + 32 * w + n;
   const bool row = r < nrows, idle = r0 + 32 * w >= nrows;   // idle: a wave without rows only loads

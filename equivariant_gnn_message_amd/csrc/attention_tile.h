@@ -12,6 +12,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "attention_slots.h"
 #include "e3conv.h"
 
 namespace e3c {
@@ -268,37 +269,22 @@ __device__ __forceinline__ float other_half(float v) {
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
-// Offset i of a segment table, kept inside [0, n] whatever the table holds.
-__device__ __forceinline__ int offset(const int* ptr, int i, long n) {
-  const int v = ptr[i];
-  return v < 0 ? 0 : (v > n ? (int)n : v);
+__device__ __forceinline__ int offset(const int* ptr, int i, long n) { return clamp_offset(ptr[i], n); }
+__device__ __forceinline__ int first_slot(const int* ptr, int g, long n, int mult, int tile) {
+  return slot_at(offset(ptr, g, n), g, mult, tile);
 }
-
-// Row tiles of graph g (rows first(g) .. first(g + 1)) take the slots first(g) / tile + g
-// and on: enough for ceil(rows / tile) tiles, without a host-side list of lengths.
-// Returns the graph of a slot: the last g whose first slot is not beyond it.  64
-// offsets are tried at a time.
 __device__ __forceinline__ int graph_of_slot(const int* ptr, int graphs, long n, int mult, int tile, int slot) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, count = graphs;
-  while (count > 1) {
-    const int step = (count + 63) >> 6, i = lane * step;
+  return __builtin_amdgcn_readfirstlane(search_graph(graphs, [&](int lo, int step, int count) {
+    const int i = lane * step;
     bool before = false;
-    if (i < count) before = offset(ptr, lo + i, n) * mult / tile + lo + i <= slot;
-    const int hits = max(__popcll(__ballot(before)), 1);
-    lo += (hits - 1) * step;
-    count = min(step, count - (hits - 1) * step);
-  }
-  return __builtin_amdgcn_readfirstlane(lo);
-}
-__device__ __forceinline__ int first_slot(const int* ptr, int g, long n, int mult, int tile) {
-  return offset(ptr, g, n) * mult / tile + g;
+    if (i < count) before = first_slot(ptr, lo + i, n, mult, tile) <= slot;
+    return __popcll(__ballot(before));
+  }));
 }
 
 // Row r of a graph's rows is head r % group of query r / group.
-__device__ __forceinline__ int query_of(const Params& p, int r) {
-  return p.group == 1 ? r : (int)(__umulhi((unsigned)r, p.magic) >> p.shift);
-}
+__device__ __forceinline__ int query_of(const Params& p, int r) { return div_group(r, p.group, p.magic, p.shift); }
 
 // A work-group's loads of a tile of ROWS rows of two operands that share their row order (k and
 // v, or q and grad_out): issue() starts them, finish() leaves the tile in LDS, with zeros
