@@ -624,7 +624,7 @@ def _written(t, name):
 
 
 def _enter(index, stream):
-    """(stream handle, stream object to record allocations on or None) of a call on a device."""
+    """(stream handle, stream object where it is not the current one, else None) of a call on a device."""
     if index != _torch._C._cuda_getDevice():
         raise ValueError(f"operands are on cuda:{index}, the current device is cuda:{_torch.cuda.current_device()}")
     current = _torch._C._cuda_getCurrentRawStream(index)
@@ -633,10 +633,12 @@ def _enter(index, stream):
     handle = int(getattr(stream, "cuda_stream", stream))
     if handle == current:
         return handle, None
+    if handle == 0:
+        return handle, _torch.cuda.default_stream(index)
     return handle, stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(handle, device=index)
 
 
-def _workspace(given, size_of, args, like, other, backward=0):
+def _workspace(given, size_of, args, like, backward=0):
     """(address, bytes, tensor) of the caller's workspace, or of one allocated for the call."""
     if given is not None:
         if given.get_device() != like.get_device() or not given.is_contiguous() or given.data_ptr() % 16:
@@ -646,15 +648,24 @@ def _workspace(given, size_of, args, like, other, backward=0):
     _check(size_of(args, backward, ctypes.byref(n)))
     if n.value == 0:
         return None, 0, None
-    t = _recorded(like.new_empty((n.value,), dtype=_torch.uint8), other)
+    t = like.new_empty((n.value,), dtype=_torch.uint8)
     return t.data_ptr(), n.value, t
 
 
-def _recorded(t, other):
-    """A new tensor; its memory, once freed, is not reused before the other stream is done with it."""
-    if other is not None:
-        t.record_stream(other)
-    return t
+def _on(other, call, *args):
+    """call(*args) on a stream that is not the current one.
+
+    Allocations come from that stream's pool: what the current stream's pool hands out may still be
+    read by work queued on the current stream, which the other one does not wait for.  Results, once
+    freed, are not reused before the current stream, where the caller goes on, is done with them.
+    """
+    current = _torch.cuda.current_stream(other.device)
+    with _torch.cuda.stream(other):
+        results = call(*args)
+    for t in results:
+        if t is not None:
+            t.record_stream(current)
+    return results
 
 
 def _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask):
@@ -698,23 +709,27 @@ def e3conv_attention(q, k, v, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None
     q (num_q, heads_q, dim_qk), k (num_k, heads_kv, dim_qk), v (num_k, heads_kv, dim_v), fp32 or bf16, any
     strides but unit along the last axis; q_ptr, k_ptr int32 offsets of the graphs; scale defaults to
     dim_qk ** -0.5; masks are bool or uint8, one value per row, 0 for padding.  lse fp32 (num_q, heads_q).
+    stream: a torch stream or raw handle in place of the current stream.  The operands have to be ready on
+    it; what the call allocates belongs to it, and the caller orders its own use of the results.
     """
     lib = _lib or load_library()
     args = _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask)
     index, shape = q.get_device(), (args.num_q, args.heads_q, args.dim_v)
     handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, e3conv_attention, q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask, out, lse, workspace)
     if out is None:
-        out = _recorded(q.new_empty(shape), other)
+        out = q.new_empty(shape)
         row, head = shape[1] * shape[2], shape[2]
     else:
         row, head, _ = _rows_of(out, "out", q.dtype, index, shape)
         _written(out, "out")
     if lse is None:
-        lse = _recorded(q.new_empty(shape[:2], dtype=_torch.float32), other)
+        lse = q.new_empty(shape[:2], dtype=_torch.float32)
     else:
         _dense(lse, "lse", _torch.float32, index, shape[0] * shape[1])
     ref = ctypes.byref(args)
-    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q, other)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q)
     _check(lib.e3conv_attention(ref, out.data_ptr(), row, head, lse.data_ptr(), ws, nbytes, handle))
     return out, lse
 
@@ -731,8 +746,11 @@ def e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale=N
     strides = _rows_of(out, "out", dt, index, shape)[:2] + _rows_of(grad_out, "grad_out", dt, index, shape)[:2]
     lse_at = _dense(lse, "lse", _torch.float32, index, shape[0] * shape[1])
     handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, e3conv_attention_backward, q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale, q_mask, k_mask,
+                   grads, workspace)
     if grads is None:
-        grads = [_recorded(_torch.empty_like(t), other) for t in (q, k, v)]
+        grads = [_torch.empty_like(t) for t in (q, k, v)]
         for t in grads:
             strides += t.stride()[:2]
     else:
@@ -741,7 +759,7 @@ def e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale=N
             _written(t, name)
     gq, gk, gv = grads
     ref = ctypes.byref(args)
-    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q, other, 1)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q, 1)
     _check(lib.e3conv_attention_backward(
         ref, out.data_ptr(), lse_at, grad_out.data_ptr(), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
         (I64 * 10)(*strides), ws, nbytes, handle))
@@ -786,15 +804,17 @@ def e3conv_group_norm(x, row_ptr, groups, weight=None, bias=None, eps=1e-5, acti
     args = _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask)
     index, shape = x.get_device(), (args.num_graphs, args.groups)
     handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, e3conv_group_norm, x, row_ptr, groups, weight, bias, eps, activation, row_mask, out, workspace)
     if out is None:
-        out, row = _recorded(x.new_empty(x.shape), other), args.channels
+        out, row = x.new_empty(x.shape), args.channels
     else:
         row, _ = _rows_of(out, "out", x.dtype, index, x.shape)
         _written(out, "out")
-    mean = _recorded(x.new_empty(shape, dtype=_torch.float32), other)
-    rstd = _recorded(_torch.empty_like(mean), other)
+    mean = x.new_empty(shape, dtype=_torch.float32)
+    rstd = _torch.empty_like(mean)
     ref = ctypes.byref(args)
-    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x, other)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x)
     _check(lib.e3conv_group_norm(ref, out.data_ptr(), row, mean.data_ptr(), rstd.data_ptr(), ws, nbytes, handle))
     return out, mean, rstd
 
@@ -810,14 +830,17 @@ def e3conv_group_norm_backward(x, row_ptr, groups, weight, bias, activation, mea
     rstd_at = _dense(rstd, "rstd", _torch.float32, index, size)
     gy_row, _ = _rows_of(grad_y, "grad_y", x.dtype, index, x.shape)
     handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, e3conv_group_norm_backward, x, row_ptr, groups, weight, bias, activation, mean, rstd, grad_y,
+                   row_mask, grad_x, workspace)
     if grad_x is None:
-        grad_x, row = _recorded(x.new_empty(x.shape), other), args.channels
+        grad_x, row = x.new_empty(x.shape), args.channels
     else:
         row, _ = _rows_of(grad_x, "grad_x", x.dtype, index, x.shape)
         _written(grad_x, "grad_x")
-    gw, gb = (None if t is None else _recorded(_torch.empty_like(t), other) for t in (weight, bias))
+    gw, gb = (None if t is None else _torch.empty_like(t) for t in (weight, bias))
     ref = ctypes.byref(args)
-    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x, other, 1)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x, 1)
     _check(lib.e3conv_group_norm_backward(
         ref, mean_at, rstd_at, grad_y.data_ptr(), gy_row, grad_x.data_ptr(), row,
         None if gw is None else gw.data_ptr(), None if gb is None else gb.data_ptr(), ws, nbytes, handle))
