@@ -1093,8 +1093,8 @@ def _attention_function():
         @staticmethod
         def forward(ctx, q, k, v, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None):
             out, lse = e3conv_attention(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask)
-            ctx.save_for_backward(q, k, v, out, lse)
-            ctx.graph = (q_ptr, k_ptr, scale, q_mask, k_mask)
+            ctx.save_for_backward(q, k, v, out, lse, q_ptr, k_ptr, q_mask, k_mask)
+            ctx.scale = scale
             return out
 
         @staticmethod
@@ -1102,7 +1102,9 @@ def _attention_function():
         def backward(ctx, grad_out):
             if grad_out.stride(-1) != 1:
                 grad_out = grad_out.contiguous()
-            return e3conv_attention_backward(*ctx.saved_tensors, grad_out, *ctx.graph) + (None,) * 5
+            q, k, v, out, lse, q_ptr, k_ptr, q_mask, k_mask = ctx.saved_tensors
+            return e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, ctx.scale, q_mask,
+                                             k_mask) + (None,) * 5
 
     return AttentionFunction
 
@@ -1120,15 +1122,15 @@ def _group_norm_function():
         def forward(ctx, x, row_ptr, groups, weight=None, bias=None, eps=1e-5, activation="none",
                     row_mask=None):
             y, mean, rstd = e3conv_group_norm(x, row_ptr, groups, weight, bias, eps, activation, row_mask)
-            ctx.save_for_backward(x, weight, bias, mean, rstd)
-            ctx.graph = (row_ptr, groups, activation, row_mask)
+            ctx.save_for_backward(x, weight, bias, mean, rstd, row_ptr, row_mask)
+            ctx.options = (groups, activation)
             return y
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, grad_y):
-            x, weight, bias, mean, rstd = ctx.saved_tensors
-            row_ptr, groups, activation, row_mask = ctx.graph
+            x, weight, bias, mean, rstd, row_ptr, row_mask = ctx.saved_tensors
+            groups, activation = ctx.options
             if grad_y.stride(-1) != 1:
                 grad_y = grad_y.contiguous()
             gx, gw, gb = e3conv_group_norm_backward(x, row_ptr, groups, weight, bias, activation, mean, rstd,
