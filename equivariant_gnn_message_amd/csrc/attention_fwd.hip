@@ -69,7 +69,10 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D
   f32x16 o[D / 32];
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) o[dt] = f32x16{};
-  float m = -INFINITY, l = 0.0f;   // of the logits in units of log 2; l: this half's keys
+  // of the logits in units of log 2; l: this half's keys, too large by `over`.  A tile's
+  // exponentials are summed by themselves and added with compensation: keys of few kinds give equal terms, whose
+  // roundings all have one sign (100 000 keys of two kinds: lse off by 3.1e-4 with l += e key by key).
+  float m = -INFINITY, l = 0.0f, over = 0.0f;
 
   const auto use = [&](Buffer& now, int from, Buffer& next) {
     Tile<P, TK, D>&kt = now.k, &vt = now.v;
@@ -100,12 +103,14 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D
       const float f = __builtin_amdgcn_exp2f(m - base);
       m = mn;
       l *= f;
+      over *= f;
 #pragma unroll
       for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[dt][i] *= f;
     }
     const float base = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
 #pragma unroll
     for (int b = 0; b < TK / 32; ++b)
 #pragma unroll
@@ -114,18 +119,23 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           e[i] = __builtin_amdgcn_exp2f(fmaf(s[b][8 * t + i], p.c, -base));
-          l += e[i];
+          sum += e[i];
         }
-        // bf16: P rounded for its product, the sum l from the unrounded values
+        // bf16: P rounded for its product, the sum from the unrounded values
         Frag<P> f;
         to_frag(e, f);
         ahead<D / 32, W, Frag<P>>([&](int dt) { return vt.columns(32 * b + 16 * t, dt, lane); },
                                   [&](int dt, const Frag<P>& x) { o[dt] = mma(x, f, o[dt]); });
       }
+    sum -= over;
+    const float both = l + sum;
+    over = (both - l) - sum;
+    l = both;
   };
   if constexpr (BUF == 2) walk<2, TK>(k0, k1, first, second, use);
   else walk<1, TK>(k0, k1, first, first, use);
 
+  l -= over;
   l += other_half(l);
   if (!row) return;
   const long at = (long)qi * a.heads_q + head;
