@@ -12,8 +12,8 @@
 //           from its chunks in chunk order (where graphs have few chunks, every
 //           work-group of the next launch does this for its graph instead);
 //   apply   per chunk: the rows; and in the reverse pass the weight and bias gradients.
-// Sums are taken about the channel's first counted value of the chunk, and chunks are
-// joined about the common mean, so a mean far from zero costs no digits of the variance.
+// Variances are squared deviations from the mean of the rows before, joined by counts and means,
+// so neither a mean far from zero nor an outlying row costs digits.
 // Memory bound: the rows are read twice and written once where a graph has more than one
 // chunk (the second time from cache where the tensor fits it), else once and once: 1M rows of
 // 64 channels bf16 in 82 us, three passes of 128 MB at 4.7 TB/s.  Calls of some MB are bound by
@@ -202,18 +202,54 @@ __device__ __forceinline__ Place place(const NormParams& p) {
   return q;
 }
 
-// Adds s1 and s2 over the threads of one unit; the result is in those of row 0.
-template <int V>
-__device__ void add_rows(const Place& q, float2* red, float (&s1)[V], float (&s2)[V]) {
+// s1 and s2 of two threads of one unit: their sums, or
+struct Add {
+  static constexpr bool COUNTED = false;
+  template <int V>
+  static __device__ __forceinline__ void join(float&, float, float (&s1)[V], float (&s2)[V], const float (&t1)[V],
+                                              const float (&t2)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s1[i] += t1[i];
+      s2[i] += t2[i];
+    }
+  }
+};
+// mean and squared deviations of n and of k values, of them all: a sum of terms that are not
+// negative, so no cancellation wherever the means lie.
+struct Moments {
+  static constexpr bool COUNTED = true;
+  template <int V>
+  static __device__ __forceinline__ void join(float& n, float k, float (&s1)[V], float (&s2)[V], const float (&t1)[V],
+                                              const float (&t2)[V]) {
+    const float all = n + k, f = all > 0.0f ? k * __builtin_amdgcn_rcpf(all) : 0.0f, g = n * f;
+    n = all;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float d = t1[i] - s1[i];
+      s1[i] = fmaf(d, f, s1[i]);
+      s2[i] += fmaf(d * d, g, t2[i]);
+    }
+  }
+};
+// Joins n, s1 and s2 over the threads of one unit; the result is in those of row 0.  Threads of a
+// row have the same n.
+template <class Join, int V>
+__device__ void join_rows(const Place& q, float2* red, float n, float (&s1)[V], float (&s2)[V]) {
+  __shared__ float counts[Join::COUNTED ? NT : 1];
   int rows = q.step, row = q.row;
   bool on = q.on;
+  float k = 0.0f, t1[V], t2[V];
   if (64 % q.width == 0) {     // within a wave first
-    for (int o = 32; o >= q.width; o >>= 1)
+    for (int o = 32; o >= q.width; o >>= 1) {
+      if (Join::COUNTED) k = __shfl_xor(n, o);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        s1[i] += __shfl_xor(s1[i], o);
-        s2[i] += __shfl_xor(s2[i], o);
+        t1[i] = __shfl_xor(s1[i], o);
+        t2[i] = __shfl_xor(s2[i], o);
       }
+      Join::template join<V>(n, k, s1, s2, t1, t2);
+    }
     rows = NT / 64;
     row = threadIdx.x >> 6;
     on = (threadIdx.x & 63) < q.width;
@@ -222,20 +258,29 @@ __device__ void add_rows(const Place& q, float2* red, float (&s1)[V], float (&s2
   while (half < rows) half <<= 1;
   const int unit = q.col;
   for (half >>= 1; half > 0; half >>= 1) {
-    if (on && row >= half && row < rows)
+    if (on && row >= half && row < rows) {
+      if (Join::COUNTED) counts[row - half] = n;
 #pragma unroll
       for (int i = 0; i < V; ++i) red[((row - half) * V + i) * q.width + unit] = make_float2(s1[i], s2[i]);
+    }
     __syncthreads();
-    if (on && row < half && row + half < rows)
+    if (on && row < half && row + half < rows) {
+      if (Join::COUNTED) k = counts[row];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float2 r = red[(row * V + i) * q.width + unit];
-        s1[i] += r.x;
-        s2[i] += r.y;
+        t1[i] = r.x;
+        t2[i] = r.y;
       }
+      Join::template join<V>(n, k, s1, s2, t1, t2);
+    }
     __syncthreads();
     rows = min(rows, half);
   }
+}
+template <int V>
+__device__ __forceinline__ void add_rows(const Place& q, float2* red, float (&s1)[V], float (&s2)[V]) {
+  join_rows<Add, V>(q, red, 0.0f, s1, s2);
 }
 
 // Counted rows of a chunk (in every thread), and the first of them (end if none).
@@ -263,11 +308,11 @@ __device__ int count_rows(const NormParams& p, const Chunk& c, int* first) {
 }
 
 // For this thread's rows of the chunk, N at a time: load(i, row) of all of them, then use(i, row,
-// keep), keep all ones for a row that counts and else 0.  Rows that do not count are computed
+// keep), keep all ones for a row that counts and else 0, then done().  Rows that do not count are computed
 // and their results cleared: a choice by condition becomes a branch for each element (reverse
 // pass of 100 000 masked rows of 64 channels bf16: 30.4 against 28.7 us).
-template <int N, bool MASK, class L, class F>
-__device__ __forceinline__ void rows_of(const NormParams& p, const Chunk& c, const Place& q, L load, F use) {
+template <int N, bool MASK, class L, class F, class D>
+__device__ __forceinline__ void rows_of(const NormParams& p, const Chunk& c, const Place& q, L load, F use, D done) {
   for (int r = c.begin + q.row; r < c.end; r += N * q.step) {
     uint32_t keep[N];
 #pragma unroll
@@ -279,13 +324,18 @@ __device__ __forceinline__ void rows_of(const NormParams& p, const Chunk& c, con
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (r + i * q.step < c.end) use(i, (long)(r + i * q.step), !MASK || keep[i] ? ~0u : 0u);
+    done();
   }
+}
+template <int N, class L, class F, class D>
+__device__ __forceinline__ void each_row(const NormParams& p, const Chunk& c, const Place& q, L load, F use, D done) {
+  if (!q.on) return;
+  if (p.a.row_mask) rows_of<N, true>(p, c, q, load, use, done);
+  else rows_of<N, false>(p, c, q, load, use, done);
 }
 template <int N, class L, class F>
 __device__ __forceinline__ void each_row(const NormParams& p, const Chunk& c, const Place& q, L load, F use) {
-  if (!q.on) return;
-  if (p.a.row_mask) rows_of<N, true>(p, c, q, load, use);
-  else rows_of<N, false>(p, c, q, load, use);
+  each_row<N>(p, c, q, load, use, [] {});
 }
 
 // Calls use(i, group) for the V channels from c0 on.
@@ -416,38 +466,61 @@ __device__ __forceinline__ void write_rows(const NormParams& p, const Chunk& c, 
   });
 }
 
+// Seven waves a SIMD: one register more than 72 costs one of them (4096 graphs of 20 rows of 32
+// channels bf16: 49 us with six, 46 with seven).
 template <class T, int V, int ACT, bool S>
-__global__ void __launch_bounds__(NT) norm_sums(NormParams p) {
+__global__ void __launch_bounds__(NT, 7) norm_sums(NormParams p) {
   const Chunk c = chunk_of(p, blockIdx.x);
   if (c.none) return;
   const Place q = place(p);
   const T* x = (const T*)p.a.x + q.unit * V;
   int first;
   const int n = count_rows(p, c, &first);
-  float at[V], s1[V], s2[V];
+  // Mean and squared deviations of the rows so far.  A batch of four rows is summed about the mean
+  // before it (the first about the chunk's first counted row), and at most the batch's share
+  // of the rows is subtracted from its squares: an outlier costs no digits, whichever row it
+  // is.  (With all rows about the first one: rstd off by 1e-3 where that one is a master
+  // node's, 10 000 times the others, in a chunk of 30 000.)
+  float at[V], mean[V], s2[V], d1[V], d2[V], count = 0.0f, batch = 0.0f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) at[i] = s1[i] = s2[i] = 0.0f;
+  for (int i = 0; i < V; ++i) at[i] = s2[i] = d1[i] = d2[i] = 0.0f;
   if (q.on && n > 0) widen<T, V>(read<T, V>(x + first * p.a.x_row), at);
+#pragma unroll
+  for (int i = 0; i < V; ++i) mean[i] = at[i];
   typename Run<T, V>::type raw[4];
   each_row<4>(p, c, q, [&](int j, long r) { raw[j] = read<T, V>(x + r * p.a.x_row); },
               [&](int j, long, uint32_t keep) {
     float v[V];
     widen<T, V>(raw[j], v);
+    batch += kept(1.0f, keep);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float d = kept(v[i] - at[i], keep);
-      s1[i] += d;
-      s2[i] = fmaf(d, d, s2[i]);
+      const float d = kept(v[i] - mean[i], keep);
+      d1[i] += d;
+      d2[i] = fmaf(d, d, d2[i]);
+    }
+  }, [&] {
+    count += batch;
+    const float inv = count > 0.0f ? __builtin_amdgcn_rcpf(count) : 0.0f;
+    batch = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float d = d1[i] * inv;
+      s2[i] += fmaf(-d, d1[i], d2[i]);
+      mean[i] += d;
+      d1[i] = d2[i] = 0.0f;
     }
   });
+  // of the chunk, per channel, the mean less `at`
+  float s1[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s1[i] = mean[i] - at[i];
   __shared__ float2 red[NT * V];
-  add_rows<V>(q, red, s1, s2);
-  // of the chunk, per channel: mean, and squared deviations from it
+  join_rows<Moments, V>(q, red, q.on ? count : 0.0f, s1, s2);
   const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    s1[i] *= inv;
-    s2[i] = fmaxf(s2[i] - (float)n * s1[i] * s1[i], 0.0f);
+    s2[i] = fmaxf(s2[i], 0.0f);
     s1[i] += at[i];
   }
   const int c0 = q.unit * V;

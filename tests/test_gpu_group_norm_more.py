@@ -1,0 +1,52 @@
+"""Group norm where its sums and its dispatch can go wrong: outlying rows, rows wider than one work-group, results
+larger than the L2s, and more groups than one launch has work-groups.  Bounds: oracle.norm.group_norm."""
+
+import numpy as np
+import pytest
+
+from oracle import norm
+from equivariant_gnn_message_amd import e3conv as E
+
+from ._gpu import say
+from .test_gpu_attention import U, dev, dtype_of, host, ptr
+
+pytestmark = pytest.mark.gpu
+
+
+def inputs(dtype, lens, channels, seed=0):
+    """x, grad_y (device), weight, bias (numpy)."""
+    import torch
+    gen = torch.Generator().manual_seed(seed + channels)
+    n = int(sum(lens))
+    x, g = (torch.randn((n, channels), generator=gen).to(dtype_of(dtype)).cuda() for _ in range(2))
+    w, b = 1 + 0.3 * torch.randn(channels, generator=gen), 0.3 * torch.randn(channels, generator=gen)
+    return x, g, w.numpy(), b.numpy()
+
+
+def compare(dtype, lens, groups, x, g, w, b, act="silu", mask=None, eps=1e-5, out=None, grad_x=None):
+    import torch
+    u, r = U[dtype]
+    p, m = dev(ptr(lens)), None if mask is None else dev(mask)
+    clean = lambda t: host(t) if mask is None else np.where(np.asarray(mask, bool)[:, None], host(t), 0.0)
+    val, tol = norm.group_norm(clean(x), ptr(lens), groups, w, b, float(np.float32(eps)), act, mask, clean(g), u, r)
+    say(f"[group norm] {dtype} rows {x.shape[0]} in {len(lens)} graphs, {x.shape[1]} channels, {groups} groups, {act}")
+    keep = x.clone() if out is x else x
+    y, mean, rstd = E.e3conv_group_norm(x, p, groups, dev(w), dev(b), eps, act, m, out=out)
+    gx, gw, gb = E.e3conv_group_norm_backward(keep, p, groups, dev(w), dev(b), act, mean, rstd, g, m, grad_x=grad_x)
+    torch.cuda.synchronize()
+    for name, t in {"mean": mean, "rstd": rstd, "y": y, "dx": gx, "dw": gw, "dc": gb}.items():
+        off = np.abs(host(t) - val[name])
+        worst = float(np.max(off - tol[name], initial=-1.0))
+        say(f"  {name}: max err {float(np.max(off, initial=0.0)):.3e}, over its bound by {worst:.3e}")
+        assert bool(np.all(np.isfinite(off))) and worst <= 1e-30, (name, worst)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("big", [100.0, 10000.0])
+@pytest.mark.parametrize("lens,channels", [([30000] + [5] * 15, 8), ([20000], 64), ([4000, 3], 64)], ids=str)
+@pytest.mark.parametrize("at", [0, 1, 2500])
+def test_one_outlying_row(dtype, big, lens, channels, at):
+    """A master node far from all others, first in its graph or not; graphs of one chunk and of many."""
+    x, g, w, b = inputs(dtype, lens, channels)
+    x[at] = big
+    compare(dtype, lens, 2, x, g, w, b)
