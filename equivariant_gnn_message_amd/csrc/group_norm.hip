@@ -603,7 +603,7 @@ template <int V>
 __device__ void finish_here(const NormParams& p, const Chunk& c, const Place& q, float2* red, Channels<V>& k) {
   const Slots s = slots_of(p, c.g);
   const int c0 = q.unit * V;
-  int some = 0;      // the first chunk with a counted row gives the value to sum about
+  int some = 0;      // means are joined less that of the first chunk with a counted row
   while (some + 1 < s.count && p.counts[s.first + some] == 0.0f) ++some;
   float n = 0.0f, base[V], s1[V], s2[V];
   read_sums<V>(p, s.first + some, c0, base, s1);
@@ -612,26 +612,18 @@ __device__ void finish_here(const NormParams& p, const Chunk& c, const Place& q,
   if (q.on)
 #pragma unroll 2
     for (int j = q.row; j < s.count; j += q.step) {
-      const float w = p.counts[s.first + j];
-      n += w;
       float m1[V], m2[V];
       read_sums<V>(p, s.first + j, c0, m1, m2);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float d = m1[i] - base[i];
-        s1[i] = fmaf(w, d, s1[i]);
-        s2[i] += fmaf(w * d, d, m2[i]);
-      }
+      for (int i = 0; i < V; ++i) m1[i] -= base[i];
+      Moments::join<V>(n, p.counts[s.first + j], s1, s2, m1, m2);
     }
-  add_rows<V>(q, red, s1, s2);
+  join_rows<Moments, V>(q, red, n, s1, s2);
   n = block_sum(q.on && q.col == 0 ? n : 0.0f);
   const float inv = n > 0.0f ? 1.0f / n : 0.0f;
   if (threadIdx.x < q.width)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float m = s1[i] * inv;
-      red[c0 + i] = make_float2(base[i] + m, fmaxf(s2[i] - n * m * m, 0.0f));
-    }
+    for (int i = 0; i < V; ++i) red[c0 + i] = make_float2(base[i] + s1[i], s2[i]);
   __syncthreads();
   int have = -1;
   float m = 0.0f, rs = 0.0f;

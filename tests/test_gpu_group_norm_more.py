@@ -50,3 +50,16 @@ def test_one_outlying_row(dtype, big, lens, channels, at):
     x, g, w, b = inputs(dtype, lens, channels)
     x[at] = big
     compare(dtype, lens, 2, x, g, w, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("big", [100.0, 10000.0])
+def test_outlying_row_alone_in_its_chunk(dtype, big):
+    """A graph of 16 chunks of 1024 rows; of the first one the mask leaves the master node alone."""
+    lens = [16000] * 64
+    x, g, w, b = inputs(dtype, lens, 8)
+    mask = np.ones(sum(lens), dtype=np.uint8)
+    for graph in (0, 7):
+        x[16000 * graph] = big
+        mask[16000 * graph + 1:16000 * graph + 1024] = 0
+    compare(dtype, lens, 2, x, g, w, b, "none", mask)
