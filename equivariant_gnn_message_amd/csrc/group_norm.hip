@@ -69,6 +69,18 @@ struct NormParams {
   float2* stats;                   // (graphs, groups): mean and rstd, or the reverse pass's means
 };
 
+// ------------------------------------------------------------- work-groups ---
+
+// n work-groups for each of the columns.  A launch takes less than 2^32 threads along an axis, so
+// more than 2^20 work-groups go on along z.
+constexpr unsigned kAlongX = 1u << 20;
+dim3 grid_of(int64_t n, unsigned columns) {
+  if (n <= kAlongX) return dim3((unsigned)n, columns);
+  return dim3(kAlongX, columns, (unsigned)((n + kAlongX - 1) / kAlongX));
+}
+// Which of the n this one is; there may be some more.
+__device__ __forceinline__ unsigned block_index() { return blockIdx.z * kAlongX + blockIdx.x; }
+
 // ------------------------------------------------------------------ graphs ---
 
 __device__ __forceinline__ int clamp_row(int v, long n) { return v < 0 ? 0 : (v > n ? (int)n : v); }
@@ -470,7 +482,9 @@ __device__ __forceinline__ void write_rows(const NormParams& p, const Chunk& c, 
 // channels bf16: 49 us with six, 46 with seven).
 template <class T, int V, int ACT, bool S>
 __global__ void __launch_bounds__(NT, 7) norm_sums(NormParams p) {
-  const Chunk c = chunk_of(p, blockIdx.x);
+  const unsigned slot = block_index();
+  if (slot >= (unsigned)p.slots) return;
+  const Chunk c = chunk_of(p, (int)slot);
   if (c.none) return;
   const Place q = place(p);
   const T* x = (const T*)p.a.x + q.unit * V;
@@ -525,8 +539,8 @@ __global__ void __launch_bounds__(NT, 7) norm_sums(NormParams p) {
   }
   const int c0 = q.unit * V;
   if (!c.only) {
-    if (threadIdx.x < q.width) write_sums<V>(p, blockIdx.x, c0, s1, s2);
-    if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = (float)n;
+    if (threadIdx.x < q.width) write_sums<V>(p, slot, c0, s1, s2);
+    if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[slot] = (float)n;
     return;
   }
   // the graph's only chunk: its groups here, each by every thread that has one of its channels,
@@ -565,7 +579,9 @@ __global__ void __launch_bounds__(NT, 7) norm_sums(NormParams p) {
 
 // One work-group per (graph, group): joins the chunks about the common mean.
 __global__ void __launch_bounds__(NT) norm_finish(NormParams p) {
-  const int g = blockIdx.x / p.a.groups, grp = blockIdx.x % p.a.groups;
+  const unsigned pair = block_index();
+  if (pair >= (unsigned)p.a.num_graphs * (unsigned)p.a.groups) return;
+  const int g = (int)(pair / p.a.groups), grp = (int)(pair % p.a.groups);
   const Slots s = slots_of(p, g);
   if (s.count == 1 && p.units <= NT) return;
   const int total = s.count * p.gc;
@@ -590,9 +606,9 @@ __global__ void __launch_bounds__(NT) norm_finish(NormParams p) {
   v = block_sum(v);
   const float rs = 1.0f / sqrtf((n > 0.0f ? v / n : 0.0f) + p.a.eps);
   if (threadIdx.x == 0) {
-    p.stats[blockIdx.x] = make_float2(m, rs);
-    if (p.mean) p.mean[blockIdx.x] = m;
-    if (p.rstd) p.rstd[blockIdx.x] = rs;
+    p.stats[pair] = make_float2(m, rs);
+    if (p.mean) p.mean[pair] = m;
+    if (p.rstd) p.rstd[pair] = rs;
   }
 }
 
@@ -652,7 +668,9 @@ __device__ void finish_here(const NormParams& p, const Chunk& c, const Place& q,
 
 template <class T, int V, int ACT, bool HERE, bool S>
 __global__ void __launch_bounds__(NT) norm_apply(NormParams p) {
-  const Chunk c = chunk_of(p, blockIdx.x);
+  const unsigned slot = block_index();
+  if (slot >= (unsigned)p.slots) return;
+  const Chunk c = chunk_of(p, (int)slot);
   if (c.none || c.only) return;
   const Place q = place(p);
   const int c0 = q.unit * V;
@@ -744,14 +762,16 @@ __device__ void group_means(const NormParams& p, const Place& q, const Channels<
 
 template <class T, int V, int ACT, bool S>
 __global__ void __launch_bounds__(NT) norm_grad_sums(NormParams p) {
-  const Chunk c = chunk_of(p, blockIdx.x);
+  const unsigned slot = block_index();
+  if (slot >= (unsigned)p.slots) return;
+  const Chunk c = chunk_of(p, (int)slot);
   const Place q = place(p);
   const int c0 = q.unit * V;
   float s1[V], s2[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
   if (c.none) {     // the weight gradient sums over all slots
-    if (threadIdx.x < q.width) write_sums<V>(p, blockIdx.x, c0, s1, s2);
+    if (threadIdx.x < q.width) write_sums<V>(p, slot, c0, s1, s2);
     return;
   }
   Channels<V> k;
@@ -773,8 +793,8 @@ __global__ void __launch_bounds__(NT) norm_grad_sums(NormParams p) {
   __shared__ float2 red[NT * V];
   add_rows<V>(q, red, s1, s2);
   n = block_sum(q.on && q.col == 0 ? n : 0.0f);
-  if (threadIdx.x < q.width) write_sums<V>(p, blockIdx.x, c0, s1, s2);
-  if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = n;
+  if (threadIdx.x < q.width) write_sums<V>(p, slot, c0, s1, s2);
+  if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[slot] = n;
   if (!c.only) return;
   float m1[V], m2[V];
   group_means<V>(p, q, k, n, red, s1, s2, m1, m2);
@@ -783,7 +803,9 @@ __global__ void __launch_bounds__(NT) norm_grad_sums(NormParams p) {
 
 // One work-group per (graph, group).
 __global__ void __launch_bounds__(NT) norm_grad_finish(NormParams p) {
-  const int g = blockIdx.x / p.a.groups, grp = blockIdx.x % p.a.groups;
+  const unsigned pair = block_index();
+  if (pair >= (unsigned)p.a.num_graphs * (unsigned)p.a.groups) return;
+  const int g = (int)(pair / p.a.groups), grp = (int)(pair % p.a.groups);
   const Slots s = slots_of(p, g);
   if (s.count == 1 && p.units <= NT) return;
   const int total = s.count * p.gc;
@@ -800,7 +822,7 @@ __global__ void __launch_bounds__(NT) norm_grad_finish(NormParams p) {
   n = fmaxf(block_sum(n), 1.0f);
   m1 = block_sum(m1) / n;
   m2 = block_sum(m2) / n;
-  if (threadIdx.x == 0) p.stats[blockIdx.x] = make_float2(m1, m2);
+  if (threadIdx.x == 0) p.stats[pair] = make_float2(m1, m2);
 }
 
 // Weight and bias gradients of four channels: 64 threads each over the slots.
@@ -833,11 +855,13 @@ __device__ void affine_grads(const NormParams& p, int c0, float2* red) {
 template <class T, int V, int ACT, bool HERE, bool S>
 __global__ void __launch_bounds__(NT) norm_grad_apply(NormParams p) {
   __shared__ float2 red[NT * V];
-  if ((int)blockIdx.x >= p.slots) {
-    if (blockIdx.y == 0) affine_grads(p, ((int)blockIdx.x - p.slots) * 4, red);
+  const unsigned slot = block_index();
+  if (slot >= (unsigned)p.slots) {
+    const unsigned c = (slot - p.slots) * 4;
+    if (blockIdx.y == 0 && c < (unsigned)p.a.channels) affine_grads(p, (int)c, red);
     return;
   }
-  const Chunk c = chunk_of(p, blockIdx.x);
+  const Chunk c = chunk_of(p, (int)slot);
   if (c.none || c.only) return;
   const Place q = place(p);
   const int c0 = q.unit * V;
@@ -884,13 +908,13 @@ __global__ void __launch_bounds__(NT) norm_grad_apply(NormParams p) {
 
 template <class T, int V, int ACT, bool S>
 hipError_t forward(const NormParams& p, bool one, hipStream_t s) {
-  const dim3 grid((unsigned)p.slots, (unsigned)((p.units + NT - 1) / NT));
+  const dim3 grid = grid_of(p.slots, (unsigned)((p.units + NT - 1) / NT));
   hipLaunchKernelGGL((norm_sums<T, V, ACT, S>), grid, dim3(NT), 0, s, p);
   if (one) return hipGetLastError();
   if (p.inline_finish) {
     hipLaunchKernelGGL((norm_apply<T, V, ACT, true, S>), grid, dim3(NT), 0, s, p);
   } else {
-    hipLaunchKernelGGL(norm_finish, dim3((unsigned)(p.a.num_graphs * p.a.groups)), dim3(NT), 0, s, p);
+    hipLaunchKernelGGL(norm_finish, grid_of((int64_t)p.a.num_graphs * p.a.groups, 1), dim3(NT), 0, s, p);
     hipLaunchKernelGGL((norm_apply<T, V, ACT, false, S>), grid, dim3(NT), 0, s, p);
   }
   return hipGetLastError();
@@ -900,13 +924,13 @@ template <class T, int V, int ACT, bool S>
 hipError_t backward(const NormParams& p, bool one, hipStream_t s) {
   const unsigned columns = (unsigned)((p.units + NT - 1) / NT);
   const unsigned affine = p.gw || p.gb ? (unsigned)((p.a.channels + 3) / 4) : 0;
-  hipLaunchKernelGGL((norm_grad_sums<T, V, ACT, S>), dim3((unsigned)p.slots, columns), dim3(NT), 0, s, p);
+  hipLaunchKernelGGL((norm_grad_sums<T, V, ACT, S>), grid_of(p.slots, columns), dim3(NT), 0, s, p);
   if (one && affine == 0) return hipGetLastError();
-  const dim3 grid((unsigned)p.slots + affine, columns);
+  const dim3 grid = grid_of((int64_t)p.slots + affine, columns);
   if (p.inline_finish || one) {
     hipLaunchKernelGGL((norm_grad_apply<T, V, ACT, true, S>), grid, dim3(NT), 0, s, p);
   } else {
-    hipLaunchKernelGGL(norm_grad_finish, dim3((unsigned)(p.a.num_graphs * p.a.groups)), dim3(NT), 0, s, p);
+    hipLaunchKernelGGL(norm_grad_finish, grid_of((int64_t)p.a.num_graphs * p.a.groups, 1), dim3(NT), 0, s, p);
     hipLaunchKernelGGL((norm_grad_apply<T, V, ACT, false, S>), grid, dim3(NT), 0, s, p);
   }
   return hipGetLastError();
@@ -972,7 +996,6 @@ hipError_t launch(NormParams p, bool back, bool vec, void* workspace, hipStream_
   const bool one = p.a.num_rows <= p.chunk && p.units <= NT;
   // with few chunks a graph, joining them in every work-group of the graph costs less than a launch
   p.inline_finish = p.units <= NT && p.a.num_rows / p.chunk <= (int64_t)16 * p.a.num_graphs;
-  if ((int64_t)p.a.num_graphs * p.a.groups > 0x7fffffff) return hipErrorInvalidValue;
   if (f32 && !vec) return by_activation<float, 1, false>(p, back, one, s);
   if (!vec) return by_activation<__bf16, 1, false>(p, back, one, s);
   if (f32 && past) return by_activation<float, 4, true>(p, back, one, s);
@@ -990,7 +1013,8 @@ e3conv_status check_sizes(const e3conv_group_norm_args* a) {
   if (a->num_graphs == 0 && a->num_rows > 0) return bad("rows without a graph");
   if (a->channels < 1 || a->channels > kMaxChannels || a->groups < 1 || a->channels % a->groups != 0)
     return bad("channels must be in [1, 4096] and a multiple of groups");
-  if (a->num_rows + a->num_graphs >= ((int64_t)1 << 31) - ((int64_t)1 << 20))
+  if (a->num_rows + a->num_graphs >= ((int64_t)1 << 31) - ((int64_t)1 << 20) ||
+      (int64_t)a->num_graphs * a->groups >= ((int64_t)1 << 31) - ((int64_t)1 << 20))
     return bad("sizes must fit int32 indices");
   if ((int)a->activation < E3CONV_ACT_NONE || (int)a->activation > E3CONV_ACT_GELU) return bad("unknown activation");
   if (!(a->eps > 0.0f) || !std::isfinite(a->eps)) return bad("eps must be positive");

@@ -541,7 +541,8 @@ typedef enum {
  *   is 0 is not counted, whatever it holds, and gets y = 0 and a zero gradient.
  * - mean, rstd: fp32 (num_graphs, groups), dense; a graph without counted rows
  *   has mean = 0 and rstd = 1 / sqrt(eps).
- * channels <= 4096, a multiple of groups; eps > 0; num_rows + num_graphs < 2^31 - 2^20. */
+ * channels <= 4096, a multiple of groups; eps > 0; num_rows + num_graphs and
+ * num_graphs * groups < 2^31 - 2^20. */
 typedef struct {
   e3conv_dtype dtype;
   int32_t num_graphs;

@@ -63,3 +63,47 @@ def test_outlying_row_alone_in_its_chunk(dtype, big):
         x[16000 * graph] = big
         mask[16000 * graph + 1:16000 * graph + 1024] = 0
     compare(dtype, lens, 2, x, g, w, b, "none", mask)
+
+
+def single_rows(graphs, channels, groups):
+    """Graphs of one row, one in eight masked: with a group's value its own mean, y = bias, dx = 0 but for the
+    rounding of dz w, grad_bias the sum of dz, grad_weight = 0."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(graphs)
+    x, g = (torch.randn((graphs, channels), generator=gen, device="cuda") for _ in range(2))
+    w, b = (torch.rand(channels, generator=gen, device="cuda") + 0.5 for _ in range(2))
+    p = torch.arange(graphs + 1, dtype=torch.int32, device="cuda")
+    mask = torch.arange(graphs, device="cuda") % 8 != 3
+    say(f"[group norm] {graphs} graphs of one row, {channels} channels, {groups} groups")
+    return x, g, w, b, p, mask
+
+
+def test_more_groups_than_one_axis_of_a_launch():
+    """5000 graphs x 4096 groups: 20 million (graph, group) pairs of 256 threads are more than 2^32 threads."""
+    import torch
+    x, g, w, b, p, mask = single_rows(5000, 4096, 4096)
+    y, mean, rstd = E.e3conv_group_norm(x, p, 4096, w, b, 1e-2, "none", mask)
+    gx, gw, gb = E.e3conv_group_norm_backward(x, p, 4096, w, b, "none", mean, rstd, g, mask)
+    torch.cuda.synchronize()
+    seen, u = mask[:, None].float(), 2.0 ** -24
+    assert torch.equal(mean, x * seen) and bool(((rstd - 10).abs() <= 40 * u).all())
+    assert torch.equal(y, b.expand_as(y) * seen)
+    assert bool((gx.abs() <= 2 * u * (g * w).abs() * 10 * seen).all()) and not gw.any()
+    want, size = (g.double() * seen).sum(0), (g.double().abs() * seen).sum(0)
+    assert bool(((gb - want).abs() <= 4 * 5000 ** 0.5 * u * size).all())
+
+
+def test_more_graphs_than_one_axis_of_a_launch():
+    """17 million graphs, a work-group of 256 threads each."""
+    import torch
+    graphs = 17 << 20
+    x, g, w, b, p, mask = single_rows(graphs, 4, 4)
+    y, mean, rstd = E.e3conv_group_norm(x, p, 4, w, b, 1e-2, "none", mask)
+    gx, gw, gb = E.e3conv_group_norm_backward(x, p, 4, w, b, "none", mean, rstd, g, mask)
+    torch.cuda.synchronize()
+    seen, u = mask[:, None].float(), 2.0 ** -24
+    assert torch.equal(mean, x * seen) and bool(((rstd - 10).abs() <= 40 * u).all())
+    assert torch.equal(y, b.expand_as(y) * seen)
+    assert bool((gx.abs() <= 2 * u * (g * w).abs() * 10 * seen).all()) and not gw.any()
+    want, size = (g.double() * seen).sum(0), (g.double().abs() * seen).sum(0)
+    assert bool(((gb - want).abs() <= 4 * graphs ** 0.5 * u * size).all())
