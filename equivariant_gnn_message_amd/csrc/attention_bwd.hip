@@ -251,12 +251,15 @@ __device__ __forceinline__ void bwd_kv(const Params& p, const Where& place, RowB
 template <class T, int D, int RW, int TK, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D) : 1) attn_bwd_q(Params p) {
   __shared__ __attribute__((aligned(16))) KeyBuffer<T, D, TK> first, second;
-  bwd_q<T, D, RW, TK, BUF, VEC>(p, where(blockIdx.x, gridDim.x, p.slots, p.splits), first, second);
+  const long b = block_index();
+  if (b < p.blocks) bwd_q<T, D, RW, TK, BUF, VEC>(p, where((int)b, p.blocks, p.slots, p.splits), first, second);
 }
 template <class T, int D, int RW, int TQ, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D) : 1) attn_bwd_kv(Params p) {
   __shared__ __attribute__((aligned(16))) RowBuffer<T, D, TQ> first, second;
-  bwd_kv<T, D, RW, TQ, BUF, VEC, false>(p, where(blockIdx.x, gridDim.x, p.slots_kv, p.splits_kv), first, second);
+  const long b = block_index();
+  if (b < p.blocks)
+    bwd_kv<T, D, RW, TQ, BUF, VEC, false>(p, where((int)b, p.blocks, p.slots_kv, p.splits_kv), first, second);
 }
 template <class T, int D, int RW, int ROWS, int BUF, bool VEC>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D) : 1) attn_bwd_both(Params p) {
@@ -265,11 +268,13 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D)
     RowBuffer<T, D, ROWS> rows;
   };
   __shared__ __attribute__((aligned(16))) Buffer first, second;
-  const int b = blockIdx.x, n = p.first_blocks;
+  const long at = block_index();
+  if (at >= p.blocks) return;
+  const int b = (int)at, n = p.first_blocks;
   if (b < n)
     bwd_q<T, D, RW, ROWS, BUF, VEC>(p, where(b, n, p.slots, p.splits), first.keys, second.keys);
   else
-    bwd_kv<T, D, RW, ROWS, BUF, VEC, true>(p, where(b - n, gridDim.x - n, p.slots_kv, p.splits_kv), first.rows,
+    bwd_kv<T, D, RW, ROWS, BUF, VEC, true>(p, where(b - n, p.blocks - n, p.slots_kv, p.splits_kv), first.rows,
                                            second.rows);
 }
 
@@ -280,7 +285,7 @@ struct Sum {
   long rows;            // (i, head)
   int width, from, dim; // elements from .. from + dim - 1 of `width`
   int heads, splits, each;
-  unsigned blocks;
+  long blocks;
   float factor;
   void* out;
   long out_row, out_head;
@@ -291,13 +296,14 @@ struct Sums {
 template <class T>
 __global__ void __launch_bounds__(256) attn_sum(Sums all) {
   __shared__ float red[4][64];
-  unsigned b = blockIdx.x;
+  long b = block_index();
   int which = 0;
   while (which < 2 && b >= all.of[which].blocks) b -= all.of[which++].blocks;
   const Sum& m = all.of[which];
+  if (b >= m.blocks) return;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const bool wide = m.each == 256;
-  const long i = (long)b * m.each + (wide ? (int)threadIdx.x : lane), at = i / m.dim;
+  const long i = b * m.each + (wide ? (int)threadIdx.x : lane), at = i / m.dim;
   const int d = (int)(i - at * m.dim);
   const float* q = m.part + at * m.width + m.from + d;
   const long step = m.rows * m.width;
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(256) attn_sum(Sums all) {
 Sum sum_of(const float* part, long rows, int width, int from, int dim, int heads, int splits, float factor, void* out,
            long row, long head) {
   Sum m{part, rows, width, from, dim, heads, splits, splits <= 8 ? 256 : 64, 0, factor, out, row, head};
-  if (splits > 1) m.blocks = (unsigned)((rows * dim + m.each - 1) / m.each);
+  if (splits > 1) m.blocks = (rows * dim + m.each - 1) / m.each;
   return m;
 }
 template <class T>
@@ -344,8 +350,8 @@ hipError_t sums(const Params& p, hipStream_t s) {
                   sum_of(p.part_kv, nk, width, 0, a.dim_qk, a.heads_kv, p.splits_kv, a.scale, p.gk, p.gk_row, p.gk_head),
                   sum_of(p.part_kv, nk, width, a.dim_qk, a.dim_v, a.heads_kv, p.splits_kv, 1.0f, p.gv, p.gv_row,
                          p.gv_head)}};
-  const unsigned blocks = all.of[0].blocks + all.of[1].blocks + all.of[2].blocks;
-  if (blocks > 0) hipLaunchKernelGGL(attn_sum<T>, dim3(blocks), dim3(256), 0, s, all);
+  const long blocks = all.of[0].blocks + all.of[1].blocks + all.of[2].blocks;
+  if (blocks > 0) hipLaunchKernelGGL(attn_sum<T>, grid_of(blocks), dim3(256), 0, s, all);
   return hipGetLastError();
 }
 
@@ -371,39 +377,39 @@ struct Tiling {
   static constexpr int BUF1 = sizeof(T) == 2 && VEC ? 2 : 1;
 };
 template <class T, int D, bool VEC>
-void launch_q(const Params& p, int rw, unsigned grid, hipStream_t s) {
+void launch_q(const Params& p, int rw, hipStream_t s) {
   typedef Tiling<T, D, VEC> L;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_q<T, D, 4, L::ROWS, L::BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_q<T, D, 1, 32, L::BUF1, VEC>), dim3(grid), dim3(64), 0, s, p);
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_q<T, D, 4, L::ROWS, L::BUF4, VEC>), grid_of(p.blocks), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_q<T, D, 1, 32, L::BUF1, VEC>), grid_of(p.blocks), dim3(64), 0, s, p);
 }
 template <class T, int D, bool VEC>
-void launch_kv(const Params& p, int rw, unsigned grid, hipStream_t s) {
+void launch_kv(const Params& p, int rw, hipStream_t s) {
   typedef Tiling<T, D, VEC> L;
   constexpr int ROWS = sizeof(T) == 2 ? 64 : L::ROWS;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_kv<T, D, 4, ROWS, L::BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_kv<T, D, 1, 32, L::BUF1, VEC>), dim3(grid), dim3(64), 0, s, p);
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_kv<T, D, 4, ROWS, L::BUF4, VEC>), grid_of(p.blocks), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_kv<T, D, 1, 32, L::BUF1, VEC>), grid_of(p.blocks), dim3(64), 0, s, p);
 }
 template <class T, int D>
-void launch_q(const Params& p, int rw, unsigned grid, hipStream_t s) {
-  if (p.vec) launch_q<T, D, true>(p, rw, grid, s);
-  else launch_q<T, D, false>(p, rw, grid, s);
+void launch_q(const Params& p, int rw, hipStream_t s) {
+  if (p.vec) launch_q<T, D, true>(p, rw, s);
+  else launch_q<T, D, false>(p, rw, s);
 }
 template <class T, int D>
-void launch_kv(const Params& p, int rw, unsigned grid, hipStream_t s) {
-  if (p.vec) launch_kv<T, D, true>(p, rw, grid, s);
-  else launch_kv<T, D, false>(p, rw, grid, s);
+void launch_kv(const Params& p, int rw, hipStream_t s) {
+  if (p.vec) launch_kv<T, D, true>(p, rw, s);
+  else launch_kv<T, D, false>(p, rw, s);
 }
 
 template <class T, int D, bool VEC>
-void launch_both(const Params& p, int rw, unsigned grid, hipStream_t s) {
+void launch_both(const Params& p, int rw, hipStream_t s) {
   typedef Tiling<T, D, VEC> L;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_both<T, D, 4, L::ROWS, L::BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_both<T, D, 1, 32, L::BUF1, VEC>), dim3(grid), dim3(64), 0, s, p);
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_both<T, D, 4, L::ROWS, L::BUF4, VEC>), grid_of(p.blocks), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_both<T, D, 1, 32, L::BUF1, VEC>), grid_of(p.blocks), dim3(64), 0, s, p);
 }
 template <class T, int D>
-void launch_both(const Params& p, int rw, unsigned grid, hipStream_t s) {
-  if (p.vec) launch_both<T, D, true>(p, rw, grid, s);
-  else launch_both<T, D, false>(p, rw, grid, s);
+void launch_both(const Params& p, int rw, hipStream_t s) {
+  if (p.vec) launch_both<T, D, true>(p, rw, s);
+  else launch_both<T, D, false>(p, rw, s);
 }
 
 // Whether both kernels go in one launch: work-groups of one size, and either of one wave without
@@ -429,19 +435,22 @@ hipError_t backward(Params p, const Shape& q, const Shape& kv, hipStream_t s) {
   if (together(a, q, kv)) {
     p.delta = nullptr;
     p.first_blocks = (int)nq;
-    if (dim <= 32) launch_both<T, 32>(p, q.rw, (unsigned)(nq + nk), s);
-    else if (dim <= 64) launch_both<T, 64>(p, q.rw, (unsigned)(nq + nk), s);
-    else launch_both<T, 128>(p, q.rw, (unsigned)(nq + nk), s);
+    p.blocks = (int)(nq + nk);
+    if (dim <= 32) launch_both<T, 32>(p, q.rw, s);
+    else if (dim <= 64) launch_both<T, 64>(p, q.rw, s);
+    else launch_both<T, 128>(p, q.rw, s);
   } else {
     if (a.num_q > 0) {
-      if (dim <= 32) launch_q<T, 32>(p, q.rw, (unsigned)nq, s);
-      else if (dim <= 64) launch_q<T, 64>(p, q.rw, (unsigned)nq, s);
-      else launch_q<T, 128>(p, q.rw, (unsigned)nq, s);
+      p.blocks = (int)nq;
+      if (dim <= 32) launch_q<T, 32>(p, q.rw, s);
+      else if (dim <= 64) launch_q<T, 64>(p, q.rw, s);
+      else launch_q<T, 128>(p, q.rw, s);
     }
     if (a.num_k > 0) {
-      if (dim <= 32) launch_kv<T, 32>(p, kv.rw, (unsigned)nk, s);
-      else if (dim <= 64) launch_kv<T, 64>(p, kv.rw, (unsigned)nk, s);
-      else launch_kv<T, 128>(p, kv.rw, (unsigned)nk, s);
+      p.blocks = (int)nk;
+      if (dim <= 32) launch_kv<T, 32>(p, kv.rw, s);
+      else if (dim <= 64) launch_kv<T, 64>(p, kv.rw, s);
+      else launch_kv<T, 128>(p, kv.rw, s);
     }
   }
   const hipError_t err = hipGetLastError();

@@ -36,7 +36,9 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
 
-  const Where place = where(blockIdx.x, gridDim.x, p.slots, p.splits);
+  const long block = block_index();
+  if (block >= p.blocks) return;
+  const Where place = where((int)block, p.blocks, p.slots, p.splits);
   const int split = place.split, slot = place.slot, c = place.c;
   constexpr int BM = 32 * RW;
   const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
@@ -163,7 +165,8 @@ template <class T>
 __global__ void __launch_bounds__(64 * kJoinWaves) attn_join(Params p) {
   const e3conv_attention_args& a = p.a;
   __shared__ float weight[kMaxSplits], sum[kJoinWaves][kMaxDim], red[2][kJoinWaves];
-  const long rows = a.num_q * a.heads_q, at = blockIdx.x;
+  const long rows = a.num_q * a.heads_q, at = block_index();
+  if (at >= rows) return;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   float m = -INFINITY, l = 0.0f;
   if (tid < p.splits) {
@@ -224,7 +227,7 @@ constexpr int kFewSplits = 32;
 template <class T>
 __global__ void __launch_bounds__(256) attn_join_rows(Params p) {
   const e3conv_attention_args& a = p.a;
-  const long rows = a.num_q * a.heads_q, i = (long)blockIdx.x * 256 + threadIdx.x, at = i / a.dim_v;
+  const long rows = a.num_q * a.heads_q, i = block_index() * 256 + threadIdx.x, at = i / a.dim_v;
   if (at >= rows) return;
   const int d = (int)(i - at * a.dim_v);
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + at;
@@ -254,33 +257,32 @@ Shape shape_of(const e3conv_attention_args& a) {
 
 // LDS: the tiles of both buffers, at most 64 KiB (two work-groups of a compute unit).
 template <class T, int D, bool VEC>
-void launch(const Params& p, int rw, unsigned grid, hipStream_t s) {
+void launch(const Params& p, int rw, hipStream_t s) {
   constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64, TILE = planes<T>() * D * 2 * 2;
   constexpr int BUF4 = 2 * TK4 * TILE <= 65536 ? 2 : 1, BUF1 = sizeof(T) == 2 && VEC ? 2 : 1;
-  if (rw == 4) hipLaunchKernelGGL((attn_fwd<T, D, 4, TK4, BUF4, VEC>), dim3(grid), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_fwd<T, D, 1, 32, BUF1, VEC>), dim3(grid), dim3(64), 0, s, p);
+  if (rw == 4) hipLaunchKernelGGL((attn_fwd<T, D, 4, TK4, BUF4, VEC>), grid_of(p.blocks), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_fwd<T, D, 1, 32, BUF1, VEC>), grid_of(p.blocks), dim3(64), 0, s, p);
 }
 template <class T, int D>
-void launch(const Params& p, int rw, unsigned grid, hipStream_t s) {
-  if (p.vec) launch<T, D, true>(p, rw, grid, s);
-  else launch<T, D, false>(p, rw, grid, s);
+void launch(const Params& p, int rw, hipStream_t s) {
+  if (p.vec) launch<T, D, true>(p, rw, s);
+  else launch<T, D, false>(p, rw, s);
 }
 
 template <class T>
-hipError_t forward(const Params& p, int rw, unsigned grid, hipStream_t s) {
+hipError_t forward(const Params& p, int rw, hipStream_t s) {
   const int dim = p.a.dim_qk > p.a.dim_v ? p.a.dim_qk : p.a.dim_v;
-  if (dim <= 32) launch<T, 32>(p, rw, grid, s);
-  else if (dim <= 64) launch<T, 64>(p, rw, grid, s);
-  else launch<T, 128>(p, rw, grid, s);
+  if (dim <= 32) launch<T, 32>(p, rw, s);
+  else if (dim <= 64) launch<T, 64>(p, rw, s);
+  else launch<T, 128>(p, rw, s);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.splits == 1) return err;
   if (p.splits <= kFewSplits) {
     const long blocks = ((long)p.a.num_q * p.a.heads_q * p.a.dim_v + 255) / 256;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(attn_join_rows<T>, dim3((unsigned)blocks), dim3(256), 0, s, p);
+    hipLaunchKernelGGL(attn_join_rows<T>, grid_of(blocks), dim3(256), 0, s, p);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(attn_join<T>, dim3((unsigned)(p.a.num_q * p.a.heads_q)), dim3(64 * kJoinWaves), 0, s, p);
+  hipLaunchKernelGGL(attn_join<T>, grid_of(p.a.num_q * p.a.heads_q), dim3(64 * kJoinWaves), 0, s, p);
   return hipGetLastError();
 }
 
@@ -304,8 +306,8 @@ hipError_t launch_forward(const Params& given, hipStream_t s) {
   p.part += ml_floats((size_t)sh.splits * p.a.num_q * p.a.heads_q);
   const long grid = (long)sh.slots * sh.splits * p.a.heads_kv;
   if (grid > 0x7fffffffL) return hipErrorInvalidValue;
-  return p.a.dtype == E3CONV_F32 ? forward<float>(p, sh.rw, (unsigned)grid, s)
-                                 : forward<__bf16>(p, sh.rw, (unsigned)grid, s);
+  p.blocks = (int)grid;
+  return p.a.dtype == E3CONV_F32 ? forward<float>(p, sh.rw, s) : forward<__bf16>(p, sh.rw, s);
 }
 
 }  // namespace attn

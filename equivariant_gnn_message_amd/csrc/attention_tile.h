@@ -39,6 +39,7 @@ struct Params {
   int vec_st;                      // elements of the outputs' aligned stores: 8 (bf16), 4 or 0
   int slots;                       // work-group slots of the row (or key) tiles
   int splits;                      // ranges of the other axis, joined by a second kernel
+  int blocks;                      // work-groups of the launch
   int first_blocks;                // reverse pass in one launch: its work-groups for grad_q,
   int slots_kv, splits_kv;         // and the slots and splits of the others
   void* out;
@@ -241,6 +242,15 @@ struct Tile {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(reinterpret_cast<const s16x4*>(p) + half));
   }
 };
+
+// n work-groups.  A launch takes less than 2^32 threads along an axis, so more than 2^20 work-groups go
+// on along y.
+constexpr unsigned kAlongX = 1u << 20;
+inline dim3 grid_of(long n) {
+  return n <= kAlongX ? dim3((unsigned)n) : dim3(kAlongX, (unsigned)((n + kAlongX - 1) / kAlongX));
+}
+// Which of the n this one is; there may be some more.
+__device__ __forceinline__ long block_index() { return (long)blockIdx.y * kAlongX + blockIdx.x; }
 
 // Work-group -> (split, slot, kv head).  Work-groups go to the eight dies in turn, each with
 // an L2 of its own: runs of 32 consecutive places, which share a graph's keys (or rows),

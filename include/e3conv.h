@@ -472,7 +472,7 @@ e3conv_status e3conv_pair_layout(const int32_t* row_ptr, const int32_t* src, int
  *   whose byte is 0 sees no key.  Both get zero gradients.
  * - A query that sees no key has out = 0, lse = -infinity and a zero gradient.
  * heads_q must be a multiple of heads_kv; num_q * heads_q and num_k * heads_kv < 2^31 - 2^20;
- * scale finite.  Offsets into the tensors are 64 bits wide. */
+ * num_graphs < 2^20; scale finite.  Offsets into the tensors are 64 bits wide. */
 typedef struct {
   e3conv_dtype dtype;
   int32_t num_graphs;

@@ -2,7 +2,7 @@
 so the error of a plain running sum grows with their number and not with its root.
 
 The bounds are those of oracle.attention.bounds for one query; all queries are the same, and enough of them to fill
-the device, so that the keys are not split.
+the device, so that the keys are not split.  And calls of more work-groups than one axis of a launch takes.
 """
 
 import numpy as np
@@ -46,3 +46,25 @@ def test_logits_of_two_values(dtype, keys, gap):
         off = np.abs(host(got[:1]) - want[name])
         say(f"  {name}: max err {off.max():.3e}, bound {tol[name].min():.3e}")
         assert np.all(off <= tol[name]), name
+
+
+def test_more_work_groups_than_one_axis_of_a_launch():
+    """A million graphs of one node with 64 heads: 69 million work-groups of 64 threads are more than 2^32 threads.
+    With one key P = 1, so out = v, lse = scale <q, k>, grad_v = grad_out, and grad_q, grad_k are the rounding of
+    dP - delta (each a sum of 8 products, in fp32) times scale k or q."""
+    import torch
+    graphs, heads, dim = (1 << 20) - 1, 64, 8
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v, g = (torch.randn((graphs, heads, dim), generator=gen, device="cuda").bfloat16() for _ in range(4))
+    p = torch.arange(graphs + 1, dtype=torch.int32, device="cuda")
+    say(f"[attention] bf16 {graphs} graphs of one node, {heads} heads of {dim}")
+    out, lse = E.e3conv_attention(q, k, v, p, p, 0.5)
+    gq, gk, gv = E.e3conv_attention_backward(q, k, v, out, lse, g, p, p, 0.5)
+    torch.cuda.synchronize()
+    u = 2.0 ** -24
+    assert torch.equal(out, v) and torch.equal(gv, g)
+    dot, size = (0.5 * (t.float()).sum(2) for t in (q * k.float(), (q * k.float()).abs()))
+    assert bool(((lse - dot).abs() <= 24 * u * (size + 1)).all())
+    slack = 24 * u * (g * v.float()).abs().sum(2)[:, :, None] * 0.5
+    for got, other in ((gq, k), (gk, q)):
+        assert bool((got.float().abs() <= slack * other.float().abs() * (1 + 2.0 ** -8) + 1e-38).all())
