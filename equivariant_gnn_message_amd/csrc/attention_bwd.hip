@@ -136,7 +136,7 @@ __device__ __forceinline__ void bwd_q(const Params& p, const Where& place, KeyBu
 
   if (!row) return;
   if (p.splits > 1) {
-    store_row(p.part + (split * (a.num_q * a.heads_q) + at) * a.dim_qk, dq, a.dim_qk, 1.0f, true, a.dim_qk % 4 == 0);
+    store_row(p.part + (split * (a.num_q * a.heads_q) + at) * a.dim_qk, dq, a.dim_qk, 1.0f, live, a.dim_qk % 4 == 0);
     return;
   }
   store_row((T*)p.gq + qi * p.gq_row + head * p.gq_head, dq, a.dim_qk, a.scale, live, p.vec_st);
