@@ -74,6 +74,7 @@ attn::Params params(const e3conv_attention_args& a) {
   const int size = a.dtype == E3CONV_F32 ? 4 : 2;
   p.vec = vector_rows(a.q, a.q_row, a.q_head, a.dim_qk, size) && vector_rows(a.k, a.k_row, a.k_head, a.dim_qk, size) &&
           vector_rows(a.v, a.v_row, a.v_head, a.dim_v, size);
+  p.full = a.dim_qk == a.dim_v && a.dim_qk == attn::padded(a.dim_qk);
   return p;
 }
 

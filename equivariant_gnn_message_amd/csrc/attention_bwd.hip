@@ -38,11 +38,11 @@ struct RowBuffer {
   float lse[ROWS], delta[ROWS];
 };
 
-template <class T, int D, int RW, int TK, int BUF, bool VEC>
+template <class T, int D, int RW, int TK, int BUF, int LOAD>
 __device__ __forceinline__ void bwd_q(const Params& p, const Where& place, KeyBuffer<T, D, TK>& first,
                                       KeyBuffer<T, D, TK>& second) {
   typedef KeyBuffer<T, D, TK> Buffer;
-  static_assert(BUF == 2 || !(sizeof(T) == 2 && VEC), "loads straight to LDS need the other buffer");
+  static_assert(BUF == 2 || !(sizeof(T) == 2 && LOAD != kElements), "loads straight to LDS need the other buffer");
   constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
@@ -68,20 +68,22 @@ __device__ __forceinline__ void bwd_q(const Params& p, const Where& place, KeyBu
   const int k0 = kb + min(split * per, tiles) * TK;
   const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
 
-  Keys<T, D, TK, 64 * RW, VEC> keys;
+  Keys<T, D, TK, 64 * RW, LOAD> keys;
   keys.begin(p, c, k0, k1);
+  keys.pair.clear(a.dim_qk, a.dim_v, first.k, first.v);
+  if (BUF == 2) keys.pair.clear(a.dim_qk, a.dim_v, second.k, second.v);
   if (k0 < k1) keys.issue(p, first.k, first.v);
 
   Frag<P> q[KS], go[KS];
   const T* gp = (const T*)p.go + qi * p.go_row + head * p.go_head;
   const T* op = (const T*)p.out + qi * p.out_row + head * p.out_head;
-  row_operand<T, D, VEC>((const T*)a.q + qi * a.q_row + head * a.q_head, a.dim_qk, live, q);
-  row_operand<T, D, VEC>(gp, a.dim_v, live, go);
+  row_operand<T, D, LOAD>((const T*)a.q + qi * a.q_row + head * a.q_head, a.dim_qk, live, q);
+  row_operand<T, D, LOAD>(gp, a.dim_v, live, go);
   float delta = 0.0f;
 #pragma unroll
   for (int t = 0; t < KS; ++t) {
     const int d = 16 * t + 8 * h;
-    const Raw<T> gr = fetch8<VEC>(gp, d, a.dim_v), orow = fetch8<VEC>(op, d, a.dim_v);
+    const Raw<T> gr = fetch8<LOAD != kElements>(gp, d, a.dim_v), orow = fetch8<LOAD != kElements>(op, d, a.dim_v);
     if (p.negate) flip_sign(q[t]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) delta = d < a.dim_v ? fmaf(gr.at(i), orow.at(i), delta) : delta;
@@ -142,11 +144,11 @@ __device__ __forceinline__ void bwd_q(const Params& p, const Where& place, KeyBu
   store_row((T*)p.gq + qi * p.gq_row + head * p.gq_head, dq, a.dim_qk, a.scale, live, p.vec_st);
 }
 
-template <class T, int D, int RW, int TQ, int BUF, bool VEC, bool OWN>
+template <class T, int D, int RW, int TQ, int BUF, int LOAD, bool OWN>
 __device__ __forceinline__ void bwd_kv(const Params& p, const Where& place, RowBuffer<T, D, TQ>& first,
                                        RowBuffer<T, D, TQ>& second) {
   typedef RowBuffer<T, D, TQ> Buffer;
-  static_assert(BUF == 2 || !(sizeof(T) == 2 && VEC), "loads straight to LDS need the other buffer");
+  static_assert(BUF == 2 || !(sizeof(T) == 2 && LOAD != kElements), "loads straight to LDS need the other buffer");
   constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31;
@@ -170,14 +172,16 @@ __device__ __forceinline__ void bwd_kv(const Params& p, const Where& place, RowB
   const int r0 = min(split * per, tiles) * TQ;
   const int r1 = min(nrows, min((split + 1) * per, tiles) * TQ);
 
-  Rows<T, D, TQ, 64 * RW, VEC, OWN> rows;
+  Rows<T, D, TQ, 64 * RW, LOAD, OWN> rows;
   rows.begin(p, c, q0, r0, r1);
+  rows.pair.clear(a.dim_qk, a.dim_v, first.q, first.g);
+  if (BUF == 2) rows.pair.clear(a.dim_qk, a.dim_v, second.q, second.g);
   if (r0 < r1) rows.issue(p, first.q, first.g);
 
   Frag<P> k[KS], v[KS];
   const int jr = key ? j : j0;
-  row_operand<T, D, VEC>((const T*)a.k + jr * a.k_row + c * a.k_head, a.dim_qk, live, k);
-  row_operand<T, D, VEC>((const T*)a.v + jr * a.v_row + c * a.v_head, a.dim_v, live, v);
+  row_operand<T, D, LOAD>((const T*)a.k + jr * a.k_row + c * a.k_head, a.dim_qk, live, k);
+  row_operand<T, D, LOAD>((const T*)a.v + jr * a.v_row + c * a.v_head, a.dim_v, live, v);
   if (p.negate)
 #pragma unroll
     for (int t = 0; t < KS; ++t) flip_sign(k[t]);
@@ -248,20 +252,20 @@ __device__ __forceinline__ void bwd_kv(const Params& p, const Where& place, RowB
   store_row((T*)p.gv + j * p.gv_row + c * p.gv_head, dv, a.dim_v, 1.0f, live, p.vec_st);
 }
 
-template <class T, int D, int RW, int TK, int BUF, bool VEC>
+template <class T, int D, int RW, int TK, int BUF, int LOAD>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_bwd(sizeof(T) == 4, D) : 1) attn_bwd_q(Params p) {
   __shared__ __attribute__((aligned(16))) KeyBuffer<T, D, TK> first, second;
   const long b = block_index();
-  if (b < p.blocks) bwd_q<T, D, RW, TK, BUF, VEC>(p, where((int)b, p.blocks, p.slots, p.splits), first, second);
+  if (b < p.blocks) bwd_q<T, D, RW, TK, BUF, LOAD>(p, where((int)b, p.blocks, p.slots, p.splits), first, second);
 }
-template <class T, int D, int RW, int TQ, int BUF, bool VEC>
+template <class T, int D, int RW, int TQ, int BUF, int LOAD>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D) : 1) attn_bwd_kv(Params p) {
   __shared__ __attribute__((aligned(16))) RowBuffer<T, D, TQ> first, second;
   const long b = block_index();
   if (b < p.blocks)
-    bwd_kv<T, D, RW, TQ, BUF, VEC, false>(p, where((int)b, p.blocks, p.slots_kv, p.splits_kv), first, second);
+    bwd_kv<T, D, RW, TQ, BUF, LOAD, false>(p, where((int)b, p.blocks, p.slots_kv, p.splits_kv), first, second);
 }
-template <class T, int D, int RW, int ROWS, int BUF, bool VEC>
+template <class T, int D, int RW, int ROWS, int BUF, int LOAD>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D) : 1) attn_bwd_both(Params p) {
   union Buffer {
     KeyBuffer<T, D, ROWS> keys;
@@ -272,9 +276,9 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D)
   if (at >= p.blocks) return;
   const int b = (int)at, n = p.first_blocks;
   if (b < n)
-    bwd_q<T, D, RW, ROWS, BUF, VEC>(p, where(b, n, p.slots, p.splits), first.keys, second.keys);
+    bwd_q<T, D, RW, ROWS, BUF, LOAD>(p, where(b, n, p.slots, p.splits), first.keys, second.keys);
   else
-    bwd_kv<T, D, RW, ROWS, BUF, VEC, true>(p, where(b - n, p.blocks - n, p.slots_kv, p.splits_kv), first.rows,
+    bwd_kv<T, D, RW, ROWS, BUF, LOAD, true>(p, where(b - n, p.blocks - n, p.slots_kv, p.splits_kv), first.rows,
                                            second.rows);
 }
 
@@ -370,46 +374,49 @@ Shape shape_kv(const e3conv_attention_args& a) {
 
 // Rows of a tile and buffers: 64 and two where they fit 64 KiB of LDS and the registers of two
 // waves a SIMD.
-template <class T, int D, bool VEC>
+template <class T, int D, int LOAD>
 struct Tiling {
   static constexpr int ROWS = D == 128 ? 32 : 64;
   static constexpr int BUF4 = 2 * ROWS * planes<T>() * D * 2 * 2 <= 65536 ? 2 : 1;
-  static constexpr int BUF1 = sizeof(T) == 2 && VEC ? 2 : 1;
+  static constexpr int BUF1 = sizeof(T) == 2 && LOAD != kElements ? 2 : 1;
 };
-template <class T, int D, bool VEC>
+template <class T, int D, int LOAD>
 void launch_q(const Params& p, int rw, hipStream_t s) {
-  typedef Tiling<T, D, VEC> L;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_q<T, D, 4, L::ROWS, L::BUF4, VEC>), grid_of(p.blocks), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_q<T, D, 1, 32, L::BUF1, VEC>), grid_of(p.blocks), dim3(64), 0, s, p);
+  typedef Tiling<T, D, LOAD> L;
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_q<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid_of(p.blocks), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_q<T, D, 1, 32, L::BUF1, LOAD>), grid_of(p.blocks), dim3(64), 0, s, p);
 }
-template <class T, int D, bool VEC>
+template <class T, int D, int LOAD>
 void launch_kv(const Params& p, int rw, hipStream_t s) {
-  typedef Tiling<T, D, VEC> L;
+  typedef Tiling<T, D, LOAD> L;
   constexpr int ROWS = sizeof(T) == 2 ? 64 : L::ROWS;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_kv<T, D, 4, ROWS, L::BUF4, VEC>), grid_of(p.blocks), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_kv<T, D, 1, 32, L::BUF1, VEC>), grid_of(p.blocks), dim3(64), 0, s, p);
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_kv<T, D, 4, ROWS, L::BUF4, LOAD>), grid_of(p.blocks), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_kv<T, D, 1, 32, L::BUF1, LOAD>), grid_of(p.blocks), dim3(64), 0, s, p);
 }
 template <class T, int D>
 void launch_q(const Params& p, int rw, hipStream_t s) {
-  if (p.vec) launch_q<T, D, true>(p, rw, s);
-  else launch_q<T, D, false>(p, rw, s);
+  if (!p.vec) launch_q<T, D, kElements>(p, rw, s);
+  else if (sizeof(T) == 2 && p.full) launch_q<T, D, sizeof(T) == 2 ? kFull : kUnits>(p, rw, s);
+  else launch_q<T, D, kUnits>(p, rw, s);
 }
 template <class T, int D>
 void launch_kv(const Params& p, int rw, hipStream_t s) {
-  if (p.vec) launch_kv<T, D, true>(p, rw, s);
-  else launch_kv<T, D, false>(p, rw, s);
+  if (!p.vec) launch_kv<T, D, kElements>(p, rw, s);
+  else if (sizeof(T) == 2 && p.full) launch_kv<T, D, sizeof(T) == 2 ? kFull : kUnits>(p, rw, s);
+  else launch_kv<T, D, kUnits>(p, rw, s);
 }
 
-template <class T, int D, bool VEC>
+template <class T, int D, int LOAD>
 void launch_both(const Params& p, int rw, hipStream_t s) {
-  typedef Tiling<T, D, VEC> L;
-  if (rw == 4) hipLaunchKernelGGL((attn_bwd_both<T, D, 4, L::ROWS, L::BUF4, VEC>), grid_of(p.blocks), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_bwd_both<T, D, 1, 32, L::BUF1, VEC>), grid_of(p.blocks), dim3(64), 0, s, p);
+  typedef Tiling<T, D, LOAD> L;
+  if (rw == 4) hipLaunchKernelGGL((attn_bwd_both<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid_of(p.blocks), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_bwd_both<T, D, 1, 32, L::BUF1, LOAD>), grid_of(p.blocks), dim3(64), 0, s, p);
 }
 template <class T, int D>
 void launch_both(const Params& p, int rw, hipStream_t s) {
-  if (p.vec) launch_both<T, D, true>(p, rw, s);
-  else launch_both<T, D, false>(p, rw, s);
+  if (!p.vec) launch_both<T, D, kElements>(p, rw, s);
+  else if (sizeof(T) == 2 && p.full) launch_both<T, D, sizeof(T) == 2 ? kFull : kUnits>(p, rw, s);
+  else launch_both<T, D, kUnits>(p, rw, s);
 }
 
 // Whether both kernels go in one launch: work-groups of one size, and either of one wave without

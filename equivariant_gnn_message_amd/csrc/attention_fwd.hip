@@ -24,14 +24,14 @@ namespace e3c {
 namespace attn {
 namespace {
 
-template <class T, int D, int RW, int TK, int BUF, bool VEC>
+template <class T, int D, int RW, int TK, int BUF, int LOAD>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D) : 1) attn_fwd(Params p) {
   constexpr int P = planes<T>(), KS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
   struct Buffer {
     Tile<P, TK, D> k, v;
     float bias[TK];
   };
-  static_assert(BUF == 2 || !(sizeof(T) == 2 && VEC), "loads straight to LDS need the other buffer");
+  static_assert(BUF == 2 || !(sizeof(T) == 2 && LOAD != kElements), "loads straight to LDS need the other buffer");
   __shared__ __attribute__((aligned(16))) Buffer first, second;
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
@@ -58,12 +58,14 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_fwd(sizeof(T) == 4, D
   const int k0 = kb + min(split * per, tiles) * TK;
   const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
 
-  Keys<T, D, TK, 64 * RW, VEC> keys;
+  Keys<T, D, TK, 64 * RW, LOAD> keys;
   keys.begin(p, c, k0, k1);
+  keys.pair.clear(a.dim_qk, a.dim_v, first.k, first.v);
+  if (BUF == 2) keys.pair.clear(a.dim_qk, a.dim_v, second.k, second.v);
   if (k0 < k1) keys.issue(p, first.k, first.v);
 
   Frag<P> q[KS];
-  row_operand<T, D, VEC>((const T*)a.q + qi * a.q_row + head * a.q_head, a.dim_qk, live, q);
+  row_operand<T, D, LOAD>((const T*)a.q + qi * a.q_row + head * a.q_head, a.dim_qk, live, q);
   if (p.negate)
 #pragma unroll
     for (int t = 0; t < KS; ++t) flip_sign(q[t]);
@@ -256,17 +258,18 @@ Shape shape_of(const e3conv_attention_args& a) {
 }
 
 // LDS: the tiles of both buffers, at most 64 KiB (two work-groups of a compute unit).
-template <class T, int D, bool VEC>
+template <class T, int D, int LOAD>
 void launch(const Params& p, int rw, hipStream_t s) {
   constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64, TILE = planes<T>() * D * 2 * 2;
-  constexpr int BUF4 = 2 * TK4 * TILE <= 65536 ? 2 : 1, BUF1 = sizeof(T) == 2 && VEC ? 2 : 1;
-  if (rw == 4) hipLaunchKernelGGL((attn_fwd<T, D, 4, TK4, BUF4, VEC>), grid_of(p.blocks), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((attn_fwd<T, D, 1, 32, BUF1, VEC>), grid_of(p.blocks), dim3(64), 0, s, p);
+  constexpr int BUF4 = 2 * TK4 * TILE <= 65536 ? 2 : 1, BUF1 = sizeof(T) == 2 && LOAD != kElements ? 2 : 1;
+  if (rw == 4) hipLaunchKernelGGL((attn_fwd<T, D, 4, TK4, BUF4, LOAD>), grid_of(p.blocks), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((attn_fwd<T, D, 1, 32, BUF1, LOAD>), grid_of(p.blocks), dim3(64), 0, s, p);
 }
 template <class T, int D>
 void launch(const Params& p, int rw, hipStream_t s) {
-  if (p.vec) launch<T, D, true>(p, rw, s);
-  else launch<T, D, false>(p, rw, s);
+  if (!p.vec) launch<T, D, kElements>(p, rw, s);
+  else if (sizeof(T) == 2 && p.full) launch<T, D, sizeof(T) == 2 ? kFull : kUnits>(p, rw, s);
+  else launch<T, D, kUnits>(p, rw, s);
 }
 
 template <class T>

@@ -36,6 +36,7 @@ struct Params {
   float c;                         // |scale| log2(e), at least the smallest normal number
   int negate;                      // scale < 0: q enters with its sign changed
   int vec;                         // 16-byte loads of q, k, v, grad_out (and out) rows
+  int full;                        // dim_qk and dim_v are both 32, 64 or 128
   int vec_st;                      // elements of the outputs' aligned stores: 8 (bf16), 4 or 0
   int slots;                       // work-group slots of the row (or key) tiles
   int splits;                      // ranges of the other axis, joined by a second kernel
@@ -296,18 +297,22 @@ __device__ __forceinline__ int graph_of_slot(const int* ptr, int graphs, long n,
 // Row r of a graph's rows is head r % group of query r / group.
 __device__ __forceinline__ int query_of(const Params& p, int r) { return div_group(r, p.group, p.magic, p.shift); }
 
+// How a kernel loads rows: element by element, in whole units of eight elements, or (bf16) in
+// whole units that fill the tile.
+constexpr int kElements = 0, kUnits = 1, kFull = 2;
+
 // A work-group's loads of a tile of ROWS rows of two operands that share their row order (k and
 // v, or q and grad_out): issue() starts them, finish() leaves the tile in LDS, with zeros
 // in place of the rows that do not count, whatever memory holds there (the caller
 // waits at a barrier after it).  bf16 rows of whole units go from memory to LDS by
-// themselves, the lane's unit chosen so that the tile's permutation comes out; dimensions
-// beyond dim then hold the row's first unit, and meet zeros in the other operand or
-// rows of the result that are not stored.  Others pass through registers: fp32 is split on
-// the way.
-template <class T, int D, int ROWS, int NT, bool VEC>
+// themselves, the lane's unit chosen so that the tile's permutation comes out; lanes of
+// units beyond dim load nothing and leave the zeros that clear() has put there (an infinity
+// would be NaN against the other operand's zeros; clearing them after each tile's loads took
+// 10 % with 96 dimensions).  Others pass through registers: fp32 is split on the way.
+template <class T, int D, int ROWS, int NT, int LOAD>
 struct Pair {
   static constexpr int P = planes<T>(), U = D / 8, E = ROWS * U / NT, STEP = NT / U;
-  static constexpr bool DMA = sizeof(T) == 2 && VEC;
+  static constexpr bool VEC = LOAD != kElements, DMA = sizeof(T) == 2 && VEC, SPARE = LOAD != kFull;
   typedef Tile<P, ROWS, D> TileT;
   static_assert(ROWS * U % NT == 0 && ROWS <= 64, "");
   Raw<T> x[DMA ? 1 : E], y[DMA ? 1 : E];
@@ -317,10 +322,19 @@ struct Pair {
     const int slot = threadIdx.x % U;
     return DMA ? slot ^ TileT::swizzle(row(e)) : slot;
   }
+  // Zeros in this thread's units beyond dim.
+  static __device__ __forceinline__ void clear(int dim_x, int dim_y, TileT& xt, TileT& yt) {
+    if constexpr (DMA && SPARE)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (unit(e) * 8 >= dim_x) xt.u[0][e * NT + threadIdx.x] = bf16x8{};
+        if (unit(e) * 8 >= dim_y) yt.u[0][e * NT + threadIdx.x] = bf16x8{};
+      }
+  }
   // First element of this thread's unit of row e, as far as the row has it.
   static __device__ __forceinline__ int first(int e, int dim) {
     const int d = unit(e) * 8;
-    return DMA && d >= dim ? 0 : d;
+    return DMA && SPARE && d >= dim ? 0 : d;
   }
   // Whether all rows of a thread have the same unit (their numbers differ by multiples of 16).
   static constexpr bool SAME = !DMA || STEP % 16 == 0;
@@ -330,8 +344,8 @@ struct Pair {
       typedef const __attribute__((address_space(1))) void* from;
       typedef __attribute__((address_space(3))) void* to;
       const int at = e * NT + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63);   // the wave's first unit
-      __builtin_amdgcn_global_load_lds((from)xp, (to)&xt.u[0][at], 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((from)yp, (to)&yt.u[0][at], 16, 0, 0);
+      if (!SPARE || unit(e) * 8 < dim_x) __builtin_amdgcn_global_load_lds((from)xp, (to)&xt.u[0][at], 16, 0, 0);
+      if (!SPARE || unit(e) * 8 < dim_y) __builtin_amdgcn_global_load_lds((from)yp, (to)&yt.u[0][at], 16, 0, 0);
     } else {
       const int d = unit(e) * 8;
       x[e] = fetch8<VEC>(xp - d, d, dim_x);
@@ -372,9 +386,9 @@ struct Pair {
 
 // The tiles of the keys of one kv head, and the starting value of each key's logits: 0, or
 // -infinity for a key that is not seen.  Rows beyond the last key read the last one.
-template <class T, int D, int ROWS, int NT, bool VEC>
+template <class T, int D, int ROWS, int NT, int LOAD>
 struct Keys {
-  typedef Pair<T, D, ROWS, NT, VEC> PairT;
+  typedef Pair<T, D, ROWS, NT, LOAD> PairT;
   typedef typename PairT::TileT TileT;
   PairT pair;
   unsigned char m;
@@ -425,9 +439,9 @@ struct Keys {
 // reverse pass walks over, and each row's lse (base 2) and -delta.  A row that sees no key
 // or lies beyond the end has lse = +infinity, which makes its P zero.  OWN: delta is formed
 // here, else it was left in memory.
-template <class T, int D, int ROWS, int NT, bool VEC, bool OWN>
+template <class T, int D, int ROWS, int NT, int LOAD, bool OWN>
 struct Rows {
-  typedef Pair<T, D, ROWS, NT, VEC> PairT;
+  typedef Pair<T, D, ROWS, NT, LOAD> PairT;
   typedef typename PairT::TileT TileT;
   PairT pair;
   float lse, delta;
@@ -480,7 +494,7 @@ struct Rows {
       const T* o = (const T*)p.out + (q0 + i) * p.out_row + ((at0 - (long)q0 * a.heads_q) + x) * p.out_head;
       delta = 0.0f;
       for (int d = 0; d < a.dim_v; d += 8) {
-        const Raw<T> u = fetch8<VEC>(g, d, a.dim_v), v = fetch8<VEC>(o, d, a.dim_v);
+        const Raw<T> u = fetch8<PairT::VEC>(g, d, a.dim_v), v = fetch8<PairT::VEC>(o, d, a.dim_v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) delta = fmaf(u.at(j), v.at(j), delta);
       }
@@ -535,13 +549,13 @@ __device__ __forceinline__ f32x16 by_row(const float* rows, int lane) {
 }
 
 // The B operands of one row (lane n's, k = 16 t + 8 h + j) from memory; zeros unless live.
-template <class T, int D, bool VEC>
+template <class T, int D, int LOAD>
 __device__ __forceinline__ void row_operand(const T* row, int dim, bool live, Frag<planes<T>()> (&f)[D / 16]) {
   const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll
   for (int t = 0; t < D / 16; ++t) {
     const int d = 16 * t + 8 * h;
-    f[t] = frag_of(fetch8<VEC>(row, d, dim), live && d < dim);
+    f[t] = frag_of(fetch8<LOAD != kElements>(row, d, dim), live && d < dim);
   }
 }
 

@@ -30,3 +30,34 @@ def test_masked_queries_of_a_graph_with_bad_keys(dtype, lens_q, lens_k, bad):
     hole = dev(~mask)
     assert not out[hole].any() and bool(torch.isneginf(lse[hole]).all())
     assert not gq[hole].any()
+
+
+@pytest.mark.parametrize("dim", [8, 24, 40, 48, 72, 96, 104])
+@pytest.mark.parametrize("lens", [[50], [9, 300], [3000]], ids=str)
+def test_infinite_key_aligned_or_not(dim, lens):
+    """bf16, an infinity in a key that gives every query a logit of -infinity: the key has no weight, and rows
+    loaded by whole units and element by element give the same bits."""
+    import torch
+    q, k, v, g = draw(4, "bf16", lens, lens, 2, 2, dim, dim)
+    q[:, :, 0] = -q[:, :, 0].abs() - 0.5
+    k[lens[0] - 1, :, 0] = float("inf")
+    p = dev(ptr(lens))
+    say(f"[attention] bf16 {lens} nodes, {dim} dimensions, an infinite key")
+
+    def shifted(t):
+        return torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape).copy_(t)
+
+    mask = torch.ones(sum(lens), dtype=torch.bool, device="cuda")
+    out, lse = E.e3conv_attention(q, k, v, p, p)
+    ref, lse_ref = E.e3conv_attention(shifted(q), shifted(k), shifted(v), p, p)
+    mask[lens[0] - 1] = False
+    k_finite = torch.where(mask[:, None, None], k, 0)
+    without, _ = E.e3conv_attention(q, k_finite, v, p, p, k_mask=mask)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(out).all()) and torch.equal(out, ref) and torch.equal(lse, lse_ref)
+    assert torch.equal(out, without)
+    grads = E.e3conv_attention_backward(q, k, v, out, lse, g, p, p)
+    refs = E.e3conv_attention_backward(shifted(q), shifted(k), shifted(v), out, lse, g, p, p)
+    torch.cuda.synchronize()
+    for a, b in zip(grads, refs):
+        assert np.array_equal(host(a), host(b), equal_nan=True)
