@@ -709,6 +709,7 @@ def e3conv_attention(q, k, v, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None
     q (num_q, heads_q, dim_qk), k (num_k, heads_kv, dim_qk), v (num_k, heads_kv, dim_v), fp32 or bf16, any
     strides but unit along the last axis; q_ptr, k_ptr int32 offsets of the graphs; scale defaults to
     dim_qk ** -0.5; masks are bool or uint8, one value per row, 0 for padding.  lse fp32 (num_q, heads_q).
+    Masked rows may hold anything; the others finite values, in fp32 at most 3.38e38 in magnitude.
     stream: a torch stream or raw handle in place of the current stream.  The operands have to be ready on
     it; what the call allocates belongs to it, and the caller orders its own use of the results.
     """

@@ -471,6 +471,10 @@ e3conv_status e3conv_pair_layout(const int32_t* row_ptr, const int32_t* src, int
  *   whose byte is 0 is not seen, whatever its k and v hold (NaN too); a query
  *   whose byte is 0 sees no key.  Both get zero gradients.
  * - A query that sees no key has out = 0, lse = -infinity and a zero gradient.
+ * - What the rows that count hold (grad_out's too) has to be finite, in fp32 at most 3.38e38 in
+ *   magnitude (the largest bf16: an operand is split into three bf16 parts, and beyond it
+ *   the first one is infinite and the others NaN; parts below 2^-110 are dropped). Anything else
+ *   leaves the results of its own graph undefined, those of its masked rows apart.
  * heads_q must be a multiple of heads_kv; num_q * heads_q and num_k * heads_kv < 2^31 - 2^20;
  * num_graphs < 2^20; scale finite.  Offsets into the tensors are 64 bits wide. */
 typedef struct {

@@ -61,3 +61,26 @@ def test_infinite_key_aligned_or_not(dim, lens):
     torch.cuda.synchronize()
     for a, b in zip(grads, refs):
         assert np.array_equal(host(a), host(b), equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [24, 33, 64])
+@pytest.mark.parametrize("lens", [[40, 50, 60], [2000, 333, 1000]], ids=str)
+def test_bad_values_stay_in_their_graph(dtype, dim, lens):
+    """Infinities and NaN in the counted rows of one graph change no bit of the others."""
+    import torch
+    p = dev(ptr(lens))
+    q, k, v, g = draw(9, dtype, lens, lens, 4, 2, dim, dim)
+    say(f"[attention] {dtype} {lens} nodes, {dim} dimensions, bad values in the second graph")
+
+    def step():
+        out, lse = E.e3conv_attention(q, k, v, p, p)
+        return [t.clone() for t in (out, lse) + E.e3conv_attention_backward(q, k, v, out, lse, g, p, p)]
+
+    want = step()
+    a, b = lens[0], lens[0] + lens[1]
+    q[a, 0, 1], k[b - 1, 1, 0], v[a + 3, 0, -1], g[b - 1, 2, 3] = float("nan"), float("-inf"), float("inf"), float("nan")
+    got = step()
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x[:a], y[:a]) and torch.equal(x[b:], y[b:])
