@@ -107,3 +107,40 @@ def test_more_graphs_than_one_axis_of_a_launch():
     assert bool((gx.abs() <= 2 * u * (g * w).abs() * 10 * seen).all()) and not gw.any()
     want, size = (g.double() * seen).sum(0), (g.double().abs() * seen).sum(0)
     assert bool(((gb - want).abs() <= 4 * graphs ** 0.5 * u * size).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("channels,groups", [(4096, 32), (2056, 8), (2056, 2056), (1028, 4), (300, 300), (300, 12),
+                                             (1001, 7), (4095, 9), (257, 257)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_rows_wider_than_a_work_group(dtype, channels, groups, masked):
+    """More than 256 runs of channels: several work-groups along a row, the last one narrower, of whole 16-byte
+    runs (fp32 by 4, bf16 by 8) and element by element; with empty graphs and graphs of one chunk and of many."""
+    lens = [3, 0, 200, 1, 0]
+    mask = None
+    if masked:
+        mask = (np.random.default_rng(channels).random(sum(lens)) < 0.7).astype(np.uint8)
+        mask[-1] = 0
+    x, g, w, b = inputs(dtype, lens, channels)
+    if masked:
+        hole = dev(mask == 0)
+        x[hole], g[hole] = float("nan"), float("inf")
+    compare(dtype, lens, groups, x, g, w, b, "silu", mask)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+@pytest.mark.parametrize("dtype,rows", [("f32", 150000), ("bf16", 300000)])
+def test_results_larger_than_the_l2s(dtype, rows, act):
+    """Results of more than 32 MiB are stored past the caches, by kernels of their own: out of place, in place, and
+    over a mask."""
+    lens = [rows - 5000, 0, 4999, 1]
+    x, g, w, b = inputs(dtype, lens, 64)
+    if act == "relu":      # keep z away from the corner: its derivative is a step there
+        z = norm.group_norm(host(x), ptr(lens), 8, w, b, float(np.float32(1e-5)), "none")[0]["y"]
+        g[dev(np.abs(z) < 1e-3)] = 0
+    compare(dtype, lens, 8, x, g, w, b, act)
+    if act == "silu":
+        y, gx = x.clone(), g.clone()
+        compare(dtype, lens, 8, y, gx, w, b, act, out=y, grad_x=gx)
+        mask = (np.arange(rows) % 5 != 2).astype(np.uint8)
+        compare(dtype, lens, 8, x, g, w, b, act, mask)
