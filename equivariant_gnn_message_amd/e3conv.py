@@ -690,8 +690,10 @@ def _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask):
     kp = qp if k_ptr is q_ptr else _dense(k_ptr, "k_ptr", i32, index, graphs + 1)
     qm = None if q_mask is None else _node_mask(q_mask, "q_mask", index, nq)
     km = None if k_mask is None else _node_mask(k_mask, "k_mask", index, nk)
-    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, d ** -0.5 if scale is None else scale, qp, kp, qm, km,
-                         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, q_head, k_row, k_head, v_row, v_head)
+    if scale is None:
+        scale = d ** -0.5 if d else 1.0       # d = 0: the library refuses it
+    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, scale, qp, kp, qm, km, q.data_ptr(), k.data_ptr(),
+                         v.data_ptr(), q_row, q_head, k_row, k_head, v_row, v_head)
 
 
 def e3conv_attention_workspace_size(args, backward=False):
@@ -803,7 +805,7 @@ def e3conv_group_norm(x, row_ptr, groups, weight=None, bias=None, eps=1e-5, acti
     """
     lib = _lib or load_library()
     args = _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask)
-    index, shape = x.get_device(), (args.num_graphs, args.groups)
+    index, shape = x.get_device(), (args.num_graphs, groups if groups > 0 else 0)   # below 1: the library refuses it
     handle, other = _enter(index, stream)
     if other is not None:
         return _on(other, e3conv_group_norm, x, row_ptr, groups, weight, bias, eps, activation, row_mask, out, workspace)
