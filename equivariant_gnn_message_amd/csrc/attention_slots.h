@@ -40,12 +40,12 @@ constexpr int tile_start(int slot, int first_slot, int tile, int nrows) {
 // r / group for 0 <= r < 2^31: ceil(2^(31 + l) / group) with 2^l >= group, by a product.
 struct GroupDiv {
   unsigned magic;
-  int shift, log2;      // log2: of a power of two, else -1
+  int shift, log2;      // log2: of a power of two, else 31 (a shift that leaves nothing of a step of rows)
 };
 constexpr GroupDiv group_div(int group) {
   int l = 0;
   while ((1 << l) < group) ++l;
-  return {(unsigned)((((uint64_t)1 << (31 + l)) + group - 1) / group), l - 1, 1 << l == group ? l : -1};
+  return {(unsigned)((((uint64_t)1 << (31 + l)) + group - 1) / group), l - 1, 1 << l == group ? l : 31};
 }
 constexpr int div_group(int r, int group, unsigned magic, int shift) {
   return group == 1 ? r : (int)((unsigned)(((uint64_t)(unsigned)r * magic) >> 32) >> shift);

@@ -32,7 +32,7 @@ struct Params {
   int group;                       // query heads per kv head
   unsigned magic;                  // r / group = (r magic) >> 32 >> shift for 0 <= r < 2^31, group > 1
   int shift;
-  int group_log2;                  // of a power of two, else -1
+  int group_log2;                  // of a power of two, else 31
   float c;                         // |scale| log2(e), at least the smallest normal number
   int negate;                      // scale < 0: q enters with its sign changed
   int vec;                         // 16-byte loads of q, k, v, grad_out (and out) rows
@@ -470,7 +470,7 @@ struct Rows {
     const e3conv_attention_args& a = p.a;
     // STEP rows on lie STEP / group queries on where the heads of a group divide STEP
     const int by = PairT::STEP >> p.group_log2;
-    if (next + ROWS <= end && p.group_log2 >= 0 && by << p.group_log2 == PairT::STEP) {
+    if (next + ROWS <= end && by << p.group_log2 == PairT::STEP) {
 #pragma unroll
       for (int e = 0; e < PairT::E; ++e)
         pair.issue(e, qp + (e * by * a.q_row + shift(e, a.dim_qk)), gp + (e * by * p.go_row + shift(e, a.dim_v)),

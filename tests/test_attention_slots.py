@@ -43,6 +43,8 @@ extern "C" int divide(int r, int group) {
   const GroupDiv by = group_div(group);
   return div_group(r, group, by.magic, by.shift);
 }
+extern "C" int step_queries(int group, int step) { return step >> group_div(group).log2 << group_div(group).log2; }
+extern "C" int log2_of(int group) { return group_div(group).log2; }
 """
 
 
@@ -101,3 +103,11 @@ def test_any_offsets_stay_inside(host, group, tile):
 def test_division(host, group):
     for r in [0, 1, group - 1, group, 2 * group - 1, 12345678, (1 << 31) - 1 - (1 << 20), (1 << 31) - 1]:
         assert host.divide(r, group) == r // group
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 6, 8, 12, 32, 100, 4096])
+@pytest.mark.parametrize("step", [4, 8, 16, 64])
+def test_rows_a_step_apart(host, group, step):
+    """A kernel shifts by log2 before it knows whether the heads of a group divide a step of rows."""
+    assert 0 <= host.log2_of(group) <= 31
+    assert (host.step_queries(group, step) == step) == (step % group == 0)
