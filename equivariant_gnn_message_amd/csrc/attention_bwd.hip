@@ -13,11 +13,11 @@
 // delta itself: there the launches are the time (16 us as two, 12 as one for 64 graphs of
 // 64 nodes).
 //
-// What bounds them: for fp32 (20 000 nodes, 4 heads of 32, 3.55 ms: 1.5 + 2.0) the products,
-// six bf16 ones for each, 55 % of the cycles, and the splitting of P and dS into their parts,
-// which do not overlap; for bf16 with 128 dimensions (50 000 ragged nodes, 553 us: 0.22 +
+// What bounds them: for fp32 (20 000 nodes, 4 heads of 32, 3.57 ms: 1.5 + 2.0) the products,
+// six bf16 ones for each, 58 % of the SIMD cycles, and the splitting of P and dS into their parts,
+// 41 %; for bf16 with 128 dimensions (50 000 ragged nodes, 548 us: 0.22 +
 // 0.33 ms) the latency of LDS and barriers at one wave a SIMD for grad_k and grad_v, whose
-// operands and sums fill 320 registers; with few rows (4 queries against 12 500 keys, 88 us)
+// operands and sums fill 371 registers; with few rows (4 queries against 12 500 keys, 89 us)
 // the bytes of k, v and their gradients.
 #include "attention_tile.h"
 #include "kernels.h"

@@ -7,16 +7,20 @@
 // a lane keeps one row: maximum and sum of its softmax are sums within the lane
 // and one exchange with the other half of the wave, and P^T is the second
 // product's operand where the first one left it.  One pass over the keys with the running
-// maximum and sum; the next tile is on its way while the current one is used.
+// maximum and sum (online softmax, Milakov and Gimelshein 2018; rescaled only when the maximum
+// has grown by more than a threshold, published as conditional rescaling); the sum over tiles
+// is compensated (Kahan 1965).  The next tile is on its way while the current one is used.
 //
-// What bounds it (100 000 nodes in ragged graphs, 8 / 2 heads of 64, bf16: 307 us,
-// 700 TFLOP/s): the vector ALU.  A tile of 64 keys costs a wave 16 products (512
-// cycles) and some 230 vector instructions, 32 of them exponentials at double cost, and the
-// two hardly overlap on a SIMD: multiply-adds of one wave and matrix instructions of another
-// take the sum of their times.  Vector instructions were 74 % of the cycles, products 32 %.
+// What bounds it (100 000 nodes in ragged graphs, 8 / 2 heads of 64, bf16: 309 us,
+// 695 TFLOP/s): vector instructions beside the products.  A tile of 64 keys costs a wave
+// 16 products (512 cycles) and 217 vector instructions (counted, start and end of a
+// work-group among them); scale, exponential, sum, maximum and packing of its 32 logits a
+// lane are about 130 of these.  The vector ALU is busy in 68 % of the SIMD cycles and the matrix
+// cores in 35 %.  In loops of nothing else, two waves of a SIMD took the sum of both times for
+// multiply-adds beside products, and 0.86 of it for exponentials.
 // LDS conflicts are none (the tiles' permutation); reads are a third of its rate.
 // fp32 has the same form with six products for one; with few rows (one query against 100 000
-// keys, 17.7 us) it is bound by the keys' bytes and the join of the splits.
+// keys, 17.3 us) it is bound by the keys' bytes and the join of the splits.
 #include "attention_tile.h"
 #include "kernels.h"
 
