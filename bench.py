@@ -188,12 +188,12 @@ def roofline(kernel, ms, nbytes, flops=None, traffic=None):
 
 def kernel_source_files():
     """Every device source of the convolution and the linear: the .hip files and every header
-    except the host builder's and those of the per-graph attention and group norm, which no
+    except the host builder's and those of the operators beside the convolution, which no
     counter record of a benched kernel depends on."""
     csrc = os.path.join(ROOT, "equivariant_gnn_message_amd", "csrc")
     return sorted(f for f in os.listdir(csrc)
                   if (f.endswith(".hip") or (f.endswith(".h") and f != "host_core.h"))
-                  and not f.startswith(("attention", "group_norm")))
+                  and not f.startswith(("attention", "group_norm", "rms_norm", "rotary", "row_units")))
 
 
 def strip_comments(src):

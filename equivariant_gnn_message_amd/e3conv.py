@@ -6,7 +6,7 @@ tensor's device pointer, and the current HIP stream of torch unless a stream
 is given).  All arithmetic runs in the library's HIP kernels; there is no
 fallback: if the library is missing every call raises.
 
-``Plan``, ``E3ConvFunction``, ``AttentionFunction`` and ``GroupNormFunction`` are
+``Plan``, ``E3ConvFunction``, ``AttentionFunction``, ``GroupNormFunction`` and ``RMSNormFunction`` are
 conveniences over the same calls.
 """
 
@@ -51,6 +51,7 @@ EXPORTED = [
     "e3conv_plan_num_variants",
     "e3conv_attention_workspace_size", "e3conv_attention", "e3conv_attention_backward",
     "e3conv_group_norm_workspace_size", "e3conv_group_norm", "e3conv_group_norm_backward",
+    "e3conv_rms_norm_workspace_size", "e3conv_rms_norm", "e3conv_rms_norm_backward",
     "e3conv_status_string", "e3conv_last_error_detail",
 ]
 
@@ -85,6 +86,14 @@ class GroupNormArgs(ctypes.Structure):
                 ("groups", ctypes.c_int32), ("activation", ctypes.c_int), ("eps", ctypes.c_float),
                 ("num_rows", I64), ("row_ptr", P), ("row_mask", P), ("x", P), ("x_row", I64),
                 ("weight", P), ("bias", P)]
+
+
+class RMSNormArgs(ctypes.Structure):
+    """e3conv_rms_norm_args."""
+    _fields_ = [("dtype", ctypes.c_int), ("channels", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("weight_channels", ctypes.c_int32), ("eps", ctypes.c_float), ("num_rows", I64),
+                ("row_mask", P), ("x", P), ("x_row", I64), ("residual", P), ("residual_row", I64),
+                ("weight", P)]
 
 
 def load_library(path=LIB_PATH):
@@ -151,6 +160,9 @@ def load_library(path=LIB_PATH):
         "e3conv_group_norm_workspace_size": ([P, ctypes.c_int, P], ctypes.c_int),
         "e3conv_group_norm": ([P, P, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "e3conv_group_norm_backward": ([P, P, P, P, I64, P, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "e3conv_rms_norm_workspace_size": ([P, P], ctypes.c_int),
+        "e3conv_rms_norm": ([P, P, I64, P, I64, P, P], ctypes.c_int),
+        "e3conv_rms_norm_backward": ([P, P, P, I64, P, I64, P, I64, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "e3conv_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "e3conv_last_error_detail": ([], ctypes.c_char_p),
     }
@@ -638,14 +650,14 @@ def _enter(index, stream):
     return handle, stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(handle, device=index)
 
 
-def _workspace(given, size_of, args, like, backward=0):
+def _workspace(given, size_of, args, like, *backward):
     """(address, bytes, tensor) of the caller's workspace, or of one allocated for the call."""
     if given is not None:
         if given.get_device() != like.get_device() or not given.is_contiguous() or given.data_ptr() % 16:
             raise ValueError(f"workspace must be a contiguous, 16-byte aligned tensor on {like.device}")
         return given.data_ptr(), given.numel() * given.element_size(), given
     n = ctypes.c_size_t()
-    _check(size_of(args, backward, ctypes.byref(n)))
+    _check(size_of(args, *backward, ctypes.byref(n)))
     if n.value == 0:
         return None, 0, None
     t = like.new_empty((n.value,), dtype=_torch.uint8)
@@ -732,7 +744,7 @@ def e3conv_attention(q, k, v, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None
     else:
         _dense(lse, "lse", _torch.float32, index, shape[0] * shape[1])
     ref = ctypes.byref(args)
-    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_attention_workspace_size, ref, q, 0)
     _check(lib.e3conv_attention(ref, out.data_ptr(), row, head, lse.data_ptr(), ws, nbytes, handle))
     return out, lse
 
@@ -817,7 +829,7 @@ def e3conv_group_norm(x, row_ptr, groups, weight=None, bias=None, eps=1e-5, acti
     mean = x.new_empty(shape, dtype=_torch.float32)
     rstd = _torch.empty_like(mean)
     ref = ctypes.byref(args)
-    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_group_norm_workspace_size, ref, x, 0)
     _check(lib.e3conv_group_norm(ref, out.data_ptr(), row, mean.data_ptr(), rstd.data_ptr(), ws, nbytes, handle))
     return out, mean, rstd
 
@@ -848,6 +860,105 @@ def e3conv_group_norm_backward(x, row_ptr, groups, weight, bias, activation, mea
         ref, mean_at, rstd_at, grad_y.data_ptr(), gy_row, grad_x.data_ptr(), row,
         None if gw is None else gw.data_ptr(), None if gb is None else gb.data_ptr(), ws, nbytes, handle))
     return grad_x, gw, gb
+
+
+# ------------------------------------------- root-mean-square norm ---
+
+def _rms_norm_args(x, weight, groups, eps, residual, row_mask):
+    if x.dim() != 2:
+        raise ValueError("x must be (num_rows, channels)")
+    code, index, dt = _dtype_code(x), x.get_device(), x.dtype
+    n, c = x.shape
+    row, _ = _rows_of(x, "x", dt, index, x.shape)
+    res = res_row = 0
+    if residual is not None:
+        res_row, _ = _rows_of(residual, "residual", dt, index, x.shape)
+        res = residual.data_ptr()
+    if weight is None:
+        period, w = c, None
+    else:
+        period = weight.numel()
+        w = _dense(weight, "weight", _torch.float32, index, period)
+    return RMSNormArgs(code, c, groups, period, eps, n, _node_mask(row_mask, "row_mask", index, n), x.data_ptr(), row,
+                       res or None, res_row, w)
+
+
+def e3conv_rms_norm_workspace_size(args):
+    """Bytes of workspace of the reverse pass for the sizes in an RMSNormArgs."""
+    n = ctypes.c_size_t()
+    _check(load_library().e3conv_rms_norm_workspace_size(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def e3conv_rms_norm(x, weight=None, groups=1, eps=1e-5, residual=None, row_mask=None, out=None, total=None,
+                    stream=None):
+    """(y, total, rstd): total = x + residual, y = weight * total / rms of each group of channels of a row.
+
+    x and residual (num_rows, channels) fp32 or bf16, unit stride along the channels; weight fp32, of a number of
+    values that divides the channels (they repeat along the row: a weight of one head for all heads, or of C
+    channels for an l-block's components), or None; row_mask bool or uint8, 0 for padding.  Without a residual
+    total is None, and x takes its place in the reverse pass.  rstd fp32 (num_rows, groups).
+    """
+    lib = _lib or load_library()
+    args = _rms_norm_args(x, weight, groups, eps, residual, row_mask)
+    index = x.get_device()
+    handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, e3conv_rms_norm, x, weight, groups, eps, residual, row_mask, out, total)
+    if out is None:
+        out, row = x.new_empty(x.shape), args.channels
+    else:
+        row, _ = _rows_of(out, "out", x.dtype, index, x.shape)
+        _written(out, "out")
+    at, total_row = None, 0
+    if residual is None:
+        if total is not None:
+            raise ValueError("total is the sum with a residual, and there is none")
+    elif total is None:
+        total, total_row = x.new_empty(x.shape), args.channels
+        at = total.data_ptr()
+    else:
+        total_row, _ = _rows_of(total, "total", x.dtype, index, x.shape)
+        _written(total, "total")
+        at = total.data_ptr()
+    rstd = x.new_empty((args.num_rows, max(groups, 0)), dtype=_torch.float32)     # below 1: the library refuses it
+    _check(lib.e3conv_rms_norm(ctypes.byref(args), out.data_ptr(), row, at, total_row, rstd.data_ptr(), handle))
+    return out, total, rstd
+
+
+def e3conv_rms_norm_backward(x, weight, groups, rstd, grad_y, grad_total=None, row_mask=None, grad_x=None,
+                             workspace=None, stream=None):
+    """(grad_x, grad_weight): x is the forward's total where it had a residual, and grad_x the gradient of both.
+
+    grad_total: the gradient that reaches the sum past the norm, or None.  grad_weight is None where weight is.
+    """
+    lib = _lib or load_library()
+    # eps is already in rstd
+    args = _rms_norm_args(x, weight, groups, 1.0, None, row_mask)
+    index, dt = x.get_device(), x.dtype
+    rstd_at = _dense(rstd, "rstd", _torch.float32, index, args.num_rows * groups)
+    gy_row, _ = _rows_of(grad_y, "grad_y", dt, index, x.shape)
+    gt, gt_row = None, 0
+    if grad_total is not None:
+        gt_row, _ = _rows_of(grad_total, "grad_total", dt, index, x.shape)
+        gt = grad_total.data_ptr()
+    handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, e3conv_rms_norm_backward, x, weight, groups, rstd, grad_y, grad_total, row_mask, grad_x,
+                   workspace)
+    if grad_x is None:
+        grad_x, row = x.new_empty(x.shape), args.channels
+    else:
+        row, _ = _rows_of(grad_x, "grad_x", dt, index, x.shape)
+        _written(grad_x, "grad_x")
+    ref = ctypes.byref(args)
+    gw, ws, nbytes = None, None, 0
+    if weight is not None:
+        gw = _torch.empty_like(weight)
+        ws, nbytes, _keep = _workspace(workspace, lib.e3conv_rms_norm_workspace_size, ref, x)
+    _check(lib.e3conv_rms_norm_backward(ref, rstd_at, grad_y.data_ptr(), gy_row, gt, gt_row, grad_x.data_ptr(), row,
+                                        None if gw is None else gw.data_ptr(), ws, nbytes, handle))
+    return grad_x, gw
 
 
 # ------------------------------------------------------ convenience ---
@@ -1143,8 +1254,40 @@ def _group_norm_function():
     return GroupNormFunction
 
 
+def _rms_norm_function():
+    import torch
+
+    class RMSNormFunction(torch.autograd.Function):
+        """y of e3conv_rms_norm, or (y, total) with a residual, differentiable in x, weight and residual.
+
+        apply(x, weight=None, groups=1, eps=1e-5, residual=None, row_mask=None).
+        """
+
+        @staticmethod
+        def forward(ctx, x, weight=None, groups=1, eps=1e-5, residual=None, row_mask=None):
+            y, total, rstd = e3conv_rms_norm(x, weight, groups, eps, residual, row_mask)
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(x if total is None else total, weight, rstd, row_mask)
+            ctx.groups, ctx.added = groups, total is not None
+            return y if total is None else (y, total)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_y, grad_total=None):
+            x, weight, rstd, row_mask = ctx.saved_tensors
+            rows = lambda g: g if g is None or g.stride(-1) == 1 else g.contiguous()
+            if grad_y is None:
+                if grad_total is None:
+                    return (None,) * 6
+                grad_y = torch.zeros_like(x)
+            gx, gw = e3conv_rms_norm_backward(x, weight, ctx.groups, rstd, rows(grad_y), rows(grad_total), row_mask)
+            return gx, gw, None, None, gx if ctx.added else None, None
+
+    return RMSNormFunction
+
+
 _FUNCTIONS = {"E3ConvFunction": _autograd_function, "AttentionFunction": _attention_function,
-              "GroupNormFunction": _group_norm_function}
+              "GroupNormFunction": _group_norm_function, "RMSNormFunction": _rms_norm_function}
 
 
 def __getattr__(name):

@@ -586,6 +586,57 @@ e3conv_status e3conv_group_norm_backward(const e3conv_group_norm_args* args, con
                                          float* grad_bias, void* workspace, size_t workspace_bytes,
                                          void* hip_stream);
 
+/* Root-mean-square norm of rows, with a residual's addition: the channels split into
+ * `groups` runs of size = channels / groups, and with s = x + residual,
+ *     rstd = 1 / sqrt(sum over the group s^2 / size + eps),
+ *     y    = weight[c mod weight_channels] s rstd.
+ * No mean is taken, so it also acts on an l > 0 block: the rows of an l = 1 block with all its
+ * 3 C values as one group and one weight a channel (weight_channels = C) keep their equivariance.
+ * With groups = heads and weight_channels = size it is the norm of each attention head.
+ * - x, residual (NULL: none), y and total (num_rows, channels) in dtype (fp32 or bf16), unit stride along
+ *   the channels, row strides in elements; weight fp32 (weight_channels) or NULL (1); statistics
+ *   and arithmetic fp32, each result rounded once (y from the unrounded sum).
+ * - row_mask: device bytes (num_rows) or NULL; a row whose byte is 0 gets y = 0, total = 0,
+ *   rstd = 1 / sqrt(eps) and a zero gradient, whatever x, residual and the gradients hold.
+ * - rstd: fp32 (num_rows, groups), dense.
+ * channels <= 65536, a multiple of groups and of weight_channels, size <= 8192; eps > 0;
+ * num_rows * groups < 2^31 - 2^20.  The squares of a group must not overflow fp32. */
+typedef struct {
+  e3conv_dtype dtype;
+  int32_t channels, groups, weight_channels;
+  float eps;
+  int64_t num_rows;
+  const uint8_t* row_mask;
+  const void* x;
+  int64_t x_row;
+  const void* residual;
+  int64_t residual_row;
+  const float* weight;
+} e3conv_rms_norm_args;
+
+/* y is fully written; total, which gets s, and rstd are too unless NULL.  y and total may each be x
+ * or residual itself, with the same stride. */
+e3conv_status e3conv_rms_norm(const e3conv_rms_norm_args* args, void* y, int64_t y_row, void* total,
+                              int64_t total_row, float* rstd, void* hip_stream);
+
+/* Bytes of device workspace (16-byte aligned) of the reverse pass where it computes grad_weight; none
+ * otherwise. */
+e3conv_status e3conv_rms_norm_workspace_size(const e3conv_rms_norm_args* args, size_t* bytes);
+
+/* Reverse pass; args holds s as x (the forward's total) and no residual, rstd is the forward's.  With
+ * xhat = s rstd and dn = weight grad_y,
+ *     grad_x = rstd (dn - xhat sum(dn xhat) / size) + grad_total,
+ *     grad_weight[j] = sum of grad_y xhat over the rows and the channels c = j mod weight_channels.
+ * grad_x is the gradient of x and of the residual alike; grad_total (NULL: none) is what reaches
+ * them past the norm.  grad_x may be grad_y or grad_total itself, with the same stride.  grad_weight is
+ * fp32 (weight_channels) or NULL (not computed).  All outputs are fully written, without atomics: the
+ * same inputs give the same bits. */
+e3conv_status e3conv_rms_norm_backward(const e3conv_rms_norm_args* args, const float* rstd,
+                                       const void* grad_y, int64_t grad_y_row, const void* grad_total,
+                                       int64_t grad_total_row, void* grad_x, int64_t grad_x_row,
+                                       float* grad_weight, void* workspace, size_t workspace_bytes,
+                                       void* hip_stream);
+
 /* Check a graph (the e3j Convolution page, __call__: indices lie in
  * [0, num_nodes); the fused kernels need edges sorted by receiver): row_ptr[0]
  * = 0, row_ptr non-decreasing and within [0, num_edges], row_ptr[num_nodes] =
