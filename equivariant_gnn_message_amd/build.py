@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libe3conv.so")
 
 SOURCES = ["host_core.cpp", "e3conv.cpp", "kernels.hip", "validate.hip", "layout_tiny.hip",
            "layout_gate.hip", "layout_mace.hip", "layout_big.hip", "linear.hip",
-           "attention.hip", "attention_fwd.hip", "attention_bwd.hip", "group_norm.hip", "rms_norm.hip"]
+           "attention.hip", "attention_fwd.hip", "attention_bwd.hip", "group_norm.hip", "rms_norm.hip",
+           "rotary.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
           "-I", INCLUDE, "-I", CSRC]

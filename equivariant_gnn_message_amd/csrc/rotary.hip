@@ -1,0 +1,434 @@
+// Rotary positions over several axes, and their reverse pass (contract in e3conv.h).
+//
+// Pair p of every head of row i is turned by angle[i, p] = sum_a positions[i, a] waves[p, a]:
+//     (u, v) -> (u cos - v sin, u sin + v cos).
+// The reverse pass turns the gradient back, (gu, gv); with d_angle[i, p] = sum over heads of (u gv - v gu),
+//     grad_positions[i, a] = sum_p d_angle waves[p, a],   grad_waves[p, a] = sum_i d_angle positions[i, a].
+// A work-group takes tiles of whole rows.  The tile's cosines and sines are formed once for all heads, the
+// angle in 64 bits and in turns (of a position of 10^4 wave lengths 32 bits leave three digits), and stand in
+// LDS; the rows then pass through registers in runs of 16 bytes, whatever their heads.  In the reverse pass
+// each pair's d_angle goes to LDS and is summed over the heads in order.  Memory bound.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "e3conv.h"
+#include "kernels.h"
+#include "row_units.h"
+
+namespace e3c {
+namespace {
+
+using namespace rows;
+
+constexpr int NT = 256;               // threads of a work-group
+constexpr int kMaxDim = 256, kMaxAxes = 4;
+constexpr int kTile = 8192;           // elements of a tile at most: one row's heads go in parts if they have more
+constexpr int kTable = 2048;          // pairs of a tile's rows at most
+
+struct RotaryParams {
+  e3conv_rotary_args a;
+  int units;                          // runs of a head: of V elements, or turned pairs of V and then V elements
+  int turning;                        // units that hold pairs
+  int tile_rows, tile_heads;
+  int tiles, blocks;
+  Div by_units, by_heads, by_pairs, by_axes;
+  float sign;
+  void* out;
+  long out_row, out_head;
+  const void* g;                      // reverse pass: the gradient, turned back
+  long g_row, g_head;
+  float* gp;
+  float* gw;
+  double* part;                       // (blocks, pairs axes)
+};
+
+// Where a unit of a row's head lies: its first elements, its second ones, and its first pair.
+template <int V, bool ADJACENT>
+struct Unit {
+  int u, v, pair;
+  bool turns;
+  __device__ __forceinline__ Unit(const RotaryParams& p, int k) {
+    turns = k < p.turning;
+    if constexpr (ADJACENT && V > 1) {            // V / 2 pairs in a run
+      u = v = k * V;
+      pair = k * (V / 2);
+    } else if (ADJACENT) {                        // one pair
+      u = turns ? 2 * k : k + p.turning;
+      v = u + 1;
+      pair = k;
+    } else {
+      u = turns ? k * V : k * V + p.turning * V;  // beyond the pairs' second halves
+      v = u + p.a.pairs;
+      pair = k * V;
+    }
+  }
+};
+
+// The cosines and sines of the tile's rows.
+__device__ __forceinline__ void fill_table(const RotaryParams& p, long row0, int nrows, float2* table) {
+  const e3conv_rotary_args& a = p.a;
+  for (int e = threadIdx.x; e < nrows * a.pairs; e += NT) {
+    const int r = p.by_pairs.of(e), k = e - r * a.pairs;
+    const long row = row0 + r;
+    float s = 0.0f, c = 1.0f;
+    if (!a.row_mask || a.row_mask[row]) {
+      double angle = 0.0;
+      for (int x = 0; x < a.axes; ++x)
+        angle = fma((double)a.positions[row * a.position_row + x], (double)a.waves[k * a.axes + x], angle);
+      const double turns = angle * 0.15915494309189533577;
+      sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+    }
+    table[e] = make_float2(c, p.sign * s);
+  }
+}
+
+// A unit's elements in registers.
+template <class T, int V, bool ADJACENT>
+struct Held {
+  typename Run<T, V>::type a, b;
+  static constexpr bool TWO = !ADJACENT || V == 1;     // second elements of the pairs apart from the first
+  __device__ __forceinline__ void load(const T* head, const Unit<V, ADJACENT>& at) {
+    a = read<T, V>(head + at.u);
+    if (TWO && at.turns) b = read<T, V>(head + at.v);
+  }
+};
+
+// Turns the pairs of a unit: x holds its run, or x the first elements of its pairs and y the second ones.
+template <int V, bool ADJACENT>
+__device__ __forceinline__ void turn(const float2* cs, int pairs, const Unit<V, ADJACENT>& at, float (&x)[V],
+                                     float (&y)[V]) {
+  if constexpr (ADJACENT && V > 1) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+      if (at.pair + i < pairs) {
+        const float2 t = cs[at.pair + i];
+        const float u = x[2 * i], v = x[2 * i + 1];
+        x[2 * i] = fmaf(u, t.x, -(v * t.y));
+        x[2 * i + 1] = fmaf(u, t.y, v * t.x);
+      }
+  } else if (at.turns) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 t = cs[at.pair + i];
+      const float u = x[i], v = y[i];
+      x[i] = fmaf(u, t.x, -(v * t.y));
+      y[i] = fmaf(u, t.y, v * t.x);
+    }
+  }
+}
+
+template <class T, int V, bool ADJACENT>
+__global__ void __launch_bounds__(NT) rotary(RotaryParams p) {
+  __shared__ float2 table[kTable];
+  const e3conv_rotary_args& a = p.a;
+  const long tile = block_index();
+  if (tile >= p.tiles) return;
+  const long row0 = tile * p.tile_rows;
+  const int nrows = (int)min((long)p.tile_rows, a.num_rows - row0);
+  const int n = nrows * a.heads * p.units;
+  constexpr int N = 4;
+  bool ready = false;
+  for (int e0 = threadIdx.x; e0 - (int)threadIdx.x < n; e0 += N * NT) {
+    Held<T, V, ADJACENT> held[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = e0 + i * NT;
+      if (e < n) {
+        const int rh = p.by_units.of(e), r = p.by_heads.of(rh);
+        held[i].load((const T*)a.x + (row0 + r) * a.x_row + (rh - r * a.heads) * a.x_head,
+                     Unit<V, ADJACENT>(p, e - rh * p.units));
+      }
+    }
+    if (!ready) {
+      fill_table(p, row0, nrows, table);
+      __syncthreads();
+      ready = true;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = e0 + i * NT;
+      if (e < n) {
+        const int rh = p.by_units.of(e), r = p.by_heads.of(rh);
+        const Unit<V, ADJACENT> at(p, e - rh * p.units);
+        float x[V], y[V];
+        widen<T, V>(held[i].a, x);
+        widen<T, V>(held[i].b, y);
+        turn<V, ADJACENT>(table + r * a.pairs, a.pairs, at, x, y);
+        if (a.row_mask && !a.row_mask[row0 + r])
+#pragma unroll
+          for (int j = 0; j < V; ++j) x[j] = y[j] = 0.0f;
+        T* to = (T*)p.out + (row0 + r) * p.out_row + (rh - r * a.heads) * p.out_head;
+        store<T, V>(to + at.u, x);
+        if (Held<T, V, ADJACENT>::TWO && at.turns) store<T, V>(to + at.v, y);
+      }
+    }
+  }
+}
+
+// With the gradients of positions or waves: turns back g and forms d_angle.  A work-group takes every
+// blocks-th tile and keeps its part of grad_waves.
+template <class T, int V, bool ADJACENT>
+__global__ void __launch_bounds__(NT) rotary_grad(RotaryParams p) {
+  __shared__ float2 table[kTable];
+  __shared__ float angles[kTile / 2];          // (row, head, pair)
+  __shared__ float sums[kTable];               // (row, pair), over the heads
+  const e3conv_rotary_args& a = p.a;
+  constexpr int W = (kMaxDim / 2 * kMaxAxes + NT - 1) / NT;
+  double gw[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) gw[i] = 0.0;
+  for (long tile = blockIdx.x; tile < p.tiles; tile += p.blocks) {
+    const long row0 = tile * p.tile_rows;
+    const int nrows = (int)min((long)p.tile_rows, a.num_rows - row0);
+    __syncthreads();                           // the last tile's sums are read
+    fill_table(p, row0, nrows, table);
+    for (int e = threadIdx.x; e < nrows * a.pairs; e += NT) sums[e] = 0.0f;
+    __syncthreads();
+    for (int h0 = 0; h0 < a.heads; h0 += p.tile_heads) {      // more than one part: the tile is one row
+      const int heads = min(p.tile_heads, a.heads - h0), n = nrows * heads * p.units;
+      for (int e = threadIdx.x; e < n; e += NT) {
+        const int rh = p.by_units.of(e), r = nrows == 1 ? 0 : p.by_heads.of(rh), h = rh - r * heads;
+        const Unit<V, ADJACENT> at(p, e - rh * p.units);
+        const long row = row0 + r;
+        Held<T, V, ADJACENT> hg, hx;
+        hg.load((const T*)p.g + row * p.g_row + (h0 + h) * p.g_head, at);
+        hx.load((const T*)a.x + row * a.x_row + (h0 + h) * a.x_head, at);
+        float gu[V], gv[V], u[V], v[V];
+        widen<T, V>(hg.a, gu);
+        widen<T, V>(hg.b, gv);
+        widen<T, V>(hx.a, u);
+        widen<T, V>(hx.b, v);
+        turn<V, ADJACENT>(table + r * a.pairs, a.pairs, at, gu, gv);
+        const bool live = !a.row_mask || a.row_mask[row];
+        if (!live)
+#pragma unroll
+          for (int j = 0; j < V; ++j) gu[j] = gv[j] = u[j] = v[j] = 0.0f;
+        T* to = (T*)p.out + row * p.out_row + (h0 + h) * p.out_head;
+        store<T, V>(to + at.u, gu);
+        if (Held<T, V, ADJACENT>::TWO && at.turns) store<T, V>(to + at.v, gv);
+        float* d = angles + (r * heads + h) * a.pairs + at.pair;
+        if constexpr (ADJACENT && V > 1) {
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j)
+            if (at.pair + j < a.pairs) d[j] = fmaf(u[2 * j], gu[2 * j + 1], -(u[2 * j + 1] * gu[2 * j]));
+        } else if (at.turns) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) d[j] = fmaf(u[j], gv[j], -(v[j] * gu[j]));
+        }
+      }
+      __syncthreads();
+      for (int e = threadIdx.x; e < nrows * a.pairs; e += NT) {
+        const int r = p.by_pairs.of(e), k = e - r * a.pairs;
+        float s = sums[e];
+        for (int h = 0; h < heads; ++h) s += angles[(r * heads + h) * a.pairs + k];
+        sums[e] = s;
+      }
+      __syncthreads();
+    }
+    if (p.gp)
+      for (int e = threadIdx.x; e < nrows * a.axes; e += NT) {
+        const int r = p.by_axes.of(e), x = e - r * a.axes;
+        float s = 0.0f;
+        for (int k = 0; k < a.pairs; ++k) s = fmaf(sums[r * a.pairs + k], a.waves[k * a.axes + x], s);
+        p.gp[(row0 + r) * a.axes + x] = s;
+      }
+    if (p.gw) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const int e = threadIdx.x + i * NT;
+        if (e < a.pairs * a.axes) {
+          const int k = p.by_axes.of(e), x = e - k * a.axes;
+          for (int r = 0; r < nrows; ++r) {
+            const float d = sums[r * a.pairs + k];
+            // a masked row has d = 0, whatever its position is
+            if (d != 0.0f) gw[i] = fma((double)d, (double)a.positions[(row0 + r) * a.position_row + x], gw[i]);
+          }
+        }
+      }
+    }
+  }
+  if (p.gw)
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int e = threadIdx.x + i * NT;
+      if (e < a.pairs * a.axes) p.part[(long)blockIdx.x * a.pairs * a.axes + e] = gw[i];
+    }
+}
+
+// grad_waves: the sum of the work-groups' parts, one wave for each value.
+__global__ void __launch_bounds__(64) rotary_join(const double* part, int blocks, int n, float* gw) {
+  double v = 0.0;
+  for (int b = threadIdx.x; b < blocks; b += 64) v += part[(long)b * n + blockIdx.x];
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if (threadIdx.x == 0) gw[blockIdx.x] = (float)v;
+}
+
+// --------------------------------------------------------------- launches ---
+
+// Rows of a tile: about four tiles to a compute unit, as far as LDS has room.
+void tiles_of(const e3conv_rotary_args& a, RotaryParams& p) {
+  const int width = a.heads * a.dim;
+  p.tile_heads = std::min<int>(a.heads, std::max(1, kTile / a.dim));
+  int64_t rows = (a.num_rows + 1023) / 1024;
+  rows = std::min<int64_t>(rows, std::min(kTile / width, a.pairs > 0 ? kTable / a.pairs : 1));
+  p.tile_rows = (int)std::max<int64_t>(rows, 1);
+  p.tiles = (int)((a.num_rows + p.tile_rows - 1) / p.tile_rows);
+  p.blocks = std::min(p.tiles, 1024);
+}
+
+template <class T, int V, bool ADJACENT>
+hipError_t run(const RotaryParams& p, hipStream_t s) {
+  if (!p.gp && !p.gw) {
+    hipLaunchKernelGGL((rotary<T, V, ADJACENT>), grid_of(p.tiles), dim3(NT), 0, s, p);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((rotary_grad<T, V, ADJACENT>), dim3(p.blocks), dim3(NT), 0, s, p);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || !p.gw) return err;
+  const int n = p.a.pairs * p.a.axes;
+  hipLaunchKernelGGL(rotary_join, dim3(n), dim3(64), 0, s, p.part, p.blocks, n, p.gw);
+  return hipGetLastError();
+}
+
+// vec: rows and heads of all tensors are 16-byte aligned.
+hipError_t launch(RotaryParams p, bool vec, hipStream_t s) {
+  const e3conv_rotary_args& a = p.a;
+  const bool f32 = a.dtype == E3CONV_F32, adjacent = a.layout == E3CONV_ROTARY_ADJACENT;
+  const int v = f32 ? 4 : 8;
+  // whole runs, and in halves no run that holds both pairs and elements beyond them
+  vec = vec && a.dim % v == 0 && (adjacent || a.pairs % v == 0);
+  const int n = vec ? v : 1;
+  if (adjacent && vec) {
+    p.units = a.dim / n;
+    p.turning = p.units;
+  } else {
+    p.turning = a.pairs / n;
+    p.units = p.turning + (a.dim - 2 * a.pairs) / n;
+  }
+  tiles_of(a, p);
+  p.by_units = div_by(p.units);
+  p.by_heads = div_by(a.heads);
+  p.by_pairs = div_by(a.pairs);
+  p.by_axes = div_by(a.axes);
+  if (f32) {
+    if (!vec) return adjacent ? run<float, 1, true>(p, s) : run<float, 1, false>(p, s);
+    return adjacent ? run<float, 4, true>(p, s) : run<float, 4, false>(p, s);
+  }
+  if (!vec) return adjacent ? run<__bf16, 1, true>(p, s) : run<__bf16, 1, false>(p, s);
+  return adjacent ? run<__bf16, 8, true>(p, s) : run<__bf16, 8, false>(p, s);
+}
+
+size_t workspace_bytes(const e3conv_rotary_args& a) {
+  RotaryParams p{};
+  tiles_of(a, p);
+  return ((size_t)p.blocks * a.pairs * a.axes * sizeof(double) + 15) / 16 * 16;
+}
+
+bool aligned(const void* p, int64_t row, int64_t head, int dtype) {
+  const int v = dtype == E3CONV_F32 ? 4 : 8;
+  return rows::aligned(p, row, v) && head % v == 0;
+}
+
+e3conv_status bad(const char* what) { return api_fail(E3CONV_ERR_INVALID_ARGUMENT, what); }
+
+e3conv_status check_sizes(const e3conv_rotary_args* a) {
+  if (!a) return bad("args is NULL");
+  if (a->dtype != E3CONV_F32 && a->dtype != E3CONV_BF16) return bad("bad dtype");
+  if (a->layout != E3CONV_ROTARY_ADJACENT && a->layout != E3CONV_ROTARY_HALVES) return bad("unknown layout");
+  if (a->num_rows < 0) return bad("negative size");
+  if (a->dim < 1 || a->dim > kMaxDim) return bad("dim must be in [1, 256]");
+  if (a->heads < 1 || a->heads > 65536) return bad("heads must be in [1, 65536]");
+  if (a->pairs < 1 || a->pairs > a->dim / 2) return bad("pairs must be in [1, dim / 2]");
+  if (a->axes < 1 || a->axes > kMaxAxes) return bad("axes must be in [1, 4]");
+  if (a->num_rows >= ((int64_t)1 << 31) - ((int64_t)1 << 20)) return bad("sizes must fit int32 indices");
+  return E3CONV_OK;
+}
+
+e3conv_status check_args(const e3conv_rotary_args* a) {
+  const e3conv_status st = check_sizes(a);
+  if (st != E3CONV_OK) return st;
+  if (a->x_row < 0 || a->x_head < 0 || a->position_row < 0) return bad("negative stride");
+  if (!a->waves) return bad("NULL device pointer");
+  if (a->num_rows > 0 && (!a->x || !a->positions)) return bad("NULL device pointer");
+  return E3CONV_OK;
+}
+
+}  // namespace
+}  // namespace e3c
+
+extern "C" {
+
+e3conv_status e3conv_rotary(const e3conv_rotary_args* a, void* out, int64_t out_row, int64_t out_head, void* stream) {
+  const e3conv_status st = e3c::check_args(a);
+  if (st != E3CONV_OK) return st;
+  if (out_row < 0 || out_head < 0) return e3c::bad("negative stride");
+  if (a->num_rows == 0) return e3c::api_ok();
+  if (!out) return e3c::bad("NULL device pointer");
+  e3c::RotaryParams p{};
+  p.a = *a;
+  p.sign = 1.0f;
+  p.out = out;
+  p.out_row = out_row;
+  p.out_head = out_head;
+  const bool vec = e3c::aligned(a->x, a->x_row, a->x_head, a->dtype) && e3c::aligned(out, out_row, out_head, a->dtype);
+  const hipError_t err = e3c::launch(p, vec, static_cast<hipStream_t>(stream));
+  if (err != hipSuccess) return e3c::api_hip_fail(err, "rotary launch");
+  return e3c::api_ok();
+}
+
+e3conv_status e3conv_rotary_workspace_size(const e3conv_rotary_args* a, size_t* bytes) {
+  const e3conv_status st = e3c::check_sizes(a);
+  if (st != E3CONV_OK) return st;
+  if (!bytes) return e3c::bad("bytes is NULL");
+  *bytes = e3c::workspace_bytes(*a);
+  return e3c::api_ok();
+}
+
+e3conv_status e3conv_rotary_backward(const e3conv_rotary_args* a, const void* grad_out, int64_t grad_out_row,
+                                     int64_t grad_out_head, void* grad_x, int64_t grad_x_row, int64_t grad_x_head,
+                                     float* grad_positions, float* grad_waves, void* workspace, size_t bytes,
+                                     void* stream) {
+  const bool angles = grad_positions || grad_waves;
+  e3conv_rotary_args args = a ? *a : e3conv_rotary_args{};
+  if (a && !angles && !args.x) args.x = grad_out;      // the features enter the angles' gradients alone
+  const e3conv_status st = e3c::check_args(a ? &args : nullptr);
+  if (st != E3CONV_OK) return st;
+  if (grad_out_row < 0 || grad_out_head < 0 || grad_x_row < 0 || grad_x_head < 0) return e3c::bad("negative stride");
+  if (a->num_rows == 0) {
+    if (!grad_waves) return e3c::api_ok();
+    const hipError_t e = e3c::launch_fill_zero(grad_waves, (size_t)a->pairs * a->axes, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? e3c::api_ok() : e3c::api_hip_fail(e, "fill launch");
+  }
+  if (!grad_out || !grad_x) return e3c::bad("NULL device pointer");
+  const size_t need = grad_waves ? e3c::workspace_bytes(*a) : 0;
+  if (bytes < need || (need > 0 && !workspace))
+    return e3c::api_fail(E3CONV_ERR_WORKSPACE, "rotary backward needs " + std::to_string(need) + " bytes");
+  e3c::RotaryParams p{};
+  p.a = args;
+  p.sign = -1.0f;
+  p.out = grad_x;
+  p.out_row = grad_x_row;
+  p.out_head = grad_x_head;
+  bool vec = e3c::aligned(grad_out, grad_out_row, grad_out_head, a->dtype) &&
+             e3c::aligned(grad_x, grad_x_row, grad_x_head, a->dtype);
+  if (angles) {
+    vec = vec && e3c::aligned(a->x, a->x_row, a->x_head, a->dtype);
+    p.g = grad_out;
+    p.g_row = grad_out_row;
+    p.g_head = grad_out_head;
+    p.gp = grad_positions;
+    p.gw = grad_waves;
+    p.part = static_cast<double*>(workspace);
+  } else {                                             // the forward kernel turns grad_out back
+    p.a.x = grad_out;
+    p.a.x_row = grad_out_row;
+    p.a.x_head = grad_out_head;
+  }
+  const hipError_t err = e3c::launch(p, vec, static_cast<hipStream_t>(stream));
+  if (err != hipSuccess) return e3c::api_hip_fail(err, "rotary backward launch");
+  return e3c::api_ok();
+}
+
+}  // extern "C"

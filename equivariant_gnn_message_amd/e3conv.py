@@ -6,8 +6,8 @@ tensor's device pointer, and the current HIP stream of torch unless a stream
 is given).  All arithmetic runs in the library's HIP kernels; there is no
 fallback: if the library is missing every call raises.
 
-``Plan``, ``E3ConvFunction``, ``AttentionFunction``, ``GroupNormFunction`` and ``RMSNormFunction`` are
-conveniences over the same calls.
+``Plan``, ``E3ConvFunction``, ``AttentionFunction``, ``GroupNormFunction``, ``RMSNormFunction`` and
+``RotaryFunction`` are conveniences over the same calls.
 """
 
 import ctypes
@@ -29,6 +29,8 @@ E3CONV_ACCUMULATE_GRAD_S = 4
 E3CONV_ACT_NONE, E3CONV_ACT_RELU, E3CONV_ACT_SILU, E3CONV_ACT_GELU = 0, 1, 2, 3
 ACTIVATIONS = {"none": E3CONV_ACT_NONE, "relu": E3CONV_ACT_RELU, "silu": E3CONV_ACT_SILU,
                "gelu": E3CONV_ACT_GELU}
+E3CONV_ROTARY_ADJACENT, E3CONV_ROTARY_HALVES = 0, 1
+ROTARY_LAYOUTS = {"adjacent": E3CONV_ROTARY_ADJACENT, "halves": E3CONV_ROTARY_HALVES}
 
 STATUS_NAMES = {
     0: "E3CONV_OK", 1: "E3CONV_ERR_INVALID_ARGUMENT", 2: "E3CONV_ERR_PARSE",
@@ -51,6 +53,7 @@ EXPORTED = [
     "e3conv_plan_num_variants",
     "e3conv_attention_workspace_size", "e3conv_attention", "e3conv_attention_backward",
     "e3conv_group_norm_workspace_size", "e3conv_group_norm", "e3conv_group_norm_backward",
+    "e3conv_rotary_workspace_size", "e3conv_rotary", "e3conv_rotary_backward",
     "e3conv_rms_norm_workspace_size", "e3conv_rms_norm", "e3conv_rms_norm_backward",
     "e3conv_status_string", "e3conv_last_error_detail",
 ]
@@ -86,6 +89,13 @@ class GroupNormArgs(ctypes.Structure):
                 ("groups", ctypes.c_int32), ("activation", ctypes.c_int), ("eps", ctypes.c_float),
                 ("num_rows", I64), ("row_ptr", P), ("row_mask", P), ("x", P), ("x_row", I64),
                 ("weight", P), ("bias", P)]
+
+
+class RotaryArgs(ctypes.Structure):
+    """e3conv_rotary_args."""
+    _fields_ = [("dtype", ctypes.c_int), ("layout", ctypes.c_int), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("pairs", ctypes.c_int32), ("axes", ctypes.c_int32), ("num_rows", I64), ("x", P), ("x_row", I64),
+                ("x_head", I64), ("positions", P), ("position_row", I64), ("waves", P), ("row_mask", P)]
 
 
 class RMSNormArgs(ctypes.Structure):
@@ -160,6 +170,9 @@ def load_library(path=LIB_PATH):
         "e3conv_group_norm_workspace_size": ([P, ctypes.c_int, P], ctypes.c_int),
         "e3conv_group_norm": ([P, P, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "e3conv_group_norm_backward": ([P, P, P, P, I64, P, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "e3conv_rotary_workspace_size": ([P, P], ctypes.c_int),
+        "e3conv_rotary": ([P, P, I64, I64, P], ctypes.c_int),
+        "e3conv_rotary_backward": ([P, P, I64, I64, P, I64, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "e3conv_rms_norm_workspace_size": ([P, P], ctypes.c_int),
         "e3conv_rms_norm": ([P, P, I64, P, I64, P, P], ctypes.c_int),
         "e3conv_rms_norm_backward": ([P, P, P, I64, P, I64, P, I64, P, P, ctypes.c_size_t, P], ctypes.c_int),
@@ -862,6 +875,88 @@ def e3conv_group_norm_backward(x, row_ptr, groups, weight, bias, activation, mea
     return grad_x, gw, gb
 
 
+# ----------------------------------------------- rotary positions ---
+
+def _rotary_args(x, positions, waves, layout, row_mask):
+    if x.dim() != 3 or positions.dim() != 2 or waves.dim() != 2:
+        raise ValueError("x (num_rows, heads, dim), positions (num_rows, axes), waves (pairs, axes)")
+    code, index, f32 = _dtype_code(x), x.get_device(), _torch.float32
+    n, heads, dim = x.shape
+    pairs, axes = waves.shape
+    row, head, _ = _rows_of(x, "x", x.dtype, index, x.shape)
+    position_row, _ = _rows_of(positions, "positions", f32, index, (n, axes))
+    which = ROTARY_LAYOUTS.get(layout, layout)
+    if not isinstance(which, int):
+        raise ValueError(f"layout must be one of {sorted(ROTARY_LAYOUTS)}, got {layout!r}")
+    return RotaryArgs(code, which, heads, dim, pairs, axes, n, x.data_ptr(), row, head, positions.data_ptr(),
+                      position_row, _dense(waves, "waves", f32, index, pairs * axes),
+                      _node_mask(row_mask, "row_mask", index, n))
+
+
+def e3conv_rotary_workspace_size(args):
+    """Bytes of workspace of the reverse pass for the sizes in a RotaryArgs."""
+    n = ctypes.c_size_t()
+    _check(load_library().e3conv_rotary_workspace_size(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def e3conv_rotary(x, positions, waves, layout="adjacent", row_mask=None, out=None, stream=None):
+    """x with every head's pairs of elements turned by the angles positions @ waves.T.
+
+    x (num_rows, heads, dim) fp32 or bf16, any strides but unit along the last axis (the queries and keys of one
+    projection together); positions fp32 (num_rows, axes), waves fp32 (pairs, axes) with pairs <= dim // 2 and at
+    most four axes; layout "adjacent" (elements 2 p, 2 p + 1) or "halves" (p, pairs + p); elements beyond 2 pairs
+    are copied; row_mask bool or uint8, 0 for padding (zeros).  out may be x.
+    """
+    lib = _lib or load_library()
+    args = _rotary_args(x, positions, waves, layout, row_mask)
+    index = x.get_device()
+    handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, _as_list, e3conv_rotary, x, positions, waves, layout, row_mask, out)[0]
+    if out is None:
+        out = x.new_empty(x.shape)
+        row, head = args.heads * args.dim, args.dim
+    else:
+        row, head, _ = _rows_of(out, "out", x.dtype, index, x.shape)
+        _written(out, "out")
+    _check(lib.e3conv_rotary(ctypes.byref(args), out.data_ptr(), row, head, handle))
+    return out
+
+
+def _as_list(call, *args):
+    return [call(*args)]
+
+
+def e3conv_rotary_backward(x, positions, waves, grad_out, layout="adjacent", row_mask=None, want_positions=True,
+                           want_waves=True, grad_x=None, workspace=None, stream=None):
+    """(grad_x, grad_positions, grad_waves); None where not wanted.  grad_x may be grad_out."""
+    lib = _lib or load_library()
+    args = _rotary_args(x, positions, waves, layout, row_mask)
+    index, dt = x.get_device(), x.dtype
+    g_row, g_head, _ = _rows_of(grad_out, "grad_out", dt, index, x.shape)
+    handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, e3conv_rotary_backward, x, positions, waves, grad_out, layout, row_mask, want_positions,
+                   want_waves, grad_x, workspace)
+    if grad_x is None:
+        grad_x = x.new_empty(x.shape)
+        row, head = args.heads * args.dim, args.dim
+    else:
+        row, head, _ = _rows_of(grad_x, "grad_x", dt, index, x.shape)
+        _written(grad_x, "grad_x")
+    gp = positions.new_empty(positions.shape) if want_positions else None
+    ref = ctypes.byref(args)
+    gw, ws, nbytes = None, None, 0
+    if want_waves:
+        gw = _torch.empty_like(waves)
+        ws, nbytes, _keep = _workspace(workspace, lib.e3conv_rotary_workspace_size, ref, x)
+    _check(lib.e3conv_rotary_backward(ref, grad_out.data_ptr(), g_row, g_head, grad_x.data_ptr(), row, head,
+                                      None if gp is None else gp.data_ptr(), None if gw is None else gw.data_ptr(), ws,
+                                      nbytes, handle))
+    return grad_x, gp, gw
+
+
 # ------------------------------------------- root-mean-square norm ---
 
 def _rms_norm_args(x, weight, groups, eps, residual, row_mask):
@@ -1286,8 +1381,37 @@ def _rms_norm_function():
     return RMSNormFunction
 
 
+def _rotary_function():
+    import torch
+
+    class RotaryFunction(torch.autograd.Function):
+        """e3conv_rotary, differentiable in x, positions and waves.
+
+        apply(x, positions, waves, layout="adjacent", row_mask=None).
+        """
+
+        @staticmethod
+        def forward(ctx, x, positions, waves, layout="adjacent", row_mask=None):
+            # x enters the gradients of the angles alone
+            ctx.save_for_backward(x if any(ctx.needs_input_grad[1:3]) else None, positions, waves, row_mask)
+            ctx.layout = layout
+            return e3conv_rotary(x, positions, waves, layout, row_mask)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_out):
+            x, positions, waves, row_mask = ctx.saved_tensors
+            if grad_out.stride(-1) != 1:
+                grad_out = grad_out.contiguous()
+            return e3conv_rotary_backward(grad_out if x is None else x, positions, waves, grad_out, ctx.layout, row_mask,
+                                          ctx.needs_input_grad[1], ctx.needs_input_grad[2]) + (None, None)
+
+    return RotaryFunction
+
+
 _FUNCTIONS = {"E3ConvFunction": _autograd_function, "AttentionFunction": _attention_function,
-              "GroupNormFunction": _group_norm_function, "RMSNormFunction": _rms_norm_function}
+              "GroupNormFunction": _group_norm_function, "RMSNormFunction": _rms_norm_function,
+              "RotaryFunction": _rotary_function}
 
 
 def __getattr__(name):

@@ -586,6 +586,55 @@ e3conv_status e3conv_group_norm_backward(const e3conv_group_norm_args* args, con
                                          float* grad_bias, void* workspace, size_t workspace_bytes,
                                          void* hip_stream);
 
+/* Rotary positions over several axes (the coordinates of nodes; time, height and width of patches): pair p
+ * of elements of every head of row i is turned by
+ *     angle[i, p] = sum_a positions[i, a] waves[p, a],
+ *     (u, v) -> (u cos - v sin, u sin + v cos),
+ * so that products of two turned rows depend on the difference of their positions alone.  Rows of waves with
+ * one nonzero entry give each axis pairs of its own; any others (learned ones too) are wave vectors.
+ * - x, out (num_rows, heads, dim) in dtype (fp32 or bf16), unit stride along dim, row and head strides in
+ *   elements; queries and keys that lie side by side in one projection take one call.  Elements beyond 2 pairs
+ *   are copied.  ADJACENT: pair p is elements 2 p and 2 p + 1; HALVES: p and pairs + p.
+ * - positions fp32 (num_rows, axes) with row stride position_row, unit stride along the axes;
+ *   waves fp32 (pairs, axes), dense.  Angles are formed in 64 bits, so far positions keep their digits.
+ * - row_mask: device bytes (num_rows) or NULL; a row whose byte is 0 gets out = 0 and zero gradients,
+ *   whatever x, its position and its gradient hold.
+ * dim in [1, 256], 1 <= pairs <= dim / 2, axes in [1, 4], heads <= 65536, num_rows < 2^31 - 2^20. */
+typedef enum { E3CONV_ROTARY_ADJACENT = 0, E3CONV_ROTARY_HALVES = 1 } e3conv_rotary_layout;
+
+typedef struct {
+  e3conv_dtype dtype;
+  e3conv_rotary_layout layout;
+  int32_t heads, dim, pairs, axes;
+  int64_t num_rows;
+  const void* x;
+  int64_t x_row, x_head;
+  const float* positions;
+  int64_t position_row;
+  const float* waves;
+  const uint8_t* row_mask;
+} e3conv_rotary_args;
+
+/* out is fully written; it may be x itself, with the same strides. */
+e3conv_status e3conv_rotary(const e3conv_rotary_args* args, void* out, int64_t out_row,
+                            int64_t out_head, void* hip_stream);
+
+/* Bytes of device workspace (16-byte aligned) of the reverse pass where it computes grad_waves; none
+ * otherwise. */
+e3conv_status e3conv_rotary_workspace_size(const e3conv_rotary_args* args, size_t* bytes);
+
+/* Reverse pass: grad_x is grad_out turned back, (gu, gv) for the pair (u, v) of x; with
+ * d_angle[i, p] = sum over the heads of u gv - v gu,
+ *     grad_positions[i, a] = sum_p d_angle waves[p, a],   grad_waves[p, a] = sum_i d_angle positions[i, a].
+ * grad_positions fp32 (num_rows, axes) and grad_waves fp32 (pairs, axes), dense, or NULL (not
+ * computed; with neither, x is not read and may be NULL).  grad_x may be grad_out itself, with the same
+ * strides.  All outputs are fully written, without atomics: the same inputs give the same bits. */
+e3conv_status e3conv_rotary_backward(const e3conv_rotary_args* args, const void* grad_out,
+                                     int64_t grad_out_row, int64_t grad_out_head, void* grad_x,
+                                     int64_t grad_x_row, int64_t grad_x_head, float* grad_positions,
+                                     float* grad_waves, void* workspace, size_t workspace_bytes,
+                                     void* hip_stream);
+
 /* Root-mean-square norm of rows, with a residual's addition: the channels split into
  * `groups` runs of size = channels / groups, and with s = x + residual,
  *     rstd = 1 / sqrt(sum over the group s^2 / size + eps),
