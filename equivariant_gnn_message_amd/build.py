@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libe3conv.so")
 
 SOURCES = ["host_core.cpp", "e3conv.cpp", "kernels.hip", "validate.hip", "layout_tiny.hip",
            "layout_gate.hip", "layout_mace.hip", "layout_big.hip", "linear.hip",
-           "attention.hip", "attention_fwd.hip", "attention_bwd.hip", "group_norm.hip", "rms_norm.hip",
+           "attention.hip", "attention_fwd.hip", "attention_bwd.hip", "attention_diff_fwd.hip",
+           "attention_diff_bwd.hip", "group_norm.hip", "rms_norm.hip",
            "rotary.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
@@ -32,7 +33,8 @@ DEVICE = ["--offload-arch=gfx950", "-munsafe-fp-atomics",
 # Matrix instructions with their accumulators in the general registers: the vector ALU works on
 # every accumulator between two products, and the copies to and from the accumulator registers
 # were a third of the instructions.
-FILE_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for f in ("attention_fwd.hip", "attention_bwd.hip")}
+FILE_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for f in ("attention_fwd.hip", "attention_bwd.hip", "attention_diff_fwd.hip",
+                                                                "attention_diff_bwd.hip")}
 
 
 def hipcc():

@@ -19,6 +19,7 @@
 // 0.33 ms) the latency of LDS and barriers at one wave a SIMD for grad_k and grad_v, whose
 // operands and sums fill 371 registers; with few rows (4 queries against 12 500 keys, 89 us)
 // the bytes of k, v and their gradients.
+#include "attention_sum.h"
 #include "attention_tile.h"
 #include "kernels.h"
 
@@ -282,77 +283,15 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? waves_kv(sizeof(T) == 4, D)
                                            second.rows);
 }
 
-// Sums the splits of all three gradients.  `each` elements to a work-group: 256, a thread each,
-// or 64, and four waves share each one's splits, eight at a time.
-struct Sum {
-  const float* part;
-  long rows;            // (i, head)
-  int width, from, dim; // elements from .. from + dim - 1 of `width`
-  int heads, splits, each;
-  long blocks;
-  float factor;
-  void* out;
-  long out_row, out_head;
-};
-struct Sums {
-  Sum of[3];
-};
-template <class T>
-__global__ void __launch_bounds__(256) attn_sum(Sums all) {
-  __shared__ float red[4][64];
-  long b = block_index();
-  int which = 0;
-  while (which < 2 && b >= all.of[which].blocks) b -= all.of[which++].blocks;
-  const Sum& m = all.of[which];
-  if (b >= m.blocks) return;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const bool wide = m.each == 256;
-  const long i = b * m.each + (wide ? (int)threadIdx.x : lane), at = i / m.dim;
-  const int d = (int)(i - at * m.dim);
-  const float* q = m.part + at * m.width + m.from + d;
-  const long step = m.rows * m.width;
-  float v = 0.0f;
-  if (at < m.rows) {
-    if (wide) {
-#pragma unroll 4
-      for (int s = 0; s < m.splits; ++s) v += q[s * step];
-    } else {
-      int s = w;
-      for (; s + 28 < m.splits; s += 32) {
-        float x[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = q[(s + 4 * k) * step];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v += x[k];
-      }
-      for (; s < m.splits; s += 4) v += q[s * step];
-    }
-  }
-  if (!wide) {
-    red[w][lane] = v;
-    __syncthreads();
-    if (w > 0) return;
-    v = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
-  }
-  if (at < m.rows)
-    ((T*)m.out)[at / m.heads * m.out_row + at % m.heads * m.out_head + d] = (T)(v * m.factor);
-}
-
-// The sums that p's splits ask for; none (blocks 0) where there is one split.
-Sum sum_of(const float* part, long rows, int width, int from, int dim, int heads, int splits, float factor, void* out,
-           long row, long head) {
-  Sum m{part, rows, width, from, dim, heads, splits, splits <= 8 ? 256 : 64, 0, factor, out, row, head};
-  if (splits > 1) m.blocks = (rows * dim + m.each - 1) / m.each;
-  return m;
-}
 template <class T>
 hipError_t sums(const Params& p, hipStream_t s) {
   const e3conv_attention_args& a = p.a;
   const long nq = a.num_q * a.heads_q, nk = a.num_k * a.heads_kv;
   const int width = a.dim_qk + a.dim_v;
-  const Sums all{{sum_of(p.part, nq, a.dim_qk, 0, a.dim_qk, a.heads_q, p.splits, a.scale, p.gq, p.gq_row, p.gq_head),
-                  sum_of(p.part_kv, nk, width, 0, a.dim_qk, a.heads_kv, p.splits_kv, a.scale, p.gk, p.gk_row, p.gk_head),
-                  sum_of(p.part_kv, nk, width, a.dim_qk, a.dim_v, a.heads_kv, p.splits_kv, 1.0f, p.gv, p.gv_row,
+  const Sums all{{sum_of(p.part, nq, a.dim_qk, 0, a.dim_qk, 1, a.heads_q, p.splits, a.scale, p.gq, p.gq_row, p.gq_head),
+                  sum_of(p.part_kv, nk, width, 0, a.dim_qk, 1, a.heads_kv, p.splits_kv, a.scale, p.gk, p.gk_row,
+                         p.gk_head),
+                  sum_of(p.part_kv, nk, width, a.dim_qk, a.dim_v, 1, a.heads_kv, p.splits_kv, 1.0f, p.gv, p.gv_row,
                          p.gv_head)}};
   const long blocks = all.of[0].blocks + all.of[1].blocks + all.of[2].blocks;
   if (blocks > 0) hipLaunchKernelGGL(attn_sum<T>, grid_of(blocks), dim3(256), 0, s, all);

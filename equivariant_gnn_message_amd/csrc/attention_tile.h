@@ -309,7 +309,8 @@ constexpr int kElements = 0, kUnits = 1, kFull = 2;
 // units beyond dim load nothing and leave the zeros that clear() has put there (an infinity
 // would be NaN against the other operand's zeros; clearing them after each tile's loads took
 // 10 % with 96 dimensions).  Others pass through registers: fp32 is split on the way.
-template <class T, int D, int ROWS, int NT, int LOAD>
+// MAPS = 2: a row of the first operand is two heads side by side, D / 2 elements of the tile each.
+template <class T, int D, int ROWS, int NT, int LOAD, int MAPS = 1>
 struct Pair {
   static constexpr int P = planes<T>(), U = D / 8, E = ROWS * U / NT, STEP = NT / U;
   static constexpr bool VEC = LOAD != kElements, DMA = sizeof(T) == 2 && VEC, SPARE = LOAD != kFull;
@@ -322,12 +323,14 @@ struct Pair {
     const int slot = threadIdx.x % U;
     return DMA ? slot ^ TileT::swizzle(row(e)) : slot;
   }
+  // Where this thread's unit of row e starts in its head of the first operand.
+  static __device__ __forceinline__ int along_x(int e) { return MAPS == 1 ? unit(e) * 8 : unit(e) % (U / 2) * 8; }
   // Zeros in this thread's units beyond dim.
   static __device__ __forceinline__ void clear(int dim_x, int dim_y, TileT& xt, TileT& yt) {
     if constexpr (DMA && SPARE)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (unit(e) * 8 >= dim_x) xt.u[0][e * NT + threadIdx.x] = bf16x8{};
+        if (along_x(e) >= dim_x) xt.u[0][e * NT + threadIdx.x] = bf16x8{};
         if (unit(e) * 8 >= dim_y) yt.u[0][e * NT + threadIdx.x] = bf16x8{};
       }
   }
@@ -335,6 +338,12 @@ struct Pair {
   static __device__ __forceinline__ int first(int e, int dim) {
     const int d = unit(e) * 8;
     return DMA && SPARE && d >= dim ? 0 : d;
+  }
+  // The same of the first operand, whose heads lie `head` apart.
+  static __device__ __forceinline__ auto first_x(int e, int dim, long head) {
+    const int d = along_x(e), from = DMA && SPARE && d >= dim ? 0 : d;
+    if constexpr (MAPS == 1) return from;
+    else return unit(e) / (U / 2) * head + from;
   }
   // Whether all rows of a thread have the same unit (their numbers differ by multiples of 16).
   static constexpr bool SAME = !DMA || STEP % 16 == 0;
@@ -344,11 +353,11 @@ struct Pair {
       typedef const __attribute__((address_space(1))) void* from;
       typedef __attribute__((address_space(3))) void* to;
       const int at = e * NT + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63);   // the wave's first unit
-      if (!SPARE || unit(e) * 8 < dim_x) __builtin_amdgcn_global_load_lds((from)xp, (to)&xt.u[0][at], 16, 0, 0);
+      if (!SPARE || along_x(e) < dim_x) __builtin_amdgcn_global_load_lds((from)xp, (to)&xt.u[0][at], 16, 0, 0);
       if (!SPARE || unit(e) * 8 < dim_y) __builtin_amdgcn_global_load_lds((from)yp, (to)&yt.u[0][at], 16, 0, 0);
     } else {
-      const int d = unit(e) * 8;
-      x[e] = fetch8<VEC>(xp - d, d, dim_x);
+      const int dx = along_x(e), d = unit(e) * 8;
+      x[e] = fetch8<VEC>(xp - dx, dx, dim_x);
       y[e] = fetch8<VEC>(yp - d, d, dim_y);
     }
   }
@@ -365,7 +374,7 @@ struct Pair {
             yt.u[0][e * NT + threadIdx.x] = bf16x8{};
           }
       }
-    } else if (whole && (!VEC || (dim_x == D && dim_y == D))) {
+    } else if (whole && (!VEC || (dim_x * MAPS == D && dim_y == D))) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         xt.store(row(e), unit(e), frag_of(x[e], true));
@@ -375,7 +384,7 @@ struct Pair {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const bool keep = seen >> row(e) & 1;
-        xt.store(row(e), unit(e), frag_of(x[e], keep && unit(e) * 8 < dim_x));
+        xt.store(row(e), unit(e), frag_of(x[e], keep && along_x(e) < dim_x));
         yt.store(row(e), unit(e), frag_of(y[e], keep && unit(e) * 8 < dim_y));
       }
     }
@@ -386,9 +395,9 @@ struct Pair {
 
 // The tiles of the keys of one kv head, and the starting value of each key's logits: 0, or
 // -infinity for a key that is not seen.  Rows beyond the last key read the last one.
-template <class T, int D, int ROWS, int NT, int LOAD>
+template <class T, int D, int ROWS, int NT, int LOAD, int MAPS = 1>
 struct Keys {
-  typedef Pair<T, D, ROWS, NT, LOAD> PairT;
+  typedef Pair<T, D, ROWS, NT, LOAD, MAPS> PairT;
   typedef typename PairT::TileT TileT;
   PairT pair;
   unsigned char m;
@@ -398,7 +407,7 @@ struct Keys {
   __device__ __forceinline__ void begin(const Params& p, int c, int k0, int k1) {
     const e3conv_attention_args& a = p.a;
     const long j = k0 + PairT::row(0);
-    kp = (const T*)a.k + c * a.k_head + j * a.k_row + PairT::first(0, a.dim_qk);
+    kp = (const T*)a.k + MAPS * c * a.k_head + j * a.k_row + PairT::first_x(0, a.dim_qk, a.k_head);
     vp = (const T*)a.v + c * a.v_head + j * a.v_row + PairT::first(0, a.dim_v);
     next = k0;
     end = k1;
@@ -406,18 +415,22 @@ struct Keys {
   static __device__ __forceinline__ int shift(int e, int dim) {
     return PairT::SAME ? 0 : PairT::first(e, dim) - PairT::first(0, dim);
   }
+  static __device__ __forceinline__ auto shift_x(int e, const e3conv_attention_args& a) {
+    const auto by = PairT::first_x(e, a.dim_qk, a.k_head) - PairT::first_x(0, a.dim_qk, a.k_head);
+    return PairT::SAME ? 0 : by;
+  }
   __device__ __forceinline__ void issue(const Params& p, TileT& kt, TileT& vt) {
     const e3conv_attention_args& a = p.a;
     if (next + ROWS <= end) {
 #pragma unroll
       for (int e = 0; e < PairT::E; ++e)
-        pair.issue(e, kp + (e * PairT::STEP * a.k_row + shift(e, a.dim_qk)),
+        pair.issue(e, kp + (e * PairT::STEP * a.k_row + shift_x(e, a)),
                    vp + (e * PairT::STEP * a.v_row + shift(e, a.dim_v)), a.dim_qk, a.dim_v, kt, vt);
     } else {
 #pragma unroll
       for (int e = 0; e < PairT::E; ++e) {
         const int back = min(end - 1 - (next + PairT::row(0)), e * PairT::STEP);
-        pair.issue(e, kp + (back * a.k_row + shift(e, a.dim_qk)), vp + (back * a.v_row + shift(e, a.dim_v)), a.dim_qk,
+        pair.issue(e, kp + (back * a.k_row + shift_x(e, a)), vp + (back * a.v_row + shift(e, a.dim_v)), a.dim_qk,
                    a.dim_v, kt, vt);
       }
     }

@@ -6,8 +6,8 @@ tensor's device pointer, and the current HIP stream of torch unless a stream
 is given).  All arithmetic runs in the library's HIP kernels; there is no
 fallback: if the library is missing every call raises.
 
-``Plan``, ``E3ConvFunction``, ``AttentionFunction``, ``GroupNormFunction``, ``RMSNormFunction`` and
-``RotaryFunction`` are conveniences over the same calls.
+``Plan``, ``E3ConvFunction``, ``AttentionFunction``, ``DiffAttentionFunction``, ``GroupNormFunction``,
+``RMSNormFunction`` and ``RotaryFunction`` are conveniences over the same calls.
 """
 
 import ctypes
@@ -53,6 +53,7 @@ EXPORTED = [
     "e3conv_plan_num_variants",
     "e3conv_attention_workspace_size", "e3conv_attention", "e3conv_attention_backward",
     "e3conv_group_norm_workspace_size", "e3conv_group_norm", "e3conv_group_norm_backward",
+    "e3conv_diff_attention_workspace_size", "e3conv_diff_attention", "e3conv_diff_attention_backward",
     "e3conv_rotary_workspace_size", "e3conv_rotary", "e3conv_rotary_backward",
     "e3conv_rms_norm_workspace_size", "e3conv_rms_norm", "e3conv_rms_norm_backward",
     "e3conv_status_string", "e3conv_last_error_detail",
@@ -170,6 +171,9 @@ def load_library(path=LIB_PATH):
         "e3conv_group_norm_workspace_size": ([P, ctypes.c_int, P], ctypes.c_int),
         "e3conv_group_norm": ([P, P, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "e3conv_group_norm_backward": ([P, P, P, P, I64, P, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "e3conv_diff_attention_workspace_size": ([P, ctypes.c_int, P], ctypes.c_int),
+        "e3conv_diff_attention": ([P, P, P, I64, I64, P, I64, I64, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "e3conv_diff_attention_backward": ([P] * 12 + [ctypes.c_size_t, P], ctypes.c_int),
         "e3conv_rotary_workspace_size": ([P, P], ctypes.c_int),
         "e3conv_rotary": ([P, P, I64, I64, P], ctypes.c_int),
         "e3conv_rotary_backward": ([P, P, I64, I64, P, I64, I64, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
@@ -794,6 +798,114 @@ def e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale=N
     return gq, gk, gv
 
 
+def _diff_attention_args(q, k, v, lam, q_ptr, k_ptr, scale, q_mask, k_mask):
+    """(AttentionArgs, address of lam)."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or q.shape[1] % 2:
+        raise ValueError("q (num_q, 2 heads_q, dim_qk), k (num_k, 2 heads_kv, dim_qk), v (num_k, heads_kv, dim_v)")
+    dt, index = q.dtype, q.get_device()
+    code, i32 = _dtype_code(q), _torch.int32
+    nq, hq, d = q.shape
+    nk, hk, dv = v.shape
+    hq //= 2
+    q_row, q_head, _ = _rows_of(q, "q", dt, index, (nq, 2 * hq, d))
+    k_row, k_head, _ = _rows_of(k, "k", dt, index, (nk, 2 * hk, d))
+    v_row, v_head, _ = _rows_of(v, "v", dt, index, (nk, hk, dv))
+    graphs = q_ptr.numel() - 1
+    if graphs < 0:
+        raise ValueError("q_ptr must hold num_graphs + 1 offsets")
+    qp = _dense(q_ptr, "q_ptr", i32, index, graphs + 1)
+    kp = qp if k_ptr is q_ptr else _dense(k_ptr, "k_ptr", i32, index, graphs + 1)
+    if scale is None:
+        scale = d ** -0.5 if d else 1.0       # d = 0: the library refuses it
+    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, scale, qp, kp, _node_mask(q_mask, "q_mask", index, nq),
+                         _node_mask(k_mask, "k_mask", index, nk), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row,
+                         q_head, k_row, k_head, v_row, v_head), _dense(lam, "lam", _torch.float32, index, hq)
+
+
+def e3conv_diff_attention_workspace_size(args, backward=False):
+    """Bytes of workspace for the sizes in an AttentionArgs."""
+    n = ctypes.c_size_t()
+    _check(load_library().e3conv_diff_attention_workspace_size(ctypes.byref(args), int(bool(backward)),
+                                                               ctypes.byref(n)))
+    return n.value
+
+
+def e3conv_diff_attention(q, k, v, lam, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None, out=None, second=None,
+                          lse=None, workspace=None, stream=None, keep=True):
+    """(out, second, lse): out = (P1 - lam P2) v, the difference of two softmax maps, per graph.
+
+    q (num_q, 2 heads_q, dim_qk) and k (num_k, 2 heads_kv, dim_qk) hold the heads of the two maps side by side
+    (2 h and 2 h + 1), v (num_k, heads_kv, dim_v), lam fp32 (heads_q); dim_qk up to 64, dim_v up to 128;
+    the rest as in e3conv_attention.  second = P2 v and lse, fp32 (num_q, heads_q, 2), are what the reverse pass
+    needs; with keep=False they are not formed (None unless given).
+    """
+    lib = _lib or load_library()
+    args, lam_at = _diff_attention_args(q, k, v, lam, q_ptr, k_ptr, scale, q_mask, k_mask)
+    index, shape = q.get_device(), (args.num_q, args.heads_q, args.dim_v)
+    handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, e3conv_diff_attention, q, k, v, lam, q_ptr, k_ptr, scale, q_mask, k_mask, out, second, lse,
+                   workspace, None, keep)
+    dense = (shape[1] * shape[2], shape[2])
+    if out is None:
+        out, strides = q.new_empty(shape), dense
+    else:
+        strides = _rows_of(out, "out", q.dtype, index, shape)[:2]
+        _written(out, "out")
+    if second is not None:
+        strides += _rows_of(second, "second", q.dtype, index, shape)[:2]
+        _written(second, "second")
+    else:
+        strides += dense
+        if keep:
+            second = q.new_empty(shape)
+    if lse is not None:
+        _dense(lse, "lse", _torch.float32, index, 2 * shape[0] * shape[1])
+    elif keep:
+        lse = q.new_empty(shape[:2] + (2,), dtype=_torch.float32)
+    ref = ctypes.byref(args)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_diff_attention_workspace_size, ref, q, 0)
+    _check(lib.e3conv_diff_attention(ref, lam_at, out.data_ptr(), *strides[:2],
+                                     None if second is None else second.data_ptr(), *strides[2:],
+                                     None if lse is None else lse.data_ptr(), ws, nbytes, handle))
+    return out, second, lse
+
+
+def e3conv_diff_attention_backward(q, k, v, lam, out, second, lse, grad_out, q_ptr, k_ptr, scale=None, q_mask=None,
+                                   k_mask=None, grads=None, workspace=None, stream=None):
+    """(grad_q, grad_k, grad_v, grad_lam) of <grad_out, out>, with out, second and lse from e3conv_diff_attention.
+
+    grads: three output tensors for q, k and v (strides free but unit along the last axis), or None.
+    """
+    lib = _lib or load_library()
+    args, lam_at = _diff_attention_args(q, k, v, lam, q_ptr, k_ptr, scale, q_mask, k_mask)
+    index, dt, shape = q.get_device(), q.dtype, (args.num_q, args.heads_q, args.dim_v)
+    strides = ()
+    for t, name in ((out, "out"), (second, "second"), (grad_out, "grad_out")):
+        strides += _rows_of(t, name, dt, index, shape)[:2]
+    lse_at = _dense(lse, "lse", _torch.float32, index, 2 * shape[0] * shape[1])
+    handle, other = _enter(index, stream)
+    if other is not None:
+        return _on(other, e3conv_diff_attention_backward, q, k, v, lam, out, second, lse, grad_out, q_ptr, k_ptr, scale,
+                   q_mask, k_mask, grads, workspace)
+    if grads is None:
+        grads = [_torch.empty_like(t) for t in (q, k, v)]
+        for t in grads:
+            strides += t.stride()[:2]
+    else:
+        for t, ref, name in zip(grads, (q, k, v), ("grad_q", "grad_k", "grad_v")):
+            strides += _rows_of(t, name, dt, index, ref.shape)[:2]
+            _written(t, name)
+    gq, gk, gv = grads
+    glam = _torch.empty_like(lam)
+    ref = ctypes.byref(args)
+    ws, nbytes, _keep = _workspace(workspace, lib.e3conv_diff_attention_workspace_size, ref, q, 1)
+    _check(lib.e3conv_diff_attention_backward(
+        ref, lam_at, out.data_ptr(), second.data_ptr(), lse_at, grad_out.data_ptr(), gq.data_ptr(), gk.data_ptr(),
+        gv.data_ptr(), glam.data_ptr(), (I64 * 12)(*strides), ws, nbytes, handle))
+    return gq, gk, gv, glam
+
+
 def _group_norm_args(x, row_ptr, groups, weight, bias, eps, activation, row_mask):
     if x.dim() != 2:
         raise ValueError("x must be (num_rows, channels)")
@@ -1318,6 +1430,34 @@ def _attention_function():
     return AttentionFunction
 
 
+def _diff_attention_function():
+    import torch
+
+    class DiffAttentionFunction(torch.autograd.Function):
+        """out of e3conv_diff_attention, differentiable in q, k, v and lam.
+
+        apply(q, k, v, lam, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None).
+        """
+
+        @staticmethod
+        def forward(ctx, q, k, v, lam, q_ptr, k_ptr, scale=None, q_mask=None, k_mask=None):
+            out, second, lse = e3conv_diff_attention(q, k, v, lam, q_ptr, k_ptr, scale, q_mask, k_mask)
+            ctx.save_for_backward(q, k, v, lam, out, second, lse, q_ptr, k_ptr, q_mask, k_mask)
+            ctx.scale = scale
+            return out
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_out):
+            if grad_out.stride(-1) != 1:
+                grad_out = grad_out.contiguous()
+            q, k, v, lam, out, second, lse, q_ptr, k_ptr, q_mask, k_mask = ctx.saved_tensors
+            return e3conv_diff_attention_backward(q, k, v, lam, out, second, lse, grad_out, q_ptr, k_ptr, ctx.scale,
+                                                  q_mask, k_mask) + (None,) * 5
+
+    return DiffAttentionFunction
+
+
 def _group_norm_function():
     import torch
 
@@ -1411,7 +1551,7 @@ def _rotary_function():
 
 _FUNCTIONS = {"E3ConvFunction": _autograd_function, "AttentionFunction": _attention_function,
               "GroupNormFunction": _group_norm_function, "RMSNormFunction": _rms_norm_function,
-              "RotaryFunction": _rotary_function}
+              "RotaryFunction": _rotary_function, "DiffAttentionFunction": _diff_attention_function}
 
 
 def __getattr__(name):

@@ -521,6 +521,45 @@ e3conv_status e3conv_attention_backward(const e3conv_attention_args* args, const
                                         void* grad_k, void* grad_v, const int64_t strides[10],
                                         void* workspace, size_t workspace_bytes, void* hip_stream);
 
+/* Differential attention among the nodes of each graph: the difference of two softmax maps with a learned
+ * weight for each head.  The arguments are those of e3conv_attention, except that q has 2 heads_q and k
+ * 2 heads_kv heads of dim_qk: heads 2 h and 2 h + 1 are the first and second map's of head h (and of kv head
+ * c = h / (heads_q / heads_kv)).  With P1 and P2 the probabilities of the two maps, each normalised by itself,
+ *     out[i, h]    = sum_j (P1[i, h, j] - lambda[h] P2[i, h, j]) v[j, c],
+ *     second[i, h] = sum_j P2[i, h, j] v[j, c],
+ *     lse[i, h, m] = the log of the sum of exponentials of map m.
+ * - lambda: device fp32 (heads_q), finite; any way of forming it from parameters is the caller's.
+ * - second: (num_q, heads_q, dim_v) in dtype, what the reverse pass keeps beside out, or NULL.
+ * - With bf16 each map's probabilities are rounded to bf16 before their product; the difference is
+ *   taken in fp32 and rounded once.
+ * - A query that sees no key has out = second = 0 and both lse = -infinity.
+ * dim_qk in [1, 64], dim_v in [1, 128]; 2 num_q heads_q and 2 num_k heads_kv < 2^31 - 2^20; for
+ * the rest (masks, strides, offsets, values) the rules of e3conv_attention hold. */
+e3conv_status e3conv_diff_attention_workspace_size(const e3conv_attention_args* args, int backward,
+                                                   size_t* bytes);
+
+/* out, second (or NULL) with their row and head strides, lse float (num_q, heads_q, 2), dense, or NULL; all fully
+ * written. */
+e3conv_status e3conv_diff_attention(const e3conv_attention_args* args, const float* lambda, void* out,
+                                    int64_t out_row, int64_t out_head, void* second,
+                                    int64_t second_row, int64_t second_head, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* Reverse pass of L = <grad_out, out>, from the forward's out, second and lse: with
+ * dP = <grad_out, v>, delta2 = <grad_out, second> and delta1 = <grad_out, out> + lambda delta2,
+ *     dS1 = P1 (dP - delta1),   dS2 = -lambda P2 (dP - delta2),
+ *     grad_q[2h + m] = scale sum_j dS_m k[2c + m],   grad_k[2c + m] = scale sum dS_m q[2h + m],
+ *     grad_v = sum (P1 - lambda P2) grad_out,        grad_lambda[h] = - sum_i sum_j P2 dP,
+ * summed over the rows and the query heads that share the kv head.  strides holds (row, head) of
+ * out, second, grad_out, grad_q, grad_k, grad_v in turn.  grad_lambda is fp32 (heads_q) or NULL (not computed).
+ * All are fully written, without atomics: the same inputs give the same bits. */
+e3conv_status e3conv_diff_attention_backward(const e3conv_attention_args* args, const float* lambda,
+                                             const void* out, const void* second, const float* lse,
+                                             const void* grad_out, void* grad_q, void* grad_k,
+                                             void* grad_v, float* grad_lambda,
+                                             const int64_t strides[12], void* workspace,
+                                             size_t workspace_bytes, void* hip_stream);
+
 /* Activations of e3conv_group_norm: z, max(z, 0), z / (1 + e^-z) and
  * z (1 + erf(z / sqrt 2)) / 2. */
 typedef enum {
