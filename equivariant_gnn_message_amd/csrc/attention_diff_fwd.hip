@@ -2,12 +2,14 @@
 //
 //     out = softmax(scale q1 k1^T) v - lambda softmax(scale q2 k2^T) v
 //
-// As the plain attention's forward, a wave owns 32 rows and walks over the keys, rows along the columns:
-//     S1^T = K1 Q1^T,  S2^T = K2 Q2^T,   O1^T += V^T P1^T,  O2^T += V^T P2^T,
-// each map with a running maximum and sum of its own, in one pass.  Each transposed operand of V is read from LDS
-// once for both maps' products.  (The difference of the maps could be taken before one product with V, but needs
-// both sums first: a second pass over all logits, whose products and exponentials cost as much as that product
-// saves with dim_v = 2 dim_qk.)
+// As the plain attention's forward, a wave owns 32 rows and walks over the keys, rows along the columns, but of one
+// map: two waves share 32 rows,
+//     S_m^T = K_m Q_m^T,   O_m^T += V^T P_m^T,
+// each with a running maximum and sum of its own, in one pass, and the second map's wave hands its result to the
+// first's through LDS at the end.  (Both maps in one wave read each operand of V once, but their sums are 128
+// registers with dim_v = 128, and the whole spills: 1200 us for 100 000 ragged nodes.  The difference of the maps
+// could be taken before one product with V, but needs both sums first: a second pass over all logits, whose
+// products and exponentials cost as much as that product saves with dim_v = 2 dim_qk.)
 #include "attention_diff_tile.h"
 #include "kernels.h"
 
@@ -15,31 +17,33 @@ namespace e3c {
 namespace attn {
 namespace {
 
-template <class T, int D, int RW, int TK, int BUF, int LOAD>
-__global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_fwd(sizeof(T) == 4, D) : 1) diff_fwd(DiffParams p) {
-  constexpr int P = planes<T>(), KS = D / 32, NB = TK / 32, W = P == 1 ? 4 : 2;   // W: operands read ahead
+// RB: blocks of 32 rows of a work-group, a pair of waves each.
+template <class T, int D, int RB, int LOAD>
+__global__ void __launch_bounds__(128 * RB, RB > 1 ? diff_waves_fwd(sizeof(T) == 4) : 1) diff_fwd(DiffParams p) {
+  constexpr int P = planes<T>(), KS = D / 32, TK = 32, BUF = P == 1 ? 2 : 1, W = P == 1 ? 4 : 2;   // W: operands read ahead
   struct Buffer {
     Tile<P, TK, D> k, v;
     float bias[TK];
   };
-  static_assert(BUF == 2 || !(sizeof(T) == 2 && LOAD != kElements), "loads straight to LDS need the other buffer");
+  static_assert(sizeof(Buffer) * BUF >= 128u * D * RB && RB <= 2, "room for the second map's results");
   __shared__ __attribute__((aligned(16))) Buffer first, second;
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
+  const int map = w & 1, block = w >> 1;
 
-  const long block = block_index();
-  if (block >= p.blocks) return;
-  const Where place = where((int)block, p.blocks, p.slots, p.splits);
+  const long index = block_index();
+  if (index >= p.blocks) return;
+  const Where place = where((int)index, p.blocks, p.slots, p.splits);
   const int split = place.split, slot = place.slot, c = place.c;
-  constexpr int BM = 32 * RW;
+  constexpr int BM = 32 * RB;
   const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
   const int q0 = offset(a.q_ptr, g, a.num_q);
   const int nrows = (offset(a.q_ptr, g + 1, a.num_q) - q0) * p.group;
   const int r0 = tile_start(slot, first_slot(a.q_ptr, g, a.num_q, p.group, BM), BM, nrows);
   if (r0 < 0) return;
 
-  const int r = r0 + 32 * w + n;
-  const bool row = r < nrows, idle = r0 + 32 * w >= nrows;   // idle: a wave without rows only loads
+  const int r = r0 + 32 * block + n;
+  const bool row = r < nrows, idle = r0 + 32 * block >= nrows;   // idle: a wave without rows only loads
   const int qi = q0 + (row ? query_of(p, r) : 0), head = c * p.group + (row ? r - (qi - q0) * p.group : 0);
   const bool live = row && (!a.q_mask || a.q_mask[qi]);
 
@@ -49,26 +53,23 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_fwd(sizeof(T) ==
   const int k0 = kb + min(split * per, tiles) * TK;
   const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
 
-  Keys<T, D, TK, 64 * RW, LOAD, 2> keys;
+  Keys<T, D, TK, 128 * RB, LOAD, 2> keys;
   keys.begin(p, c, k0, k1);
   keys.pair.clear(a.dim_qk, a.dim_v, first.k, first.v);
   if (BUF == 2) keys.pair.clear(a.dim_qk, a.dim_v, second.k, second.v);
   if (k0 < k1) keys.issue(p, first.k, first.v);
 
-  Frag<P> q[2][KS];
+  Frag<P> q[KS];
+  row_operand<T, D / 2, LOAD>((const T*)a.q + qi * a.q_row + (2 * head + map) * a.q_head, a.dim_qk, live, q);
+  if (p.negate)
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    row_operand<T, D / 2, LOAD>((const T*)a.q + qi * a.q_row + (2 * head + x) * a.q_head, a.dim_qk, live, q[x]);
-    if (p.negate)
-#pragma unroll
-      for (int t = 0; t < KS; ++t) flip_sign(q[x][t]);
-  }
+    for (int t = 0; t < KS; ++t) flip_sign(q[t]);
 
-  f32x16 o[2][D / 32];
+  f32x16 o[D / 32];
 #pragma unroll
-  for (int dt = 0; dt < D / 32; ++dt) o[0][dt] = o[1][dt] = f32x16{};
+  for (int dt = 0; dt < D / 32; ++dt) o[dt] = f32x16{};
   // of the logits in units of log 2; l: this half's keys, too large by `over` (compensated from tile to tile)
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, over[2] = {0.0f, 0.0f};
+  float m = -INFINITY, l = 0.0f, over = 0.0f;
 
   const auto use = [&](Buffer& now, int from, Buffer& next) {
     Tile<P, TK, D>&kt = now.k, &vt = now.v;
@@ -78,172 +79,164 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_fwd(sizeof(T) ==
     if (from + TK < k1) keys.issue(p, next.k, next.v);
     if (idle) return;
 
-    Frag<P> f[2][2 * NB];
+    f32x16 s = by_row(now.bias, lane);
+    ahead<KS, W, Frag<P>>([&](int i) { return kt.rows(0, map * KS + i, lane); },
+                          [&](int i, const Frag<P>& x) { s = mma(x, q[i], s); });
+    float top = s[0];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      f32x16 s[NB];
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    top = fmaxf(top, other_half(top)) * p.c;
+    // m is the maximum only to within 2^kSlack, so that o and l are scaled again in few tiles
+    constexpr float kSlack = 8.0f;
+    if (__ballot(top > m + kSlack)) {
+      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
+      const float f = __builtin_amdgcn_exp2f(m - base);
+      m = mn;
+      l *= f;
+      over *= f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) s[b] = by_row(now.bias + 32 * b, lane);
-      ahead<NB * KS, W, Frag<P>>([&](int i) { return kt.rows(32 * (i % NB), x * KS + i / NB, lane); },
-                                 [&](int i, const Frag<P>& y) { s[i % NB] = mma(y, q[x][i / NB], s[i % NB]); });
-      float top = s[0][0];
+      for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-      top = fmaxf(top, other_half(top)) * p.c;
-      // m is the maximum only to within 2^kSlack, so that o and l are scaled again in few tiles
-      constexpr float kSlack = 8.0f;
-      if (__ballot(top > m[x] + kSlack)) {
-        const float mn = fmaxf(m[x], top), base = mn == -INFINITY ? 0.0f : mn;
-        const float by = __builtin_amdgcn_exp2f(m[x] - base);
-        m[x] = mn;
-        l[x] *= by;
-        over[x] *= by;
-#pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[x][dt][i] *= by;
-      }
-      const float base = m[x] == -INFINITY ? 0.0f : m[x];
-      float sum = 0.0f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float e[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            e[i] = __builtin_amdgcn_exp2f(fmaf(s[b][8 * t + i], p.c, -base));
-            sum += e[i];
-          }
-          // bf16: P rounded for its product, the sum from the unrounded values
-          to_frag(e, f[x][2 * b + t]);
-        }
-      sum -= over[x];
-      const float both = l[x] + sum;
-      over[x] = (both - l[x]) - sum;
-      l[x] = both;
+        for (int i = 0; i < 16; ++i) o[dt][i] *= f;
     }
+    const float base = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 2 * NB; ++t)
+    for (int t = 0; t < 2; ++t) {
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        e[i] = __builtin_amdgcn_exp2f(fmaf(s[8 * t + i], p.c, -base));
+        sum += e[i];
+      }
+      // bf16: P rounded for its product, the sum from the unrounded values
+      Frag<P> f;
+      to_frag(e, f);
       ahead<D / 32, W, Frag<P>>([&](int dt) { return vt.columns(16 * t, dt, lane); },
-                                [&](int dt, const Frag<P>& y) {
-                                  o[0][dt] = mma(y, f[0][t], o[0][dt]);
-                                  o[1][dt] = mma(y, f[1][t], o[1][dt]);
-                                });
+                                [&](int dt, const Frag<P>& x) { o[dt] = mma(x, f, o[dt]); });
+    }
+    sum -= over;
+    const float both = l + sum;
+    over = (both - l) - sum;
+    l = both;
   };
   if constexpr (BUF == 2) walk<2, TK>(k0, k1, first, second, use);
   else walk<1, TK>(k0, k1, first, first, use);
 
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    l[x] -= over[x];
-    l[x] += other_half(l[x]);
-  }
-  if (!row) return;
+  l -= over;
+  l += other_half(l);
   const long at = (long)qi * a.heads_q + head;
   if (!live) {
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.0f;
+    m = -INFINITY;
+    l = 0.0f;
   }
   if (p.splits > 1) {
-    const long rows = 2 * a.num_q * a.heads_q;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const long i = split * rows + 2 * at + x;
-      store_row(p.part + i * a.dim_v, o[x], a.dim_v, 1.0f, true, a.dim_v % 4 == 0);
-      if (h == 0) reinterpret_cast<float2*>(p.part_ml)[i] = make_float2(m[x], l[x]);
-    }
+    if (!row) return;
+    const long i = split * (2 * a.num_q * a.heads_q) + 2 * at + map;
+    store_row(p.part + i * a.dim_v, o, a.dim_v, 1.0f, true, a.dim_v % 4 == 0);
+    if (h == 0) reinterpret_cast<float2*>(p.part_ml)[i] = make_float2(m, l);
     return;
   }
-  const float inv0 = l[0] == 0.0f ? 0.0f : 1.0f / l[0], inv1 = l[1] == 0.0f ? 0.0f : 1.0f / l[1];
-  const float lam = p.lam[head];
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      o[1][dt][i] *= inv1;
-      o[0][dt][i] = fmaf(-lam, o[1][dt][i], o[0][dt][i] * inv0);
-    }
-  store_row((T*)p.out + qi * p.out_row + head * p.out_head, o[0], a.dim_v, 1.0f, live, p.vec_st);
-  if (p.second)
-    store_row((T*)p.second + qi * p.second_row + head * p.second_head, o[1], a.dim_v, 1.0f, live, p.vec_st);
-  if (h == 0 && p.lse) {
-    const auto lse = [](float m, float l) { return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2; };
-    reinterpret_cast<float2*>(p.lse)[at] = make_float2(lse(m[0], l[0]), lse(m[1], l[1]));
+    for (int i = 0; i < 16; ++i) o[dt][i] *= inv;
+  // the second map's result, register by register
+  float* const hand = reinterpret_cast<float*>(BUF == 2 && block == 1 ? &second : &first) +
+                      (BUF == 2 ? 0 : block * 32 * D) + lane;
+  __syncthreads();
+  if (map == 1)
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) hand[(16 * dt + i) * 64] = o[dt][i];
+  __syncthreads();
+  if (!row) return;
+  if (map == 0) {
+    const float lam = p.lam[head];
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[dt][i] = fmaf(-lam, hand[(16 * dt + i) * 64], o[dt][i]);
+    store_row((T*)p.out + qi * p.out_row + head * p.out_head, o, a.dim_v, 1.0f, live, p.vec_st);
+  } else if (p.second) {
+    store_row((T*)p.second + qi * p.second_row + head * p.second_head, o, a.dim_v, 1.0f, live, p.vec_st);
   }
+  if (h == 0 && p.lse) p.lse[2 * at + map] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// Joins the splits of one row: each map's o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, and their difference.
-// Sixteen waves take the splits of one map, then of the other, in turn.
-constexpr int kJoinWaves = 16;
+// Joins the splits of 32 elements of one row: each map's o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, and
+// their difference.  32 threads take the splits of an element and map in turn, all their loads in flight at once
+// (a work-group for all of a row's elements, one map after the other: 32 us for 461 splits of four rows).
+constexpr int kJoinLanes = 32;
 template <class T>
-__global__ void __launch_bounds__(64 * kJoinWaves) diff_join(DiffParams p) {
+__global__ void __launch_bounds__(32 * kJoinLanes) diff_join(DiffParams p) {
   const e3conv_attention_args& a = p.a;
-  __shared__ float weight[kMaxSplits], sum[kJoinWaves][kMaxDim], red[2][kJoinWaves];
-  const long rows = 2 * a.num_q * a.heads_q, at = block_index();
+  constexpr int N = kMaxSplits / kJoinLanes, WAVES = kJoinLanes / 2;
+  __shared__ float weight[2][kMaxSplits], red[4][WAVES], sum[2][WAVES][32];
+  const int columns = (a.dim_v + 31) / 32;
+  const long rows = 2 * a.num_q * a.heads_q, index = block_index(), at = index / columns;
   if (2 * at >= rows) return;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  float result[2], lse[2];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, first = tid >> 5;
+  const int d = (int)(index - at * columns) * 32 + (tid & 31);
+  float4 ml = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);       // maximum and sum of both maps
+  if (tid < p.splits) ml = *reinterpret_cast<const float4*>(p.part_ml + 2 * (tid * rows + 2 * at));
+  float v[2][N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int s = first + i * kJoinLanes;
+    const float* o = p.part + (s * rows + 2 * at) * a.dim_v + d;
+    const bool on = s < p.splits && d < a.dim_v;
+    v[0][i] = on ? o[0] : 0.0f;
+    v[1][i] = on ? o[a.dim_v] : 0.0f;
+  }
+  float m[2] = {ml.x, ml.z}, l[2] = {ml.y, ml.w}, top[2] = {ml.x, ml.z};
+#pragma unroll
   for (int x = 0; x < 2; ++x) {
-    float m = -INFINITY, l = 0.0f;
-    if (tid < p.splits) {
-      const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[tid * rows + 2 * at + x];
-      m = ml.x;
-      l = ml.y;
+    for (int o = 32; o > 0; o >>= 1) top[x] = fmaxf(top[x], __shfl_xor(top[x], o));
+    if (lane == 0) red[x][w] = top[x];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    top[x] = red[x][0];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) top[x] = fmaxf(top[x], red[x][i]);
+    const float f = __builtin_amdgcn_exp2f(m[x] - (top[x] == -INFINITY ? 0.0f : top[x]));
+    if (tid < kMaxSplits) weight[x][tid] = f;
+    l[x] *= f;
+    for (int o = 32; o > 0; o >>= 1) l[x] += __shfl_xor(l[x], o);
+    if (lane == 0) red[2 + x][w] = l[x];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s = fmaf(weight[x][first + i * kJoinLanes], v[x][i], s);
+    s += __shfl_xor(s, 32);
+    if (lane < 32) sum[x][w][lane] = s;
+  }
+  __syncthreads();
+  if (tid >= 32 || d >= a.dim_v) return;
+  float result[2], lse[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    float s = 0.0f, all = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      s += sum[x][i][tid];
+      all += red[2 + x][i];
     }
-    const float* part = p.part + (2 * at + x) * a.dim_v;
-    constexpr int N = kMaxSplits / kJoinWaves;
-    float v0[N], v1[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int s = w + i * kJoinWaves;
-      const float* o = part + s * rows * a.dim_v;
-      v0[i] = s < p.splits && lane < a.dim_v ? o[lane] : 0.0f;
-      v1[i] = s < p.splits && lane + 64 < a.dim_v ? o[lane + 64] : 0.0f;
-    }
-    float top = m;
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    if (lane == 0) red[0][w] = top;
-    __syncthreads();
-    top = red[0][0];
-#pragma unroll
-    for (int i = 1; i < kJoinWaves; ++i) top = fmaxf(top, red[0][i]);
-    const float base = top == -INFINITY ? 0.0f : top, f = __builtin_amdgcn_exp2f(m - base);
-    if (tid < kMaxSplits) weight[tid] = f;
-    l *= f;
-    for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
-    if (lane == 0) red[1][w] = l;
-    __syncthreads();
-    l = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kJoinWaves; ++i) l += red[1][i];
-    float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float by = weight[w + i * kJoinWaves];
-      a0 = fmaf(by, v0[i], a0);
-      a1 = fmaf(by, v1[i], a1);
-    }
-    sum[w][lane] = a0;
-    sum[w][lane + 64] = a1;
-    __syncthreads();
-    float v = 0.0f;
-    if (tid < a.dim_v)
-#pragma unroll
-      for (int i = 0; i < kJoinWaves; ++i) v += sum[i][tid];
-    result[x] = l == 0.0f ? 0.0f : v / l;
-    lse[x] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
-    __syncthreads();
+    result[x] = all == 0.0f ? 0.0f : s / all;
+    lse[x] = all == 0.0f ? -INFINITY : (top[x] + __builtin_amdgcn_logf(all)) * kLn2;
   }
   const int head = (int)(at % a.heads_q);
   const long qi = at / a.heads_q;
-  if (tid < a.dim_v) {
-    ((T*)p.out)[qi * p.out_row + head * p.out_head + tid] = (T)fmaf(-p.lam[head], result[1], result[0]);
-    if (p.second) ((T*)p.second)[qi * p.second_row + head * p.second_head + tid] = (T)result[1];
-  }
-  if (tid == 0 && p.lse) reinterpret_cast<float2*>(p.lse)[at] = make_float2(lse[0], lse[1]);
+  ((T*)p.out)[qi * p.out_row + head * p.out_head + d] = (T)fmaf(-p.lam[head], result[1], result[0]);
+  if (p.second) ((T*)p.second)[qi * p.second_row + head * p.second_head + d] = (T)result[1];
+  if (d == 0 && p.lse) reinterpret_cast<float2*>(p.lse)[at] = make_float2(lse[0], lse[1]);
 }
 
 // The same for many rows of few splits: a thread for each element, consecutive ones side by side.
@@ -279,20 +272,19 @@ __global__ void __launch_bounds__(256) diff_join_rows(DiffParams p) {
   if (d == 0 && p.lse) reinterpret_cast<float2*>(p.lse)[at] = make_float2(lse[0], lse[1]);
 }
 
+// Blocks of 32 rows of a work-group where graphs have more than 64 rows.
+constexpr int kBlocks = 2;
+
 Shape shape_of(const e3conv_attention_args& a) {
   const bool f32 = a.dtype == E3CONV_F32;
-  const int width = diff_width(a);
-  return choose(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv, diff_waves_fwd(f32, width),
-                diff_unit_us(f32, width, false), 2 * a.dim_v);
+  return choose(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv, diff_waves_fwd(f32),
+                diff_unit_us(f32, diff_width(a), false) / 2, 2 * a.dim_v, kBlocks);
 }
 
-// LDS: the tiles of both buffers, at most 64 KiB (two work-groups of a compute unit).
 template <class T, int D, int LOAD>
 void launch(const DiffParams& p, int rw, hipStream_t s) {
-  constexpr int TK4 = sizeof(T) == 4 && D == 128 ? 32 : 64, TILE = planes<T>() * D * 2 * 2;
-  constexpr int BUF4 = 2 * TK4 * TILE <= 65536 ? 2 : 1, BUF1 = sizeof(T) == 2 && LOAD != kElements ? 2 : 1;
-  if (rw == 4) hipLaunchKernelGGL((diff_fwd<T, D, 4, TK4, BUF4, LOAD>), grid_of(p.blocks), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((diff_fwd<T, D, 1, 32, BUF1, LOAD>), grid_of(p.blocks), dim3(64), 0, s, p);
+  if (rw == kBlocks) hipLaunchKernelGGL((diff_fwd<T, D, kBlocks, LOAD>), grid_of(p.blocks), dim3(128 * kBlocks), 0, s, p);
+  else hipLaunchKernelGGL((diff_fwd<T, D, 1, LOAD>), grid_of(p.blocks), dim3(128), 0, s, p);
 }
 template <class T, int D>
 void launch(const DiffParams& p, int rw, hipStream_t s) {
@@ -312,7 +304,8 @@ hipError_t forward(const DiffParams& p, int rw, hipStream_t s) {
     hipLaunchKernelGGL(diff_join_rows<T>, grid_of(blocks), dim3(256), 0, s, p);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(diff_join<T>, grid_of(p.a.num_q * p.a.heads_q), dim3(64 * kJoinWaves), 0, s, p);
+  const long blocks = (long)p.a.num_q * p.a.heads_q * ((p.a.dim_v + 31) / 32);
+  hipLaunchKernelGGL(diff_join<T>, grid_of(blocks), dim3(32 * kJoinLanes), 0, s, p);
   return hipGetLastError();
 }
 

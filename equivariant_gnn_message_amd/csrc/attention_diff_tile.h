@@ -110,7 +110,7 @@ __device__ __forceinline__ void by_half(const float* rows, int t, int lane, floa
 }
 
 // Waves of a SIMD that the registers are kept to: forward, grad_q, grad_k with grad_v.
-constexpr int diff_waves_fwd(bool f32, int d) { return f32 ? (d == 64 ? 2 : 1) : 2; }
+constexpr int diff_waves_fwd(bool f32) { return f32 ? 2 : 3; }
 constexpr int diff_waves_q(bool f32, int d) { return f32 ? 1 : 2; }
 constexpr int diff_waves_kv(bool f32, int d) { return f32 ? 1 : (d == 64 ? 2 : 1); }
 

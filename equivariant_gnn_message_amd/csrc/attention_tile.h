@@ -661,13 +661,14 @@ struct Shape {
 // quarter each: 4.3 against 3.7 ms for the reverse pass of 20 000 nodes).  The choice minimises
 // an estimate from `unit`, the us of one work-group for one row of the other axis (below),
 // and the partial results' bytes.  Lengths are on the device: averages stand for them.
-inline Shape choose(long rows, long others, int graphs, int heads, int waves, double unit, int width) {
+// wide: blocks of 32 rows of a work-group where a graph has more than 64 rows.
+inline Shape choose(long rows, long others, int graphs, int heads, int waves, double unit, int width, int wide = 4) {
   const long g = graphs > 0 ? graphs : 1, avg = (rows + g - 1) / g, avg_o = (others + g - 1) / g;
   Shape s;
-  s.rw = avg > 64 ? 4 : 1;
+  s.rw = avg > 64 ? wide : 1;
   s.slots = (int)(rows / (32 * s.rw) + graphs);
   const long n = g * ((avg + 32 * s.rw - 1) / (32 * s.rw)) * heads;
-  const long places = 256 * (s.rw == 4 ? waves : 4);
+  const long places = 256 * (s.rw > 1 ? waves : 4);
   long most = (avg_o + 127) / 128;
   if (most > kMaxSplits) most = kMaxSplits;
   double best = 1e30;

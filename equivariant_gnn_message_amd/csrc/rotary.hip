@@ -26,6 +26,7 @@ constexpr int NT = 256;               // threads of a work-group
 constexpr int kMaxDim = 256, kMaxAxes = 4;
 constexpr int kTile = 8192;           // elements of a tile at most: one row's heads go in parts if they have more
 constexpr int kTable = 2048;          // pairs of a tile's rows at most
+constexpr int kTileRows = 128;
 
 struct RotaryParams {
   e3conv_rotary_args a;
@@ -33,7 +34,7 @@ struct RotaryParams {
   int turning;                        // units that hold pairs
   int tile_rows, tile_heads;
   int tiles, blocks;
-  Div by_units, by_heads, by_pairs, by_axes;
+  Div by_units, by_heads, by_pairs, by_axes, by_values;
   float sign;
   void* out;
   long out_row, out_head;
@@ -168,60 +169,84 @@ __global__ void __launch_bounds__(NT) rotary(RotaryParams p) {
 }
 
 // With the gradients of positions or waves: turns back g and forms d_angle.  A work-group takes every
-// blocks-th tile and keeps its part of grad_waves.
+// blocks-th tile and keeps its part of grad_waves: a thread has one value of it (or two) and one of the rows in turn.
 template <class T, int V, bool ADJACENT>
 __global__ void __launch_bounds__(NT) rotary_grad(RotaryParams p) {
   __shared__ float2 table[kTable];
   __shared__ float angles[kTile / 2];          // (row, head, pair)
   __shared__ float sums[kTable];               // (row, pair), over the heads
+  __shared__ float waves[kMaxDim / 2 * kMaxAxes], places[kTileRows * kMaxAxes];
   const e3conv_rotary_args& a = p.a;
-  constexpr int W = (kMaxDim / 2 * kMaxAxes + NT - 1) / NT;
+  constexpr int N = 2, W = kMaxDim / 2 * kMaxAxes / NT;
+  const int values = a.pairs * a.axes;
+  for (int e = threadIdx.x; e < values; e += NT) waves[e] = a.waves[e];
+  const int lanes = values <= NT ? p.by_values.of(NT) : 1;                  // rows in turn for each value
+  const int lane = values <= NT ? p.by_values.of(threadIdx.x) : 0;
   double gw[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) gw[i] = 0.0;
   for (long tile = blockIdx.x; tile < p.tiles; tile += p.blocks) {
     const long row0 = tile * p.tile_rows;
     const int nrows = (int)min((long)p.tile_rows, a.num_rows - row0);
-    __syncthreads();                           // the last tile's sums are read
-    fill_table(p, row0, nrows, table);
-    for (int e = threadIdx.x; e < nrows * a.pairs; e += NT) sums[e] = 0.0f;
-    __syncthreads();
     for (int h0 = 0; h0 < a.heads; h0 += p.tile_heads) {      // more than one part: the tile is one row
       const int heads = min(p.tile_heads, a.heads - h0), n = nrows * heads * p.units;
-      for (int e = threadIdx.x; e < n; e += NT) {
-        const int rh = p.by_units.of(e), r = nrows == 1 ? 0 : p.by_heads.of(rh), h = rh - r * heads;
-        const Unit<V, ADJACENT> at(p, e - rh * p.units);
-        const long row = row0 + r;
-        Held<T, V, ADJACENT> hg, hx;
-        hg.load((const T*)p.g + row * p.g_row + (h0 + h) * p.g_head, at);
-        hx.load((const T*)a.x + row * a.x_row + (h0 + h) * a.x_head, at);
-        float gu[V], gv[V], u[V], v[V];
-        widen<T, V>(hg.a, gu);
-        widen<T, V>(hg.b, gv);
-        widen<T, V>(hx.a, u);
-        widen<T, V>(hx.b, v);
-        turn<V, ADJACENT>(table + r * a.pairs, a.pairs, at, gu, gv);
-        const bool live = !a.row_mask || a.row_mask[row];
-        if (!live)
+      for (int e0 = threadIdx.x; e0 - (int)threadIdx.x < n; e0 += N * NT) {
+        Held<T, V, ADJACENT> hg[N], hx[N];
 #pragma unroll
-          for (int j = 0; j < V; ++j) gu[j] = gv[j] = u[j] = v[j] = 0.0f;
-        T* to = (T*)p.out + row * p.out_row + (h0 + h) * p.out_head;
-        store<T, V>(to + at.u, gu);
-        if (Held<T, V, ADJACENT>::TWO && at.turns) store<T, V>(to + at.v, gv);
-        float* d = angles + (r * heads + h) * a.pairs + at.pair;
-        if constexpr (ADJACENT && V > 1) {
+        for (int i = 0; i < N; ++i) {
+          const int e = e0 + i * NT;
+          if (e < n) {
+            const int rh = p.by_units.of(e), r = nrows == 1 ? 0 : p.by_heads.of(rh), h = h0 + rh - r * heads;
+            const Unit<V, ADJACENT> at(p, e - rh * p.units);
+            hg[i].load((const T*)p.g + (row0 + r) * p.g_row + h * p.g_head, at);
+            hx[i].load((const T*)a.x + (row0 + r) * a.x_row + h * a.x_head, at);
+          }
+        }
+        if (h0 == 0 && e0 == (int)threadIdx.x) {              // while the first loads are on their way
+          __syncthreads();                                    // the last tile's sums and places are read
+          fill_table(p, row0, nrows, table);
+          for (int e = threadIdx.x; e < nrows * a.axes; e += NT) {
+            const int r = p.by_axes.of(e);
+            places[e] = a.positions[(row0 + r) * a.position_row + (e - r * a.axes)];
+          }
+          for (int e = threadIdx.x; e < nrows * a.pairs; e += NT) sums[e] = 0.0f;
+          __syncthreads();
+        }
 #pragma unroll
-          for (int j = 0; j < V / 2; ++j)
-            if (at.pair + j < a.pairs) d[j] = fmaf(u[2 * j], gu[2 * j + 1], -(u[2 * j + 1] * gu[2 * j]));
-        } else if (at.turns) {
+        for (int i = 0; i < N; ++i) {
+          const int e = e0 + i * NT;
+          if (e >= n) break;
+          const int rh = p.by_units.of(e), r = nrows == 1 ? 0 : p.by_heads.of(rh), h = rh - r * heads;
+          const Unit<V, ADJACENT> at(p, e - rh * p.units);
+          const long row = row0 + r;
+          float gu[V], gv[V], u[V], v[V];
+          widen<T, V>(hg[i].a, gu);
+          widen<T, V>(hg[i].b, gv);
+          widen<T, V>(hx[i].a, u);
+          widen<T, V>(hx[i].b, v);
+          turn<V, ADJACENT>(table + r * a.pairs, a.pairs, at, gu, gv);
+          if (a.row_mask && !a.row_mask[row])
 #pragma unroll
-          for (int j = 0; j < V; ++j) d[j] = fmaf(u[j], gv[j], -(v[j] * gu[j]));
+            for (int j = 0; j < V; ++j) gu[j] = gv[j] = u[j] = v[j] = 0.0f;
+          T* to = (T*)p.out + row * p.out_row + (h0 + h) * p.out_head;
+          store<T, V>(to + at.u, gu);
+          if (Held<T, V, ADJACENT>::TWO && at.turns) store<T, V>(to + at.v, gv);
+          float* d = angles + (r * heads + h) * a.pairs + at.pair;
+          if constexpr (ADJACENT && V > 1) {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j)
+              if (at.pair + j < a.pairs) d[j] = fmaf(u[2 * j], gu[2 * j + 1], -(u[2 * j + 1] * gu[2 * j]));
+          } else if (at.turns) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[j] = fmaf(u[j], gv[j], -(v[j] * gu[j]));
+          }
         }
       }
       __syncthreads();
       for (int e = threadIdx.x; e < nrows * a.pairs; e += NT) {
         const int r = p.by_pairs.of(e), k = e - r * a.pairs;
         float s = sums[e];
+#pragma unroll 4
         for (int h = 0; h < heads; ++h) s += angles[(r * heads + h) * a.pairs + k];
         sums[e] = s;
       }
@@ -231,38 +256,62 @@ __global__ void __launch_bounds__(NT) rotary_grad(RotaryParams p) {
       for (int e = threadIdx.x; e < nrows * a.axes; e += NT) {
         const int r = p.by_axes.of(e), x = e - r * a.axes;
         float s = 0.0f;
-        for (int k = 0; k < a.pairs; ++k) s = fmaf(sums[r * a.pairs + k], a.waves[k * a.axes + x], s);
-        p.gp[(row0 + r) * a.axes + x] = s;
+#pragma unroll 4
+        for (int k = 0; k < a.pairs; ++k) s = fmaf(sums[r * a.pairs + k], waves[k * a.axes + x], s);
+        p.gp[row0 * a.axes + e] = s;
       }
-    if (p.gw) {
+    if (p.gw && lane < lanes) {
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const int e = threadIdx.x + i * NT;
-        if (e < a.pairs * a.axes) {
-          const int k = p.by_axes.of(e), x = e - k * a.axes;
-          for (int r = 0; r < nrows; ++r) {
-            const float d = sums[r * a.pairs + k];
-            // a masked row has d = 0, whatever its position is
-            if (d != 0.0f) gw[i] = fma((double)d, (double)a.positions[(row0 + r) * a.position_row + x], gw[i]);
-          }
+        const int e = threadIdx.x - lane * values + i * NT;
+        if (e >= values) break;
+        const int k = p.by_axes.of(e), x = e - k * a.axes;
+#pragma unroll 4
+        for (int r = lane; r < nrows; r += lanes) {
+          const float d = sums[r * a.pairs + k];
+          // a masked row has d = 0, whatever its position is
+          if (d != 0.0f) gw[i] = fma((double)d, (double)places[r * a.axes + x], gw[i]);
         }
       }
     }
   }
-  if (p.gw)
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const int e = threadIdx.x + i * NT;
-      if (e < a.pairs * a.axes) p.part[(long)blockIdx.x * a.pairs * a.axes + e] = gw[i];
+  if (!p.gw) return;
+  if (lanes > 1) {                             // the parts of a value's rows, in order
+    double* parts = reinterpret_cast<double*>(table);
+    __syncthreads();
+    parts[threadIdx.x] = gw[0];
+    __syncthreads();
+    if (threadIdx.x < (unsigned)values) {
+      double v = parts[threadIdx.x];
+      for (int i = 1; i < lanes; ++i) v += parts[threadIdx.x + i * values];
+      p.part[(long)blockIdx.x * values + threadIdx.x] = v;
     }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const int e = threadIdx.x + i * NT;
+    if (e < values) p.part[(long)blockIdx.x * values + e] = gw[i];
+  }
 }
 
-// grad_waves: the sum of the work-groups' parts, one wave for each value.
-__global__ void __launch_bounds__(64) rotary_join(const double* part, int blocks, int n, float* gw) {
+// grad_waves: the sum of the work-groups' parts.  Eight values to a work-group, whole 64-byte lines of the parts, and
+// 32 threads for each.
+__global__ void __launch_bounds__(NT) rotary_join(const double* part, int blocks, int n, float* gw) {
+  __shared__ double red[32][9];
+  const int col = threadIdx.x & 7, lane = threadIdx.x >> 3, at = blockIdx.x * 8 + col;
   double v = 0.0;
-  for (int b = threadIdx.x; b < blocks; b += 64) v += part[(long)b * n + blockIdx.x];
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if (threadIdx.x == 0) gw[blockIdx.x] = (float)v;
+  if (at < n)
+#pragma unroll 8
+    for (int b = lane; b < blocks; b += 32) v += part[(long)b * n + at];
+  red[lane][col] = v;
+  __syncthreads();
+  if (threadIdx.x < 8 && at < n) {
+    v = 0.0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v += red[i][col];
+    gw[at] = (float)v;
+  }
 }
 
 // --------------------------------------------------------------- launches ---
@@ -272,7 +321,7 @@ void tiles_of(const e3conv_rotary_args& a, RotaryParams& p) {
   const int width = a.heads * a.dim;
   p.tile_heads = std::min<int>(a.heads, std::max(1, kTile / a.dim));
   int64_t rows = (a.num_rows + 1023) / 1024;
-  rows = std::min<int64_t>(rows, std::min(kTile / width, a.pairs > 0 ? kTable / a.pairs : 1));
+  rows = std::min<int64_t>(rows, std::min({kTile / width, kTable / a.pairs, kTileRows}));
   p.tile_rows = (int)std::max<int64_t>(rows, 1);
   p.tiles = (int)((a.num_rows + p.tile_rows - 1) / p.tile_rows);
   p.blocks = std::min(p.tiles, 1024);
@@ -288,7 +337,7 @@ hipError_t run(const RotaryParams& p, hipStream_t s) {
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || !p.gw) return err;
   const int n = p.a.pairs * p.a.axes;
-  hipLaunchKernelGGL(rotary_join, dim3(n), dim3(64), 0, s, p.part, p.blocks, n, p.gw);
+  hipLaunchKernelGGL(rotary_join, dim3((n + 7) / 8), dim3(NT), 0, s, p.part, p.blocks, n, p.gw);
   return hipGetLastError();
 }
 
@@ -312,6 +361,7 @@ hipError_t launch(RotaryParams p, bool vec, hipStream_t s) {
   p.by_heads = div_by(a.heads);
   p.by_pairs = div_by(a.pairs);
   p.by_axes = div_by(a.axes);
+  p.by_values = div_by(a.pairs * a.axes);
   if (f32) {
     if (!vec) return adjacent ? run<float, 1, true>(p, s) : run<float, 1, false>(p, s);
     return adjacent ? run<float, 4, true>(p, s) : run<float, 4, false>(p, s);

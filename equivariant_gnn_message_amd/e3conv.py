@@ -807,9 +807,14 @@ def _diff_attention_args(q, k, v, lam, q_ptr, k_ptr, scale, q_mask, k_mask):
     nq, hq, d = q.shape
     nk, hk, dv = v.shape
     hq //= 2
-    q_row, q_head, _ = _rows_of(q, "q", dt, index, (nq, 2 * hq, d))
-    k_row, k_head, _ = _rows_of(k, "k", dt, index, (nk, 2 * hk, d))
-    v_row, v_head, _ = _rows_of(v, "v", dt, index, (nk, hk, dv))
+    q_row, q_head, q_one = q.stride()
+    k_row, k_head, k_one = k.stride()
+    v_row, v_head, v_one = v.stride()
+    if not (index >= 0 and k.dtype is dt and v.dtype is dt and k.get_device() == index and v.get_device() == index
+            and k.shape == (nk, 2 * hk, d) and q_one == 1 and k_one == 1 and v_one == 1):
+        _rows_of(q, "q", dt, index, (nq, 2 * hq, d))      # says what is wrong, if anything
+        _rows_of(k, "k", dt, index, (nk, 2 * hk, d))
+        _rows_of(v, "v", dt, index, (nk, hk, dv))
     graphs = q_ptr.numel() - 1
     if graphs < 0:
         raise ValueError("q_ptr must hold num_graphs + 1 offsets")
@@ -817,9 +822,11 @@ def _diff_attention_args(q, k, v, lam, q_ptr, k_ptr, scale, q_mask, k_mask):
     kp = qp if k_ptr is q_ptr else _dense(k_ptr, "k_ptr", i32, index, graphs + 1)
     if scale is None:
         scale = d ** -0.5 if d else 1.0       # d = 0: the library refuses it
-    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, scale, qp, kp, _node_mask(q_mask, "q_mask", index, nq),
-                         _node_mask(k_mask, "k_mask", index, nk), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row,
-                         q_head, k_row, k_head, v_row, v_head), _dense(lam, "lam", _torch.float32, index, hq)
+    qm = None if q_mask is None else _node_mask(q_mask, "q_mask", index, nq)
+    km = None if k_mask is None else _node_mask(k_mask, "k_mask", index, nk)
+    return AttentionArgs(code, graphs, hq, hk, d, dv, nq, nk, scale, qp, kp, qm, km, q.data_ptr(), k.data_ptr(),
+                         v.data_ptr(), q_row, q_head, k_row, k_head, v_row,
+                         v_head), _dense(lam, "lam", _torch.float32, index, hq)
 
 
 def e3conv_diff_attention_workspace_size(args, backward=False):
@@ -858,7 +865,7 @@ def e3conv_diff_attention(q, k, v, lam, q_ptr, k_ptr, scale=None, q_mask=None, k
     else:
         strides += dense
         if keep:
-            second = q.new_empty(shape)
+            second = _torch.empty_like(out) if out.is_contiguous() else q.new_empty(shape)
     if lse is not None:
         _dense(lse, "lse", _torch.float32, index, 2 * shape[0] * shape[1])
     elif keep:
@@ -995,14 +1002,16 @@ def _rotary_args(x, positions, waves, layout, row_mask):
     code, index, f32 = _dtype_code(x), x.get_device(), _torch.float32
     n, heads, dim = x.shape
     pairs, axes = waves.shape
-    row, head, _ = _rows_of(x, "x", x.dtype, index, x.shape)
+    row, head, one = x.stride()
+    if index < 0 or one != 1:
+        _rows_of(x, "x", x.dtype, index, x.shape)    # says what is wrong, if anything
     position_row, _ = _rows_of(positions, "positions", f32, index, (n, axes))
     which = ROTARY_LAYOUTS.get(layout, layout)
     if not isinstance(which, int):
         raise ValueError(f"layout must be one of {sorted(ROTARY_LAYOUTS)}, got {layout!r}")
     return RotaryArgs(code, which, heads, dim, pairs, axes, n, x.data_ptr(), row, head, positions.data_ptr(),
                       position_row, _dense(waves, "waves", f32, index, pairs * axes),
-                      _node_mask(row_mask, "row_mask", index, n))
+                      None if row_mask is None else _node_mask(row_mask, "row_mask", index, n))
 
 
 def e3conv_rotary_workspace_size(args):
@@ -1027,7 +1036,7 @@ def e3conv_rotary(x, positions, waves, layout="adjacent", row_mask=None, out=Non
     if other is not None:
         return _on(other, _as_list, e3conv_rotary, x, positions, waves, layout, row_mask, out)[0]
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _like(x)
         row, head = args.heads * args.dim, args.dim
     else:
         row, head, _ = _rows_of(out, "out", x.dtype, index, x.shape)
@@ -1071,23 +1080,34 @@ def e3conv_rotary_backward(x, positions, waves, grad_out, layout="adjacent", row
 
 # ------------------------------------------- root-mean-square norm ---
 
+def _like(t):
+    """A contiguous tensor of t's shape, dtype and device."""
+    return _torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _rms_norm_args(x, weight, groups, eps, residual, row_mask):
     if x.dim() != 2:
         raise ValueError("x must be (num_rows, channels)")
-    code, index, dt = _dtype_code(x), x.get_device(), x.dtype
-    n, c = x.shape
-    row, _ = _rows_of(x, "x", dt, index, x.shape)
-    res = res_row = 0
+    code, index, dt, shape = _dtype_code(x), x.get_device(), x.dtype, x.shape
+    n, c = shape
+    row, one = x.stride()
+    if index < 0 or one != 1:
+        _rows_of(x, "x", dt, index, shape)           # says what is wrong, if anything
+    res, res_row = None, 0
     if residual is not None:
-        res_row, _ = _rows_of(residual, "residual", dt, index, x.shape)
+        if residual.shape == shape and residual.dtype is dt and residual.get_device() == index:
+            res_row, one = residual.stride()
+        if one != 1 or not res_row:
+            res_row, _ = _rows_of(residual, "residual", dt, index, shape)
         res = residual.data_ptr()
     if weight is None:
         period, w = c, None
     else:
         period = weight.numel()
         w = _dense(weight, "weight", _torch.float32, index, period)
-    return RMSNormArgs(code, c, groups, period, eps, n, _node_mask(row_mask, "row_mask", index, n), x.data_ptr(), row,
-                       res or None, res_row, w)
+    return RMSNormArgs(code, c, groups, period, eps, n,
+                       None if row_mask is None else _node_mask(row_mask, "row_mask", index, n), x.data_ptr(), row, res,
+                       res_row, w)
 
 
 def e3conv_rms_norm_workspace_size(args):
@@ -1113,7 +1133,7 @@ def e3conv_rms_norm(x, weight=None, groups=1, eps=1e-5, residual=None, row_mask=
     if other is not None:
         return _on(other, e3conv_rms_norm, x, weight, groups, eps, residual, row_mask, out, total)
     if out is None:
-        out, row = x.new_empty(x.shape), args.channels
+        out, row = _like(x), args.channels
     else:
         row, _ = _rows_of(out, "out", x.dtype, index, x.shape)
         _written(out, "out")
@@ -1122,7 +1142,7 @@ def e3conv_rms_norm(x, weight=None, groups=1, eps=1e-5, residual=None, row_mask=
         if total is not None:
             raise ValueError("total is the sum with a residual, and there is none")
     elif total is None:
-        total, total_row = x.new_empty(x.shape), args.channels
+        total, total_row = _like(x), args.channels
         at = total.data_ptr()
     else:
         total_row, _ = _rows_of(total, "total", x.dtype, index, x.shape)
