@@ -25,21 +25,24 @@ using namespace rows;
 constexpr int NT = 256;               // threads of a work-group
 constexpr int kMaxDim = 256, kMaxAxes = 4;
 constexpr int kTile = 8192;           // elements of a tile at most: one row's heads go in parts if they have more
-constexpr int kTable = 2048;          // pairs of a tile's rows at most
-constexpr int kTileRows = 128;
+constexpr int kGradTile = 4096;       // the same of the reverse pass, which keeps half as many values in LDS
+constexpr int kTileRows = 128;        // a tile has at most NT angles: each thread forms one
+constexpr int kTable = 512;           // and its rows in the table are whole runs: 128 rows of 4 at most, or 256 + 85 3
 
 struct RotaryParams {
   e3conv_rotary_args a;
   int units;                          // runs of a head: of V elements, or turned pairs of V and then V elements
   int turning;                        // units that hold pairs
+  int stride;                         // pairs of a row of the table, whole runs
   int tile_rows, tile_heads;
   int tiles, blocks;
   Div by_units, by_heads, by_pairs, by_axes, by_values;
   float sign;
+  unsigned x_row, x_head;             // strides in elements
   void* out;
-  long out_row, out_head;
+  unsigned out_row, out_head;
   const void* g;                      // reverse pass: the gradient, turned back
-  long g_row, g_head;
+  unsigned g_row, g_head;
   float* gp;
   float* gw;
   double* part;                       // (blocks, pairs axes)
@@ -67,23 +70,60 @@ struct Unit {
   }
 };
 
-// The cosines and sines of the tile's rows.
-__device__ __forceinline__ void fill_table(const RotaryParams& p, long row0, int nrows, float2* table) {
-  const e3conv_rotary_args& a = p.a;
-  for (int e = threadIdx.x; e < nrows * a.pairs; e += NT) {
-    const int r = p.by_pairs.of(e), k = e - r * a.pairs;
-    const long row = row0 + r;
-    float s = 0.0f, c = 1.0f;
-    if (!a.row_mask || a.row_mask[row]) {
-      double angle = 0.0;
-      for (int x = 0; x < a.axes; ++x)
-        angle = fma((double)a.positions[row * a.position_row + x], (double)a.waves[k * a.axes + x], angle);
-      const double turns = angle * 0.15915494309189533577;
-      sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-    }
-    table[e] = make_float2(c, p.sign * s);
-  }
+// cos and sin of 2 pi t, |t| <= 1/2: within 2 units of fp32's last place.  The nearest quarter turn leaves
+// |x| <= pi / 4, where the Taylor series to x^9 and x^10 err by less than 2^-28.
+__device__ __forceinline__ float2 cos_sin(float t) {
+  const float quarter = rintf(4.0f * t);
+  const float x = 6.28318530717958648f * fmaf(-0.25f, quarter, t), y = x * x;
+  float s = fmaf(y, 1.0f / 362880, -1.0f / 5040), c = fmaf(y, -1.0f / 3628800, 1.0f / 40320);
+  s = fmaf(y, s, 1.0f / 120);
+  c = fmaf(y, c, -1.0f / 720);
+  s = fmaf(y, s, -1.0f / 6);
+  c = fmaf(y, c, 1.0f / 24);
+  s = fmaf(x * y, s, x);
+  c = fmaf(y, c, -0.5f);
+  c = fmaf(y, c, 1.0f);
+  const int q = (int)quarter;
+  const float a = q & 1 ? s : c, b = q & 1 ? c : s;
+  return make_float2(((q + 1) & 2) ? -a : a, (q & 2) ? -b : b);
 }
+
+// The cosine and sine that this thread forms for the tile.  begin() starts its loads, ahead of the rows' own (loads
+// arrive in order), all of them without a branch; finish() leaves it in LDS.
+struct Angle {
+  float x[kMaxAxes], w[kMaxAxes];
+  unsigned char live;
+  int r, k;
+  __device__ __forceinline__ void begin(const RotaryParams& p, long row0, int nrows) {
+    const e3conv_rotary_args& a = p.a;
+    const int e = min((int)threadIdx.x, nrows * a.pairs - 1);
+    r = p.by_pairs.of(e);
+    k = e - r * a.pairs;
+    const float *at = a.positions + (row0 + r) * a.position_row, *wave = a.waves + k * a.axes;
+    live = a.row_mask ? a.row_mask[row0 + r] : 1;
+#pragma unroll
+    for (int i = 0; i < kMaxAxes; ++i) {
+      const int j = min(i, a.axes - 1);
+      x[i] = at[j];
+      w[i] = wave[j];
+    }
+  }
+  // lives: which rows count.
+  __device__ __forceinline__ void finish(const RotaryParams& p, int nrows, float2* table, unsigned char* lives) const {
+    const e3conv_rotary_args& a = p.a;
+    double angle = 0.0;
+#pragma unroll
+    for (int i = 0; i < kMaxAxes; ++i) angle = fma((double)x[i], i < a.axes ? (double)w[i] : 0.0, angle);
+    const double turns = angle * 0.15915494309189533577;
+    float2 cs = cos_sin((float)(turns - rint(turns)));
+    cs.y *= p.sign;
+    if ((int)threadIdx.x < nrows * a.pairs) {
+      // a masked row's position may be anything
+      table[r * p.stride + k] = live ? cs : make_float2(1.0f, 0.0f);
+      if (k == 0) lives[r] = live;
+    }
+  }
+};
 
 // A unit's elements in registers.
 template <class T, int V, bool ADJACENT>
@@ -94,21 +134,30 @@ struct Held {
     a = read<T, V>(head + at.u);
     if (TWO && at.turns) b = read<T, V>(head + at.v);
   }
+  __device__ __forceinline__ void clear() {
+    a = typename Run<T, V>::type{};
+    b = typename Run<T, V>::type{};
+  }
 };
 
-// Turns the pairs of a unit: x holds its run, or x the first elements of its pairs and y the second ones.
+// Turns the pairs of a unit: x holds its run, or x the first elements of its pairs and y the second ones.  cs: its row
+// of the table.
 template <int V, bool ADJACENT>
-__device__ __forceinline__ void turn(const float2* cs, int pairs, const Unit<V, ADJACENT>& at, float (&x)[V],
+__device__ __forceinline__ void turn(const float2* cs, const RotaryParams& p, const Unit<V, ADJACENT>& at, float (&x)[V],
                                      float (&y)[V]) {
   if constexpr (ADJACENT && V > 1) {
+    float4 t[V / 4];
+    const float4* from = reinterpret_cast<const float4*>(cs + (at.pair < p.stride ? at.pair : 0));
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i)
-      if (at.pair + i < pairs) {
-        const float2 t = cs[at.pair + i];
-        const float u = x[2 * i], v = x[2 * i + 1];
-        x[2 * i] = fmaf(u, t.x, -(v * t.y));
-        x[2 * i + 1] = fmaf(u, t.y, v * t.x);
-      }
+    for (int i = 0; i < V / 4; ++i) t[i] = from[i];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {            // chosen, not branched around: a run may end beyond the pairs
+      const float c = i & 1 ? t[i / 2].z : t[i / 2].x, s = i & 1 ? t[i / 2].w : t[i / 2].y;
+      const float u = x[2 * i], v = x[2 * i + 1], a = fmaf(u, c, -(v * s)), b = fmaf(u, s, v * c);
+      const bool on = at.pair + i < p.a.pairs;
+      x[2 * i] = on ? a : u;
+      x[2 * i + 1] = on ? b : v;
+    }
   } else if (at.turns) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -120,50 +169,52 @@ __device__ __forceinline__ void turn(const float2* cs, int pairs, const Unit<V, 
   }
 }
 
+// Row r and head h of a tensor of which `first` is the tile's first row.
+template <class T>
+__device__ __forceinline__ T* place(T* first, unsigned row, unsigned head, int r, int h) {
+  return first + ((uint64_t)row * (unsigned)r + (uint64_t)head * (unsigned)h);
+}
+
 template <class T, int V, bool ADJACENT>
 __global__ void __launch_bounds__(NT) rotary(RotaryParams p) {
-  __shared__ float2 table[kTable];
+  __shared__ __attribute__((aligned(16))) float2 table[kTable];
+  __shared__ unsigned char live[kTileRows];
   const e3conv_rotary_args& a = p.a;
   const long tile = block_index();
   if (tile >= p.tiles) return;
   const long row0 = tile * p.tile_rows;
   const int nrows = (int)min((long)p.tile_rows, a.num_rows - row0);
+  const T* const from = (const T*)a.x + row0 * p.x_row;
+  T* const to = (T*)p.out + row0 * p.out_row;
   const int n = nrows * a.heads * p.units;
   constexpr int N = 4;
-  bool ready = false;
+  Angle angle;
+  angle.begin(p, row0, nrows);
   for (int e0 = threadIdx.x; e0 - (int)threadIdx.x < n; e0 += N * NT) {
     Held<T, V, ADJACENT> held[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = e0 + i * NT;
-      if (e < n) {
-        const int rh = p.by_units.of(e), r = p.by_heads.of(rh);
-        held[i].load((const T*)a.x + (row0 + r) * a.x_row + (rh - r * a.heads) * a.x_head,
-                     Unit<V, ADJACENT>(p, e - rh * p.units));
-      }
+      const int e = min(e0 + i * NT, n - 1), rh = p.by_units.of(e), r = p.by_heads.of(rh);
+      held[i].load(place(from, p.x_row, p.x_head, r, rh - r * a.heads), Unit<V, ADJACENT>(p, e - rh * p.units));
     }
-    if (!ready) {
-      fill_table(p, row0, nrows, table);
+    if (e0 == (int)threadIdx.x) {                // while the first loads are on their way
+      angle.finish(p, nrows, table, live);
       __syncthreads();
-      ready = true;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = e0 + i * NT;
-      if (e < n) {
-        const int rh = p.by_units.of(e), r = p.by_heads.of(rh);
-        const Unit<V, ADJACENT> at(p, e - rh * p.units);
-        float x[V], y[V];
-        widen<T, V>(held[i].a, x);
-        widen<T, V>(held[i].b, y);
-        turn<V, ADJACENT>(table + r * a.pairs, a.pairs, at, x, y);
-        if (a.row_mask && !a.row_mask[row0 + r])
-#pragma unroll
-          for (int j = 0; j < V; ++j) x[j] = y[j] = 0.0f;
-        T* to = (T*)p.out + (row0 + r) * p.out_row + (rh - r * a.heads) * p.out_head;
-        store<T, V>(to + at.u, x);
-        if (Held<T, V, ADJACENT>::TWO && at.turns) store<T, V>(to + at.v, y);
-      }
+      if (e >= n) break;
+      const int rh = p.by_units.of(e), r = p.by_heads.of(rh);
+      const Unit<V, ADJACENT> at(p, e - rh * p.units);
+      if (!live[r]) held[i].clear();
+      float x[V], y[V];
+      widen<T, V>(held[i].a, x);
+      widen<T, V>(held[i].b, y);
+      turn<V, ADJACENT>(table + r * p.stride, p, at, x, y);
+      T* head = place(to, p.out_row, p.out_head, r, rh - r * a.heads);
+      store<T, V>(head + at.u, x);
+      if (Held<T, V, ADJACENT>::TWO && at.turns) store<T, V>(head + at.v, y);
     }
   }
 }
@@ -172,10 +223,11 @@ __global__ void __launch_bounds__(NT) rotary(RotaryParams p) {
 // blocks-th tile and keeps its part of grad_waves: a thread has one value of it (or two) and one of the rows in turn.
 template <class T, int V, bool ADJACENT>
 __global__ void __launch_bounds__(NT) rotary_grad(RotaryParams p) {
-  __shared__ float2 table[kTable];
-  __shared__ float angles[kTile / 2];          // (row, head, pair)
-  __shared__ float sums[kTable];               // (row, pair), over the heads
+  __shared__ __attribute__((aligned(16))) float2 table[kTable];
+  __shared__ float angles[kGradTile / 2];      // (row, head, pair)
+  __shared__ float sums[NT];                   // (row, pair), over the heads
   __shared__ float waves[kMaxDim / 2 * kMaxAxes], places[kTileRows * kMaxAxes];
+  __shared__ unsigned char live[kTileRows];
   const e3conv_rotary_args& a = p.a;
   constexpr int N = 2, W = kMaxDim / 2 * kMaxAxes / NT;
   const int values = a.pairs * a.axes;
@@ -188,28 +240,29 @@ __global__ void __launch_bounds__(NT) rotary_grad(RotaryParams p) {
   for (long tile = blockIdx.x; tile < p.tiles; tile += p.blocks) {
     const long row0 = tile * p.tile_rows;
     const int nrows = (int)min((long)p.tile_rows, a.num_rows - row0);
+    const int sum_r = p.by_pairs.of(threadIdx.x), sum_k = threadIdx.x - sum_r * a.pairs;   // this thread's (row, pair)
+    float sum = 0.0f;
+    Angle angle;
+    angle.begin(p, row0, nrows);
     for (int h0 = 0; h0 < a.heads; h0 += p.tile_heads) {      // more than one part: the tile is one row
       const int heads = min(p.tile_heads, a.heads - h0), n = nrows * heads * p.units;
       for (int e0 = threadIdx.x; e0 - (int)threadIdx.x < n; e0 += N * NT) {
         Held<T, V, ADJACENT> hg[N], hx[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const int e = e0 + i * NT;
-          if (e < n) {
-            const int rh = p.by_units.of(e), r = nrows == 1 ? 0 : p.by_heads.of(rh), h = h0 + rh - r * heads;
-            const Unit<V, ADJACENT> at(p, e - rh * p.units);
-            hg[i].load((const T*)p.g + (row0 + r) * p.g_row + h * p.g_head, at);
-            hx[i].load((const T*)a.x + (row0 + r) * a.x_row + h * a.x_head, at);
-          }
+          const int e = min(e0 + i * NT, n - 1), rh = p.by_units.of(e), r = nrows == 1 ? 0 : p.by_heads.of(rh);
+          const int h = h0 + rh - r * heads;
+          const Unit<V, ADJACENT> at(p, e - rh * p.units);
+          hg[i].load(place((const T*)p.g + row0 * p.g_row, p.g_row, p.g_head, r, h), at);
+          hx[i].load(place((const T*)a.x + row0 * p.x_row, p.x_row, p.x_head, r, h), at);
         }
         if (h0 == 0 && e0 == (int)threadIdx.x) {              // while the first loads are on their way
           __syncthreads();                                    // the last tile's sums and places are read
-          fill_table(p, row0, nrows, table);
+          angle.finish(p, nrows, table, live);
           for (int e = threadIdx.x; e < nrows * a.axes; e += NT) {
             const int r = p.by_axes.of(e);
             places[e] = a.positions[(row0 + r) * a.position_row + (e - r * a.axes)];
           }
-          for (int e = threadIdx.x; e < nrows * a.pairs; e += NT) sums[e] = 0.0f;
           __syncthreads();
         }
 #pragma unroll
@@ -218,17 +271,17 @@ __global__ void __launch_bounds__(NT) rotary_grad(RotaryParams p) {
           if (e >= n) break;
           const int rh = p.by_units.of(e), r = nrows == 1 ? 0 : p.by_heads.of(rh), h = rh - r * heads;
           const Unit<V, ADJACENT> at(p, e - rh * p.units);
-          const long row = row0 + r;
+          if (!live[r]) {
+            hg[i].clear();
+            hx[i].clear();
+          }
           float gu[V], gv[V], u[V], v[V];
           widen<T, V>(hg[i].a, gu);
           widen<T, V>(hg[i].b, gv);
           widen<T, V>(hx[i].a, u);
           widen<T, V>(hx[i].b, v);
-          turn<V, ADJACENT>(table + r * a.pairs, a.pairs, at, gu, gv);
-          if (a.row_mask && !a.row_mask[row])
-#pragma unroll
-            for (int j = 0; j < V; ++j) gu[j] = gv[j] = u[j] = v[j] = 0.0f;
-          T* to = (T*)p.out + row * p.out_row + (h0 + h) * p.out_head;
+          turn<V, ADJACENT>(table + r * p.stride, p, at, gu, gv);
+          T* to = place((T*)p.out + row0 * p.out_row, p.out_row, p.out_head, r, h0 + h);
           store<T, V>(to + at.u, gu);
           if (Held<T, V, ADJACENT>::TWO && at.turns) store<T, V>(to + at.v, gv);
           float* d = angles + (r * heads + h) * a.pairs + at.pair;
@@ -243,15 +296,13 @@ __global__ void __launch_bounds__(NT) rotary_grad(RotaryParams p) {
         }
       }
       __syncthreads();
-      for (int e = threadIdx.x; e < nrows * a.pairs; e += NT) {
-        const int r = p.by_pairs.of(e), k = e - r * a.pairs;
-        float s = sums[e];
+      if (sum_r < nrows)
 #pragma unroll 4
-        for (int h = 0; h < heads; ++h) s += angles[(r * heads + h) * a.pairs + k];
-        sums[e] = s;
-      }
-      __syncthreads();
+        for (int h = 0; h < heads; ++h) sum += angles[(sum_r * heads + h) * a.pairs + sum_k];
+      if (h0 + p.tile_heads < a.heads) __syncthreads();
     }
+    sums[threadIdx.x] = sum;
+    __syncthreads();
     if (p.gp)
       for (int e = threadIdx.x; e < nrows * a.axes; e += NT) {
         const int r = p.by_axes.of(e), x = e - r * a.axes;
@@ -269,8 +320,8 @@ __global__ void __launch_bounds__(NT) rotary_grad(RotaryParams p) {
 #pragma unroll 4
         for (int r = lane; r < nrows; r += lanes) {
           const float d = sums[r * a.pairs + k];
-          // a masked row has d = 0, whatever its position is
-          if (d != 0.0f) gw[i] = fma((double)d, (double)places[r * a.axes + x], gw[i]);
+          // a masked row's position may be anything
+          if (live[r]) gw[i] = fma((double)d, (double)places[r * a.axes + x], gw[i]);
         }
       }
     }
@@ -316,12 +367,12 @@ __global__ void __launch_bounds__(NT) rotary_join(const double* part, int blocks
 
 // --------------------------------------------------------------- launches ---
 
-// Rows of a tile: about four tiles to a compute unit, as far as LDS has room.
-void tiles_of(const e3conv_rotary_args& a, RotaryParams& p) {
-  const int width = a.heads * a.dim;
-  p.tile_heads = std::min<int>(a.heads, std::max(1, kTile / a.dim));
+// Rows of a tile: about four tiles to a compute unit, as far as the angles' threads and LDS have room.
+void tiles_of(const e3conv_rotary_args& a, bool grad, RotaryParams& p) {
+  const int most = grad ? kGradTile : kTile, width = a.heads * a.dim;
+  p.tile_heads = std::min<int>(a.heads, std::max(1, most / a.dim));
   int64_t rows = (a.num_rows + 1023) / 1024;
-  rows = std::min<int64_t>(rows, std::min({kTile / width, kTable / a.pairs, kTileRows}));
+  rows = std::min<int64_t>(rows, std::min({most / width, NT / a.pairs, kTileRows}));
   p.tile_rows = (int)std::max<int64_t>(rows, 1);
   p.tiles = (int)((a.num_rows + p.tile_rows - 1) / p.tile_rows);
   p.blocks = std::min(p.tiles, 1024);
@@ -346,6 +397,8 @@ hipError_t launch(RotaryParams p, bool vec, hipStream_t s) {
   const e3conv_rotary_args& a = p.a;
   const bool f32 = a.dtype == E3CONV_F32, adjacent = a.layout == E3CONV_ROTARY_ADJACENT;
   const int v = f32 ? 4 : 8;
+  p.x_row = (unsigned)a.x_row;
+  p.x_head = (unsigned)a.x_head;
   // whole runs, and in halves no run that holds both pairs and elements beyond them
   vec = vec && a.dim % v == 0 && (adjacent || a.pairs % v == 0);
   const int n = vec ? v : 1;
@@ -356,7 +409,9 @@ hipError_t launch(RotaryParams p, bool vec, hipStream_t s) {
     p.turning = a.pairs / n;
     p.units = p.turning + (a.dim - 2 * a.pairs) / n;
   }
-  tiles_of(a, p);
+  tiles_of(a, p.gp || p.gw, p);
+  const int whole = adjacent && vec ? v / 2 : 1;
+  p.stride = (a.pairs + whole - 1) / whole * whole;
   p.by_units = div_by(p.units);
   p.by_heads = div_by(a.heads);
   p.by_pairs = div_by(a.pairs);
@@ -372,9 +427,13 @@ hipError_t launch(RotaryParams p, bool vec, hipStream_t s) {
 
 size_t workspace_bytes(const e3conv_rotary_args& a) {
   RotaryParams p{};
-  tiles_of(a, p);
+  tiles_of(a, true, p);
   return ((size_t)p.blocks * a.pairs * a.axes * sizeof(double) + 15) / 16 * 16;
 }
+
+// Row and head strides are kept in 32 bits.
+bool strides(int64_t row, int64_t head) { return row >= 0 && row <= 0xffffffffL && head >= 0 && head <= 0xffffffffL; }
+constexpr const char* kStrides = "strides must be in [0, 2^32)";
 
 bool aligned(const void* p, int64_t row, int64_t head, int dtype) {
   const int v = dtype == E3CONV_F32 ? 4 : 8;
@@ -399,7 +458,8 @@ e3conv_status check_sizes(const e3conv_rotary_args* a) {
 e3conv_status check_args(const e3conv_rotary_args* a) {
   const e3conv_status st = check_sizes(a);
   if (st != E3CONV_OK) return st;
-  if (a->x_row < 0 || a->x_head < 0 || a->position_row < 0) return bad("negative stride");
+  if (!strides(a->x_row, a->x_head)) return bad(kStrides);
+  if (a->position_row < 0) return bad("negative stride");
   if (!a->waves) return bad("NULL device pointer");
   if (a->num_rows > 0 && (!a->x || !a->positions)) return bad("NULL device pointer");
   return E3CONV_OK;
@@ -413,15 +473,15 @@ extern "C" {
 e3conv_status e3conv_rotary(const e3conv_rotary_args* a, void* out, int64_t out_row, int64_t out_head, void* stream) {
   const e3conv_status st = e3c::check_args(a);
   if (st != E3CONV_OK) return st;
-  if (out_row < 0 || out_head < 0) return e3c::bad("negative stride");
+  if (!e3c::strides(out_row, out_head)) return e3c::bad(e3c::kStrides);
   if (a->num_rows == 0) return e3c::api_ok();
   if (!out) return e3c::bad("NULL device pointer");
   e3c::RotaryParams p{};
   p.a = *a;
   p.sign = 1.0f;
   p.out = out;
-  p.out_row = out_row;
-  p.out_head = out_head;
+  p.out_row = (unsigned)out_row;
+  p.out_head = (unsigned)out_head;
   const bool vec = e3c::aligned(a->x, a->x_row, a->x_head, a->dtype) && e3c::aligned(out, out_row, out_head, a->dtype);
   const hipError_t err = e3c::launch(p, vec, static_cast<hipStream_t>(stream));
   if (err != hipSuccess) return e3c::api_hip_fail(err, "rotary launch");
@@ -445,7 +505,7 @@ e3conv_status e3conv_rotary_backward(const e3conv_rotary_args* a, const void* gr
   if (a && !angles && !args.x) args.x = grad_out;      // the features enter the angles' gradients alone
   const e3conv_status st = e3c::check_args(a ? &args : nullptr);
   if (st != E3CONV_OK) return st;
-  if (grad_out_row < 0 || grad_out_head < 0 || grad_x_row < 0 || grad_x_head < 0) return e3c::bad("negative stride");
+  if (!e3c::strides(grad_out_row, grad_out_head) || !e3c::strides(grad_x_row, grad_x_head)) return e3c::bad(e3c::kStrides);
   if (a->num_rows == 0) {
     if (!grad_waves) return e3c::api_ok();
     const hipError_t e = e3c::launch_fill_zero(grad_waves, (size_t)a->pairs * a->axes, static_cast<hipStream_t>(stream));
@@ -459,15 +519,15 @@ e3conv_status e3conv_rotary_backward(const e3conv_rotary_args* a, const void* gr
   p.a = args;
   p.sign = -1.0f;
   p.out = grad_x;
-  p.out_row = grad_x_row;
-  p.out_head = grad_x_head;
+  p.out_row = (unsigned)grad_x_row;
+  p.out_head = (unsigned)grad_x_head;
   bool vec = e3c::aligned(grad_out, grad_out_row, grad_out_head, a->dtype) &&
              e3c::aligned(grad_x, grad_x_row, grad_x_head, a->dtype);
   if (angles) {
     vec = vec && e3c::aligned(a->x, a->x_row, a->x_head, a->dtype);
     p.g = grad_out;
-    p.g_row = grad_out_row;
-    p.g_head = grad_out_head;
+    p.g_row = (unsigned)grad_out_row;
+    p.g_head = (unsigned)grad_out_head;
     p.gp = grad_positions;
     p.gw = grad_waves;
     p.part = static_cast<double*>(workspace);

@@ -638,7 +638,8 @@ e3conv_status e3conv_group_norm_backward(const e3conv_group_norm_args* args, con
  *   waves fp32 (pairs, axes), dense.  Angles are formed in 64 bits, so far positions keep their digits.
  * - row_mask: device bytes (num_rows) or NULL; a row whose byte is 0 gets out = 0 and zero gradients,
  *   whatever x, its position and its gradient hold.
- * dim in [1, 256], 1 <= pairs <= dim / 2, axes in [1, 4], heads <= 65536, num_rows < 2^31 - 2^20. */
+ * dim in [1, 256], 1 <= pairs <= dim / 2, axes in [1, 4], heads <= 65536, num_rows < 2^31 - 2^20; row and
+ * head strides below 2^32 elements (offsets are 64 bits wide). */
 typedef enum { E3CONV_ROTARY_ADJACENT = 0, E3CONV_ROTARY_HALVES = 1 } e3conv_rotary_layout;
 
 typedef struct {

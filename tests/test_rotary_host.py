@@ -35,7 +35,8 @@ def backward(a, g=FAKE, gx=FAKE, gp=FAKE, gw=FAKE, strides=(64, 16, 64, 16), ws=
 
 
 @pytest.mark.parametrize("change", BAD_SIZES + [dict(x=None), dict(positions=None), dict(waves=None), dict(x_row=-1),
-                                                dict(x_head=-1), dict(position_row=-1)], ids=str)
+                                                dict(x_head=-1), dict(position_row=-1),
+                                                dict(x_row=1 << 32), dict(x_head=1 << 32)], ids=str)
 def test_refuses(change):
     a = args_of(**change)
     assert forward(a) == 1 and E.e3conv_last_error_detail()
@@ -50,9 +51,11 @@ def test_refuses_outputs_and_workspace():
     a = args_of()
     assert forward(None) == 1 and backward(None) == 1
     assert forward(a, out=None) == 1 and forward(a, row=-1) == 1 and forward(a, head=-1) == 1
+    assert forward(a, row=1 << 32) == 1 and forward(a, head=1 << 32) == 1
     assert backward(a, g=None) == 1 and backward(a, gx=None) == 1
     for i in range(4):
         assert backward(a, strides=[-1 if i == j else 16 for j in range(4)]) == 1
+        assert backward(a, strides=[1 << 32 if i == j else 16 for j in range(4)]) == 1
     assert backward(a, ws=None, n=0) == 6 and backward(a, n=8) == 6 and "bytes" in E.e3conv_last_error_detail()
     assert E.load_library().e3conv_rotary_workspace_size(ctypes.byref(a), None) == 1
 
