@@ -94,60 +94,82 @@ __device__ __forceinline__ void weights(const RmsParams& p, int c, float (&w)[V]
   }
 }
 
-// U: runs of a thread.  BIG: the work-group is one team.
+// U: runs of a thread.  BIG: the work-group is one team.  A team takes items that meet the same weights, and the
+// next one's loads are issued before this one is used: all of an item's together, the mask's byte too; runs
+// beyond the group read its first, and what does not count is cleared afterwards.
 template <class T, int V, int U, bool BIG>
 __global__ void __launch_bounds__(NT) rms_norm(RmsParams p) {
   __shared__ float red[4];
   const e3conv_rms_norm_args& a = p.a;
-  const int t = BIG ? threadIdx.x : threadIdx.x & (p.team - 1);
-  const long at = BIG ? block_index() : block_index() * (NT >> p.team_log2) + (threadIdx.x >> p.team_log2);
-  if (at >= p.items) return;      // whole teams, and whole work-groups where they meet at a barrier
-  const int item = (int)at, row = p.by_groups.of(item), c0 = (item - row * a.groups) * p.size;
-  const bool live = !a.row_mask || a.row_mask[row];
-  const T* x = (const T*)a.x + row * a.x_row + c0;
-  const T* res = a.residual ? (const T*)a.residual + row * a.residual_row + c0 : nullptr;
-  typename Run<T, V>::type rx[U], rr[U];
+  const int t = BIG ? threadIdx.x : threadIdx.x & (p.team - 1), mine = BIG ? 0 : threadIdx.x >> p.team_log2;
+  const long first_item = (long)blockIdx.x * p.used + mine;
+  if (mine >= p.used || first_item >= p.items) return;      // whole teams; a team that is a work-group meets at barriers
+  float w[U][V];
 #pragma unroll
   for (int k = 0; k < U; ++k) {
-    const int u = t + k * p.team;
-    if (live && u < p.units) {
-      rx[k] = read<T, V>(x + u * V);
-      if (res) rr[k] = read<T, V>(res + u * V);
-    }
+    const int u = t + k * p.team, g = (int)(first_item % p.residues);
+    weights<V>(p, g * p.size + (u < p.units ? u * V : 0), w[k]);
   }
-  float s[U][V], sum = 0.0f;
+  struct Item {
+    typename Run<T, V>::type x[U], r[U];
+    unsigned char mask;
+  };
+  const auto load = [&](long at, Item& to) {
+    const int item = (int)at, row = p.by_groups.of(item), c0 = (item - row * a.groups) * p.size;
+    const T* x = (const T*)a.x + row * a.x_row + c0;
+    to.mask = a.row_mask ? a.row_mask[row] : 1;
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const bool on = live && t + k * p.team < p.units;
-    widen<T, V>(rx[k], s[k]);
-    if (res) {
-      float r[V];
-      widen<T, V>(rr[k], r);
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[k][i] += r[i];
+    for (int k = 0; k < U; ++k) {
+      const int u = t + k * p.team;
+      to.x[k] = read<T, V>(x + (u < p.units ? u * V : 0));
     }
+    if (a.residual) {
+      const T* res = (const T*)a.residual + row * a.residual_row + c0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (!on) s[k][i] = 0.0f;
-      sum = fmaf(s[k][i], s[k][i], sum);
+      for (int k = 0; k < U; ++k) {
+        const int u = t + k * p.team;
+        to.r[k] = read<T, V>(res + (u < p.units ? u * V : 0));
+      }
     }
-  }
-  sum = team_sum<BIG>(sum, p.team, red);
-  const float rstd = 1.0f / sqrtf(sum / (float)p.size + a.eps);
-  if (t == 0 && p.rstd) p.rstd[item] = rstd;
-  T* y = (T*)p.y + row * p.y_row + c0;
-  T* total = p.total ? (T*)p.total + row * p.total_row + c0 : nullptr;
+  };
+  Item next;
+  load(first_item, next);
+  for (long at = first_item; at < p.items; at += p.stride) {
+    const Item now = next;
+    if (at + p.stride < p.items) load(at + p.stride, next);
+    const int item = (int)at, row = p.by_groups.of(item), c0 = (item - row * a.groups) * p.size;
+    float s[U][V], sum = 0.0f;
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const int u = t + k * p.team;
-    if (u >= p.units) break;
-    if (total) store<T, V>(total + u * V, s[k]);
-    float w[V];
-    weights<V>(p, c0 + u * V, w);
-    // y from the unrounded sum
+    for (int k = 0; k < U; ++k) {
+      const bool on = now.mask && t + k * p.team < p.units;
+      widen<T, V>(now.x[k], s[k]);
+      if (a.residual) {
+        float r[V];
+        widen<T, V>(now.r[k], r);
 #pragma unroll
-    for (int i = 0; i < V; ++i) w[i] *= s[k][i] * rstd;
-    store<T, V>(y + u * V, w);
+        for (int i = 0; i < V; ++i) s[k][i] += r[i];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s[k][i] = on ? s[k][i] : 0.0f;
+        sum = fmaf(s[k][i], s[k][i], sum);
+      }
+    }
+    sum = team_sum<BIG>(sum, p.team, red);
+    const float rstd = 1.0f / sqrtf(sum / (float)p.size + a.eps);
+    if (t == 0 && p.rstd) p.rstd[item] = rstd;
+    T* y = (T*)p.y + row * p.y_row + c0;
+    T* total = p.total ? (T*)p.total + row * p.total_row + c0 : nullptr;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int u = t + k * p.team;
+      if (u >= p.units) break;
+      if (total) store<T, V>(total + u * V, s[k]);
+      float v[V];      // y from the unrounded sum
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = w[k][i] * (s[k][i] * rstd);
+      store<T, V>(y + u * V, v);
+    }
   }
 }
 
@@ -157,44 +179,62 @@ __global__ void __launch_bounds__(NT) rms_norm_grad(RmsParams p) {
   __shared__ float parts[BIG ? 1 : NT * V * U];
   const e3conv_rms_norm_args& a = p.a;
   const int t = BIG ? threadIdx.x : threadIdx.x & (p.team - 1), mine = BIG ? 0 : threadIdx.x >> p.team_log2;
-  float gw[U][V];
+  const long first_item = (long)blockIdx.x * p.used + mine;
+  float gw[U][V], w[U][V];
 #pragma unroll
-  for (int k = 0; k < U; ++k)
+  for (int k = 0; k < U; ++k) {
+    const int u = t + k * p.team, g = (int)(first_item % p.residues);
+    weights<V>(p, g * p.size + (u < p.units ? u * V : 0), w[k]);
 #pragma unroll
     for (int i = 0; i < V; ++i) gw[k][i] = 0.0f;
-  if (mine < p.used)
-    for (long at = (long)blockIdx.x * p.used + mine; at < p.items; at += p.stride) {
-      const int item = (int)at, row = p.by_groups.of(item), c0 = (item - row * a.groups) * p.size;
-      const bool live = !a.row_mask || a.row_mask[row];
-      const T* x = (const T*)a.x + row * a.x_row + c0;
-      const T* gy = (const T*)p.gy + row * p.gy_row + c0;
-      const T* gt = p.gt ? (const T*)p.gt + row * p.gt_row + c0 : nullptr;
-      typename Run<T, V>::type rx[U], rg[U], rt[U];
+  }
+  // an item's loads; the next one's are issued before this one is used
+  struct Item {
+    typename Run<T, V>::type x[U], g[U], t[U];
+    float rstd;
+    unsigned char mask;
+  };
+  const auto load = [&](long at, Item& to) {
+    const int item = (int)at, row = p.by_groups.of(item), c0 = (item - row * a.groups) * p.size;
+    const T *x = (const T*)a.x + row * a.x_row + c0, *g = (const T*)p.gy + row * p.gy_row + c0;
+    to.mask = a.row_mask ? a.row_mask[row] : 1;
+    to.rstd = p.rstd[item];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int u = t + k * p.team, e = u < p.units ? u * V : 0;
+      to.x[k] = read<T, V>(x + e);
+      to.g[k] = read<T, V>(g + e);
+    }
+    if (p.gt) {
+      const T* gt = (const T*)p.gt + row * p.gt_row + c0;
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int u = t + k * p.team;
-        if (live && u < p.units) {
-          rx[k] = read<T, V>(x + u * V);
-          rg[k] = read<T, V>(gy + u * V);
-          if (gt) rt[k] = read<T, V>(gt + u * V);
-        }
+        to.t[k] = read<T, V>(gt + (u < p.units ? u * V : 0));
       }
-      const float rstd = live ? p.rstd[item] : 0.0f;
+    }
+  };
+  Item next;
+  if (mine < p.used && first_item < p.items) load(first_item, next);
+  if (mine < p.used)
+    for (long at = first_item; at < p.items; at += p.stride) {
+      const Item now = next;
+      if (at + p.stride < p.items) load(at + p.stride, next);
+      const int item = (int)at, row = p.by_groups.of(item), c0 = (item - row * a.groups) * p.size;
+      const float rstd = now.mask ? now.rstd : 0.0f;
       float xh[U][V], dn[U][V], dot = 0.0f;
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int u = t + k * p.team;
-        const bool on = live && u < p.units;
+        const bool on = now.mask && t + k * p.team < p.units;
         float g[V];
-        widen<T, V>(rx[k], xh[k]);
-        widen<T, V>(rg[k], g);
-        if (u < p.units) weights<V>(p, c0 + u * V, dn[k]);
+        widen<T, V>(now.x[k], xh[k]);
+        widen<T, V>(now.g[k], g);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           xh[k][i] = on ? xh[k][i] * rstd : 0.0f;
           g[i] = on ? g[i] : 0.0f;
           gw[k][i] = fmaf(g[i], xh[k][i], gw[k][i]);
-          dn[k][i] = on ? dn[k][i] * g[i] : 0.0f;
+          dn[k][i] = w[k][i] * g[i];
           dot = fmaf(dn[k][i], xh[k][i], dot);
         }
       }
@@ -205,11 +245,11 @@ __global__ void __launch_bounds__(NT) rms_norm_grad(RmsParams p) {
         const int u = t + k * p.team;
         if (u >= p.units) break;
         float v[V];
-        if (gt) widen<T, V>(rt[k], v);
+        widen<T, V>(now.t[k], v);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float d = rstd * fmaf(-xh[k][i], dot, dn[k][i]);
-          v[i] = !live ? 0.0f : gt ? v[i] + d : d;
+          v[i] = !now.mask ? 0.0f : p.gt ? v[i] + d : d;
         }
         store<T, V>(gx + u * V, v);
       }
@@ -287,7 +327,7 @@ struct Sharing {
   int residues, used, part_rows;
   int64_t blocks;
 };
-Sharing sharing_of(const e3conv_rms_norm_args& a, const Shape& s) {
+Sharing sharing_of(const e3conv_rms_norm_args& a, const Shape& s, bool back) {
   Sharing h;
   const int size = a.channels / a.groups, teams = NT >> s.team_log2;
   h.residues = a.weight_channels / std::gcd(a.weight_channels, size);
@@ -296,7 +336,7 @@ Sharing sharing_of(const e3conv_rms_norm_args& a, const Shape& s) {
   const int64_t items = a.num_rows * a.groups;
   // work-groups: their teams' number is a multiple of `residues`
   const int whole = h.residues <= teams ? 1 : h.residues / std::gcd(h.residues, teams);
-  int64_t n = std::min<int64_t>((items + h.used - 1) / h.used, 1024);
+  int64_t n = std::min<int64_t>((items + h.used - 1) / h.used, back ? 512 : 2048);
   h.blocks = (std::max<int64_t>(n, 1) + whole - 1) / whole * whole;
   return h;
 }
@@ -305,7 +345,7 @@ size_t workspace_bytes(const e3conv_rms_norm_args& a) {
   // the element-wise form has the most parts a work-group; either may run
   size_t most = 0;
   for (int v : {1, vector_width(a)}) {
-    const Sharing h = sharing_of(a, shape_of(a.channels / a.groups, v));
+    const Sharing h = sharing_of(a, shape_of(a.channels / a.groups, v), true);
     most = std::max(most, (size_t)h.blocks * h.part_rows * (a.channels / a.groups) * sizeof(float));
   }
   return (most + 15) / 16 * 16;
@@ -321,8 +361,7 @@ hipError_t run(const RmsParams& p, bool back, hipStream_t s) {
     hipLaunchKernelGGL(rms_norm_join, dim3((p.a.weight_channels + 15) / 16), dim3(NT), 0, s, p.part, rows,
                        p.residues * p.size, p.a.weight_channels, p.gw);
   } else {
-    const int64_t teams = BIG ? 1 : NT >> p.team_log2;
-    hipLaunchKernelGGL((rms_norm<T, V, U, BIG>), grid_of((p.items + teams - 1) / teams), dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((rms_norm<T, V, U, BIG>), dim3(p.blocks), dim3(NT), 0, s, p);
   }
   return hipGetLastError();
 }
@@ -350,7 +389,7 @@ hipError_t launch(RmsParams p, bool back, bool vec, void* workspace, hipStream_t
   p.by_period = div_by(a.weight_channels);
   p.items = (int)(a.num_rows * a.groups);
   p.vec_weight = reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
-  const Sharing h = sharing_of(a, sh);
+  const Sharing h = sharing_of(a, sh, back);
   p.residues = h.residues;
   p.used = h.used;
   p.blocks = (int)h.blocks;
