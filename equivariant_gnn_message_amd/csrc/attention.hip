@@ -87,6 +87,9 @@ attn::DiffParams diff_params(const e3conv_attention_args& a, const float* lam) {
   attn::DiffParams p{};
   set_params(a, p);
   p.full = 2 * a.dim_qk == a.dim_v && a.dim_v == attn::diff_width(a);
+  const int size = a.dtype == E3CONV_F32 ? 4 : 2;
+  p.vec = p.vec && attn::near_rows(a.q_row, a.q_head, size) && attn::near_rows(a.k_row, a.k_head, size) &&
+          attn::near_rows(a.v_row, a.v_head, size);
   p.lam = lam;
   return p;
 }
@@ -229,7 +232,8 @@ e3conv_status e3conv_diff_attention_backward(const e3conv_attention_args* a, con
   const int size = a->dtype == E3CONV_F32 ? 4 : 2;
   p.vec = p.vec && e3c::vector_rows(out, p.out_row, p.out_head, a->dim_v, size) &&
           e3c::vector_rows(second, p.second_row, p.second_head, a->dim_v, size) &&
-          e3c::vector_rows(grad_out, p.go_row, p.go_head, a->dim_v, size);
+          e3c::vector_rows(grad_out, p.go_row, p.go_head, a->dim_v, size) &&
+          e3c::attn::near_rows(p.go_row, p.go_head, size);
   p.vec_st = std::min({e3c::vector_stores(grad_q, p.gq_row, p.gq_head, a->dim_qk, size),
                        e3c::vector_stores(grad_k, p.gk_row, p.gk_head, a->dim_qk, size),
                        e3c::vector_stores(grad_v, p.gv_row, p.gv_head, a->dim_v, size)});

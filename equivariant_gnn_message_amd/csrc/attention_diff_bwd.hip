@@ -80,7 +80,7 @@ __device__ __forceinline__ void bwd_q(const DiffParams& p, const Where& place, K
   const int k0 = kb + min(split * per, tiles) * TK;
   const int k1 = min(ke, kb + min((split + 1) * per, tiles) * TK);
 
-  Keys<T, D, TK, 64 * RW, LOAD, 2> keys;
+  DiffKeys<T, D, TK, 64 * RW, LOAD> keys;
   keys.begin(p, c, k0, k1);
   keys.pair.clear(a.dim_qk, a.dim_v, first.k, first.v);
   if (BUF == 2) keys.pair.clear(a.dim_qk, a.dim_v, second.k, second.v);
@@ -140,29 +140,29 @@ __device__ __forceinline__ void bwd_q(const DiffParams& p, const Where& place, K
             if (i & 1) dp = mma(y, go[j], dp);
             else s[j / KS] = mma(y, q[j / KS][j % KS], s[j / KS]);
           });
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[0][i] = __builtin_amdgcn_exp2f(fmaf(s[0][i], p.c, -lse[0])) * (dp[i] - delta0);
-        const float p1 = __builtin_amdgcn_exp2f(fmaf(s[1][i], p.c, -lse[1])), less = dp[i] - delta1;
-        lam_sum = fmaf(p1, less, lam_sum);     // explicit: every form of the loads gives the same bits
-        s[1][i] = p1 * less;
-      }
+      // the first operands of K come while dS is formed
+      Ahead<D / 16, W, Frag<P>> keys_of;
+      const auto load = [&](int i) { return kt.columns(32 * b + 16 * (i / (D / 32)), i % (D / 32), lane); };
+      keys_of.start(load);
+      Frag<P> f[2][2];   // bf16: dS rounded for its product
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        Frag<P> f[2];   // bf16: dS rounded for its product
+        float e[2][8];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float e[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = s[x][8 * t + i];
-          to_frag(e, f[x]);
+        for (int i = 0; i < 8; ++i) {
+          const int y = 8 * t + i;
+          e[0][i] = __builtin_amdgcn_exp2f(fmaf(s[0][y], p.c, -lse[0])) * (dp[y] - delta0);
+          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[1][y], p.c, -lse[1])), less = dp[y] - delta1;
+          lam_sum = fmaf(p1, less, lam_sum);     // explicit: every form of the loads gives the same bits
+          e[1][i] = p1 * less;
         }
-        ahead<D / 32, W, Frag<P>>([&](int dt) { return kt.columns(32 * b + 16 * t, dt, lane); },
-                                  [&](int dt, const Frag<P>& y) {
-                                    const int x = dt / (D / 64), d = dt % (D / 64);
-                                    dq[x][d] = mma(y, f[x], dq[x][d]);
-                                  });
+        to_frag(e[0], f[0][t]);
+        to_frag(e[1], f[1][t]);
       }
+      keys_of.run(load, [&](int i, const Frag<P>& y) {
+        const int dt = i % (D / 32), x = dt / (D / 64), d = dt % (D / 64);
+        dq[x][d] = mma(y, f[x][i / (D / 32)], dq[x][d]);
+      });
     }
   };
   if constexpr (BUF == 2) walk<2, TK>(k0, k1, first, second, use);
@@ -182,7 +182,10 @@ __device__ __forceinline__ void bwd_q(const DiffParams& p, const Where& place, K
   }
 }
 
-template <class T, int D, int RW, int TQ, int BUF, int LOAD, bool OWN>
+// What a work-group forms of its keys: both gradients, or one of them (the products with q, and the exponentials,
+// are then formed twice).
+enum Role { kBothGrads, kGradK, kGradV };
+template <class T, int D, int RW, int TQ, int BUF, int LOAD, bool OWN, Role ROLE>
 __device__ __forceinline__ void bwd_kv(const DiffParams& p, const Where& place, RowBuffer<T, D, TQ>& first,
                                        RowBuffer<T, D, TQ>& second) {
   typedef RowBuffer<T, D, TQ> Buffer;
@@ -225,7 +228,7 @@ __device__ __forceinline__ void bwd_kv(const DiffParams& p, const Where& place, 
 #pragma unroll
       for (int t = 0; t < KS; ++t) flip_sign(k[x][t]);
   }
-  row_operand<T, D, LOAD>((const T*)a.v + jr * a.v_row + c * a.v_head, a.dim_v, live, v);
+  if (ROLE != kGradV) row_operand<T, D, LOAD>((const T*)a.v + jr * a.v_row + c * a.v_head, a.dim_v, live, v);
 
   f32x16 dk[2][D / 64], dv[D / 32];
 #pragma unroll
@@ -245,15 +248,21 @@ __device__ __forceinline__ void bwd_kv(const DiffParams& p, const Where& place, 
     for (int b = 0; b < TQ / 32; ++b) {
       if (b > 0 && from + 32 * b >= r1) break;
       // dP - delta1 from the start: the rows' -delta1 are the accumulator's first values
-      f32x16 s[2], dp = by_row(now.values[kDelta] + 32 * b, lane);
+      f32x16 s[2], dp;
       s[0] = s[1] = f32x16{};
-      ahead<2 * VS, W, Frag<P>>(
-          [&](int i) { return i & 1 ? gt.rows(32 * b, i >> 1, lane) : qt.rows(32 * b, i >> 1, lane); },
-          [&](int i, const Frag<P>& y) {
-            const int x = i >> 1;
-            if (i & 1) dp = mma(y, v[x], dp);
-            else s[x / KS] = mma(y, k[x / KS][x % KS], s[x / KS]);
-          });
+      if constexpr (ROLE == kGradV) {
+        ahead<VS, W, Frag<P>>([&](int i) { return qt.rows(32 * b, (i & 1) * KS + (i >> 1), lane); },
+                              [&](int i, const Frag<P>& y) { s[i & 1] = mma(y, k[i & 1][i >> 1], s[i & 1]); });
+      } else {
+        dp = by_row(now.values[kDelta] + 32 * b, lane);
+        ahead<2 * VS, W, Frag<P>>(
+            [&](int i) { return i & 1 ? gt.rows(32 * b, i >> 1, lane) : qt.rows(32 * b, i >> 1, lane); },
+            [&](int i, const Frag<P>& y) {
+              const int x = i >> 1;
+              if (i & 1) dp = mma(y, v[x], dp);
+              else s[x / KS] = mma(y, k[x / KS][x % KS], s[x / KS]);
+            });
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float e[3][8], lse0[8], lse1[8], lam[8], less[8];
@@ -261,27 +270,36 @@ __device__ __forceinline__ void bwd_kv(const DiffParams& p, const Where& place, 
         by_half(now.values[kLse0] + 32 * b, t, lane, lse0);
         by_half(now.values[kLse1] + 32 * b, t, lane, lse1);
         by_half(now.values[kLam] + 32 * b, t, lane, lam);
-        by_half(now.values[kLess] + 32 * b, t, lane, less);
+        if (ROLE != kGradV) by_half(now.values[kLess] + 32 * b, t, lane, less);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int y = 8 * t + i;
           const float p0 = __builtin_amdgcn_exp2f(fmaf(s[0][y], p.c, -lse0[i]));
           const float p1 = __builtin_amdgcn_exp2f(fmaf(s[1][y], p.c, -lse1[i]));
-          e[0][i] = p0 * dp[y];
-          e[1][i] = p1 * lam[i] * (dp[y] + less[i]);
-          e[2][i] = fmaf(p1, lam[i], p0);
+          if (ROLE != kGradV) {
+            e[0][i] = p0 * dp[y];
+            e[1][i] = p1 * lam[i] * (dp[y] + less[i]);
+          }
+          if (ROLE != kGradK) e[2][i] = fmaf(p1, lam[i], p0);
         }
 #pragma unroll
-        for (int x = 0; x < 3; ++x) to_frag(e[x], f[x]);
-        ahead<D / 16, W, Frag<P>>(
-            [&](int i) {
-              return i & 1 ? qt.columns(32 * b + 16 * t, i >> 1, lane) : gt.columns(32 * b + 16 * t, i >> 1, lane);
-            },
-            [&](int i, const Frag<P>& y) {
-              const int dt = i >> 1, x = dt / (D / 64), d = dt % (D / 64);
-              if (i & 1) dk[x][d] = mma(y, f[x], dk[x][d]);
-              else dv[dt] = mma(y, f[2], dv[dt]);
-            });
+        for (int x = 0; x < 3; ++x)
+          if (x < 2 ? ROLE != kGradV : ROLE != kGradK) to_frag(e[x], f[x]);
+        const auto add_k = [&](int dt, const Frag<P>& y) {
+          const int x = dt / (D / 64), d = dt % (D / 64);
+          dk[x][d] = mma(y, f[x], dk[x][d]);
+        };
+        const auto add_v = [&](int dt, const Frag<P>& y) { dv[dt] = mma(y, f[2], dv[dt]); };
+        const auto of_q = [&](int dt) { return qt.columns(32 * b + 16 * t, dt, lane); };
+        const auto of_g = [&](int dt) { return gt.columns(32 * b + 16 * t, dt, lane); };
+        if constexpr (ROLE == kGradK) ahead<D / 32, W, Frag<P>>(of_q, add_k);
+        else if constexpr (ROLE == kGradV) ahead<D / 32, W, Frag<P>>(of_g, add_v);
+        else
+          ahead<D / 16, W, Frag<P>>([&](int i) { return i & 1 ? of_q(i >> 1) : of_g(i >> 1); },
+                                    [&](int i, const Frag<P>& y) {
+                                      if (i & 1) add_k(i >> 1, y);
+                                      else add_v(i >> 1, y);
+                                    });
       }
     }
   };
@@ -293,15 +311,18 @@ __device__ __forceinline__ void bwd_kv(const DiffParams& p, const Where& place, 
     const int width = 2 * a.dim_qk + a.dim_v;
     float* to = p.part_kv + (split * (a.num_k * a.heads_kv) + (long)j * a.heads_kv + c) * width;
     const bool vec = a.dim_qk % 4 == 0 && a.dim_v % 4 == 0;
-    store_row(to, dk[0], a.dim_qk, 1.0f, live, vec);
-    store_row(to + a.dim_qk, dk[1], a.dim_qk, 1.0f, live, vec);
-    store_row(to + 2 * a.dim_qk, dv, a.dim_v, 1.0f, live, vec);
+    if (ROLE != kGradV) {
+      store_row(to, dk[0], a.dim_qk, 1.0f, live, vec);
+      store_row(to + a.dim_qk, dk[1], a.dim_qk, 1.0f, live, vec);
+    }
+    if (ROLE != kGradK) store_row(to + 2 * a.dim_qk, dv, a.dim_v, 1.0f, live, vec);
     return;
   }
+  if (ROLE != kGradV)
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
-    store_row((T*)p.gk + j * p.gk_row + (2 * c + x) * p.gk_head, dk[x], a.dim_qk, a.scale, live, p.vec_st);
-  store_row((T*)p.gv + j * p.gv_row + c * p.gv_head, dv, a.dim_v, 1.0f, live, p.vec_st);
+    for (int x = 0; x < 2; ++x)
+      store_row((T*)p.gk + j * p.gk_row + (2 * c + x) * p.gk_head, dk[x], a.dim_qk, a.scale, live, p.vec_st);
+  if (ROLE != kGradK) store_row((T*)p.gv + j * p.gv_row + c * p.gv_head, dv, a.dim_v, 1.0f, live, p.vec_st);
 }
 
 template <class T, int D, int RW, int TK, int BUF, int LOAD>
@@ -310,17 +331,25 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_q(sizeof(T) == 4
   __shared__ float lam_rows[32 * RW];
   const long b = block_index();
   if (b < p.blocks)
-    bwd_q<T, D, RW, TK, BUF, LOAD>(p, where((int)b, p.blocks, p.slots, p.splits), first, second, lam_rows);
+    bwd_q<T, D, RW, TK, BUF, LOAD>(p, where<kRun>((int)b, p.blocks, p.slots, p.splits), first, second, lam_rows);
 }
 template <class T, int D, int RW, int TQ, int BUF, int LOAD>
 __global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_kv(sizeof(T) == 4, D) : 1) diff_bwd_kv(DiffParams p) {
   __shared__ __attribute__((aligned(16))) RowBuffer<T, D, TQ> first, second;
   const long b = block_index();
-  if (b < p.blocks)
-    bwd_kv<T, D, RW, TQ, BUF, LOAD, false>(p, where((int)b, p.blocks, p.slots_kv, p.splits_kv), first, second);
+  if (b >= p.blocks) return;
+  if constexpr (diff_two_roles(sizeof(T) == 4, D, RW)) {
+    const int n = p.blocks / 2;
+    if (b < n)
+      bwd_kv<T, D, RW, TQ, BUF, LOAD, false, kGradK>(p, where<kRun>((int)b, n, p.slots_kv, p.splits_kv), first, second);
+    else
+      bwd_kv<T, D, RW, TQ, BUF, LOAD, false, kGradV>(p, where<kRun>((int)b - n, n, p.slots_kv, p.splits_kv), first, second);
+  } else {
+    bwd_kv<T, D, RW, TQ, BUF, LOAD, false, kBothGrads>(p, where<kRun>((int)b, p.blocks, p.slots_kv, p.splits_kv), first, second);
+  }
 }
 template <class T, int D, int RW, int ROWS, int BUF, int LOAD>
-__global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_kv(sizeof(T) == 4, D) : 1) diff_bwd_both(DiffParams p) {
+__global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_both(sizeof(T) == 4, D) : 1) diff_bwd_both(DiffParams p) {
   union Buffer {
     KeyBuffer<T, D, ROWS> keys;
     RowBuffer<T, D, ROWS> rows;
@@ -331,10 +360,10 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_kv(sizeof(T) == 
   if (at >= p.blocks) return;
   const int b = (int)at, n = p.first_blocks;
   if (b < n)
-    bwd_q<T, D, RW, ROWS, BUF, LOAD>(p, where(b, n, p.slots, p.splits), first.keys, second.keys, lam_rows);
+    bwd_q<T, D, RW, ROWS, BUF, LOAD>(p, where<kRun>(b, n, p.slots, p.splits), first.keys, second.keys, lam_rows);
   else
-    bwd_kv<T, D, RW, ROWS, BUF, LOAD, true>(p, where(b - n, p.blocks - n, p.slots_kv, p.splits_kv), first.rows,
-                                           second.rows);
+    bwd_kv<T, D, RW, ROWS, BUF, LOAD, true, kBothGrads>(p, where<kRun>(b - n, p.blocks - n, p.slots_kv, p.splits_kv),
+                                                        first.rows, second.rows);
 }
 
 template <class T>
@@ -358,17 +387,27 @@ hipError_t sums(const DiffParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Small graphs leave most of the chip idle, and a launch that adds parts (lambda's) follows in any case: the other axis
+// is split down to its tiles of 32 while all work-groups of both kernels find a place (64 graphs of 64 nodes, fp32:
+// 17.8 -> 14.6 us).
+Shape split_small(Shape s, long others, int graphs, int heads) {
+  const long g = graphs > 0 ? graphs : 1, tiles = ((others + g - 1) / g + 31) / 32;
+  if (s.rw == 1 && s.splits == 1)
+    while (2 * s.splits <= tiles && 2l * s.splits * s.slots * heads <= 512) s.splits *= 2;
+  return s;
+}
 Shape shape_q(const e3conv_attention_args& a) {
   const bool f32 = a.dtype == E3CONV_F32;
   const int width = diff_width(a);
-  return choose(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv, diff_waves_q(f32, width),
-                diff_unit_us(f32, width, true), 2 * a.dim_qk);
+  return split_small(choose(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv, diff_waves_q(f32, width),
+                            diff_unit_us(f32, width, true), 2 * a.dim_qk), a.num_k, a.num_graphs, a.heads_kv);
 }
 Shape shape_kv(const e3conv_attention_args& a) {
   const bool f32 = a.dtype == E3CONV_F32;
   const int width = diff_width(a);
-  return choose(a.num_k, a.num_q * (a.heads_q / a.heads_kv), a.num_graphs, a.heads_kv, diff_waves_kv(f32, width),
-                diff_unit_us(f32, width, true), 2 * a.dim_qk + a.dim_v);
+  const long rows = a.num_q * (a.heads_q / a.heads_kv);
+  return split_small(choose(a.num_k, rows, a.num_graphs, a.heads_kv, diff_waves_kv(f32, width),
+                            diff_unit_us(f32, width, true), 2 * a.dim_qk + a.dim_v), rows, a.num_graphs, a.heads_kv);
 }
 
 // Rows of a tile and buffers: 64 and two where they fit 64 KiB of LDS and the registers.
@@ -387,8 +426,7 @@ void launch(const DiffParams& p, Which which, int rw, hipStream_t s) {
     if (rw == 4) hipLaunchKernelGGL((diff_bwd_q<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((diff_bwd_q<T, D, 1, 32, L::BUF1, LOAD>), grid, dim3(64), 0, s, p);
   } else if (which == kKv) {
-    constexpr int ROWS = sizeof(T) == 2 ? 64 : L::ROWS;
-    if (rw == 4) hipLaunchKernelGGL((diff_bwd_kv<T, D, 4, ROWS, L::BUF4, LOAD>), grid, dim3(256), 0, s, p);
+    if (rw == 4) hipLaunchKernelGGL((diff_bwd_kv<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((diff_bwd_kv<T, D, 1, 32, L::BUF1, LOAD>), grid, dim3(64), 0, s, p);
   } else {
     if (rw == 4) hipLaunchKernelGGL((diff_bwd_both<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid, dim3(256), 0, s, p);
@@ -413,7 +451,7 @@ bool together(const e3conv_attention_args& a, const Shape& q, const Shape& kv) {
   if (q.rw != kv.rw) return false;
   const long blocks = ((long)q.slots * q.splits + (long)kv.slots * kv.splits) * a.heads_kv;
   if (q.rw == 1 && q.splits == 1 && kv.splits == 1) return blocks <= 0x7fffffffL;
-  return blocks <= 256 * (q.rw == 1 ? 4 : diff_waves_kv(a.dtype == E3CONV_F32, diff_width(a)));
+  return blocks <= 256 * (q.rw == 1 ? 4 : diff_waves_both(a.dtype == E3CONV_F32, diff_width(a)));
 }
 
 template <class T>
@@ -424,7 +462,7 @@ hipError_t backward(DiffParams p, const Shape& q, const Shape& kv, hipStream_t s
   p.slots_kv = kv.slots;
   p.splits_kv = kv.splits;
   const long nq = (long)q.slots * q.splits * a.heads_kv, nk = (long)kv.slots * kv.splits * a.heads_kv;
-  if (nq > 0x7fffffffL || nk > 0x7fffffffL) return hipErrorInvalidValue;
+  if (nq > 0x7fffffffL || nk > 0x3fffffffL) return hipErrorInvalidValue;
   if (together(a, q, kv)) {
     p.delta = nullptr;
     p.first_blocks = (int)nq;
@@ -436,7 +474,7 @@ hipError_t backward(DiffParams p, const Shape& q, const Shape& kv, hipStream_t s
       by_width<T>(p, kQ, q.rw, s);
     }
     if (a.num_k > 0) {
-      p.blocks = (int)nk;
+      p.blocks = (int)nk * (diff_two_roles(sizeof(T) == 4, diff_width(a), kv.rw) ? 2 : 1);
       by_width<T>(p, kKv, kv.rw, s);
     }
   }

@@ -259,8 +259,9 @@ __device__ __forceinline__ long block_index() { return (long)blockIdx.y * kAlong
 struct Where {
   int split, slot, c;
 };
+template <int RUN = 32>
 __device__ __forceinline__ Where where(int b, int blocks, int slots, int splits) {
-  constexpr int DIES = 8, RUN = 32;
+  constexpr int DIES = 8;
   const int whole = blocks / (DIES * RUN) * (DIES * RUN);
   if (b < whole) {
     const int r = b % (DIES * RUN);

@@ -889,7 +889,10 @@ def e3conv_diff_attention_backward(q, k, v, lam, out, second, lse, grad_out, q_p
     index, dt, shape = q.get_device(), q.dtype, (args.num_q, args.heads_q, args.dim_v)
     strides = ()
     for t, name in ((out, "out"), (second, "second"), (grad_out, "grad_out")):
-        strides += _rows_of(t, name, dt, index, shape)[:2]
+        row, head, one = t.stride()
+        if one != 1 or t.shape != shape or t.dtype is not dt or t.get_device() != index:
+            _rows_of(t, name, dt, index, shape)      # says what is wrong, if anything
+        strides += (row, head)
     lse_at = _dense(lse, "lse", _torch.float32, index, 2 * shape[0] * shape[1])
     handle, other = _enter(index, stream)
     if other is not None:
