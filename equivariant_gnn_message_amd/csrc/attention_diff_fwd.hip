@@ -86,27 +86,15 @@ __global__ void __launch_bounds__(128 * RB, RB > 1 ? diff_waves_fwd(sizeof(T) ==
     Ahead<D / 16, W, Frag<P>> values;
     const auto load = [&](int i) { return vt.columns(16 * (i / (D / 32)), i % (D / 32), lane); };
     values.start(load);
-    // Exponentials against the maximum so far; only where a row's sum shows that it has grown by much (or no key has
-    // been seen yet) is the tile's maximum taken, o and l scaled to it, and the exponentials formed again: maxima of
-    // every tile were an eighth of the loop's vector instructions.  P and l may grow to kMost.
-    constexpr float kMost = 1024.0f;
-    float e[16], sum;
-    const auto exponentials = [&] {
-      const float base = m == -INFINITY ? 0.0f : m;
-      sum = 0.0f;
+    float top = s[0];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        e[i] = __builtin_amdgcn_exp2f(fmaf(s[i], p.c, -base));
-        sum += e[i];
-      }
-    };
-    exponentials();
-    if (__ballot(!(sum <= kMost) || m == -INFINITY)) {
-      float top = s[0];
-#pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-      top = fmaxf(top, other_half(top)) * p.c;
-      const float mn = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    top = fmaxf(top, other_half(top)) * p.c;
+    // m is the maximum only to within 2^kSlack, so that o and l are scaled again in few tiles
+    constexpr float kSlack = 8.0f;
+    if (__ballot(top > m + kSlack)) {
+      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
+      const float f = __builtin_amdgcn_exp2f(m - base);
       m = mn;
       l *= f;
       over *= f;
@@ -114,15 +102,20 @@ __global__ void __launch_bounds__(128 * RB, RB > 1 ? diff_waves_fwd(sizeof(T) ==
       for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[dt][i] *= f;
-      exponentials();
     }
+    const float base = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
     Frag<P> f[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      float half[8];
+      float e[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) half[i] = e[8 * t + i];
-      to_frag(half, f[t]);      // bf16: P rounded for its product, the sum from the unrounded values
+      for (int i = 0; i < 8; ++i) {
+        e[i] = __builtin_amdgcn_exp2f(fmaf(s[8 * t + i], p.c, -base));
+        sum += e[i];
+      }
+      // bf16: P rounded for its product, the sum from the unrounded values
+      to_frag(e, f[t]);
     }
     values.run(load, [&](int i, const Frag<P>& x) {
       const int dt = i % (D / 32);
