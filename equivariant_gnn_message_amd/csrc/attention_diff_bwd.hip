@@ -5,10 +5,14 @@
 // one product for dP and one for dv serve both maps.  As in the plain attention's reverse pass, two kernels, none
 // with atomics:
 //
-// diff_bwd_q   a wave owns 32 rows and walks over the keys, rows along the columns; it forms the deltas from out
-//              and O2 (delta1 = <grad_out, out> + lambda delta2), and each row's part of dlambda as
-//              delta2 + sum P2 (dP - delta2) with the unrounded P2: what O2 lost to the rounding of P2 and of its
-//              own storage is in the sum (with bf16 the deltas alone are off by about 2^-9);
+// diff_bwd_q   a wave owns 32 rows (of one map with bf16: its sums and operands leave two waves a SIMD) and walks over
+//              the keys, rows along the columns.  It starts from deltas of out and O2 (delta1 = <grad_out, out> +
+//              lambda delta2), which are off by the rounding of out and O2: where v and grad_out have means by
+//              2^-9 of delta with bf16, and dq, a sum over keys whose dS cancel, by that times sum_j P k_j (a
+//              hundredth of dq for 20 000 keys).  So it also sums r_m = sum_j P_m (dP - delta_m), which a true
+//              delta makes 0, and B_m = sum_j P_m k_m by one product more for each operand of K, and takes
+//                dq_m = scale (sum dS_m k_m - r_m B_m),   delta_m + r_m for diff_bwd_kv,
+//                dlambda = -sum over the rows of delta2 + r_2;
 // diff_bwd_kv  a wave owns 32 keys and walks over the rows of all query heads that share its kv head.
 // Where the work-groups are few both run in one launch (diff_bwd_both), the second forming the deltas itself.
 #include "attention_diff_tile.h"
@@ -32,17 +36,23 @@ struct RowBuffer {
 };
 
 // Sums of the rows' values for each of the query heads that share kv head c; all threads of the work-group
-// come here.  Row i of the work-group's rows is head (r0 + i) % group.
-template <int BM>
-__device__ __forceinline__ void sum_lam(const DiffParams& p, float* rows, float value, int r0, float* to) {
-  if ((threadIdx.x & 32) == 0) rows[(threadIdx.x >> 6) * 32 + (threadIdx.x & 31)] = value;
+// come here.  Row i of the work-group's rows is head (r0 + i) % group; `block` is this wave's, or -1.
+template <int BM, int NT>
+__device__ __forceinline__ void sum_lam(const DiffParams& p, float* rows, float value, int block, int r0, float* to) {
+  if (block >= 0 && (threadIdx.x & 32) == 0) rows[block * 32 + (threadIdx.x & 31)] = value;
   __syncthreads();
   const int first = r0 - query_of(p, r0) * p.group;
-  for (int x = threadIdx.x; x < p.group; x += 2 * BM) {
+  for (int x = threadIdx.x; x < p.group; x += NT) {
     float v = 0.0f;
     for (int i = x >= first ? x - first : x - first + p.group; i < BM; i += p.group) v += rows[i];
     to[x] = v;
   }
+}
+
+// Of P for B alone: its leading part is enough (B is multiplied by r, a rounding error).
+template <int P>
+__device__ __forceinline__ f32x16 mma_leading(const Frag<P>& a, const Frag<1>& b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
 }
 
 template <class T, int D, int RW, int TK, int BUF, int LOAD>
@@ -51,11 +61,13 @@ __device__ __forceinline__ void bwd_q(const DiffParams& p, const Where& place, K
   typedef KeyBuffer<T, D, TK> Buffer;
   static_assert(BUF == 2 || !(sizeof(T) == 2 && LOAD != kElements), "loads straight to LDS need the other buffer");
   constexpr int P = planes<T>(), KS = D / 32, VS = D / 16, W = P == 1 ? 4 : 2;   // W: operands read ahead
+  constexpr int NM = diff_maps(P == 3, D, RW), DT = D / 64;
   const e3conv_attention_args& a = p.a;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
+  const int map0 = NM == 1 ? w & 1 : 0, block = NM == 1 ? w >> 1 : w;
 
   const int split = place.split, slot = place.slot, c = place.c;
-  constexpr int BM = 32 * RW;
+  constexpr int BM = 32 * RW * NM / 2;
   const int g = graph_of_slot(a.q_ptr, a.num_graphs, a.num_q, p.group, BM, slot);
   const int q0 = offset(a.q_ptr, g, a.num_q);
   const int nrows = (offset(a.q_ptr, g + 1, a.num_q) - q0) * p.group;
@@ -66,14 +78,13 @@ __device__ __forceinline__ void bwd_q(const DiffParams& p, const Where& place, K
     return;
   }
 
-  const int r = r0 + 32 * w + n;
-  const bool row = r < nrows, idle = r0 + 32 * w >= nrows;   // idle: a wave without rows only loads
+  const int r = r0 + 32 * block + n;
+  const bool row = r < nrows, idle = r0 + 32 * block >= nrows;   // idle: a wave without rows only loads
   const int qi = q0 + (row ? query_of(p, r) : 0), head = c * p.group + (row ? r - (qi - q0) * p.group : 0);
   const long at = (long)qi * a.heads_q + head;
   const float2 both = reinterpret_cast<const float2*>(p.lse)[at];
   const float lam = p.lam[head];
   const bool live = row && (!a.q_mask || a.q_mask[qi]) && both.x != -INFINITY;
-  const float lse[2] = {live ? both.x * kLog2e : 0.0f, live ? both.y * kLog2e : 0.0f};
 
   const int kb = offset(a.k_ptr, g, a.num_k), ke = offset(a.k_ptr, g + 1, a.num_k);
   const int tiles = ke > kb ? (ke - kb + TK - 1) / TK : 0, per = (tiles + p.splits - 1) / p.splits;
@@ -86,13 +97,13 @@ __device__ __forceinline__ void bwd_q(const DiffParams& p, const Where& place, K
   if (BUF == 2) keys.pair.clear(a.dim_qk, a.dim_v, second.k, second.v);
   if (k0 < k1) keys.issue(p, first.k, first.v);
 
-  Frag<P> q[2][KS], go[VS];
+  Frag<P> q[NM][KS], go[VS];
   const T* gp = (const T*)p.go + qi * p.go_row + head * p.go_head;
   const T* op = (const T*)p.out + qi * p.out_row + head * p.out_head;
   const T* sp = (const T*)p.second + qi * p.second_row + head * p.second_head;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    row_operand<T, D / 2, LOAD>((const T*)a.q + qi * a.q_row + (2 * head + x) * a.q_head, a.dim_qk, live, q[x]);
+  for (int x = 0; x < NM; ++x) {
+    row_operand<T, D / 2, LOAD>((const T*)a.q + qi * a.q_row + (2 * head + map0 + x) * a.q_head, a.dim_qk, live, q[x]);
     if (p.negate)
 #pragma unroll
       for (int t = 0; t < KS; ++t) flip_sign(q[x][t]);
@@ -113,12 +124,19 @@ __device__ __forceinline__ void bwd_q(const DiffParams& p, const Where& place, K
   }
   delta1 = live ? delta1 + other_half(delta1) : 0.0f;
   delta0 = live ? fmaf(lam, delta1, delta0 + other_half(delta0)) : 0.0f;
-  if (p.delta && row && h == 0 && split == 0) reinterpret_cast<float2*>(p.delta)[at] = make_float2(delta0, delta1);
-
-  f32x16 dq[2][D / 64];
+  float lse[NM], delta[NM], rest[NM];
 #pragma unroll
-  for (int dt = 0; dt < D / 64; ++dt) dq[0][dt] = dq[1][dt] = f32x16{};
-  float lam_sum = 0.0f;
+  for (int x = 0; x < NM; ++x) {
+    lse[x] = !live ? 0.0f : (map0 + x == 0 ? both.x : both.y) * kLog2e;
+    delta[x] = map0 + x == 0 ? delta0 : delta1;
+    rest[x] = 0.0f;
+  }
+
+  f32x16 dq[NM][DT], bar[NM][DT];
+#pragma unroll
+  for (int x = 0; x < NM; ++x)
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) dq[x][dt] = bar[x][dt] = f32x16{};
 
   const auto use = [&](Buffer& now, int from, Buffer& next) {
     Tile<P, TK, D>&kt = now.k, &vt = now.v;
@@ -131,54 +149,80 @@ __device__ __forceinline__ void bwd_q(const DiffParams& p, const Where& place, K
 #pragma unroll
     for (int b = 0; b < TK / 32; ++b) {
       if (b > 0 && from + 32 * b >= k1) break;
-      f32x16 s[2], dp = f32x16{};
-      s[0] = s[1] = by_row(now.bias + 32 * b, lane);
-      ahead<2 * VS, W, Frag<P>>(
-          [&](int i) { return i & 1 ? vt.rows(32 * b, i >> 1, lane) : kt.rows(32 * b, i >> 1, lane); },
+      f32x16 s[NM], dp = f32x16{};
+      s[0] = by_row(now.bias + 32 * b, lane);
+      if (NM == 2) s[NM - 1] = s[0];
+      // operands of K and V in turn; with one map K has half as many
+      constexpr int N = NM == 2 ? 2 * VS : VS + KS;
+      const auto is_v = [](int i) { return NM == 2 ? i & 1 : i % 3 > 0; };
+      const auto index = [](int i) { return NM == 2 ? i >> 1 : i % 3 > 0 ? i / 3 * 2 + i % 3 - 1 : i / 3; };
+      ahead<N, W, Frag<P>>(
+          [&](int i) {
+            return is_v(i) ? vt.rows(32 * b, index(i), lane) : kt.rows(32 * b, map0 * KS + index(i), lane);
+          },
           [&](int i, const Frag<P>& y) {
-            const int j = i >> 1;
-            if (i & 1) dp = mma(y, go[j], dp);
+            const int j = index(i);
+            if (is_v(i)) dp = mma(y, go[j], dp);
             else s[j / KS] = mma(y, q[j / KS][j % KS], s[j / KS]);
           });
       // the first operands of K come while dS is formed
-      Ahead<D / 16, W, Frag<P>> keys_of;
-      const auto load = [&](int i) { return kt.columns(32 * b + 16 * (i / (D / 32)), i % (D / 32), lane); };
+      Ahead<2 * NM * DT, W, Frag<P>> keys_of;
+      const auto load = [&](int i) {
+        return kt.columns(32 * b + 16 * (i / (NM * DT)), map0 * DT + i % (NM * DT), lane);
+      };
       keys_of.start(load);
-      Frag<P> f[2][2];   // bf16: dS rounded for its product
+      Frag<P> f[NM][2];   // bf16: dS rounded for its product
+      Frag<1> prob[NM][2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float e[2][8];
+      for (int x = 0; x < NM; ++x)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int y = 8 * t + i;
-          e[0][i] = __builtin_amdgcn_exp2f(fmaf(s[0][y], p.c, -lse[0])) * (dp[y] - delta0);
-          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[1][y], p.c, -lse[1])), less = dp[y] - delta1;
-          lam_sum = fmaf(p1, less, lam_sum);     // explicit: every form of the loads gives the same bits
-          e[1][i] = p1 * less;
+        for (int t = 0; t < 2; ++t) {
+          float e[8], pr[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int y = 8 * t + i;
+            pr[i] = __builtin_amdgcn_exp2f(fmaf(s[x][y], p.c, -lse[x]));
+            const float less = dp[y] - delta[x];
+            rest[x] = fmaf(pr[i], less, rest[x]);     // explicit: every form of the loads gives the same bits
+            e[i] = pr[i] * less;
+          }
+          to_frag(e, f[x][t]);
+          to_frag(pr, prob[x][t]);
         }
-        to_frag(e[0], f[0][t]);
-        to_frag(e[1], f[1][t]);
-      }
       keys_of.run(load, [&](int i, const Frag<P>& y) {
-        const int dt = i % (D / 32), x = dt / (D / 64), d = dt % (D / 64);
-        dq[x][d] = mma(y, f[x][i / (D / 32)], dq[x][d]);
+        const int t = i / (NM * DT), dt = i % (NM * DT), x = dt / DT, d = dt % DT;
+        dq[x][d] = mma(y, f[x][t], dq[x][d]);
+        bar[x][d] = mma_leading(y, prob[x][t], bar[x][d]);
       });
     }
   };
   if constexpr (BUF == 2) walk<2, TK>(k0, k1, first, second, use);
   else walk<1, TK>(k0, k1, first, first, use);
 
-  lam_sum += other_half(lam_sum);
-  sum_lam<BM>(p, lam_rows, live ? (split == 0 ? delta1 + lam_sum : lam_sum) : 0.0f, r0, lam_to);
+#pragma unroll
+  for (int x = 0; x < NM; ++x) rest[x] += other_half(rest[x]);
+  const float of_lam = split == 0 ? delta[NM - 1] + rest[NM - 1] : rest[NM - 1];
+  sum_lam<BM, 64 * RW>(p, lam_rows, live ? of_lam : 0.0f, map0 + NM == 2 ? block : -1, r0, lam_to);
   if (!row) return;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const float factor = x == 0 ? 1.0f : -lam;      // dS2 without its -lambda above
-    if (p.splits > 1)
-      store_row(p.part + ((split * (a.num_q * a.heads_q) + at) * 2 + x) * a.dim_qk, dq[x], a.dim_qk, factor, live,
-                a.dim_qk % 4 == 0);
-    else
-      store_row((T*)p.gq + qi * p.gq_row + (2 * head + x) * p.gq_head, dq[x], a.dim_qk, a.scale * factor, live, p.vec_st);
+  for (int x = 0; x < NM; ++x) {
+    const int m = map0 + x;
+    const float factor = m == 0 ? 1.0f : -lam;      // dS2 without its -lambda above
+    // a split's r is not the row's: the join takes the row's off, and the deltas stay as they were given
+    if (p.delta && h == 0 && split == 0) p.delta[2 * at + m] = p.splits > 1 || !live ? delta[x] : delta[x] + rest[x];
+    if (p.splits > 1) {
+      const long i = (split * (a.num_q * a.heads_q) + at) * 2 + m;
+      float* to = p.part + i * 2 * a.dim_qk;
+      store_row(to, dq[x], a.dim_qk, factor, live, a.dim_qk % 4 == 0);
+      store_row(to + a.dim_qk, bar[x], a.dim_qk, factor, live, a.dim_qk % 4 == 0);
+      if (h == 0) p.part_rest[i] = live ? rest[x] : 0.0f;
+    } else {
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dq[x][dt][i] = fmaf(-rest[x], bar[x][dt][i], dq[x][dt][i]);
+      store_row((T*)p.gq + qi * p.gq_row + (2 * head + m) * p.gq_head, dq[x], a.dim_qk, a.scale * factor, live, p.vec_st);
+    }
   }
 }
 
@@ -371,7 +415,8 @@ hipError_t sums(const DiffParams& p, hipStream_t s) {
   const e3conv_attention_args& a = p.a;
   const long nq = a.num_q * a.heads_q, nk = a.num_k * a.heads_kv;
   const int width = 2 * a.dim_qk + a.dim_v;
-  Sums all{{sum_of(p.part, nq, 2 * a.dim_qk, 0, 2 * a.dim_qk, 2, a.heads_q, p.splits, a.scale, p.gq, p.gq_row, p.gq_head),
+  Sums all{{sum_of(p.part, 2 * nq, 2 * a.dim_qk, 0, a.dim_qk, 1, 2 * a.heads_q, p.splits, a.scale, p.gq, p.gq_row,
+                   p.gq_head, p.part_rest),
             sum_of(p.part_kv, nk, width, 0, 2 * a.dim_qk, 2, a.heads_kv, p.splits_kv, a.scale, p.gk, p.gk_row, p.gk_head),
             sum_of(p.part_kv, nk, width, 2 * a.dim_qk, a.dim_v, 1, a.heads_kv, p.splits_kv, 1.0f, p.gv, p.gv_row,
                    p.gv_head)}};
@@ -398,9 +443,9 @@ Shape split_small(Shape s, long others, int graphs, int heads) {
 }
 Shape shape_q(const e3conv_attention_args& a) {
   const bool f32 = a.dtype == E3CONV_F32;
-  const int width = diff_width(a);
+  const int width = diff_width(a), wide = 2 * diff_maps(f32, width, 4);    // blocks of 32 rows of four waves
   return split_small(choose(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv, diff_waves_q(f32, width),
-                            diff_unit_us(f32, width, true), 2 * a.dim_qk), a.num_k, a.num_graphs, a.heads_kv);
+                            diff_unit_us(f32, width, true) * wide / 4, 4 * a.dim_qk, wide), a.num_k, a.num_graphs, a.heads_kv);
 }
 Shape shape_kv(const e3conv_attention_args& a) {
   const bool f32 = a.dtype == E3CONV_F32;
@@ -416,6 +461,7 @@ struct Tiling {
   static constexpr int ROWS = D == 128 ? 32 : 64;
   static constexpr int BUF4 = 2 * ROWS * planes<T>() * D * 2 * 2 <= 65536 ? 2 : 1;
   static constexpr int BUF1 = sizeof(T) == 2 && LOAD != kElements ? 2 : 1;
+  static constexpr int LEAST = diff_maps(sizeof(T) == 4, D, 2) == 1 ? 2 : 1;   // waves of 32 rows
 };
 enum Which { kQ, kKv, kBoth };
 template <class T, int D, int LOAD>
@@ -424,13 +470,14 @@ void launch(const DiffParams& p, Which which, int rw, hipStream_t s) {
   const dim3 grid = grid_of(p.blocks);
   if (which == kQ) {
     if (rw == 4) hipLaunchKernelGGL((diff_bwd_q<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((diff_bwd_q<T, D, 1, 32, L::BUF1, LOAD>), grid, dim3(64), 0, s, p);
+    else hipLaunchKernelGGL((diff_bwd_q<T, D, L::LEAST, 32, L::BUF1, LOAD>), grid, dim3(64 * L::LEAST), 0, s, p);
   } else if (which == kKv) {
     if (rw == 4) hipLaunchKernelGGL((diff_bwd_kv<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((diff_bwd_kv<T, D, 1, 32, L::BUF1, LOAD>), grid, dim3(64), 0, s, p);
   } else {
     if (rw == 4) hipLaunchKernelGGL((diff_bwd_both<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((diff_bwd_both<T, D, 1, 32, L::BUF1, LOAD>), grid, dim3(64), 0, s, p);
+    else if constexpr (L::LEAST == 1)
+      hipLaunchKernelGGL((diff_bwd_both<T, D, 1, 32, L::BUF1, LOAD>), grid, dim3(64), 0, s, p);
   }
 }
 template <class T, int D>
@@ -448,7 +495,8 @@ void by_width(const DiffParams& p, Which which, int rw, hipStream_t s) {
 // Whether both kernels go in one launch: work-groups of one size, and either of one wave without
 // splits (small graphs), or not more of them than places.
 bool together(const e3conv_attention_args& a, const Shape& q, const Shape& kv) {
-  if (q.rw != kv.rw) return false;
+  if ((q.rw == 1) != (kv.rw == 1)) return false;
+  if (q.rw == 1 && diff_maps(a.dtype == E3CONV_F32, diff_width(a), 2) == 1) return false;
   const long blocks = ((long)q.slots * q.splits + (long)kv.slots * kv.splits) * a.heads_kv;
   if (q.rw == 1 && q.splits == 1 && kv.splits == 1) return blocks <= 0x7fffffffL;
   return blocks <= 256 * (q.rw == 1 ? 4 : diff_waves_both(a.dtype == E3CONV_F32, diff_width(a)));
@@ -467,11 +515,11 @@ hipError_t backward(DiffParams p, const Shape& q, const Shape& kv, hipStream_t s
     p.delta = nullptr;
     p.first_blocks = (int)nq;
     p.blocks = (int)(nq + nk);
-    by_width<T>(p, kBoth, q.rw, s);
+    by_width<T>(p, kBoth, kv.rw, s);
   } else {
     if (a.num_q > 0) {
       p.blocks = (int)nq;
-      by_width<T>(p, kQ, q.rw, s);
+      by_width<T>(p, kQ, q.rw == 1 ? 1 : 4, s);
     }
     if (a.num_k > 0) {
       p.blocks = (int)nk * (diff_two_roles(sizeof(T) == 4, diff_width(a), kv.rw) ? 2 : 1);
@@ -484,12 +532,13 @@ hipError_t backward(DiffParams p, const Shape& q, const Shape& kv, hipStream_t s
 
 // Floats of the workspace: the deltas (where the kernels are two), the partial results, and lambda's.
 struct Space {
-  size_t delta, q, kv, lam;
+  size_t delta, q, rest, kv, lam;
 };
 Space space(const e3conv_attention_args& a, const Shape& q, const Shape& kv) {
   const size_t nq = (size_t)a.num_q * a.heads_q, nk = (size_t)a.num_k * a.heads_kv;
   const auto aligned = [](size_t n) { return (n + 3) / 4 * 4; };
-  return {together(a, q, kv) ? 0 : aligned(2 * nq), q.splits > 1 ? aligned(q.splits * nq * 2 * a.dim_qk) : 0,
+  return {together(a, q, kv) ? 0 : aligned(2 * nq), q.splits > 1 ? aligned(q.splits * nq * 4 * a.dim_qk) : 0,
+          q.splits > 1 ? aligned(q.splits * nq * 2) : 0,
           kv.splits > 1 ? aligned(kv.splits * nk * (2 * a.dim_qk + a.dim_v)) : 0,
           aligned((size_t)q.slots * q.splits * a.heads_q)};
 }
@@ -498,7 +547,7 @@ Space space(const e3conv_attention_args& a, const Shape& q, const Shape& kv) {
 
 size_t diff_backward_workspace(const e3conv_attention_args& a) {
   const Space n = space(a, shape_q(a), shape_kv(a));
-  return (n.delta + n.q + n.kv + n.lam) * sizeof(float);
+  return (n.delta + n.q + n.rest + n.kv + n.lam) * sizeof(float);
 }
 
 hipError_t launch_diff_backward(const DiffParams& given, hipStream_t s) {
@@ -506,7 +555,8 @@ hipError_t launch_diff_backward(const DiffParams& given, hipStream_t s) {
   const Shape q = shape_q(p.a), kv = shape_kv(p.a);
   const Space n = space(p.a, q, kv);
   p.part = p.delta + n.delta;
-  p.part_kv = p.part + n.q;
+  p.part_rest = p.part + n.q;
+  p.part_kv = p.part_rest + n.rest;
   p.part_lam = p.part_kv + n.kv;
   return p.a.dtype == E3CONV_F32 ? backward<float>(p, q, kv, s) : backward<__bf16>(p, q, kv, s);
 }

@@ -14,6 +14,7 @@ struct DiffParams : Params {
   void* second;                    // the second map's result, or NULL
   long second_row, second_head;
   float* glam;                     // (heads_q)
+  float* part_rest;                // (splits, num_q, heads_q, 2): r of the splits
   float* part_lam;                 // (splits slots, heads_q), their sum is -glam
 };
 
@@ -244,6 +245,9 @@ constexpr int diff_waves_fwd(bool f32) { return f32 ? 2 : 3; }
 constexpr int diff_waves_q(bool f32, int d) { return f32 ? 1 : 2; }
 constexpr int diff_waves_kv(bool f32, int d) { return f32 ? 1 : 2; }
 constexpr int diff_waves_both(bool f32, int d) { return f32 || d == 128 ? 1 : 2; }
+// Maps of a wave of diff_bwd_q: with one, two waves share 32 rows.  Sums and operands of two maps do not fit the
+// registers of two waves a SIMD with bf16, nor those of one with fp32 and 128 dimensions.
+constexpr int diff_maps(bool f32, int d, int rw) { return rw > 1 && (f32 ? d == 128 : rw == 4) ? 1 : 2; }
 // Whether work-groups of four waves form grad_k or grad_v, not both.
 constexpr bool diff_two_roles(bool f32, int d, int rw) { return !f32 && d == 128 && rw == 4; }
 

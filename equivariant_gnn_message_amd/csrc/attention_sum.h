@@ -19,6 +19,7 @@ struct Sum {
   float factor;
   void* out;
   long out_row, out_head;
+  const float* rest;    // or NULL: (splits, rows), whose sum times that of the elements `dim` on is taken off
 };
 struct Sums {
   Sum of[3];
@@ -51,29 +52,41 @@ __global__ void __launch_bounds__(256) attn_sum(Sums all) {
   const int d = (int)(i - at * m.dim);
   const float* q = m.part + at * m.width + m.from + d;
   const long step = m.rows * m.width;
-  float v = 0.0f;
+  float v = 0.0f, bar = 0.0f, rest = 0.0f;
   if (at < m.rows) {
-    if (wide) {
-#pragma unroll 4
-      for (int s = 0; s < m.splits; ++s) v += q[s * step];
-    } else {
-      int s = w;
-      for (; s + 28 < m.splits; s += 32) {
-        float x[8];
+    int s = wide ? 0 : w;
+    const int by = wide ? 1 : 4;
+    for (; s + 7 * by < m.splits; s += 8 * by) {
+      float x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = q[(s + 4 * k) * step];
+      for (int k = 0; k < 8; ++k) x[k] = q[(s + k * by) * step];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v += x[k];
-      }
-      for (; s < m.splits; s += 4) v += q[s * step];
+      for (int k = 0; k < 8; ++k) v += x[k];
     }
+    for (; s < m.splits; s += by) v += q[s * step];
+    if (m.rest)
+#pragma unroll 4
+      for (s = wide ? 0 : w; s < m.splits; s += by) {
+        bar += q[s * step + m.dim];
+        rest += m.rest[s * m.rows + at];
+      }
   }
   if (!wide) {
-    red[w][lane] = v;
-    __syncthreads();
+    const auto all = [&](float x) {
+      red[w][lane] = x;
+      __syncthreads();
+      x = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+      __syncthreads();
+      return x;
+    };
+    v = all(v);
+    if (m.rest) {
+      bar = all(bar);
+      rest = all(rest);
+    }
     if (w > 0) return;
-    v = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
   }
+  if (m.rest) v = fmaf(-rest, bar, v);
   if (at < m.rows) {
     const int second = m.maps == 2 && d >= m.dim / 2;
     ((T*)m.out)[at / m.heads * m.out_row + (at % m.heads * m.maps + second) * m.out_head + d - second * (m.dim / 2)] =
@@ -83,8 +96,8 @@ __global__ void __launch_bounds__(256) attn_sum(Sums all) {
 
 // The sums that a gradient's splits ask for; none (blocks 0) where there is one split.
 Sum sum_of(const float* part, long rows, int width, int from, int dim, int maps, int heads, int splits, float factor,
-           void* out, long row, long head) {
-  Sum m{part, rows, width, from, dim, maps, heads, splits, splits <= 8 ? 256 : 64, 0, factor, out, row, head};
+           void* out, long row, long head, const float* rest = nullptr) {
+  Sum m{part, rows, width, from, dim, maps, heads, splits, splits <= 8 ? 256 : 64, 0, factor, out, row, head, rest};
   if (splits > 1) m.blocks = (rows * dim + m.each - 1) / m.each;
   return m;
 }

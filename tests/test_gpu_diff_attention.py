@@ -76,6 +76,67 @@ def test_cross_attention(dtype, lens_q, lens_k):
         check(dtype, *draw(7, dtype, lens_q, lens_k, *heads, d, dv), lens_q, lens_k)
 
 
+def means_bound(q, k, v, lam, g, scale, u, r, out, second):
+    """dq of one graph (heads of q and k alike) in 64 bits from out and second as given, and how far it may be off.
+
+    Roundings of the keys are independent, so a sum of n of them is within four times the root of their squares:
+    dS by r; P by its logits' rounding and dP by its dot product's, 4 sqrt(dims) u of their magnitudes; the running
+    sum by u of its size in every step.  The row's own errors scale dq: lse's and the result's rounding.  What
+    the deltas of out and second are off is taken off again, up to B's rounding, by 2^-8 whatever the type, and
+    to the rounding of r's sum; it does not stand here times B itself.
+    """
+    want, tol = np.zeros_like(q), np.zeros_like(q)
+    n, dims = len(k), 4 * np.sqrt(max(q.shape[2], v.shape[2]))
+    for h in range(len(lam)):
+        dp = g[:, h] @ v[:, h].T
+        size = np.abs(g[:, h]) @ np.abs(v[:, h]).T
+        d1 = (g[:, h] * second[:, h]).sum(1, keepdims=True)
+        d0 = (g[:, h] * out[:, h]).sum(1, keepdims=True) + lam[h] * d1
+        for m, given, f in ((0, d0, 1.0), (1, d1, -lam[h])):
+            qh, kh = q[:, 2 * h + m], k[:, 2 * h + m]
+            s = scale * qh @ kh.T
+            top = s.max(1, keepdims=True)
+            lse = top + np.log(np.exp(s - top).sum(1, keepdims=True))
+            p = np.exp(s - lse)
+            delta = (p * dp).sum(1, keepdims=True)
+            ds = p * (dp - delta)
+            a = abs(scale * f)
+            want[:, 2 * h + m] = scale * f * ds @ kh
+            logit = u * (dims * scale * (np.abs(qh) @ np.abs(kh).T) + 4 * np.abs(s) + 4 * np.abs(top) + 8)
+            each = (r + logit) * np.abs(ds) + p * u * (dims * size + 4 * (np.abs(dp) + np.abs(delta)))
+            row = logit.max(1, keepdims=True) + 4 * u * (np.abs(lse) + np.sqrt(n))
+            sums = 4 * np.sqrt(n) * u * 4 * np.sqrt(ds ** 2 @ kh ** 2)
+            rest = np.abs(given - delta)
+            left = (4 * np.sqrt(n) * u * (p * np.abs(dp - given)).sum(1, keepdims=True) * np.abs(p @ kh)
+                    + rest * 4 * 2.0 ** -8 * np.sqrt(p ** 2 @ kh ** 2) + rest * (4 * np.sqrt(n) + 8) * u * (p @ np.abs(kh)))
+            tol[:, 2 * h + m] = a * (4 * np.sqrt(each ** 2 @ kh ** 2) + sums + left) \
+                + (r + row) * np.abs(want[:, 2 * h + m])
+    return want, tol
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,keys,heads,d,dv", [(2500, 2500, 2, 32, 64), (2500, 2500, 1, 64, 128), (3, 20011, 2, 64, 128),
+                                                  (70, 3001, 2, 33, 40), (50, 900, 1, 16, 32)])
+def test_gradient_of_q_where_v_has_a_mean(dtype, rows, keys, heads, d, dv):
+    """Long graphs, v and grad_out of mean 2: what out and second lose in their roundings is off delta by a multiple of
+    what the keys' own terms differ by, and is not in grad_q."""
+    import torch
+    gen = torch.Generator().manual_seed(rows + d)
+    q, k, v, g = [(mean + torch.randn(s, generator=gen)).to(dtype_of(dtype)).cuda() for mean, s in (
+        (0.0, (rows, 2 * heads, d)), (0.0, (keys, 2 * heads, d)), (2.0, (keys, heads, dv)), (2.0, (rows, heads, dv)))]
+    lam = torch.linspace(0.3, 0.8, heads).cuda()
+    qp, kp = dev(ptr([rows])), dev(ptr([keys]))
+    say(f"[diff means] {dtype} {rows} x {keys} heads {heads} {d} {dv}")
+    out, second, lse = E.e3conv_diff_attention(q, k, v, lam, qp, kp)
+    grads = E.e3conv_diff_attention_backward(q, k, v, lam, out, second, lse, g, qp, kp)
+    torch.cuda.synchronize()
+    u, r = U[dtype]
+    want, tol = means_bound(*map(host, (q, k, v, lam, g)), float(np.float32(d ** -0.5)), u, r, host(out), host(second))
+    off = np.abs(host(grads[0]) - want)
+    worst = float(np.max(off / tol))
+    say(f"  dq: max err {off.max():.3e}, {worst:.2f} of its bound")
+    assert worst <= 1.0
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_long_axis_of_few_rows(dtype):
     """One query over many keys, and many queries over one key: split axes, joined."""
