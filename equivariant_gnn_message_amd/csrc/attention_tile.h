@@ -396,9 +396,9 @@ struct Pair {
 
 // The tiles of the keys of one kv head, and the starting value of each key's logits: 0, or
 // -infinity for a key that is not seen.  Rows beyond the last key read the last one.
-template <class T, int D, int ROWS, int NT, int LOAD, int MAPS = 1>
+template <class T, int D, int ROWS, int NT, int LOAD>
 struct Keys {
-  typedef Pair<T, D, ROWS, NT, LOAD, MAPS> PairT;
+  typedef Pair<T, D, ROWS, NT, LOAD> PairT;
   typedef typename PairT::TileT TileT;
   PairT pair;
   unsigned char m;
@@ -408,7 +408,7 @@ struct Keys {
   __device__ __forceinline__ void begin(const Params& p, int c, int k0, int k1) {
     const e3conv_attention_args& a = p.a;
     const long j = k0 + PairT::row(0);
-    kp = (const T*)a.k + MAPS * c * a.k_head + j * a.k_row + PairT::first_x(0, a.dim_qk, a.k_head);
+    kp = (const T*)a.k + c * a.k_head + j * a.k_row + PairT::first(0, a.dim_qk);
     vp = (const T*)a.v + c * a.v_head + j * a.v_row + PairT::first(0, a.dim_v);
     next = k0;
     end = k1;
@@ -416,22 +416,18 @@ struct Keys {
   static __device__ __forceinline__ int shift(int e, int dim) {
     return PairT::SAME ? 0 : PairT::first(e, dim) - PairT::first(0, dim);
   }
-  static __device__ __forceinline__ auto shift_x(int e, const e3conv_attention_args& a) {
-    const auto by = PairT::first_x(e, a.dim_qk, a.k_head) - PairT::first_x(0, a.dim_qk, a.k_head);
-    return PairT::SAME ? 0 : by;
-  }
   __device__ __forceinline__ void issue(const Params& p, TileT& kt, TileT& vt) {
     const e3conv_attention_args& a = p.a;
     if (next + ROWS <= end) {
 #pragma unroll
       for (int e = 0; e < PairT::E; ++e)
-        pair.issue(e, kp + (e * PairT::STEP * a.k_row + shift_x(e, a)),
+        pair.issue(e, kp + (e * PairT::STEP * a.k_row + shift(e, a.dim_qk)),
                    vp + (e * PairT::STEP * a.v_row + shift(e, a.dim_v)), a.dim_qk, a.dim_v, kt, vt);
     } else {
 #pragma unroll
       for (int e = 0; e < PairT::E; ++e) {
         const int back = min(end - 1 - (next + PairT::row(0)), e * PairT::STEP);
-        pair.issue(e, kp + (back * a.k_row + shift_x(e, a)), vp + (back * a.v_row + shift(e, a.dim_v)), a.dim_qk,
+        pair.issue(e, kp + (back * a.k_row + shift(e, a.dim_qk)), vp + (back * a.v_row + shift(e, a.dim_v)), a.dim_qk,
                    a.dim_v, kt, vt);
       }
     }
