@@ -15,6 +15,10 @@
 //                dlambda = -sum over the rows of delta2 + r_2;
 // diff_bwd_kv  a wave owns 32 keys and walks over the rows of all query heads that share its kv head.
 // Where the work-groups are few both run in one launch (diff_bwd_both), the second forming the deltas itself.
+// 50 000 nodes in ragged graphs, four heads of two maps of 64 over two kv heads, dim_v 128, bf16: 323 us for grad_q
+// (matrix 39 %, vector 46 % of the SIMD cycles) and 456 us for the others (29 % and 41 %); 20 000 nodes in one graph, two
+// heads of 32 and 64 in fp32: 1910 and 2280 us, 45 % of the cycles products (six for each of fp32).  With two waves a SIMD
+// (one in fp32) the chain of products, exponentials and roundings bounds them.
 #include "attention_diff_tile.h"
 #include "attention_sum.h"
 #include "kernels.h"

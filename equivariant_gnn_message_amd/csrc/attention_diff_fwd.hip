@@ -10,6 +10,10 @@
 // registers with dim_v = 128, and the whole spills: 1200 us for 100 000 ragged nodes.  The difference of the maps
 // could be taken before one product with V, but needs both sums first: a second pass over all logits, whose
 // products and exponentials cost as much as that product saves with dim_v = 2 dim_qk.)
+// 100 000 nodes in ragged graphs, four heads of two maps of 64 over two kv heads, dim_v 128, bf16: 478 us, 450 TFLOP/s
+// of products.  Vector instructions take 55 % and products 33 % of the SIMD cycles, LDS has no conflicts; neither fewer
+// LDS reads nor fewer vector instructions change the time, the chain logits - exponentials - product of
+// two to three waves a SIMD does.
 #include "attention_diff_tile.h"
 #include "kernels.h"
 
