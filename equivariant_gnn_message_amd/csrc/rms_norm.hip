@@ -437,6 +437,7 @@ e3conv_status e3conv_rms_norm(const e3conv_rms_norm_args* a, void* y, int64_t y_
   if (y_row < 0 || total_row < 0) return e3c::bad("negative stride");
   if (a->num_rows == 0) return e3c::api_ok();
   if (!y) return e3c::bad("NULL device pointer");
+  if (y == total) return e3c::bad("y and total are one array");
   e3c::RmsParams p{};
   p.a = *a;
   p.y = y;

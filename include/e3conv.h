@@ -705,7 +705,7 @@ typedef struct {
 } e3conv_rms_norm_args;
 
 /* y is fully written; total, which gets s, and rstd are too unless NULL.  y and total may each be x
- * or residual itself, with the same stride. */
+ * or residual itself, with the same stride, but not one array. */
 e3conv_status e3conv_rms_norm(const e3conv_rms_norm_args* args, void* y, int64_t y_row, void* total,
                               int64_t total_row, float* rstd, void* hip_stream);
 

@@ -127,3 +127,9 @@ def test_oracle_norm_commutes_with_rotations():
     w = rng.standard_normal(8)
     f = lambda t: rms.rms_norm(t.reshape(5, 24), 1, w)[0]["y"].reshape(5, 3, 8)
     np.testing.assert_allclose(f(np.einsum("ij,njc->nic", turn, x)), np.einsum("ij,njc->nic", turn, f(x)), atol=1e-12)
+
+
+def test_refuses_one_array_for_both_results():
+    """x may take y or the sum, not both."""
+    assert forward(args_of(residual=FAKE, residual_row=32), FAKE, 32, FAKE, 32) == 1
+    assert "one array" in E.e3conv_last_error_detail()
