@@ -27,7 +27,8 @@ namespace {
 using namespace rows;
 
 constexpr int NT = 256;               // threads of a work-group
-constexpr int kMaxSize = 8192, kMaxChannels = 65536;
+constexpr int kMaxSize = 16383, kMaxChannels = 65536;
+constexpr int kWide = 8192;           // groups beyond it take work-groups of 2 NT threads
 
 struct RmsParams {
   e3conv_rms_norm_args a;
@@ -56,15 +57,17 @@ struct RmsParams {
   int part_rows;
 };
 
-// Sum over the threads of a team; every thread has it.
-template <bool BIG>
+// Sum over the threads of a team; every thread has it.  WAVES: those of the one team of a work-group, or 0 where
+// the teams are parts of waves.
+template <int WAVES>
 __device__ __forceinline__ float team_sum(float v, int team, float* red) {
-  if constexpr (BIG) {
+  if constexpr (WAVES > 0) {
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    v = (red[0] + red[1]) + (red[2] + red[3]);
+    return WAVES == 4 ? v : v + ((red[4] + red[5]) + (red[6] + red[7]));
   } else {
     for (int o = team >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o);
     return v;
@@ -95,12 +98,16 @@ __device__ __forceinline__ void weights(const RmsParams& p, int c, float (&w)[V]
   }
 }
 
-// U: runs of a thread.  BIG: the work-group is one team.  A team takes items that meet the same weights, and the
+constexpr int threads_of(int waves) { return waves == 8 ? 2 * NT : NT; }
+
+// U: runs of a thread.  WAVES: as above.  A team takes items that meet the same weights, and the
 // next one's loads are issued before this one is used: all of an item's together, the mask's byte too; runs
-// beyond the group read its first, and what does not count is cleared afterwards.
-template <class T, int V, int U, bool BIG>
-__global__ void __launch_bounds__(NT) rms_norm(RmsParams p) {
-  __shared__ float red[4];
+// beyond the group read its first, and what does not count is cleared afterwards.  (Not with 8 waves: the next item's
+// loads would take the registers of the second work-group.)
+template <class T, int V, int U, int WAVES>
+__global__ void __launch_bounds__(threads_of(WAVES)) rms_norm(RmsParams p) {
+  constexpr bool BIG = WAVES > 0, AHEAD = WAVES < 8;
+  __shared__ float red[8];
   const e3conv_rms_norm_args& a = p.a;
   const int t = BIG ? threadIdx.x : threadIdx.x & (p.team - 1), mine = BIG ? 0 : threadIdx.x >> p.team_log2;
   const long first_item = (long)blockIdx.x * p.used + mine;
@@ -134,10 +141,11 @@ __global__ void __launch_bounds__(NT) rms_norm(RmsParams p) {
     }
   };
   Item next;
-  load(first_item, next);
+  if (AHEAD) load(first_item, next);
   for (long at = first_item; at < p.items; at += p.stride) {
-    const Item now = next;
-    if (at + p.stride < p.items) load(at + p.stride, next);
+    Item now = next;
+    if (!AHEAD) load(at, now);
+    else if (at + p.stride < p.items) load(at + p.stride, next);
     const int item = (int)at, row = p.by_groups.of(item), c0 = (item - row * a.groups) * p.size;
     float s[U][V], sum = 0.0f;
 #pragma unroll
@@ -156,7 +164,7 @@ __global__ void __launch_bounds__(NT) rms_norm(RmsParams p) {
         sum = fmaf(s[k][i], s[k][i], sum);
       }
     }
-    sum = team_sum<BIG>(sum, p.team, red);
+    sum = team_sum<WAVES>(sum, p.team, red);
     const float rstd = 1.0f / sqrtf(sum / (float)p.size + a.eps);
     if (t == 0 && p.rstd) p.rstd[item] = rstd;
     T* y = (T*)p.y + row * p.y_row + c0;
@@ -174,9 +182,10 @@ __global__ void __launch_bounds__(NT) rms_norm(RmsParams p) {
   }
 }
 
-template <class T, int V, int U, bool BIG>
-__global__ void __launch_bounds__(NT) rms_norm_grad(RmsParams p) {
-  __shared__ float red[4];
+template <class T, int V, int U, int WAVES>
+__global__ void __launch_bounds__(threads_of(WAVES)) rms_norm_grad(RmsParams p) {
+  constexpr bool BIG = WAVES > 0, AHEAD = WAVES < 8;
+  __shared__ float red[8];
   __shared__ float parts[BIG ? 1 : NT * V * U];
   const e3conv_rms_norm_args& a = p.a;
   const int t = BIG ? threadIdx.x : threadIdx.x & (p.team - 1), mine = BIG ? 0 : threadIdx.x >> p.team_log2;
@@ -216,11 +225,12 @@ __global__ void __launch_bounds__(NT) rms_norm_grad(RmsParams p) {
     }
   };
   Item next;
-  if (mine < p.used && first_item < p.items) load(first_item, next);
+  if (AHEAD && mine < p.used && first_item < p.items) load(first_item, next);
   if (mine < p.used)
     for (long at = first_item; at < p.items; at += p.stride) {
-      const Item now = next;
-      if (at + p.stride < p.items) load(at + p.stride, next);
+      Item now = next;
+      if (!AHEAD) load(at, now);
+      else if (at + p.stride < p.items) load(at + p.stride, next);
       const int item = (int)at, row = p.by_groups.of(item), c0 = (item - row * a.groups) * p.size;
       const float rstd = now.mask ? now.rstd : 0.0f;
       float xh[U][V], dn[U][V], dot = 0.0f;
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(NT) rms_norm_grad(RmsParams p) {
           dot = fmaf(dn[k][i], xh[k][i], dot);
         }
       }
-      dot = team_sum<BIG>(dot, p.team, red) / (float)p.size;
+      dot = team_sum<WAVES>(dot, p.team, red) / (float)p.size;
       T* gx = (T*)p.gx + row * p.gx_row + c0;
 #pragma unroll
       for (int k = 0; k < U; ++k) {
@@ -307,7 +317,8 @@ __global__ void __launch_bounds__(NT) rms_norm_join(const float* part, long rows
 
 int vector_width(const e3conv_rms_norm_args& a) { return a.dtype == E3CONV_F32 ? 4 : 8; }
 
-// Teams: the threads of one wave or fewer up to 256 runs, else the work-group.
+// Teams: the threads of one wave or fewer up to 256 runs, else the work-group, of twice the threads beyond kWide channels
+// (their values are 64 registers' worth and more in 256).
 struct Shape {
   int units, team, team_log2, runs;
   bool big;
@@ -317,7 +328,7 @@ Shape shape_of(int size, int v) {
   s.units = (size + v - 1) / v;
   s.big = s.units > 256;
   while (!s.big && s.team_log2 < 6 && (1 << s.team_log2) < s.units) ++s.team_log2;
-  if (s.big) s.team_log2 = 8;
+  if (s.big) s.team_log2 = size > kWide ? 9 : 8;
   s.team = 1 << s.team_log2;
   s.runs = (s.units + s.team - 1) / s.team;
   return s;
@@ -330,7 +341,7 @@ struct Sharing {
 };
 Sharing sharing_of(const e3conv_rms_norm_args& a, const Shape& s, bool back) {
   Sharing h;
-  const int size = a.channels / a.groups, teams = NT >> s.team_log2;
+  const int size = a.channels / a.groups, teams = std::max(1, NT >> s.team_log2);
   h.residues = a.weight_channels / std::gcd(a.weight_channels, size);
   h.used = h.residues <= teams ? teams / h.residues * h.residues : teams;
   h.part_rows = std::min(h.residues, h.used);
@@ -352,28 +363,29 @@ size_t workspace_bytes(const e3conv_rms_norm_args& a) {
   return (most + 15) / 16 * 16;
 }
 
-template <class T, int V, int U, bool BIG>
+template <class T, int V, int U, int WAVES>
 hipError_t run(const RmsParams& p, bool back, hipStream_t s) {
   if (back) {
-    hipLaunchKernelGGL((rms_norm_grad<T, V, U, BIG>), dim3(p.blocks), dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((rms_norm_grad<T, V, U, WAVES>), dim3(p.blocks), dim3(threads_of(WAVES)), 0, s, p);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || !p.gw) return err;
     const long rows = (long)p.blocks * p.part_rows / p.residues;
     hipLaunchKernelGGL(rms_norm_join, dim3((p.a.weight_channels + 15) / 16), dim3(NT), 0, s, p.part, rows,
                        p.residues * p.size, p.a.weight_channels, p.gw);
   } else {
-    hipLaunchKernelGGL((rms_norm<T, V, U, BIG>), dim3(p.blocks), dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((rms_norm<T, V, U, WAVES>), dim3(p.blocks), dim3(threads_of(WAVES)), 0, s, p);
   }
   return hipGetLastError();
 }
 template <class T, int V>
 hipError_t by_runs(const RmsParams& p, const Shape& sh, bool back, hipStream_t s) {
-  if (!sh.big) return sh.runs == 1 ? run<T, V, 1, false>(p, back, s)
-                    : sh.runs == 2 ? run<T, V, 2, false>(p, back, s) : run<T, V, 4, false>(p, back, s);
-  if (sh.runs <= 2) return run<T, V, 2, true>(p, back, s);
-  if (V == 8 || sh.runs <= 4) return run<T, V, 4, true>(p, back, s);
-  if (V == 4 || sh.runs <= 8) return run<T, V, V == 8 ? 4 : 8, true>(p, back, s);
-  return run<T, V, V == 1 ? 32 : 4, true>(p, back, s);
+  if (!sh.big) return sh.runs == 1 ? run<T, V, 1, 0>(p, back, s)
+                    : sh.runs == 2 ? run<T, V, 2, 0>(p, back, s) : run<T, V, 4, 0>(p, back, s);
+  if (sh.team > NT) return run<T, V, 32 / V, 8>(p, back, s);
+  if (sh.runs <= 2) return run<T, V, 2, 4>(p, back, s);
+  if (V == 8 || sh.runs <= 4) return run<T, V, 4, 4>(p, back, s);
+  if (V == 4 || sh.runs <= 8) return run<T, V, V == 8 ? 4 : 8, 4>(p, back, s);
+  return run<T, V, V == 1 ? 32 : 4, 4>(p, back, s);
 }
 
 hipError_t launch(RmsParams p, bool back, bool vec, void* workspace, hipStream_t s) {
@@ -409,7 +421,7 @@ e3conv_status check_sizes(const e3conv_rms_norm_args* a) {
   if (a->num_rows < 0) return bad("negative size");
   if (a->channels < 1 || a->channels > kMaxChannels || a->groups < 1 || a->channels % a->groups != 0 ||
       a->channels / a->groups > kMaxSize)
-    return bad("channels must be in [1, 65536] and a multiple of groups, with at most 8192 in a group");
+    return bad("channels must be in [1, 65536] and a multiple of groups, with fewer than 16384 in a group");
   if (a->weight_channels < 1 || a->channels % a->weight_channels != 0)
     return bad("channels must be a multiple of weight_channels");
   if (a->num_rows >= (((int64_t)1 << 31) - ((int64_t)1 << 20)) / a->groups) return bad("sizes must fit int32 indices");

@@ -689,7 +689,7 @@ e3conv_status e3conv_rotary_backward(const e3conv_rotary_args* args, const void*
  * - row_mask: device bytes (num_rows) or NULL; a row whose byte is 0 gets y = 0, total = 0,
  *   rstd = 1 / sqrt(eps) and a zero gradient, whatever x, residual and the gradients hold.
  * - rstd: fp32 (num_rows, groups), dense.
- * channels <= 65536, a multiple of groups and of weight_channels, size <= 8192; eps > 0;
+ * channels <= 65536, a multiple of groups and of weight_channels, size < 16384; eps > 0;
  * num_rows * groups < 2^31 - 2^20.  The squares of a group must not overflow fp32. */
 typedef struct {
   e3conv_dtype dtype;

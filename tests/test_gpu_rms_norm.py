@@ -86,6 +86,17 @@ def test_shapes(dtype, c, groups, period):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,c,groups,period", [(3, 8193, 1, 8193), (19, 10240, 1, 2048), (1500, 10240, 1, 2048), (700, 14336, 1, 2048),
+                                               (5, 16383, 1, 16383), (1, 16376, 1, 16376), (31, 20480, 2, 10240),
+                                               (9, 36864, 3, 36864), (7, 65532, 4, 16383), (4, 27000, 3, 5)])
+def test_wide_groups(dtype, n, c, groups, period):
+    """More channels in a group than a work-group of 256 threads holds, up to the limit."""
+    check(dtype, draw(1, dtype, n, c), groups, weight_of(period), residual=draw(2, dtype, n, c), gt=draw(3, dtype, n, c))
+    mask = (np.random.default_rng(n).random(n) < 0.6).astype(np.uint8)
+    check(dtype, draw(4, dtype, n, c), groups, mask=mask)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("n,c,groups,period", [(70001, 16, 1, 16), (20000, 128, 4, 32), (9001, 24, 3, 24),
                                                (3000, 1600, 100, 1600), (5000, 2304, 1, 768), (100000, 3, 1, 3)])
 def test_many_rows(dtype, n, c, groups, period):
