@@ -13,8 +13,12 @@
 //              delta makes 0, and B_m = sum_j P_m k_m by one product more for each operand of K, and takes
 //                dq_m = scale (sum dS_m k_m - r_m B_m),   delta_m + r_m for diff_bwd_kv,
 //                dlambda = -sum over the rows of delta2 + r_2;
+//              where the keys are split, diff_join_delta adds the r of a row's splits to its deltas;
 // diff_bwd_kv  a wave owns 32 keys and walks over the rows of all query heads that share its kv head.
-// Where the work-groups are few both run in one launch (diff_bwd_both), the second forming the deltas itself.
+// In fp32, where the work-groups are few, both run in one launch (diff_bwd_both), the second forming the deltas of out and
+// O2 itself: their rounding of 2^-24 is that of dP's own dot product.  With bf16 it is not, so grad_k waits for the deltas:
+// with v and grad_out of mean 2 the error of grad_k (rms) is 2.0e-3 instead of 3.8e-3 for 64 graphs of 64 nodes, for 2.6 us
+// (21.1 -> 23.7), and 2.3e-3 instead of 3.6e-3 for three rows of 20 011 keys.
 // 50 000 nodes in ragged graphs, four heads of two maps of 64 over two kv heads, dim_v 128, bf16: 323 us for grad_q
 // (matrix 39 %, vector 46 % of the SIMD cycles) and 456 us for the others (29 % and 41 %); 20 000 nodes in one graph, two
 // heads of 32 and 64 in fp32: 1910 and 2280 us, 45 % of the cycles products (six for each of fp32).  With two waves a SIMD
@@ -212,7 +216,7 @@ __device__ __forceinline__ void bwd_q(const DiffParams& p, const Where& place, K
   for (int x = 0; x < NM; ++x) {
     const int m = map0 + x;
     const float factor = m == 0 ? 1.0f : -lam;      // dS2 without its -lambda above
-    // a split's r is not the row's: the join takes the row's off, and the deltas stay as they were given
+    // a split's r is not the row's: the joins take the row's off, of grad_q and of the deltas
     if (p.delta && h == 0 && split == 0) p.delta[2 * at + m] = p.splits > 1 || !live ? delta[x] : delta[x] + rest[x];
     if (p.splits > 1) {
       const long i = (split * (a.num_q * a.heads_q) + at) * 2 + m;
@@ -396,8 +400,19 @@ __global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_kv(sizeof(T) == 
     bwd_kv<T, D, RW, TQ, BUF, LOAD, false, kBothGrads>(p, where<kRun>((int)b, p.blocks, p.slots_kv, p.splits_kv), first, second);
   }
 }
+// delta + r of each row and map whose keys are split: a wave sums its splits, in a fixed order (2 to 5 us, a launch).
+__global__ void __launch_bounds__(256) diff_join_delta(DiffParams p) {
+  const long n = 2 * p.a.num_q * p.a.heads_q, i = block_index() * 4 + (threadIdx.x >> 6);
+  if (i >= n) return;
+  const int lane = threadIdx.x & 63;
+  float r = 0.0f;
+#pragma unroll 4
+  for (int s = lane; s < p.splits; s += 64) r += p.part_rest[s * n + i];
+  for (int o = 32; o > 0; o >>= 1) r += __shfl_xor(r, o);
+  if (lane == 0) p.delta[i] += r;
+}
 template <class T, int D, int RW, int ROWS, int BUF, int LOAD>
-__global__ void __launch_bounds__(64 * RW, RW == 4 ? diff_waves_both(sizeof(T) == 4, D) : 1) diff_bwd_both(DiffParams p) {
+__global__ void __launch_bounds__(64 * RW, 1) diff_bwd_both(DiffParams p) {
   union Buffer {
     KeyBuffer<T, D, ROWS> keys;
     RowBuffer<T, D, ROWS> rows;
@@ -448,8 +463,9 @@ Shape split_small(Shape s, long others, int graphs, int heads) {
 Shape shape_q(const e3conv_attention_args& a) {
   const bool f32 = a.dtype == E3CONV_F32;
   const int width = diff_width(a), wide = 2 * diff_maps(f32, width, 4);    // blocks of 32 rows of four waves
-  return split_small(choose(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv, diff_waves_q(f32, width),
-                            diff_unit_us(f32, width, true) * wide / 4, 4 * a.dim_qk, wide), a.num_k, a.num_graphs, a.heads_kv);
+  const Shape s = choose(a.num_q * (a.heads_q / a.heads_kv), a.num_k, a.num_graphs, a.heads_kv, diff_waves_q(f32, width),
+                         diff_unit_us(f32, width, true) * wide / 4, 4 * a.dim_qk, wide);
+  return f32 ? split_small(s, a.num_k, a.num_graphs, a.heads_kv) : s;
 }
 Shape shape_kv(const e3conv_attention_args& a) {
   const bool f32 = a.dtype == E3CONV_F32;
@@ -478,7 +494,7 @@ void launch(const DiffParams& p, Which which, int rw, hipStream_t s) {
   } else if (which == kKv) {
     if (rw == 4) hipLaunchKernelGGL((diff_bwd_kv<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((diff_bwd_kv<T, D, 1, 32, L::BUF1, LOAD>), grid, dim3(64), 0, s, p);
-  } else {
+  } else if constexpr (sizeof(T) == 4) {
     if (rw == 4) hipLaunchKernelGGL((diff_bwd_both<T, D, 4, L::ROWS, L::BUF4, LOAD>), grid, dim3(256), 0, s, p);
     else if constexpr (L::LEAST == 1)
       hipLaunchKernelGGL((diff_bwd_both<T, D, 1, 32, L::BUF1, LOAD>), grid, dim3(64), 0, s, p);
@@ -496,14 +512,14 @@ void by_width(const DiffParams& p, Which which, int rw, hipStream_t s) {
   else by_load<T, 128>(p, which, rw, s);
 }
 
-// Whether both kernels go in one launch: work-groups of one size, and either of one wave without
+// Whether both kernels go in one launch: fp32, work-groups of one size, and either of one wave without
 // splits (small graphs), or not more of them than places.
 bool together(const e3conv_attention_args& a, const Shape& q, const Shape& kv) {
-  if ((q.rw == 1) != (kv.rw == 1)) return false;
-  if (q.rw == 1 && diff_maps(a.dtype == E3CONV_F32, diff_width(a), 2) == 1) return false;
+  if (a.dtype != E3CONV_F32 || (q.rw == 1) != (kv.rw == 1)) return false;
+  if (q.rw == 1 && diff_maps(true, diff_width(a), 2) == 1) return false;
   const long blocks = ((long)q.slots * q.splits + (long)kv.slots * kv.splits) * a.heads_kv;
   if (q.rw == 1 && q.splits == 1 && kv.splits == 1) return blocks <= 0x7fffffffL;
-  return blocks <= 256 * (q.rw == 1 ? 4 : diff_waves_both(a.dtype == E3CONV_F32, diff_width(a)));
+  return blocks <= 256 * (q.rw == 1 ? 4 : 1);
 }
 
 template <class T>
@@ -524,6 +540,8 @@ hipError_t backward(DiffParams p, const Shape& q, const Shape& kv, hipStream_t s
     if (a.num_q > 0) {
       p.blocks = (int)nq;
       by_width<T>(p, kQ, q.rw == 1 ? 1 : 4, s);
+      if (q.splits > 1 && a.num_k > 0)
+        hipLaunchKernelGGL(diff_join_delta, grid_of((2 * a.num_q * a.heads_q + 3) / 4), dim3(256), 0, s, p);
     }
     if (a.num_k > 0) {
       p.blocks = (int)nk * (diff_two_roles(sizeof(T) == 4, diff_width(a), kv.rw) ? 2 : 1);

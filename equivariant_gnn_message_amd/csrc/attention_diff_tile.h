@@ -240,14 +240,13 @@ __device__ __forceinline__ void by_half(const float* rows, int t, int lane, floa
 // 479 us for 100 000 ragged nodes) and the reverse pass (771, 760, 776 us for 50 000), whose work-groups are few.
 constexpr int kRun = 8;
 
-// Waves of a SIMD that the registers are kept to: forward, grad_q, grad_k with grad_v, all three.  The bf16 forward's three
+// Waves of a SIMD that the registers are kept to: forward, grad_q, grad_k with grad_v.  The bf16 forward's three
 // spill 30 registers with 128 dimensions and are faster than two all the same (473 against 495 us for 100 000 ragged nodes);
 // two of the fp32 reverse pass need a map, or a gradient, to a wave and lose (20 000 nodes: grad_q 4285 -> 4530 us for
 // the whole, grad_k and grad_v 5040).
 constexpr int diff_waves_fwd(bool f32) { return f32 ? 2 : 3; }
 constexpr int diff_waves_q(bool f32, int d) { return f32 ? 1 : 2; }
 constexpr int diff_waves_kv(bool f32, int d) { return f32 ? 1 : 2; }
-constexpr int diff_waves_both(bool f32, int d) { return f32 || d == 128 ? 1 : 2; }
 // Maps of a wave of diff_bwd_q: with one, two waves share 32 rows.  Sums and operands of two maps do not fit the
 // registers of two waves a SIMD with bf16, nor those of one with fp32 and 128 dimensions (all others: 64 dimensions in fp32
 // take 4285 us for 20 000 nodes with two, 4530 with one).

@@ -550,8 +550,9 @@ e3conv_status e3conv_diff_attention(const e3conv_attention_args* args, const flo
  *     dS1 = P1 (dP - delta1),   dS2 = -lambda P2 (dP - delta2),
  *     grad_q[2h + m] = scale sum_j dS_m k[2c + m],   grad_k[2c + m] = scale sum dS_m q[2h + m],
  *     grad_v = sum (P1 - lambda P2) grad_out,        grad_lambda[h] = - sum_i sum_j P2 dP,
- * summed over the rows and the query heads that share the kv head.  out and second are as they were stored;
- * grad_q and grad_lambda are corrected by sum_j P_m (dP - delta_m), which their rounding leaves different from 0.
+ * summed over the rows and the query heads that share the kv head.  out and second are as they were stored; what
+ * their rounding leaves of sum_j P_m (dP - delta_m), 0 but for it, corrects grad_q and grad_lambda, and delta_m for
+ * grad_k (in fp32 not where one launch forms all: the rounding there is that of the other products).
  * strides holds (row, head) of out, second, grad_out, grad_q, grad_k, grad_v in turn.  grad_lambda is fp32 (heads_q) or NULL (not computed).
  * All are fully written, without atomics: the same inputs give the same bits. */
 e3conv_status e3conv_diff_attention_backward(const e3conv_attention_args* args, const float* lambda,

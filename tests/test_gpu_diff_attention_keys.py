@@ -1,0 +1,81 @@
+"""The gradient of the keys of differential attention where v and grad_out have means, over the forms that the reverse
+pass takes for different sizes: one launch and two, queries split over the keys and not."""
+
+import numpy as np
+import pytest
+
+from equivariant_gnn_message_amd import e3conv as E
+
+from ._gpu import say
+from .test_gpu_attention import U, dev, dtype_of, host, ptr
+
+pytestmark = pytest.mark.gpu
+
+
+def keys_bound(q, k, v, lam, g, scale, u, r, out, second):
+    """dk of one graph (heads of q and k alike) in 64 bits, and how far it may be off.
+
+    The terms of a key come from one row each, whose roundings are independent, so a sum over n rows is within four
+    times the root of their squares.  A term: dS by its rounding r, by its logits' (a dot product's, the
+    scaling's and the exponential's) and by its row's lse; dP by its dot product's, 4 sqrt(dims) u of the magnitudes.
+    delta is sum_j P dP as it is formed from the deltas of out and second as given and r_m = sum_j P (dP - given):
+    off by the roundings of that sum and of dP, and not by what out and second lost in storage where that is more
+    than fp32's (bf16).  In fp32 delta may be the given one: off by |given - delta|, a few u of its terms, as dP is.
+    """
+    want, tol = np.zeros_like(k), np.zeros_like(k)
+    rows, n, dims = len(q), len(k), 4 * np.sqrt(max(q.shape[2], v.shape[2]))
+    for h in range(len(lam)):
+        dp = g[:, h] @ v[:, h].T
+        size = np.abs(g[:, h]) @ np.abs(v[:, h]).T
+        d1 = (g[:, h] * second[:, h]).sum(1, keepdims=True)
+        d0 = (g[:, h] * out[:, h]).sum(1, keepdims=True) + lam[h] * d1
+        for m, given, f in ((0, d0, 1.0), (1, d1, -lam[h])):
+            qh, kh = q[:, 2 * h + m], k[:, 2 * h + m]
+            s = scale * qh @ kh.T
+            top = s.max(1, keepdims=True)
+            lse = top + np.log(np.exp(s - top).sum(1, keepdims=True))
+            p = np.exp(s - lse)
+            delta = (p * dp).sum(1, keepdims=True)
+            ds = p * (dp - delta)
+            a = abs(scale * f)
+            want[:, 2 * h + m] = scale * f * ds.T @ qh
+            logit = u * (dims * scale * (np.abs(qh) @ np.abs(kh).T) + 4 * np.abs(s) + 4 * np.abs(top) + 8)
+            row = logit.max(1, keepdims=True) + 4 * u * (np.abs(lse) + np.sqrt(n))
+            rest = np.abs(given - delta)
+            off = ((logit.max(1, keepdims=True) + 4 * np.sqrt(n) * u) * (p * np.abs(dp - given)).sum(1, keepdims=True)
+                   + u * dims * (p * size).sum(1, keepdims=True) + row * rest + 8 * u * (np.abs(given) + np.abs(delta)))
+            if r == 0.0:
+                off = off + rest
+            each = (r + logit + row) * np.abs(ds) + p * (u * (dims * size + 4 * (np.abs(dp) + np.abs(delta))) + off)
+            tol[:, 2 * h + m] = a * (4 * np.sqrt((each ** 2).T @ qh ** 2)
+                                     + 16 * np.sqrt(rows) * u * np.sqrt((ds ** 2).T @ qh ** 2)) \
+                + (r + 4 * u) * np.abs(want[:, 2 * h + m])
+    return want, tol
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("graphs,rows,keys,heads,d,dv", [
+    (64, 64, 64, 1, 16, 32), (3, 100, 100, 2, 64, 128), (1, 2500, 2500, 2, 32, 64), (1, 3, 20011, 2, 64, 128),
+    (1, 300, 5000, 2, 64, 128), (1, 5000, 4, 1, 33, 40), (5, 7, 900, 2, 24, 48), (2, 1, 1, 1, 8, 16)])
+def test_gradient_of_k_where_v_has_a_mean(dtype, graphs, rows, keys, heads, d, dv):
+    import torch
+    gen = torch.Generator().manual_seed(rows + keys + d)
+    n, m = graphs * rows, graphs * keys
+    q, k, v, g = [(mean + torch.randn(s, generator=gen)).to(dtype_of(dtype)).cuda() for mean, s in (
+        (0.5, (n, 2 * heads, d)), (0.0, (m, 2 * heads, d)), (2.0, (m, heads, dv)), (2.0, (n, heads, dv)))]
+    lam = torch.linspace(0.3, 0.8, heads).cuda()
+    qp, kp = dev(ptr([rows] * graphs)), dev(ptr([keys] * graphs))
+    say(f"[diff keys] {dtype} {graphs} graphs of {rows} x {keys} heads {heads} {d} {dv}")
+    out, second, lse = E.e3conv_diff_attention(q, k, v, lam, qp, kp)
+    got = host(E.e3conv_diff_attention_backward(q, k, v, lam, out, second, lse, g, qp, kp)[1])
+    torch.cuda.synchronize()
+    u, r = U[dtype]
+    of_rows, of_keys = [host(t) for t in (q, g, out, second)], [host(t) for t in (k, v)]
+    worst = 0.0
+    for i in range(graphs):
+        a, b = slice(i * rows, (i + 1) * rows), slice(i * keys, (i + 1) * keys)
+        (qi, gi, oi, si), (ki, vi) = [t[a] for t in of_rows], [t[b] for t in of_keys]
+        want, tol = keys_bound(qi, ki, vi, host(lam), gi, float(np.float32(d ** -0.5)), u, r, oi, si)
+        worst = max(worst, float(np.max(np.abs(got[b] - want) / tol)))
+    say(f"  dk: {worst:.2f} of its bound")
+    assert worst <= 1.0
