@@ -535,7 +535,7 @@ hipError_t backward(DiffParams p, const Shape& q, const Shape& kv, hipStream_t s
     p.delta = nullptr;
     p.first_blocks = (int)nq;
     p.blocks = (int)(nq + nk);
-    by_width<T>(p, kBoth, kv.rw, s);
+    if (p.blocks > 0) by_width<T>(p, kBoth, kv.rw, s);     // none without graphs
   } else {
     if (a.num_q > 0) {
       p.blocks = (int)nq;
