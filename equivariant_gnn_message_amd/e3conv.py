@@ -623,7 +623,7 @@ def _rows_of(t, name, dtype, index, shape):
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     strides = t.stride()
-    if strides[-1] != 1 and shape[-1] > 1:
+    if strides[-1] != 1 and shape[-1] > 1 and t.numel() > 0:     # without elements any strides will do
         raise ValueError(f"{name} must have unit stride along its last axis")
     return strides
 
