@@ -697,6 +697,13 @@ def _on(other, call, *args):
     return results
 
 
+def _gradient_like(t):
+    """A tensor for the gradient of t: as t lies, unless its rows overlap in memory in a way that would put another axis
+    before the last one."""
+    g = _torch.empty_like(t)
+    return g if g.stride(-1) == 1 or t.shape[-1] == 1 else t.new_empty(t.shape)
+
+
 def _attention_args(q, k, v, q_ptr, k_ptr, scale, q_mask, k_mask):
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q (num_q, heads_q, dim_qk), k (num_k, heads_kv, dim_qk), v (num_k, heads_kv, dim_v)")
@@ -782,7 +789,7 @@ def e3conv_attention_backward(q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale=N
         return _on(other, e3conv_attention_backward, q, k, v, out, lse, grad_out, q_ptr, k_ptr, scale, q_mask, k_mask,
                    grads, workspace)
     if grads is None:
-        grads = [_torch.empty_like(t) for t in (q, k, v)]
+        grads = [_gradient_like(t) for t in (q, k, v)]
         for t in grads:
             strides += t.stride()[:2]
     else:
@@ -899,7 +906,7 @@ def e3conv_diff_attention_backward(q, k, v, lam, out, second, lse, grad_out, q_p
         return _on(other, e3conv_diff_attention_backward, q, k, v, lam, out, second, lse, grad_out, q_ptr, k_ptr, scale,
                    q_mask, k_mask, grads, workspace)
     if grads is None:
-        grads = [_torch.empty_like(t) for t in (q, k, v)]
+        grads = [_gradient_like(t) for t in (q, k, v)]
         for t in grads:
             strides += t.stride()[:2]
     else:
