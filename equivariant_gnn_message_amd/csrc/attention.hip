@@ -185,6 +185,7 @@ e3conv_status e3conv_diff_attention(const e3conv_attention_args* a, const float*
   const size_t need = e3c::attn::diff_forward_workspace(*a);
   if (bytes < need || (need > 0 && !workspace))
     return e3c::api_fail(E3CONV_ERR_WORKSPACE, "differential attention needs " + std::to_string(need) + " bytes");
+  if (second == out) return e3c::bad("out and second are one array");
   e3c::attn::DiffParams p = e3c::diff_params(*a, lambda);
   p.out = out;
   p.out_row = out_row;

@@ -529,7 +529,7 @@ e3conv_status e3conv_attention_backward(const e3conv_attention_args* args, const
  *     second[i, h] = sum_j P2[i, h, j] v[j, c],
  *     lse[i, h, m] = the log of the sum of exponentials of map m.
  * - lambda: device fp32 (heads_q), finite; any way of forming it from parameters is the caller's.
- * - second: (num_q, heads_q, dim_v) in dtype, what the reverse pass keeps beside out, or NULL.
+ * - second: (num_q, heads_q, dim_v) in dtype, what the reverse pass keeps beside out, or NULL; not out itself.
  * - With bf16 each map's probabilities are rounded to bf16 before their product; the difference is
  *   taken in fp32 and rounded once.
  * - A query that sees no key has out = second = 0 and both lse = -infinity.
