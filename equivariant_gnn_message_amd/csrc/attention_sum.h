@@ -72,17 +72,17 @@ __global__ void __launch_bounds__(256) attn_sum(Sums all) {
       }
   }
   if (!wide) {
-    const auto all = [&](float x) {
+    const auto of_waves = [&](float x) {
       red[w][lane] = x;
       __syncthreads();
       x = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
       __syncthreads();
       return x;
     };
-    v = all(v);
+    v = of_waves(v);
     if (m.rest) {
-      bar = all(bar);
-      rest = all(rest);
+      bar = of_waves(bar);
+      rest = of_waves(rest);
     }
     if (w > 0) return;
   }

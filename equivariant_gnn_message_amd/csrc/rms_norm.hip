@@ -383,9 +383,13 @@ hipError_t by_runs(const RmsParams& p, const Shape& sh, bool back, hipStream_t s
                     : sh.runs == 2 ? run<T, V, 2, 0>(p, back, s) : run<T, V, 4, 0>(p, back, s);
   if (sh.team > NT) return run<T, V, 32 / V, 8>(p, back, s);
   if (sh.runs <= 2) return run<T, V, 2, 4>(p, back, s);
-  if (V == 8 || sh.runs <= 4) return run<T, V, 4, 4>(p, back, s);
-  if (V == 4 || sh.runs <= 8) return run<T, V, V == 8 ? 4 : 8, 4>(p, back, s);
-  return run<T, V, V == 1 ? 32 : 4, 4>(p, back, s);
+  if constexpr (V == 8) {
+    return run<T, V, 4, 4>(p, back, s);
+  } else {
+    if (sh.runs <= 4) return run<T, V, 4, 4>(p, back, s);
+    if (V == 4 || sh.runs <= 8) return run<T, V, 8, 4>(p, back, s);
+    return run<T, V, V == 1 ? 32 : 8, 4>(p, back, s);
+  }
 }
 
 hipError_t launch(RmsParams p, bool back, bool vec, void* workspace, hipStream_t s) {

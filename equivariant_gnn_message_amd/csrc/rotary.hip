@@ -26,8 +26,9 @@ using namespace rows;
 
 constexpr int NT = 256;               // threads of a work-group
 constexpr int kMaxDim = 256, kMaxAxes = 4;
-constexpr int kTile = 8192;           // elements of a tile at most: one row's heads go in parts if they have more
-constexpr int kGradTile = 4096;       // the same of the reverse pass, which keeps half as many values in LDS
+constexpr int kTile = 8192;           // elements of a tile, or one row's: the forward kernel's loop takes any number of them
+constexpr int kGradTile = 4096;       // the same of the reverse pass, which keeps half as many values in LDS: a row's heads
+                                      // go in parts if they have more
 constexpr int kTileRows = 128;        // a tile has at most NT angles: each thread forms one
 constexpr int kTable = 512;           // and its rows in the table are whole runs: 128 rows of 4 at most, or 256 + 85 3
 
@@ -36,7 +37,8 @@ struct RotaryParams {
   int units;                          // runs of a head: of V elements, or turned pairs of V and then V elements
   int turning;                        // units that hold pairs
   int stride;                         // pairs of a row of the table, whole runs
-  int tile_rows, tile_heads;
+  int tile_rows;
+  int tile_heads;                     // reverse pass
   int tiles, blocks;
   Div by_units, by_heads, by_pairs, by_axes, by_values;
   float sign;
