@@ -19,9 +19,9 @@
 // O2 itself: their rounding of 2^-24 is that of dP's own dot product.  With bf16 it is not, so grad_k waits for the deltas:
 // with v and grad_out of mean 2 the error of grad_k (rms) is 2.0e-3 instead of 3.8e-3 for 64 graphs of 64 nodes, for 2.6 us
 // (21.1 -> 23.7), and 2.3e-3 instead of 3.6e-3 for three rows of 20 011 keys.
-// 50 000 nodes in ragged graphs, four heads of two maps of 64 over two kv heads, dim_v 128, bf16: 323 us for grad_q
-// (matrix 39 %, vector 46 % of the SIMD cycles) and 456 us for the others (29 % and 41 %); 20 000 nodes in one graph, two
-// heads of 32 and 64 in fp32: 1910 and 2280 us, 45 % of the cycles products (six for each of fp32).  With two waves a SIMD
+// 50 000 nodes in ragged graphs, four heads of two maps of 64 over two kv heads, dim_v 128, bf16: 332 us for grad_q
+// (matrix 39 %, vector 46 % of the SIMD cycles) and 469 us for the others (29 % and 41 %); 20 000 nodes in one graph, two
+// heads of 32 and 64 in fp32: 1914 and 2292 us, 45 % of the cycles products (six for each of fp32).  With two waves a SIMD
 // (one in fp32) the chain of products, exponentials and roundings bounds them.
 #include "attention_diff_tile.h"
 #include "attention_sum.h"

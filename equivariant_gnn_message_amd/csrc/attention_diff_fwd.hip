@@ -10,10 +10,11 @@
 // registers with dim_v = 128, and the whole spills: 1200 us for 100 000 ragged nodes.  The difference of the maps
 // could be taken before one product with V, but needs both sums first: a second pass over all logits, whose
 // products and exponentials cost as much as that product saves with dim_v = 2 dim_qk.)
-// 100 000 nodes in ragged graphs, four heads of two maps of 64 over two kv heads, dim_v 128, bf16: 478 us, 450 TFLOP/s
-// of products.  Vector instructions take 55 % and products 33 % of the SIMD cycles, LDS has no conflicts; neither fewer
-// LDS reads nor fewer vector instructions change the time, the chain logits - exponentials - product of
-// two to three waves a SIMD does.
+// 100 000 nodes in ragged graphs, four heads of two maps of 64 over two kv heads, dim_v 128, bf16: 477 us, 675 TFLOP/s
+// of products (both results take two with V: 252 us at a library product's rate).  Vector instructions take 55 % and
+// products 33 % of the SIMD cycles, LDS has no conflicts, and neither fewer LDS reads nor fewer vector instructions
+// change the time: no unit bounds it.  Every tile of 32 keys ends in a wait for all of its loads and a barrier, one
+// tile is in flight, and two to three waves a SIMD are too few to cover that and the chain logits - exponentials - product.
 #include "attention_diff_tile.h"
 #include "kernels.h"
 

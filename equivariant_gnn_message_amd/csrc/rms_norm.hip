@@ -7,9 +7,11 @@
 //     grad_s = rstd (dn - xhat sum(dn xhat) / size) + grad_total,   grad_weight = sum grad_y xhat.
 // A team of threads takes an item (a group of a row), each thread every team-th run of 16 bytes; the row stays
 // in registers between its statistics and its result, so everything is read once and written once.  Memory
-// bound: 100 000 rows of 512 channels in bf16, each of four heads by itself, take 33 us for 205 MB (6.1 TB/s, a
-// stream copy's rate), the reverse pass with a residual 73 us for 410 MB (5.6 TB/s) and 5 us for the join.  In the reverse pass a team takes many items, always of the same weights, and keeps its part of their
-// gradient in registers; parts are joined within the work-group, then by a second launch, in a fixed order.
+// bound: 100 000 rows of 512 channels in bf16, each of four heads by itself, take the kernel 33 us for 205 MB (6.1 TB/s, a
+// stream copy's rate; 40 us a call among others), the reverse pass with a residual 73 us for 410 MB (5.6 TB/s) and
+// 5 us for the join (76 us a call).  In the reverse pass a team takes many items, always of the same weights, and keeps
+// its part of their gradient in registers; parts are joined within the work-group, then by a second launch, in a fixed
+// order.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -27,7 +29,7 @@ namespace {
 using namespace rows;
 
 constexpr int NT = 256;               // threads of a work-group
-constexpr int kMaxSize = 16383, kMaxChannels = 65536;
+constexpr int kMaxSize = 16383, kMaxChannels = 65536;   // 2 NT threads hold 32 values each; the contract ends below 16 384
 constexpr int kWide = 8192;           // groups beyond it take work-groups of 2 NT threads
 
 struct RmsParams {

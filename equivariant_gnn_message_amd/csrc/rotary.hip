@@ -8,8 +8,9 @@
 // angle in 64 bits and in turns (of a position of 10^4 wave lengths 32 bits leave three digits), and stand in
 // LDS; the rows then pass through registers in runs of 16 bytes, whatever their heads.  In the reverse pass
 // each pair's d_angle goes to LDS and is summed over the heads in order.  Memory bound: 100 000 rows of 12 heads of 64
-// in bf16 take 50 us for 307 MB (6.1 TB/s, the rate of a stream copy); the reverse pass of 20 000 rows of 8 heads of 32
-// in fp32 15 us for 62 MB, where the chain of a work-group's few tiles shows, and 4 us to join grad_waves.
+// in bf16 take the kernel 49 us for 307 MB (6.2 TB/s, the rate of a stream copy; 55.6 us a call among others); the reverse
+// pass of 20 000 rows of 8 heads of 32 in fp32 15 us for 62 MB, where the chain of a work-group's few tiles shows, and
+// 4 us to join grad_waves (18.3 us a call).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -850,8 +850,8 @@ def e3conv_diff_attention(q, k, v, lam, q_ptr, k_ptr, scale=None, q_mask=None, k
 
     q (num_q, 2 heads_q, dim_qk) and k (num_k, 2 heads_kv, dim_qk) hold the heads of the two maps side by side
     (2 h and 2 h + 1), v (num_k, heads_kv, dim_v), lam fp32 (heads_q); dim_qk up to 64, dim_v up to 128;
-    the rest as in e3conv_attention.  second = P2 v and lse, fp32 (num_q, heads_q, 2), are what the reverse pass
-    needs; with keep=False they are not formed (None unless given).
+    the rest as in e3conv_attention.  second = P2 v (not out's array) and lse, fp32 (num_q, heads_q, 2), are what the
+    reverse pass needs; with keep=False they are not formed (None unless given).
     """
     lib = _lib or load_library()
     args, lam_at = _diff_attention_args(q, k, v, lam, q_ptr, k_ptr, scale, q_mask, k_mask)
@@ -1037,7 +1037,8 @@ def e3conv_rotary(x, positions, waves, layout="adjacent", row_mask=None, out=Non
     x (num_rows, heads, dim) fp32 or bf16, any strides but unit along the last axis (the queries and keys of one
     projection together); positions fp32 (num_rows, axes), waves fp32 (pairs, axes) with pairs <= dim // 2 and at
     most four axes; layout "adjacent" (elements 2 p, 2 p + 1) or "halves" (p, pairs + p); elements beyond 2 pairs
-    are copied; row_mask bool or uint8, 0 for padding (zeros).  out may be x.
+    are copied; row_mask bool or uint8, 0 for padding (zeros).  out may be x.  Products of turned rows depend on differences
+    of positions: moving all positions changes none of them, rotating them does.
     """
     lib = _lib or load_library()
     args = _rotary_args(x, positions, waves, layout, row_mask)

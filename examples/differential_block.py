@@ -5,7 +5,8 @@ On the gate-points workload (64 graphs of 64 nodes, 32x0e+32x1o) one forward and
     conv    Plan.forward: messages from the neighbours within the cutoff,
     norm    RMSNormFunction: total = node scalars + the convolution's scalar (l = 0) channels, and its norm,
     turn    RotaryFunction: queries and keys of both maps, as one strided part of the projection, turned by the
-            nodes' positions along learned wave vectors (their products then depend on differences of positions),
+            nodes' positions along learned wave vectors (their products then depend on differences of positions: a
+            translation of a graph changes nothing, a rotation does, so the block is not rotation invariant),
     attend  DiffAttentionFunction: every node of a graph to every other, two heads of two maps each, with a learned
             weight of the second map,
     heads   RMSNormFunction: each head's result by itself, one weight for all heads,

@@ -633,6 +633,8 @@ e3conv_status e3conv_group_norm_backward(const e3conv_group_norm_args* args, con
  *     (u, v) -> (u cos - v sin, u sin + v cos),
  * so that products of two turned rows depend on the difference of their positions alone.  Rows of waves with
  * one nonzero entry give each axis pairs of its own; any others (learned ones too) are wave vectors.
+ * Translations of all positions change no product; rotations and reflections do (the waves stay where they are),
+ * so a model with it is not rotation equivariant, unlike one of e3conv's convolutions alone.
  * - x, out (num_rows, heads, dim) in dtype (fp32 or bf16), unit stride along dim, row and head strides in
  *   elements; queries and keys that lie side by side in one projection take one call.  Elements beyond 2 pairs
  *   are copied.  ADJACENT: pair p is elements 2 p and 2 p + 1; HALVES: p and pairs + p.
