@@ -79,3 +79,34 @@ def test_gradient_of_k_where_v_has_a_mean(dtype, graphs, rows, keys, heads, d, d
         worst = max(worst, float(np.max(np.abs(got[b] - want) / tol)))
     say(f"  dk: {worst:.2f} of its bound")
     assert worst <= 1.0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens_q,lens_k", [([3, 1], [9001, 40]), ([64] * 9, [64] * 9), ([300], [5000])], ids=str)
+def test_same_bits_where_deltas_are_joined(dtype, lens_q, lens_k):
+    """Split and whole, again, on another stream and in replays, whose buffers other work has used in between."""
+    import torch
+    gen = torch.Generator().manual_seed(9)
+    n, m = sum(lens_q), sum(lens_k)
+    q, k, v, g = [torch.randn(s, generator=gen).to(dtype_of(dtype)).cuda()
+                  for s in ((n, 4, 64), (m, 4, 64), (m, 2, 128), (n, 2, 128))]
+    lam, qp, kp = torch.tensor([0.3, 0.7], device="cuda"), dev(ptr(lens_q)), dev(ptr(lens_k))
+    kept = E.e3conv_diff_attention(q, k, v, lam, qp, kp)
+    step = lambda stream=None: E.e3conv_diff_attention_backward(q, k, v, lam, *kept, g, qp, kp, stream=stream)
+    want = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.fill_(3)
+        other = torch.full((1 << 22,), 5.0, device="cuda")
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and bool((other == 5).all())
+        assert all(torch.equal(a, b) for a, b in zip(step(), want))
